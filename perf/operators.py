@@ -286,7 +286,7 @@ def run(state):
                    renormalize=True, scale=2.5, ids=c["ids"], weights=c["weights"])
         if op == "gate":
             return c["ids"], c["weights"]
-        W.fp8b_moe_layer(c["x"], c["ids"], c["weights"], c["w13"], c["s13"], c["w2"], c["s2"], out=c["out"],
+        W.fp8b_moe_layer(c["x"], c["ids"], c["weights"], c["w13"], c["s13"], c["w2"], c["s2"], c["I"], out=c["out"],
                          workspace=c["work"])
         return c["ids"], c["weights"], c["out"]
     if op == "quant":
