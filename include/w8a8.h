@@ -578,6 +578,119 @@ int w8a8_w4a16_moe_grouped(int fmt, const uint16_t* x_rows, const int64_t* group
                            int64_t H, int64_t I, const void* w13_packed, const void* w2_packed, uint16_t* y,
                            void* workspace, int64_t ws_bytes, void* stream);
 
+/*
+ * Expert router.  [DSV4 §三: the expert runner is handed topk_ids and
+ * topk_weights; the router that makes them is not on the page, the definition
+ * is this library's.]
+ *   logits       device, [T, E] of `dtype`, row stride ld >= E elements
+ *   bias         device, float [E], or NULL
+ *   topk_ids     device, int32 [T, top_k], written; input of w8a8_moe_route
+ *   topk_weights device, float [T, top_k], written; input of the combine
+ * score[e] = 1 / (1 + exp(-l[e])) (W8A8_GATE_SIGMOID) or exp(l[e] - max) / sum
+ * (W8A8_GATE_SOFTMAX); key[e] = score[e] + bias[e]. An expert whose logit is
+ * NaN or -inf, or whose key is NaN or -inf, is out (a mask of -inf switches
+ * experts off for a token); a logit of +inf counts as the largest float.
+ * n_group > 1: the mark of a group of E / n_group consecutive experts is the
+ * sum of its two largest keys (the key if one is in); only the topk_group
+ * groups of largest mark stay, lowest index first among equals. The top_k
+ * experts of largest key follow in that order, lowest index first among
+ * equals; a slot that no expert fills gets id -1 (w8a8_moe_route drops it) and
+ * weight 0. The weight of an expert is its score, divided by the sum of the
+ * selected scores if renormalize (0 if that sum is 0), times scale. Keys are
+ * compared as doubles, weights rounded once to float.
+ * 1 <= E <= 1024, n_group <= 64 dividing E, top_k <= 64 and no more than the
+ * experts of topk_group groups, T * top_k < 2^31, scale finite.
+ */
+typedef enum {
+  W8A8_DT_F32 = 0,
+  W8A8_DT_BF16 = 1,
+  W8A8_DT_F16 = 2
+} w8a8_dtype;
+#define W8A8_GATE_SOFTMAX 0
+#define W8A8_GATE_SIGMOID 1
+int w8a8_moe_gate(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int scoring,
+                  int64_t n_group, int64_t topk_group, int64_t top_k, int renormalize, float scale,
+                  int32_t* topk_ids, float* topk_weights, void* stream);
+
+/*
+ * Block-scaled FP8.  ["Qwen3.8-FP8 on Ascend 950: Why Weights Become MXFP8 at
+ * Load Time", Deep Dive 1: E4M3 weights with one fp32 weight_scale_inv per
+ * 128 x 128 tile. These entry points multiply that form as it is.]
+ *
+ * w8a8_fp8b_quant: BF16 rows -> E4M3 codes with one fp32 scale per row and
+ *   block of 128 columns.
+ *     x      device, BF16 [M, K] (W8A8_ACT_NONE) or [gate | up] [M, 2K]
+ *            (W8A8_ACT_SWIGLU), row stride ldx elements
+ *     q      device, uint8 [M, Kp], Kp = K rounded up to 128, 16-byte aligned,
+ *            written whole (codes past K are 0)
+ *     scale  device, float [ceil(K/128), M], written (block-major: the scales
+ *            of one block of all rows lie together)
+ *   v = x, or silu(gate) * up by the fixed fp32 sequence of
+ *   w8a8_swiglu_quant; scale = max|v| / 448 over the block, the code is E4M3
+ *   (half to even, saturating at 448) of v / scale, both one IEEE fp32
+ *   division; a block of zeros gets scale 0 and codes 0. scale_alg 1 takes the
+ *   smallest power of two (at least 2^-126) not below max|v| / 448 instead. A
+ *   NaN or infinity in a block makes its scale NaN or infinite.
+ * w8a8_fp8b_packed_bytes / w8a8_fp8b_prepack_weight: E4M3 codes w [E, N, K] ->
+ *   the load-time layout of the products: 2 KB blocks [e][n/16][k/128] of two
+ *   1 KB pieces, byte 16 l + j of piece h = w[16 (n/16) + l % 16][128 (k/128) +
+ *   64 h + 16 (l/16) + j], N zero-padded to 16 and K to 128. 16-byte aligned.
+ * w8a8_fp8b_linear: y[m, n] = BF16(sum over blocks b of s_x[m, b] *
+ *   s_w[n/128, b] * sum of the block's code products + bias[n]).
+ *     x        BF16 [M, K], row stride ldx (x_scale NULL: quantized inside, as
+ *              w8a8_fp8b_quant with scale_alg), or E4M3 codes [M, Kp] with
+ *              x_scale [ceil(K/128), M] as w8a8_fp8b_quant writes them
+ *              (16-byte aligned, ldx % 16 == 0)
+ *     w_scale  float [ceil(N/128), ceil(K/128)], the checkpoint's
+ *     bias     BF16 [N] or NULL; y BF16 [M, N], row stride ldy
+ *     workspace  w8a8_fp8b_linear_workspace_bytes(M, N, K) bytes, 256-byte
+ *              aligned, rewritten by every call
+ *   The products of a block are summed by the FP8 matrix unit, which cuts each
+ *   product to a multiple of 2^(E - 13), E the largest exponent sum of the
+ *   products of 8 consecutive k; everything after is fp32.
+ * w8a8_fp8b_grouped_gemm: rows grouped by expert (group_list as for
+ *   w8a8_grouped_gemm), a = codes [a_rows, Kp], a_scale [ceil(K/128), a_rows].
+ *   Output row r reads row row_index[r] of a (clamped to [0, a_rows)), or row
+ *   r if row_index is NULL: the rows of a token need no copy per expert. w,
+ *   w_scale stacked over E. Rows past the counts are left as they are.
+ *   workspace: w8a8_fp8b_grouped_workspace_bytes(R, E, N, K) bytes.
+ * w8a8_fp8b_moe_grouped: the expert chain on expert-grouped rows, BF16 [R, H]
+ *   (x_scale NULL) or codes [R, Hp] with x_scale [ceil(H/128), R]: W13 (N =
+ *   2I, [gate | up]) -> BF16 -> w8a8_fp8b_quant(ACT_SWIGLU) -> W2 -> y BF16
+ *   [R, H]. w13_scale [E, ceil(2I/128), ceil(H/128)], w2_scale [E,
+ *   ceil(H/128), ceil(I/128)].
+ * w8a8_fp8b_moe_layer: x BF16 [T, H] -> out BF16 [T, H]: quantize the tokens
+ *   once, route (w8a8_moe_route), the chain with the tokens' rows read through
+ *   the routing, combine (w8a8_moe_combine). topk_ids, topk_weights as
+ *   w8a8_moe_gate writes them.
+ * 1 <= K, H, I <= W8A8_MAX_K, N, 2I <= 2^22, M, R, T * top_k < 2^30. Workspaces
+ * 256-byte aligned and rewritten by every call: two calls that may overlap
+ * need two.
+ */
+int w8a8_fp8b_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int act, int scale_alg, uint8_t* q,
+                    float* scale, void* stream);
+int64_t w8a8_fp8b_packed_bytes(int64_t E, int64_t N, int64_t K);
+int w8a8_fp8b_prepack_weight(const uint8_t* w, int64_t E, int64_t N, int64_t K, void* w_packed, void* stream);
+int64_t w8a8_fp8b_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int w8a8_fp8b_linear(const void* x, int64_t ldx, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
+                     const float* w_scale, int64_t N, const uint16_t* bias, uint16_t* y, int64_t ldy, int scale_alg,
+                     void* workspace, int64_t ws_bytes, void* stream);
+int64_t w8a8_fp8b_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K);
+int w8a8_fp8b_grouped_gemm(const uint8_t* a, const float* a_scale, int64_t a_rows, const int32_t* row_index,
+                           const int64_t* group_list, int64_t R, int64_t E, int64_t N, int64_t K,
+                           const void* w_packed, const float* w_scale, uint16_t* y, void* workspace,
+                           int64_t ws_bytes, void* stream);
+int64_t w8a8_fp8b_moe_workspace_bytes(int64_t R, int64_t E, int64_t H, int64_t I);
+int w8a8_fp8b_moe_grouped(const void* x_rows, const float* x_scale, const int64_t* group_list, int64_t R, int64_t E,
+                          int64_t H, int64_t I, const void* w13_packed, const float* w13_scale,
+                          const void* w2_packed, const float* w2_scale, int scale_alg, uint16_t* y, void* workspace,
+                          int64_t ws_bytes, void* stream);
+int64_t w8a8_fp8b_moe_layer_workspace_bytes(int64_t T, int64_t top_k, int64_t E, int64_t H, int64_t I);
+int w8a8_fp8b_moe_layer(const uint16_t* x, int64_t T, int64_t H, const int32_t* topk_ids, const float* topk_weights,
+                        int64_t top_k, int64_t E, int64_t I, const void* w13_packed, const float* w13_scale,
+                        const void* w2_packed, const float* w2_scale, int scale_alg, uint16_t* out, void* workspace,
+                        int64_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -76,6 +76,20 @@ __all__ = [
     "static_quant_packed",
     "static_prepare",
     "static_linear",
+    "GATE_SOFTMAX",
+    "GATE_SIGMOID",
+    "moe_gate",
+    "fp8b_quant",
+    "fp8b_packed_bytes",
+    "fp8b_prepack_weight",
+    "fp8b_linear_workspace_bytes",
+    "fp8b_linear",
+    "fp8b_grouped_workspace_bytes",
+    "fp8b_grouped_gemm",
+    "fp8b_moe_workspace_bytes",
+    "fp8b_moe_grouped",
+    "fp8b_moe_layer_workspace_bytes",
+    "fp8b_moe_layer",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw8a8.so")
@@ -177,6 +191,27 @@ def _load():
                                                ctypes.c_float, _c_p, _c_p, _c_p]),
         "w8a8_static_linear": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p,
                                               ctypes.c_int, _c_p]),
+        "w8a8_moe_gate": (ctypes.c_int, [_c_p, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_p, ctypes.c_int,
+                                         _c_i64, _c_i64, _c_i64, ctypes.c_int, ctypes.c_float, _c_p,
+                                         _c_p, _c_p]),
+        "w8a8_fp8b_quant": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, ctypes.c_int, ctypes.c_int,
+                                           _c_p, _c_p, _c_p]),
+        "w8a8_fp8b_packed_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64]),
+        "w8a8_fp8b_prepack_weight": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p]),
+        "w8a8_fp8b_linear_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64]),
+        "w8a8_fp8b_linear": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p,
+                                            _c_p, _c_i64, ctypes.c_int, _c_p, _c_i64, _c_p]),
+        "w8a8_fp8b_grouped_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_i64]),
+        "w8a8_fp8b_grouped_gemm": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_i64,
+                                                  _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_p]),
+        "w8a8_fp8b_moe_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_i64]),
+        "w8a8_fp8b_moe_grouped": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p,
+                                                 _c_p, _c_p, _c_p, ctypes.c_int, _c_p, _c_p, _c_i64,
+                                                 _c_p]),
+        "w8a8_fp8b_moe_layer_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64]),
+        "w8a8_fp8b_moe_layer": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_i64,
+                                               _c_p, _c_p, _c_p, _c_p, ctypes.c_int, _c_p, _c_p, _c_i64,
+                                               _c_p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -1072,3 +1107,285 @@ def static_linear(q: torch.Tensor, w_packed: torch.Tensor, deq_scale: torch.Tens
     _check(lib.w8a8_static_linear(_ptr(q), M, K, _ptr(w_packed), _ptr(deq_scale), _ptr(quant_bias), N,
                                   _ptr(y), out | flag, _stream()))
     return y
+
+
+# ---------------------------------------------------------------------------
+# expert router
+# ---------------------------------------------------------------------------
+GATE_SOFTMAX, GATE_SIGMOID = 0, 1
+_LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _here(*tensors):
+    """Every given tensor on the current device, whose stream the call uses."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def moe_gate(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None,
+             scoring: int = GATE_SOFTMAX, n_group: int = 1, topk_group: int = 1,
+             renormalize: bool = True, scale: float = 1.0, ids: torch.Tensor | None = None,
+             weights: torch.Tensor | None = None):
+    """Router logits [T, E] (float32, bfloat16 or float16, rows contiguous) ->
+    (topk_ids int32 [T, top_k], topk_weights float32 [T, top_k]) for moe_layer,
+    fp8b_moe_layer, moe_route and moe_combine. Scores are sigmoids or the softmax;
+    ``bias`` (float32 [E]) moves the choice but not the weights; with n_group > 1
+    only the topk_group best groups are chosen from. A logit of -inf switches an
+    expert off for a token; slots that no expert fills get id -1, weight 0."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _LOGIT_TYPES:
+        raise TypeError("logits must be a float32, bfloat16 or float16 tensor")
+    ld = _rows(logits, logits.dtype, "logits")
+    T, E = logits.shape
+    if ids is None:
+        ids = torch.empty((T, max(top_k, 0)), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, max(top_k, 0)), dtype=torch.float32, device=logits.device)
+    _need(ids, torch.int32, "ids", 2)
+    _need(weights, torch.float32, "weights", 2)
+    if tuple(ids.shape) != (T, top_k) or tuple(weights.shape) != (T, top_k):
+        raise ValueError("ids / weights must be [T, top_k]")
+    if bias is not None:
+        _need(bias, torch.float32, "bias", 1)
+        if bias.shape[0] != E:
+            raise ValueError("bias must be [E]")
+    _here(logits, bias, ids, weights)
+    _check(lib.w8a8_moe_gate(_ptr(logits), _LOGIT_TYPES[logits.dtype], T, E, ld, _ptr(bias), scoring,
+                             n_group, topk_group, top_k, int(bool(renormalize)), scale, _ptr(ids),
+                             _ptr(weights), _stream()))
+    return ids, weights
+
+
+# ---------------------------------------------------------------------------
+# block-scaled FP8
+# ---------------------------------------------------------------------------
+def _fp8_blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def fp8b_quant(x: torch.Tensor, act: int = ACT_NONE, scale_alg: int = 0, q: torch.Tensor | None = None,
+               scale: torch.Tensor | None = None):
+    """BF16 [M, K], or [gate | up] [M, 2K] with act=ACT_SWIGLU (rows contiguous, a row
+    stride is fine) -> (E4M3 codes uint8 [M, K rounded up to 128], float32 scales
+    [ceil(K/128), M])."""
+    ldx = _rows(x, torch.bfloat16, "x")
+    M, K = x.shape
+    if act == ACT_SWIGLU:
+        if K % 2:
+            raise ValueError("ACT_SWIGLU needs [gate | up] rows of even width")
+        K //= 2
+    B = _fp8_blocks(K)
+    if q is None:
+        q = torch.empty((M, 128 * B), dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = torch.empty((B, M), dtype=torch.float32, device=x.device)
+    _need(q, torch.uint8, "q", 2)
+    _need(scale, torch.float32, "scale", 2)
+    if tuple(q.shape) != (M, 128 * B) or tuple(scale.shape) != (B, M):
+        raise ValueError("q must be [M, K rounded up to 128], scale [ceil(K/128), M]")
+    _here(x, q, scale)
+    _check(lib.w8a8_fp8b_quant(_ptr(x), M, K, ldx, act, scale_alg, _ptr(q), _ptr(scale), _stream()))
+    return q, scale
+
+
+def fp8b_packed_bytes(E: int, N: int, K: int) -> int:
+    return int(lib.w8a8_fp8b_packed_bytes(E, N, K))
+
+
+def fp8b_prepack_weight(w_e4m3: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """E4M3 codes uint8 [N, K] or [E, N, K] -> packed uint8 buffer (stable, caller-owned)."""
+    _need(w_e4m3, torch.uint8, "w_e4m3")
+    if w_e4m3.dim() == 2:
+        E, (N, K) = 1, w_e4m3.shape
+    elif w_e4m3.dim() == 3:
+        E, N, K = w_e4m3.shape
+    else:
+        raise ValueError("w_e4m3 must be [N, K] or [E, N, K]")
+    nbytes = fp8b_packed_bytes(E, N, K)
+    if out is None:
+        out = torch.empty((nbytes,), dtype=torch.uint8, device=w_e4m3.device)
+    _need(out, torch.uint8, "out", 1)
+    if out.numel() < nbytes:
+        raise ValueError(f"out needs {nbytes} bytes")
+    _here(w_e4m3, out)
+    _check(lib.w8a8_fp8b_prepack_weight(_ptr(w_e4m3), E, N, K, _ptr(out), _stream()))
+    return out
+
+
+def fp8b_linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib.w8a8_fp8b_linear_workspace_bytes(M, N, K))
+
+
+def fp8b_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor, N: int,
+                x_scale: torch.Tensor | None = None, K: int | None = None,
+                bias: torch.Tensor | None = None, scale_alg: int = 0, y: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Block-scaled FP8 linear: BF16 x [M, K] (quantized inside), or the codes and scales
+    of fp8b_quant (x uint8 [M, K rounded up to 128], x_scale; K if it is not a multiple
+    of 128), times a packed E4M3 weight with w_scale float32 [ceil(N/128), ceil(K/128)]
+    -> BF16 [M, N]. x and y may be row-strided."""
+    if x_scale is None:
+        ldx = _rows(x, torch.bfloat16, "x")
+        M, Kx = x.shape
+        if K is not None and K != Kx:
+            raise ValueError("K must be the width of a BF16 x")
+        K = Kx
+    else:
+        ldx = _rows(x, torch.uint8, "x")
+        M = x.shape[0]
+        K = x.shape[1] if K is None else K
+        if x.shape[1] != 128 * _fp8_blocks(K):
+            raise ValueError("E4M3 x must be [M, K rounded up to 128]")
+        _need(x_scale, torch.float32, "x_scale", 2)
+        if tuple(x_scale.shape) != (_fp8_blocks(K), M):
+            raise ValueError("x_scale must be [ceil(K/128), M]")
+    _need(w_packed, torch.uint8, "w_packed", 1)
+    _need(w_scale, torch.float32, "w_scale", 2)
+    if w_packed.numel() < fp8b_packed_bytes(1, N, K):
+        raise ValueError("w_packed too small for [N, K]")
+    if tuple(w_scale.shape) != (_fp8_blocks(N), _fp8_blocks(K)):
+        raise ValueError("w_scale must be [ceil(N/128), ceil(K/128)]")
+    if bias is not None:
+        _need(bias, torch.bfloat16, "bias", 1)
+        if bias.shape[0] != N:
+            raise ValueError("bias shape mismatch")
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    ldy = _rows(y, torch.bfloat16, "y")
+    if tuple(y.shape) != (M, N):
+        raise ValueError("y shape mismatch")
+    ws, ws_n = _workspace(fp8b_linear_workspace_bytes(M, N, K) if x_scale is None else 0, x.device, workspace)
+    _here(x, x_scale, w_packed, w_scale, bias, y, ws)
+    _check(lib.w8a8_fp8b_linear(_ptr(x), ldx, _ptr(x_scale), M, K, _ptr(w_packed), _ptr(w_scale), N,
+                                _ptr(bias), _ptr(y), ldy, scale_alg, _ptr(ws), ws_n, _stream()))
+    return y
+
+
+def fp8b_grouped_workspace_bytes(R: int, E: int, N: int, K: int) -> int:
+    return int(lib.w8a8_fp8b_grouped_workspace_bytes(R, E, N, K))
+
+
+def fp8b_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, group_list: torch.Tensor,
+                      w_packed: torch.Tensor, w_scale: torch.Tensor, N: int, K: int | None = None,
+                      row_index: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Expert-grouped codes and scales of fp8b_quant (a uint8 [A, K rounded up to 128],
+    a_scale [ceil(K/128), A]) times each expert's packed weight (w_scale [E, ceil(N/128),
+    ceil(K/128)]) -> BF16 [R, N]. Output row r reads row row_index[r] of a (int32 [R]), or
+    row r without it (R = A)."""
+    _need(a, torch.uint8, "a", 2)
+    _need(a_scale, torch.float32, "a_scale", 2)
+    _need(group_list, torch.int64, "group_list", 1)
+    _need(w_packed, torch.uint8, "w_packed", 1)
+    _need(w_scale, torch.float32, "w_scale", 3)
+    A = a.shape[0]
+    K = a.shape[1] if K is None else K
+    E = group_list.shape[0]
+    B = _fp8_blocks(K)
+    if a.shape[1] != 128 * B or tuple(a_scale.shape) != (B, A):
+        raise ValueError("a must be [A, K rounded up to 128], a_scale [ceil(K/128), A]")
+    if tuple(w_scale.shape) != (E, _fp8_blocks(N), B):
+        raise ValueError("w_scale must be [E, ceil(N/128), ceil(K/128)]")
+    if w_packed.numel() < fp8b_packed_bytes(E, N, K):
+        raise ValueError("w_packed too small for [E, N, K]")
+    R = A
+    if row_index is not None:
+        _need(row_index, torch.int32, "row_index", 1)
+        R = row_index.shape[0]
+    if y is None:
+        y = torch.empty((R, N), dtype=torch.bfloat16, device=a.device)
+    _need(y, torch.bfloat16, "y", 2)
+    if tuple(y.shape) != (R, N):
+        raise ValueError("y shape mismatch")
+    ws, ws_n = _workspace(fp8b_grouped_workspace_bytes(R, E, N, K), a.device, workspace)
+    _here(a, a_scale, group_list, w_packed, w_scale, row_index, y, ws)
+    _check(lib.w8a8_fp8b_grouped_gemm(_ptr(a), _ptr(a_scale), A, _ptr(row_index), _ptr(group_list), R, E,
+                                      N, K, _ptr(w_packed), _ptr(w_scale), _ptr(y), _ptr(ws), ws_n,
+                                      _stream()))
+    return y
+
+
+def fp8b_moe_workspace_bytes(R: int, E: int, H: int, I: int) -> int:
+    return int(lib.w8a8_fp8b_moe_workspace_bytes(R, E, H, I))
+
+
+def _fp8b_experts(w13_packed, w13_scale, w2_packed, w2_scale, E: int, H: int, I: int):
+    for t, n in ((w13_packed, "w13_packed"), (w2_packed, "w2_packed")):
+        _need(t, torch.uint8, n, 1)
+    for t, n in ((w13_scale, "w13_scale"), (w2_scale, "w2_scale")):
+        _need(t, torch.float32, n, 3)
+    if tuple(w13_scale.shape) != (E, _fp8_blocks(2 * I), _fp8_blocks(H)) or \
+            tuple(w2_scale.shape) != (E, _fp8_blocks(H), _fp8_blocks(I)):
+        raise ValueError("w13_scale must be [E, ceil(2I/128), ceil(H/128)], w2_scale [E, ceil(H/128), ceil(I/128)]")
+    if w13_packed.numel() < fp8b_packed_bytes(E, 2 * I, H) or \
+            w2_packed.numel() < fp8b_packed_bytes(E, H, I):
+        raise ValueError("packed weights too small")
+
+
+def fp8b_moe_grouped(x_rows: torch.Tensor, group_list: torch.Tensor, w13_packed: torch.Tensor,
+                     w13_scale: torch.Tensor, w2_packed: torch.Tensor, w2_scale: torch.Tensor, I: int,
+                     H: int | None = None, x_scale: torch.Tensor | None = None, scale_alg: int = 0,
+                     y: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Expert chain on expert-grouped rows, BF16 [R, H] or the codes and scales of
+    fp8b_quant: W13 -> SwiGLU + quant -> W2 -> BF16 [R, H]. I: the width between."""
+    if x_scale is None:
+        _need(x_rows, torch.bfloat16, "x_rows", 2)
+    else:
+        _need(x_rows, torch.uint8, "x_rows", 2)
+        _need(x_scale, torch.float32, "x_scale", 2)
+    _need(group_list, torch.int64, "group_list", 1)
+    R = x_rows.shape[0]
+    H = x_rows.shape[1] if H is None else H
+    E = group_list.shape[0]
+    if x_rows.shape[1] != (H if x_scale is None else 128 * _fp8_blocks(H)):
+        raise ValueError("x_rows does not match H")
+    if x_scale is not None and tuple(x_scale.shape) != (_fp8_blocks(H), R):
+        raise ValueError("x_scale must be [ceil(H/128), R]")
+    _fp8b_experts(w13_packed, w13_scale, w2_packed, w2_scale, E, H, I)
+    if y is None:
+        y = torch.empty((R, H), dtype=torch.bfloat16, device=x_rows.device)
+    _need(y, torch.bfloat16, "y", 2)
+    if tuple(y.shape) != (R, H):
+        raise ValueError("y shape mismatch")
+    ws, ws_n = _workspace(fp8b_moe_workspace_bytes(R, E, H, I), x_rows.device, workspace)
+    _here(x_rows, x_scale, group_list, w13_packed, w13_scale, w2_packed, w2_scale, y, ws)
+    _check(lib.w8a8_fp8b_moe_grouped(_ptr(x_rows), _ptr(x_scale), _ptr(group_list), R, E, H, I,
+                                     _ptr(w13_packed), _ptr(w13_scale), _ptr(w2_packed), _ptr(w2_scale),
+                                     scale_alg, _ptr(y), _ptr(ws), ws_n, _stream()))
+    return y
+
+
+def fp8b_moe_layer_workspace_bytes(T: int, top_k: int, E: int, H: int, I: int) -> int:
+    return int(lib.w8a8_fp8b_moe_layer_workspace_bytes(T, top_k, E, H, I))
+
+
+def fp8b_moe_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.Tensor,
+                   w13_packed: torch.Tensor, w13_scale: torch.Tensor, w2_packed: torch.Tensor,
+                   w2_scale: torch.Tensor, I: int, scale_alg: int = 0,
+                   out: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Whole MoE layer on block-scaled FP8 experts: BF16 tokens [T, H] -> quantize once,
+    route, W13 -> SwiGLU + quant -> W2, weighted combine -> BF16 [T, H]. topk_ids and
+    topk_weights as moe_gate writes them. I: the width between."""
+    _need(x, torch.bfloat16, "x", 2)
+    _need(topk_ids, torch.int32, "topk_ids", 2)
+    _need(topk_weights, torch.float32, "topk_weights", 2)
+    _need(w13_scale, torch.float32, "w13_scale", 3)
+    T, H = x.shape
+    k = topk_ids.shape[1]
+    E = w13_scale.shape[0]
+    if topk_ids.shape[0] != T or tuple(topk_weights.shape) != tuple(topk_ids.shape):
+        raise ValueError("topk_ids / topk_weights must be [T, top_k]")
+    _fp8b_experts(w13_packed, w13_scale, w2_packed, w2_scale, E, H, I)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    _need(out, torch.bfloat16, "out", 2)
+    if tuple(out.shape) != (T, H):
+        raise ValueError("out shape mismatch")
+    ws, ws_n = _workspace(fp8b_moe_layer_workspace_bytes(T, k, E, H, I), x.device, workspace)
+    _here(x, topk_ids, topk_weights, w13_packed, w13_scale, w2_packed, w2_scale, out, ws)
+    _check(lib.w8a8_fp8b_moe_layer(_ptr(x), T, H, _ptr(topk_ids), _ptr(topk_weights), k, E, I,
+                                   _ptr(w13_packed), _ptr(w13_scale), _ptr(w2_packed), _ptr(w2_scale),
+                                   scale_alg, _ptr(out), _ptr(ws), ws_n, _stream()))
+    return out

@@ -1,6 +1,7 @@
 // C ABI of the W8A8_DYNAMIC library: argument checks, workspace sizing and the
 // MoE chain. Declarations and contracts are in include/w8a8.h.
 #include <algorithm>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -10,6 +11,7 @@
 #include <vector>
 
 #include "../../include/w8a8.h"
+#include "fp8b.hpp"
 #include "launch.hpp"
 #include "mx.hpp"
 #include "w4.hpp"
@@ -990,6 +992,371 @@ int w8a8_w4a16_linear(const uint16_t* x, int64_t M, int64_t K, const void* w_pac
   return launched(w8a8::launch_w4a16_linear(x, M, K, reinterpret_cast<const uint8_t*>(w_packed), N, y, workspace,
                                             (hipStream_t)stream),
                   "w4a16_linear");
+}
+
+// ---------------------------------------------------------------------------
+// Expert router
+// ---------------------------------------------------------------------------
+int w8a8_moe_gate(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int scoring,
+                  int64_t n_group, int64_t topk_group, int64_t top_k, int renormalize, float scale,
+                  int32_t* topk_ids, float* topk_weights, void* stream) {
+  if (T < 0 || E < 1 || top_k < 1 || T * top_k >= kMaxDim || ld < E || T >= kMaxDim)
+    return fail(W8A8_ERR_SHAPE, "moe_gate: need T >= 0, E >= 1, ld >= E, top_k >= 1 and T * top_k < 2^31");
+  if (dtype != W8A8_DT_F32 && dtype != W8A8_DT_BF16 && dtype != W8A8_DT_F16)
+    return fail(W8A8_ERR_UNSUPPORTED, "moe_gate: unknown logit type %d", dtype);
+  if (scoring != W8A8_GATE_SOFTMAX && scoring != W8A8_GATE_SIGMOID)
+    return fail(W8A8_ERR_UNSUPPORTED, "moe_gate: unknown scoring %d", scoring);
+  if (E > kMaxExperts) return fail(W8A8_ERR_UNSUPPORTED, "moe_gate: at most %lld experts", (long long)kMaxExperts);
+  if (n_group < 1 || n_group > 64 || E % n_group || topk_group < 1 || topk_group > n_group)
+    return fail(W8A8_ERR_SHAPE,
+                "moe_gate: need 1 <= n_group <= 64 dividing E and 1 <= topk_group <= n_group (E=%lld n_group=%lld "
+                "topk_group=%lld)", (long long)E, (long long)n_group, (long long)topk_group);
+  if (top_k > 64 || top_k > topk_group * (E / n_group))
+    return fail(W8A8_ERR_SHAPE, "moe_gate: top_k = %lld is past 64 or past the experts of topk_group groups",
+                (long long)top_k);
+  if (!std::isfinite(scale)) return fail(W8A8_ERR_SHAPE, "moe_gate: scale must be finite");
+  if (T == 0) return ok();
+  if (!logits || !topk_ids || !topk_weights) return fail(W8A8_ERR_NULL, "moe_gate: null pointer");
+  if (!aligned(logits, dtype == W8A8_DT_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(topk_ids, 4) ||
+      !aligned(topk_weights, 4))
+    return fail(W8A8_ERR_ALIGN, "moe_gate: misaligned buffer");
+  w8a8::GateArgs g{};
+  g.logits = logits;
+  g.dtype = dtype;
+  g.T = T;
+  g.ld = ld;
+  g.E = (int)E;
+  g.bias = bias;
+  g.scoring = scoring;
+  g.n_group = (int)n_group;
+  g.topk_group = (int)topk_group;
+  g.top_k = (int)top_k;
+  g.renormalize = renormalize != 0;
+  g.scale = scale;
+  g.ids = topk_ids;
+  g.weights = topk_weights;
+  return launched(w8a8::launch_gate(g, (hipStream_t)stream), "moe_gate");
+}
+
+// ---------------------------------------------------------------------------
+// Block-scaled FP8
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kFp8MaxN = (int64_t)1 << 22;  // columns: the tile grids stay within 65535
+
+int64_t fp8b_pad(int64_t K) { return w8a8::round_up(K, w8a8::kFp8Block); }
+int64_t fp8b_kb(int64_t K) { return w8a8::ceil_div(K, w8a8::kFp8Block); }
+
+int check_fp8b(const char* who, int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 1 || K < 1 || M >= kMaxDim / 2 || N > kFp8MaxN || K > W8A8_MAX_K)
+    return fail(W8A8_ERR_SHAPE, "%s: need 0 <= M < 2^30, 1 <= N <= 2^22 and 1 <= K <= %d (M=%lld N=%lld K=%lld)", who,
+                W8A8_MAX_K, (long long)M, (long long)N, (long long)K);
+  return W8A8_OK;
+}
+
+int check_fp8b_grouped(const char* who, int64_t R, int64_t E, int64_t N, int64_t K) {
+  int st = check_fp8b(who, R, N, K);
+  if (st) return st;
+  if (E < 1) return fail(W8A8_ERR_SHAPE, "%s: need E >= 1", who);
+  if (E > kMaxExperts) return fail(W8A8_ERR_UNSUPPORTED, "%s: at most %lld experts", who, (long long)kMaxExperts);
+  return W8A8_OK;
+}
+
+int check_scale_alg(const char* who, int alg) {
+  if (alg != 0 && alg != 1) return fail(W8A8_ERR_UNSUPPORTED, "%s: scale_alg must be 0 or 1", who);
+  return W8A8_OK;
+}
+
+// E4M3 codes [M][K padded] and scales [KB][M]
+int64_t fp8b_codes_bytes(int64_t M, int64_t K) { return align256(M * fp8b_pad(K)); }
+int64_t fp8b_scales_bytes(int64_t M, int64_t K) { return align256(M * fp8b_kb(K) * 4); }
+
+struct Fp8bMoeWs {
+  int64_t q1, s1, h, q2, s2, sched, total;
+};
+
+// T rows quantized for W13, R rows through the chain
+Fp8bMoeWs fp8b_moe_layout(int64_t T, int64_t R, int64_t E, int64_t H, int64_t I) {
+  Fp8bMoeWs w{};
+  int64_t o = 0;
+  w.q1 = o; o += fp8b_codes_bytes(T, H);
+  w.s1 = o; o += fp8b_scales_bytes(T, H);
+  w.h = o;  o += align256(R * 2 * I * 2);  // BF16 [R, 2I]
+  w.q2 = o; o += fp8b_codes_bytes(R, I);
+  w.s2 = o; o += fp8b_scales_bytes(R, I);
+  w.sched = o; o += align256(w8a8::fp8b_sched_bytes(E));
+  w.total = o;
+  return w;
+}
+
+w8a8::Fp8bGemm fp8b_args(const uint8_t* a, int64_t lda, const float* a_scale, int64_t a_rows, int64_t M, int64_t K,
+                         const void* w, const float* w_scale, int64_t N, uint16_t* y) {
+  w8a8::Fp8bGemm p{};
+  p.a = a;
+  p.lda = lda;
+  p.a_scale = a_scale;
+  p.a_rows = a_rows;
+  p.M = M;
+  p.KB = fp8b_kb(K);
+  p.w = reinterpret_cast<const uint8_t*>(w);
+  p.w_scale = w_scale;
+  p.N = N;
+  p.y = y;
+  p.ldy = N;
+  return p;
+}
+
+// W13 -> SwiGLU + quant -> W2 on quantized rows: `a` [a_rows][H padded] with
+// scales [KB][a_rows], read at row_index (null: row r itself)
+hipError_t fp8b_chain(const uint8_t* a, const float* a_scale, int64_t a_rows, const int32_t* row_index,
+                      const int64_t* group_list, int64_t R, int64_t E, int64_t H, int64_t I, const void* w13,
+                      const float* w13_scale, const void* w2, const float* w2_scale, int alg, uint16_t* y, char* ws,
+                      const Fp8bMoeWs& L, hipStream_t s) {
+  uint16_t* h = reinterpret_cast<uint16_t*>(ws + L.h);
+  uint8_t* q2 = reinterpret_cast<uint8_t*>(ws + L.q2);
+  float* s2 = reinterpret_cast<float*>(ws + L.s2);
+  w8a8::Fp8bGemm p = fp8b_args(a, fp8b_pad(H), a_scale, a_rows, R, H, w13, w13_scale, 2 * I, h);
+  p.row_index = row_index;
+  p.group_list = group_list;
+  p.E = E;
+  p.ws = ws + L.sched;
+  hipError_t err = w8a8::launch_fp8b_gemm(p, s);
+  if (err != hipSuccess) return err;
+  err = w8a8::launch_fp8b_quant(h, R, I, 2 * I, 1, alg, q2, s2, s);
+  if (err != hipSuccess) return err;
+  p = fp8b_args(q2, fp8b_pad(I), s2, R, R, I, w2, w2_scale, H, y);
+  p.group_list = group_list;
+  p.E = E;
+  p.ws = ws + L.sched;
+  return w8a8::launch_fp8b_gemm(p, s);
+}
+
+}  // namespace
+
+int w8a8_fp8b_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int act, int scale_alg, uint8_t* q,
+                    float* scale, void* stream) {
+  int st = check_fp8b("fp8b_quant", M, 1, K);
+  if (st) return st;
+  st = check_scale_alg("fp8b_quant", scale_alg);
+  if (st) return st;
+  if (act != W8A8_ACT_NONE && act != W8A8_ACT_SWIGLU)
+    return fail(W8A8_ERR_UNSUPPORTED, "fp8b_quant: unknown act %d", act);
+  if (ldx < K * (act == W8A8_ACT_SWIGLU ? 2 : 1))
+    return fail(W8A8_ERR_SHAPE, "fp8b_quant: ldx = %lld is below the row width", (long long)ldx);
+  if (M == 0) return ok();
+  if (!x || !q || !scale) return fail(W8A8_ERR_NULL, "fp8b_quant: null pointer");
+  if (!aligned(x, 2) || !aligned(q, 16) || !aligned(scale, 4))
+    return fail(W8A8_ERR_ALIGN, "fp8b_quant: x needs 2-byte, q 16-byte and scale 4-byte alignment");
+  return launched(w8a8::launch_fp8b_quant(x, M, K, ldx, act, scale_alg, q, scale, (hipStream_t)stream),
+                  "fp8b_quant");
+}
+
+int64_t w8a8_fp8b_packed_bytes(int64_t E, int64_t N, int64_t K) {
+  if (E < 0 || N < 0 || K < 0) return -1;
+  return E * w8a8::fp8b_packed_bytes(N, K);
+}
+
+int w8a8_fp8b_prepack_weight(const uint8_t* w, int64_t E, int64_t N, int64_t K, void* w_packed, void* stream) {
+  int st = check_fp8b("fp8b_prepack_weight", 0, N, K);
+  if (st) return st;
+  if (E < 1) return fail(W8A8_ERR_SHAPE, "fp8b_prepack_weight: need E >= 1");
+  if (!w || !w_packed) return fail(W8A8_ERR_NULL, "fp8b_prepack_weight: null pointer");
+  if (!aligned(w_packed, 16)) return fail(W8A8_ERR_ALIGN, "fp8b_prepack_weight: w_packed not 16-byte aligned");
+  return launched(w8a8::launch_fp8b_prepack(w, E, N, K, w_packed, (hipStream_t)stream), "fp8b_prepack_weight");
+}
+
+int64_t w8a8_fp8b_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return fp8b_codes_bytes(M, K) + fp8b_scales_bytes(M, K);
+}
+
+int w8a8_fp8b_linear(const void* x, int64_t ldx, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
+                     const float* w_scale, int64_t N, const uint16_t* bias, uint16_t* y, int64_t ldy, int scale_alg,
+                     void* workspace, int64_t ws_bytes, void* stream) {
+  int st = check_fp8b("fp8b_linear", M, N, K);
+  if (st) return st;
+  st = check_scale_alg("fp8b_linear", scale_alg);
+  if (st) return st;
+  if (ldy < N || ldx < (x_scale ? fp8b_pad(K) : K))
+    return fail(W8A8_ERR_SHAPE, "fp8b_linear: ldx = %lld or ldy = %lld is below the row width", (long long)ldx,
+                (long long)ldy);
+  if (M == 0) return ok();
+  if (!x || !w_packed || !w_scale || !y) return fail(W8A8_ERR_NULL, "fp8b_linear: null pointer");
+  if (!aligned(w_packed, 16) || !aligned(w_scale, 4) || !aligned(bias, 2) || !aligned(y, 2) ||
+      !aligned(x_scale, 4) || !aligned(x, x_scale ? 16 : 2) || (x_scale && ldx % 16))
+    return fail(W8A8_ERR_ALIGN, "fp8b_linear: w_packed and E4M3 rows need 16-byte, scales 4-byte, BF16 2-byte "
+                                "alignment");
+  hipStream_t s = (hipStream_t)stream;
+  const uint8_t* a = reinterpret_cast<const uint8_t*>(x);
+  const float* as = x_scale;
+  int64_t lda = ldx;
+  if (!x_scale) {
+    const int64_t need = w8a8_fp8b_linear_workspace_bytes(M, N, K);
+    if (!workspace || ws_bytes < need || !aligned(workspace, 256))
+      return fail(W8A8_ERR_WORKSPACE, "fp8b_linear: BF16 input needs %lld workspace bytes (256-byte aligned), got %lld",
+                  (long long)need, (long long)ws_bytes);
+    uint8_t* q = reinterpret_cast<uint8_t*>(workspace);
+    float* sc = reinterpret_cast<float*>(q + fp8b_codes_bytes(M, K));
+    hipError_t err = w8a8::launch_fp8b_quant(reinterpret_cast<const uint16_t*>(x), M, K, ldx, 0, scale_alg, q, sc, s);
+    if (err != hipSuccess) return launched(err, "fp8b_linear: quant");
+    a = q;
+    as = sc;
+    lda = fp8b_pad(K);
+  }
+  w8a8::Fp8bGemm p = fp8b_args(a, lda, as, M, M, K, w_packed, w_scale, N, y);
+  p.bias = bias;
+  p.ldy = ldy;
+  return launched(w8a8::launch_fp8b_gemm(p, s), "fp8b_linear");
+}
+
+int64_t w8a8_fp8b_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K) {
+  if (R <= 0 || E <= 0 || N <= 0 || K <= 0) return 0;
+  return w8a8::fp8b_sched_bytes(E);
+}
+
+int w8a8_fp8b_grouped_gemm(const uint8_t* a, const float* a_scale, int64_t a_rows, const int32_t* row_index,
+                           const int64_t* group_list, int64_t R, int64_t E, int64_t N, int64_t K,
+                           const void* w_packed, const float* w_scale, uint16_t* y, void* workspace,
+                           int64_t ws_bytes, void* stream) {
+  int st = check_fp8b_grouped("fp8b_grouped_gemm", R, E, N, K);
+  if (st) return st;
+  if (R == 0) return ok();
+  if (a_rows < 1 || a_rows >= kMaxDim / 2 || (!row_index && a_rows < R))
+    return fail(W8A8_ERR_SHAPE, "fp8b_grouped_gemm: a_rows = %lld rows do not cover R = %lld", (long long)a_rows,
+                (long long)R);
+  if (!a || !a_scale || !group_list || !w_packed || !w_scale || !y)
+    return fail(W8A8_ERR_NULL, "fp8b_grouped_gemm: null pointer");
+  if (!aligned(a, 16) || !aligned(a_scale, 4) || !aligned(row_index, 4) || !aligned(group_list, 8) ||
+      !aligned(w_packed, 16) || !aligned(w_scale, 4) || !aligned(y, 2))
+    return fail(W8A8_ERR_ALIGN, "fp8b_grouped_gemm: misaligned buffer");
+  const int64_t need = w8a8::fp8b_sched_bytes(E);
+  if (!workspace || ws_bytes < need || !aligned(workspace, 256))
+    return fail(W8A8_ERR_WORKSPACE, "fp8b_grouped_gemm: needs %lld workspace bytes (256-byte aligned), got %lld",
+                (long long)need, (long long)ws_bytes);
+  st = check_group_list("fp8b_grouped_gemm", group_list, E, R, stream);
+  if (st) return st;
+  w8a8::Fp8bGemm p = fp8b_args(a, fp8b_pad(K), a_scale, a_rows, R, K, w_packed, w_scale, N, y);
+  p.row_index = row_index;
+  p.group_list = group_list;
+  p.E = E;
+  p.ws = workspace;
+  return launched(w8a8::launch_fp8b_gemm(p, (hipStream_t)stream), "fp8b_grouped_gemm");
+}
+
+int64_t w8a8_fp8b_moe_workspace_bytes(int64_t R, int64_t E, int64_t H, int64_t I) {
+  if (R <= 0 || E <= 0 || H <= 0 || I <= 0) return 0;
+  return fp8b_moe_layout(R, R, E, H, I).total;
+}
+
+int w8a8_fp8b_moe_grouped(const void* x_rows, const float* x_scale, const int64_t* group_list, int64_t R, int64_t E,
+                          int64_t H, int64_t I, const void* w13_packed, const float* w13_scale,
+                          const void* w2_packed, const float* w2_scale, int scale_alg, uint16_t* y, void* workspace,
+                          int64_t ws_bytes, void* stream) {
+  int st = check_fp8b_grouped("fp8b_moe_grouped", R, E, 2 * I, H);
+  if (st) return st;
+  st = check_fp8b_grouped("fp8b_moe_grouped", R, E, H, I);
+  if (st) return st;
+  st = check_scale_alg("fp8b_moe_grouped", scale_alg);
+  if (st) return st;
+  if (R == 0) return ok();
+  if (!x_rows || !group_list || !w13_packed || !w13_scale || !w2_packed || !w2_scale || !y)
+    return fail(W8A8_ERR_NULL, "fp8b_moe_grouped: null pointer");
+  if (!aligned(x_rows, x_scale ? 16 : 2) || !aligned(x_scale, 4) || !aligned(group_list, 8) ||
+      !aligned(w13_packed, 16) || !aligned(w13_scale, 4) || !aligned(w2_packed, 16) || !aligned(w2_scale, 4) ||
+      !aligned(y, 2))
+    return fail(W8A8_ERR_ALIGN, "fp8b_moe_grouped: misaligned buffer");
+  const Fp8bMoeWs L = fp8b_moe_layout(R, R, E, H, I);
+  if (!workspace || ws_bytes < L.total || !aligned(workspace, 256))
+    return fail(W8A8_ERR_WORKSPACE, "fp8b_moe_grouped: needs %lld workspace bytes (256-byte aligned), got %lld",
+                (long long)L.total, (long long)ws_bytes);
+  st = check_group_list("fp8b_moe_grouped", group_list, E, R, stream);
+  if (st) return st;
+  hipStream_t s = (hipStream_t)stream;
+  char* ws = reinterpret_cast<char*>(workspace);
+  const uint8_t* a = reinterpret_cast<const uint8_t*>(x_rows);
+  const float* as = x_scale;
+  if (!x_scale) {
+    uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.q1);
+    float* sc = reinterpret_cast<float*>(ws + L.s1);
+    hipError_t err = w8a8::launch_fp8b_quant(reinterpret_cast<const uint16_t*>(x_rows), R, H, H, 0, scale_alg, q, sc, s);
+    if (err != hipSuccess) return launched(err, "fp8b_moe_grouped: quant");
+    a = q;
+    as = sc;
+  }
+  return launched(fp8b_chain(a, as, R, nullptr, group_list, R, E, H, I, w13_packed, w13_scale, w2_packed, w2_scale,
+                             scale_alg, y, ws, L, s),
+                  "fp8b_moe_grouped");
+}
+
+namespace {
+
+struct Fp8bLayerWs {
+  int64_t gl, rt, pr, y, chain, total;
+};
+
+Fp8bLayerWs fp8b_layer_layout(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+  const int64_t P = T * k;
+  Fp8bLayerWs w{};
+  int64_t o = 0;
+  w.gl = o; o += align256(E * 8);      // int64 [E]
+  w.rt = o; o += align256(P * 4);      // int32 [T * k]
+  w.pr = o; o += align256(P * 4);      // int32 [T, k]
+  w.y = o;  o += align256(P * H * 2);  // BF16 [T * k, H]
+  w.chain = o;
+  o += fp8b_moe_layout(T, P, E, H, I).total;
+  w.total = o;
+  return w;
+}
+
+}  // namespace
+
+int64_t w8a8_fp8b_moe_layer_workspace_bytes(int64_t T, int64_t top_k, int64_t E, int64_t H, int64_t I) {
+  if (T <= 0 || top_k <= 0 || E <= 0 || H <= 0 || I <= 0) return 0;
+  return fp8b_layer_layout(T, top_k, E, H, I).total;
+}
+
+int w8a8_fp8b_moe_layer(const uint16_t* x, int64_t T, int64_t H, const int32_t* topk_ids, const float* topk_weights,
+                        int64_t top_k, int64_t E, int64_t I, const void* w13_packed, const float* w13_scale,
+                        const void* w2_packed, const float* w2_scale, int scale_alg, uint16_t* out, void* workspace,
+                        int64_t ws_bytes, void* stream) {
+  int st = check_route("fp8b_moe_layer", T, top_k, E);
+  if (st) return st;
+  const int64_t P = T * top_k;
+  st = check_fp8b_grouped("fp8b_moe_layer", P, E, 2 * I, H);
+  if (st) return st;
+  st = check_fp8b_grouped("fp8b_moe_layer", P, E, H, I);
+  if (st) return st;
+  st = check_scale_alg("fp8b_moe_layer", scale_alg);
+  if (st) return st;
+  if (T == 0) return ok();
+  if (!x || !topk_ids || !topk_weights || !w13_packed || !w13_scale || !w2_packed || !w2_scale || !out)
+    return fail(W8A8_ERR_NULL, "fp8b_moe_layer: null pointer");
+  if (!aligned(x, 2) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(w13_packed, 16) ||
+      !aligned(w2_packed, 16) || !aligned(w13_scale, 4) || !aligned(w2_scale, 4) || !aligned(out, 2))
+    return fail(W8A8_ERR_ALIGN, "fp8b_moe_layer: misaligned buffer");
+  const Fp8bLayerWs L = fp8b_layer_layout(T, top_k, E, H, I);
+  if (!workspace || ws_bytes < L.total || !aligned(workspace, 256))
+    return fail(W8A8_ERR_WORKSPACE, "fp8b_moe_layer: needs %lld workspace bytes (256-byte aligned), got %lld",
+                (long long)L.total, (long long)ws_bytes);
+  hipStream_t s = (hipStream_t)stream;
+  char* ws = reinterpret_cast<char*>(workspace);
+  int64_t* gl = reinterpret_cast<int64_t*>(ws + L.gl);
+  int32_t* rt = reinterpret_cast<int32_t*>(ws + L.rt);
+  int32_t* pr = reinterpret_cast<int32_t*>(ws + L.pr);
+  uint16_t* y = reinterpret_cast<uint16_t*>(ws + L.y);
+  char* chain = ws + L.chain;
+  const Fp8bMoeWs C = fp8b_moe_layout(T, P, E, H, I);
+  uint8_t* q = reinterpret_cast<uint8_t*>(chain + C.q1);
+  float* sc = reinterpret_cast<float*>(chain + C.s1);
+  hipError_t err = w8a8::launch_fp8b_quant(x, T, H, H, 0, scale_alg, q, sc, s);
+  if (err != hipSuccess) return launched(err, "fp8b_moe_layer: quant");
+  err = w8a8::launch_route(topk_ids, T, top_k, E, gl, rt, pr, s);
+  if (err != hipSuccess) return launched(err, "fp8b_moe_layer: route");
+  err = fp8b_chain(q, sc, T, rt, gl, P, E, H, I, w13_packed, w13_scale, w2_packed, w2_scale, scale_alg, y, chain, C,
+                   s);
+  if (err != hipSuccess) return launched(err, "fp8b_moe_layer: experts");
+  return launched(w8a8::launch_combine(y, pr, topk_weights, T, top_k, P, H, out, s), "fp8b_moe_layer: combine");
 }
 
 }  // extern "C"

@@ -27,5 +27,6 @@ from . import static_ref as static  # noqa: F401
 from . import moe_io_ref as moe_io  # noqa: F401
 from . import mx_moe_ref as mx_moe  # noqa: F401
 from . import w4a16_ref as w4a16  # noqa: F401
+from . import fp8b_ref as fp8b  # noqa: F401
 from .w8a8_ref import *  # noqa: F401,F403
 from .w8a8_ref import __all__  # noqa: F401

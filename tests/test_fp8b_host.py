@@ -1,0 +1,147 @@
+"""Refusals and sizes of the router and the block-scaled FP8 entry points (CPU only):
+every call fails its checks before anything is launched, or does nothing."""
+
+from __future__ import annotations
+
+import ctypes
+import math
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+from tests.test_kernel_resources import CSRC, MAX_SCRATCH, _flags, _hipcc, _innermost_mfma_loops
+
+OK, NULL, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3, 4, 5
+P = ctypes.c_void_p(256)      # never dereferenced: the checks fail first
+ODD = ctypes.c_void_p(257)
+
+
+@pytest.fixture(scope="module")
+def w():
+    import moe_token_amax_amd as w
+    return w
+
+
+def _gate(L, logits=P, dtype=0, T=4, E=64, ld=64, bias=None, scoring=1, n_group=1, topk_group=1, top_k=2, renorm=1,
+          scale=1.0, ids=P, weights=P):
+    return L.w8a8_moe_gate(logits, dtype, T, E, ld, bias, scoring, n_group, topk_group, top_k, renorm, scale, ids,
+                           weights, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), SHAPE), (dict(E=0), SHAPE), (dict(ld=63), SHAPE), (dict(top_k=0), SHAPE),
+    (dict(T=1 << 30, top_k=2), SHAPE), (dict(dtype=3), UNSUPPORTED), (dict(scoring=2), UNSUPPORTED),
+    (dict(E=1025, ld=1025), UNSUPPORTED), (dict(n_group=0), SHAPE), (dict(n_group=3), SHAPE),
+    (dict(E=130, ld=130, n_group=65), SHAPE), (dict(n_group=4, topk_group=5), SHAPE), (dict(topk_group=0), SHAPE),
+    (dict(top_k=65, E=128, ld=128), SHAPE), (dict(n_group=8, topk_group=1, top_k=9), SHAPE),
+    (dict(scale=math.inf), SHAPE), (dict(scale=math.nan), SHAPE), (dict(logits=None), NULL), (dict(ids=None), NULL),
+    (dict(weights=None), NULL), (dict(logits=ODD), ALIGN), (dict(bias=ODD), ALIGN), (dict(ids=ODD), ALIGN),
+    (dict(T=0, logits=None, ids=None, weights=None), OK)])
+def test_gate_refusals(w, kw, status):
+    assert _gate(w.lib, **kw) == status
+    assert (w.lib.w8a8_last_error() == b"") == (status == OK)
+
+
+def _quant(L, x=P, M=4, K=64, ldx=64, act=0, alg=0, q=P, s=P):
+    return L.w8a8_fp8b_quant(x, M, K, ldx, act, alg, q, s, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), SHAPE), (dict(K=0), SHAPE), (dict(K=200000, ldx=200000), SHAPE), (dict(M=1 << 30), SHAPE),
+    (dict(ldx=63), SHAPE), (dict(act=1, ldx=127), SHAPE), (dict(act=2), UNSUPPORTED), (dict(alg=2), UNSUPPORTED),
+    (dict(x=None), NULL), (dict(q=None), NULL), (dict(s=None), NULL), (dict(x=ODD), ALIGN),
+    (dict(q=ctypes.c_void_p(264)), ALIGN), (dict(s=ODD), ALIGN), (dict(M=0, x=None, q=None, s=None), OK)])
+def test_quant_refusals(w, kw, status):
+    assert _quant(w.lib, **kw) == status
+
+
+def _linear(L, x=P, ldx=64, xs=None, M=4, K=64, wp=P, ws=P, N=8, bias=None, y=P, ldy=8, alg=0, room=P, n=1 << 20):
+    return L.w8a8_fp8b_linear(x, ldx, xs, M, K, wp, ws, N, bias, y, ldy, alg, room, n, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=-1), SHAPE), (dict(N=0), SHAPE), (dict(N=(1 << 22) + 1, ldy=1 << 23), SHAPE), (dict(ldx=63), SHAPE),
+    (dict(ldy=7), SHAPE), (dict(xs=P, ldx=64), SHAPE), (dict(alg=-1), UNSUPPORTED), (dict(x=None), NULL),
+    (dict(wp=None), NULL), (dict(ws=None), NULL), (dict(y=None), NULL), (dict(wp=ctypes.c_void_p(264)), ALIGN),
+    (dict(x=ODD), ALIGN), (dict(bias=ODD), ALIGN), (dict(xs=P, ldx=136), ALIGN),
+    (dict(xs=P, ldx=128, x=ctypes.c_void_p(264)), ALIGN), (dict(n=100), WORKSPACE), (dict(room=None), WORKSPACE),
+    (dict(room=ctypes.c_void_p(128)), WORKSPACE), (dict(M=0, x=None, wp=None, ws=None, y=None), OK)])
+def test_linear_refusals(w, kw, status):
+    assert _linear(w.lib, **kw) == status
+
+
+def _grouped(L, a=P, s=P, rows=8, index=None, gl=P, R=8, E=4, N=16, K=64, wp=P, ws=P, y=P, room=P, n=1 << 20):
+    return L.w8a8_fp8b_grouped_gemm(a, s, rows, index, gl, R, E, N, K, wp, ws, y, room, n, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(R=-1), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), UNSUPPORTED), (dict(K=0), SHAPE), (dict(rows=7), SHAPE),
+    (dict(rows=0, index=P), SHAPE), (dict(gl=None), NULL), (dict(a=None), NULL), (dict(gl=ctypes.c_void_p(260)), ALIGN),
+    (dict(a=ctypes.c_void_p(264)), ALIGN), (dict(index=ODD), ALIGN), (dict(n=8), WORKSPACE), (dict(room=None), WORKSPACE),
+    (dict(R=0, a=None, gl=None), OK)])
+def test_grouped_refusals(w, kw, status):
+    assert _grouped(w.lib, **kw) == status
+
+
+def test_chain_and_layer_refusals(w):
+    L = w.lib
+
+    def chain(x=P, xs=None, gl=P, R=16, E=4, H=64, I=32, wp=P, alg=0, y=P, room=P, n=1 << 24):
+        return L.w8a8_fp8b_moe_grouped(x, xs, gl, R, E, H, I, wp, P, wp, P, alg, y, room, n, None)
+
+    def layer(x=P, T=4, H=64, ids=P, wts=P, k=2, E=4, I=32, wp=P, alg=0, out=P, room=P, n=1 << 24):
+        return L.w8a8_fp8b_moe_layer(x, T, H, ids, wts, k, E, I, wp, P, wp, P, alg, out, room, n, None)
+
+    assert chain(E=0) == SHAPE and chain(I=0) == SHAPE and chain(R=-1) == SHAPE and chain(E=2000) == UNSUPPORTED
+    assert chain(alg=7) == UNSUPPORTED and chain(x=None) == NULL and chain(wp=ctypes.c_void_p(264)) == ALIGN
+    assert chain(xs=P, x=ctypes.c_void_p(264)) == ALIGN and chain(n=64) == WORKSPACE and chain(room=None) == WORKSPACE
+    assert chain(R=0, x=None) == OK
+    assert layer(T=-1) == SHAPE and layer(k=0) == SHAPE and layer(E=1025) == UNSUPPORTED and layer(H=0) == SHAPE
+    assert layer(alg=2) == UNSUPPORTED and layer(ids=None) == NULL and layer(out=ODD) == ALIGN
+    assert layer(n=64) == WORKSPACE and layer(room=ODD) == WORKSPACE and layer(T=0, x=None) == OK
+    assert L.w8a8_fp8b_prepack_weight(P, 0, 16, 64, P, None) == SHAPE
+    assert L.w8a8_fp8b_prepack_weight(None, 1, 16, 64, P, None) == NULL
+    assert L.w8a8_fp8b_prepack_weight(P, 1, 16, 64, ctypes.c_void_p(264), None) == ALIGN
+
+
+def test_sizes(w):
+    assert w.fp8b_packed_bytes(1, 128, 256) == 128 * 256
+    assert w.fp8b_packed_bytes(3, 17, 129) == 3 * 32 * 256       # N to 16, K to 128
+    assert w.fp8b_linear_workspace_bytes(3, 16, 200) == 3 * 256 + 256
+    assert w.fp8b_linear_workspace_bytes(0, 16, 200) == 0
+    assert w.fp8b_moe_workspace_bytes(0, 4, 64, 32) == 0
+    assert w.fp8b_moe_layer_workspace_bytes(4, 2, 4, 64, 32) > w.fp8b_moe_workspace_bytes(8, 4, 64, 32) - 8 * 128
+
+
+def test_binding_refusals_without_a_gpu(w):
+    t = torch.zeros((4, 64))
+    with pytest.raises(ValueError):
+        w.moe_gate(t, 2)                                         # not on a GPU
+    with pytest.raises(TypeError):
+        w.moe_gate(torch.zeros((4, 64), dtype=torch.float64), 2)
+    with pytest.raises(TypeError):
+        w.fp8b_quant(t)
+    with pytest.raises(TypeError):
+        w.fp8b_linear(t, t, t, 8)
+
+
+@pytest.mark.skipif(_hipcc() is None, reason="hipcc not available")
+@pytest.mark.parametrize("src", ["fp8b.hip", "gate.hip"])
+def test_kernels_keep_out_of_scratch(src, tmp_path):
+    out = tmp_path / "k.s"
+    r = subprocess.run([_hipcc(), *_flags(), "-S", os.path.join(CSRC, src), "-o", str(out),
+                        "-Rpass-analysis=kernel-resource-usage"], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
+    names = re.findall(r"Function Name: (\S+)", r.stderr)
+    scratch = [int(v) for v in re.findall(r"ScratchSize \[bytes/lane\]: (\d+)", r.stderr)]
+    assert names and len(names) == len(scratch)
+    assert not {n: s for n, s in zip(names, scratch) if s > MAX_SCRATCH}
+    lines = out.read_text().split("\n")
+    assert not any("v_pk_fma_f32" in x or "v_pk_mul_f32" in x or "v_pk_add_f32" in x for x in lines)
+    if src == "fp8b.hip":
+        loops = _innermost_mfma_loops(lines)
+        assert loops
+        assert not [1 for a, b in loops for x in lines[a:b + 1] if "scratch_" in x]

@@ -1,0 +1,160 @@
+"""The expert router through the C ABI against the float64 oracle.
+
+Ids are compared exactly. Weights: a softmax that is not renormalized divides by a
+sum of up to 1024 float32 exponentials and is held to 2^-20 relative; every other
+weight to 2^-23 (one rounding to float32 and one of the factor).
+"""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from tests.conftest import gpu_available
+from tests.gpu_util import DEV, dev, host, show, sync
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+
+
+@pytest.fixture(scope="module")
+def w():
+    import moe_token_amax_amd as w
+    return w
+
+
+def _check(w, l, k, bias=None, scoring="sigmoid", G=1, keep=1, renorm=True, scale=1.0, ids=None, wts=None):
+    """l: CPU tensor of logits in the type under test"""
+    show(f"gate {tuple(l.shape)} {l.dtype} k={k} {scoring} groups={G}/{keep} bias={bias is not None}")
+    b = None if bias is None else dev(bias.astype(np.float32))
+    got_i, got_w = w.moe_gate(l.to(DEV), k, bias=b, scoring=w.GATE_SIGMOID if scoring == "sigmoid" else w.GATE_SOFTMAX,
+                              n_group=G, topk_group=keep, renormalize=renorm, scale=scale, ids=ids, weights=wts)
+    sync()
+    want_i, want_w = O.fp8b.gate(l.double().numpy(), k, None if bias is None else bias.astype(np.float32), scoring, G,
+                                 keep, renorm, np.float64(np.float32(scale)))
+    gi = host(got_i)
+    bad = np.argwhere(gi != want_i)
+    assert bad.size == 0, (bad[:4].tolist(), gi[bad[0][0]], want_i[bad[0][0]])
+    tol = 2.0 ** (-20 if scoring == "softmax" and not renorm else -23)
+    off = np.abs(host(got_w).astype(np.float64) - want_w)
+    assert (off <= tol * np.abs(want_w) + 1e-38).all(), float((off / np.maximum(np.abs(want_w), 1e-38)).max())
+
+
+def _logits(T, E, dtype, seed, spread=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (spread * torch.randn((T, E), generator=g)).to(dtype)
+
+
+CASES = [  # T, E, k, scoring, groups, keep, dtype
+    (1, 1, 1, "softmax", 1, 1, torch.float32), (3, 8, 2, "softmax", 1, 1, torch.bfloat16),
+    (5, 60, 4, "softmax", 1, 1, torch.float16), (7, 64, 6, "sigmoid", 1, 1, torch.bfloat16),
+    (16, 256, 8, "sigmoid", 8, 4, torch.float32), (65, 256, 8, "sigmoid", 8, 4, torch.bfloat16),
+    (33, 160, 6, "softmax", 8, 3, torch.float32), (9, 99, 5, "sigmoid", 3, 2, torch.float32),
+    (130, 384, 8, "sigmoid", 1, 1, torch.float32), (17, 513, 16, "softmax", 1, 1, torch.float32),
+    (4, 1024, 64, "sigmoid", 64, 40, torch.float32), (6, 1000, 9, "softmax", 5, 2, torch.float16),
+    (11, 64, 3, "sigmoid", 64, 7, torch.float32), (2, 12, 12, "sigmoid", 4, 4, torch.float32),
+    (257, 128, 8, "sigmoid", 4, 1, torch.bfloat16), (70, 32, 32, "softmax", 2, 2, torch.bfloat16),
+]
+
+
+@pytest.mark.parametrize("renorm,scale", [(True, 2.5), (False, 1.0)])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("T,E,k,scoring,G,keep,dtype", CASES)
+def test_gate(w, T, E, k, scoring, G, keep, dtype, with_bias, renorm, scale):
+    bias = 0.1 * np.random.default_rng(E).standard_normal(E) if with_bias else None
+    _check(w, _logits(T, E, dtype, 7 * T + E), k, bias, scoring, G, keep, renorm, scale)
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("G,keep", [(1, 1), (4, 2), (16, 3)])
+def test_gate_ties_go_to_the_lowest_index(w, scoring, G, keep):
+    # three distinct logits over 64 experts: nearly every comparison is a tie
+    l = torch.from_numpy(np.random.default_rng(5).integers(0, 3, (40, 64)).astype(np.float32))
+    _check(w, l, 8, None, scoring, G, keep)
+    _check(w, l.to(torch.bfloat16), 8, np.zeros(64), scoring, G, keep)
+    _check(w, torch.zeros((3, 64)), 8, np.repeat([0.5, 0.25], 32), scoring, G, keep)
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("G,keep", [(1, 1), (4, 2)])
+@pytest.mark.parametrize("E", [32, 256])
+def test_gate_masks_and_specials(w, scoring, G, keep, E):
+    rng = np.random.default_rng(E)
+    l = rng.standard_normal((24, E)).astype(np.float32)
+    l[0] = -np.inf                       # nothing left
+    l[1, 1:] = -np.inf                   # one expert
+    l[2] = np.nan
+    l[3, ::2] = np.nan
+    l[4, 3] = np.inf
+    l[5] = np.inf
+    l[6] = np.finfo(np.float32).min
+    l[7, : E // 2] = -np.inf             # half of the groups have no expert
+    l[8] = 1e30
+    l[9, 5] = -1e30
+    l[10] *= 200.0                       # sigmoids at 0 and 1
+    l[11, : E - 3] = -np.inf             # fewer experts than slots
+    b = 0.1 * rng.standard_normal(E)
+    b[7], b[9] = -np.inf, np.inf         # an expert switched off, one forced
+    for bias in (None, b):
+        for renorm in (True, False):
+            _check(w, torch.from_numpy(l), 5, bias, scoring, G, keep, renorm)
+
+
+def _nudge(x, n):
+    """x moved by n float32 steps"""
+    return (x.view(np.int32) + np.asarray(n, np.int32)).view(np.float32)
+
+
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("G,keep", [(1, 1), (8, 3)])
+def test_gate_close_keys(w, scoring, G, keep):
+    """Logits a few float32 steps apart: the scores differ by less than a float32 step."""
+    rng = np.random.default_rng(11)
+    base = rng.uniform(2.0, 6.0, (64, 1)).astype(np.float32)
+    l = _nudge(np.repeat(base, 128, 1), rng.integers(-3, 4, (64, 128)))
+    _check(w, torch.from_numpy(l), 8, None, scoring, G, keep)
+    # keys close through the bias: score + bias of two experts meet within 1e-9
+    l2 = rng.uniform(-1.0, 1.0, (64, 128)).astype(np.float32)
+    b = np.zeros(128)
+    l2[:, 64:] = l2[:, :64]
+    b[64:] = 2.0 ** -31 * rng.integers(-2, 3, 64)
+    _check(w, torch.from_numpy(l2), 8, b, scoring, G, keep)
+
+
+def test_gate_many_tokens(w):
+    # more tokens than one pass of the chip; every token exact against the oracle on a sample
+    T, E, k = 9001, 256, 8
+    l = _logits(T, E, torch.float32, 3)
+    b = 0.05 * np.random.default_rng(0).standard_normal(E).astype(np.float32)
+    ids, wts = w.moe_gate(l.to(DEV), k, bias=dev(b), scoring=w.GATE_SIGMOID, n_group=8, topk_group=4, scale=2.5)
+    sync()
+    pick = np.r_[0:40, 4480:4520, T - 41:T]
+    want, ww = O.fp8b.gate(l.double().numpy()[pick], k, b, "sigmoid", 8, 4, True, 2.5)
+    assert np.array_equal(host(ids)[pick], want)
+    assert np.abs(host(wts)[pick] - ww).max() <= 2.0 ** -23 * 2.5
+
+
+def test_gate_strided_rows_and_given_outputs(w):
+    wide = _logits(21, 300, torch.bfloat16, 1).to(DEV)
+    view = wide[:, 3:131]                 # rows of 128 inside 300, not 16-byte aligned
+    ids = torch.full((21, 4), 77, dtype=torch.int32, device=DEV)
+    wts = torch.full((21, 4), 9.0, device=DEV)
+    w.moe_gate(view, 4, scoring=w.GATE_SIGMOID, n_group=4, topk_group=2, ids=ids, weights=wts)
+    sync()
+    want, ww = O.fp8b.gate(view.double().cpu().numpy(), 4, None, "sigmoid", 4, 2)
+    assert np.array_equal(host(ids), want) and np.abs(host(wts) - ww).max() <= 2.0 ** -23
+    i, x = w.moe_gate(torch.empty((0, 64), device=DEV), 4)
+    assert i.shape == (0, 4) and x.shape == (0, 4)
+
+
+def test_gate_on_another_stream(w):
+    l = _logits(300, 256, torch.float32, 2).to(DEV)
+    a = w.moe_gate(l, 8, scoring=w.GATE_SIGMOID, n_group=8, topk_group=4)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b = w.moe_gate(l, 8, scoring=w.GATE_SIGMOID, n_group=8, topk_group=4)
+    sync()
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
