@@ -653,6 +653,9 @@ int w8a8_moe_gate(const void* logits, int dtype, int64_t T, int64_t E, int64_t l
  *   Output row r reads row row_index[r] of a (clamped to [0, a_rows)), or row
  *   r if row_index is NULL: the rows of a token need no copy per expert. w,
  *   w_scale stacked over E. Rows past the counts are left as they are.
+ *   exact != 0: no product is cut (the codes are multiplied as BF16, at half
+ *   the matrix rate); for an output that is quantized again, as the chain's
+ *   W13 is.
  *   workspace: w8a8_fp8b_grouped_workspace_bytes(R, E, N, K) bytes.
  * w8a8_fp8b_moe_grouped: the expert chain on expert-grouped rows, BF16 [R, H]
  *   (x_scale NULL) or codes [R, Hp] with x_scale [ceil(H/128), R]: W13 (N =
@@ -678,7 +681,7 @@ int w8a8_fp8b_linear(const void* x, int64_t ldx, const float* x_scale, int64_t M
 int64_t w8a8_fp8b_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K);
 int w8a8_fp8b_grouped_gemm(const uint8_t* a, const float* a_scale, int64_t a_rows, const int32_t* row_index,
                            const int64_t* group_list, int64_t R, int64_t E, int64_t N, int64_t K,
-                           const void* w_packed, const float* w_scale, uint16_t* y, void* workspace,
+                           const void* w_packed, const float* w_scale, uint16_t* y, int exact, void* workspace,
                            int64_t ws_bytes, void* stream);
 int64_t w8a8_fp8b_moe_workspace_bytes(int64_t R, int64_t E, int64_t H, int64_t I);
 int w8a8_fp8b_moe_grouped(const void* x_rows, const float* x_scale, const int64_t* group_list, int64_t R, int64_t E,

@@ -203,7 +203,8 @@ def _load():
                                             _c_p, _c_i64, ctypes.c_int, _c_p, _c_i64, _c_p]),
         "w8a8_fp8b_grouped_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_i64]),
         "w8a8_fp8b_grouped_gemm": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_i64,
-                                                  _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_p]),
+                                                  _c_i64, _c_p, _c_p, _c_p, ctypes.c_int, _c_p, _c_i64,
+                                                  _c_p]),
         "w8a8_fp8b_moe_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_i64]),
         "w8a8_fp8b_moe_grouped": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p,
                                                  _c_p, _c_p, _c_p, ctypes.c_int, _c_p, _c_p, _c_i64,
@@ -1268,12 +1269,14 @@ def fp8b_grouped_workspace_bytes(R: int, E: int, N: int, K: int) -> int:
 
 def fp8b_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, group_list: torch.Tensor,
                       w_packed: torch.Tensor, w_scale: torch.Tensor, N: int, K: int | None = None,
-                      row_index: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                      row_index: torch.Tensor | None = None, exact: bool = False,
+                      y: torch.Tensor | None = None,
                       workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Expert-grouped codes and scales of fp8b_quant (a uint8 [A, K rounded up to 128],
     a_scale [ceil(K/128), A]) times each expert's packed weight (w_scale [E, ceil(N/128),
     ceil(K/128)]) -> BF16 [R, N]. Output row r reads row row_index[r] of a (int32 [R]), or
-    row r without it (R = A)."""
+    row r without it (R = A). ``exact``: no product is cut, for an output that is quantized
+    again (the chain's W13)."""
     _need(a, torch.uint8, "a", 2)
     _need(a_scale, torch.float32, "a_scale", 2)
     _need(group_list, torch.int64, "group_list", 1)
@@ -1301,8 +1304,8 @@ def fp8b_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, group_list: torch.
     ws, ws_n = _workspace(fp8b_grouped_workspace_bytes(R, E, N, K), a.device, workspace)
     _here(a, a_scale, group_list, w_packed, w_scale, row_index, y, ws)
     _check(lib.w8a8_fp8b_grouped_gemm(_ptr(a), _ptr(a_scale), A, _ptr(row_index), _ptr(group_list), R, E,
-                                      N, K, _ptr(w_packed), _ptr(w_scale), _ptr(y), _ptr(ws), ws_n,
-                                      _stream()))
+                                      N, K, _ptr(w_packed), _ptr(w_scale), _ptr(y), int(bool(exact)),
+                                      _ptr(ws), ws_n, _stream()))
     return y
 
 

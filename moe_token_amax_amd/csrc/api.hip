@@ -1060,6 +1060,9 @@ int check_fp8b_grouped(const char* who, int64_t R, int64_t E, int64_t N, int64_t
   if (st) return st;
   if (E < 1) return fail(W8A8_ERR_SHAPE, "%s: need E >= 1", who);
   if (E > kMaxExperts) return fail(W8A8_ERR_UNSUPPORTED, "%s: at most %lld experts", who, (long long)kMaxExperts);
+  if ((R / 128 + E) * w8a8::ceil_div(N, 64) > (int64_t)1 << 23)
+    return fail(W8A8_ERR_UNSUPPORTED, "%s: R = %lld rows of N = %lld columns are past one launch", who, (long long)R,
+                (long long)N);
   return W8A8_OK;
 }
 
@@ -1085,7 +1088,7 @@ Fp8bMoeWs fp8b_moe_layout(int64_t T, int64_t R, int64_t E, int64_t H, int64_t I)
   w.h = o;  o += align256(R * 2 * I * 2);  // BF16 [R, 2I]
   w.q2 = o; o += fp8b_codes_bytes(R, I);
   w.s2 = o; o += fp8b_scales_bytes(R, I);
-  w.sched = o; o += align256(w8a8::fp8b_sched_bytes(E));
+  w.sched = o; o += align256(w8a8::fp8b_sched_bytes(R, E));
   w.total = o;
   return w;
 }
@@ -1121,7 +1124,10 @@ hipError_t fp8b_chain(const uint8_t* a, const float* a_scale, int64_t a_rows, co
   p.group_list = group_list;
   p.E = E;
   p.ws = ws + L.sched;
-  hipError_t err = w8a8::launch_fp8b_gemm(p, s);
+  p.exact = 1;  // its output is quantized again, which would amplify the cuts of the FP8 products
+  hipError_t err = w8a8::launch_fp8b_schedule(group_list, E, R, ws + L.sched, s);
+  if (err != hipSuccess) return err;
+  err = w8a8::launch_fp8b_gemm(p, s);
   if (err != hipSuccess) return err;
   err = w8a8::launch_fp8b_quant(h, R, I, 2 * I, 1, alg, q2, s2, s);
   if (err != hipSuccess) return err;
@@ -1212,12 +1218,12 @@ int w8a8_fp8b_linear(const void* x, int64_t ldx, const float* x_scale, int64_t M
 
 int64_t w8a8_fp8b_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K) {
   if (R <= 0 || E <= 0 || N <= 0 || K <= 0) return 0;
-  return w8a8::fp8b_sched_bytes(E);
+  return w8a8::fp8b_sched_bytes(R, E);
 }
 
 int w8a8_fp8b_grouped_gemm(const uint8_t* a, const float* a_scale, int64_t a_rows, const int32_t* row_index,
                            const int64_t* group_list, int64_t R, int64_t E, int64_t N, int64_t K,
-                           const void* w_packed, const float* w_scale, uint16_t* y, void* workspace,
+                           const void* w_packed, const float* w_scale, uint16_t* y, int exact, void* workspace,
                            int64_t ws_bytes, void* stream) {
   int st = check_fp8b_grouped("fp8b_grouped_gemm", R, E, N, K);
   if (st) return st;
@@ -1230,7 +1236,7 @@ int w8a8_fp8b_grouped_gemm(const uint8_t* a, const float* a_scale, int64_t a_row
   if (!aligned(a, 16) || !aligned(a_scale, 4) || !aligned(row_index, 4) || !aligned(group_list, 8) ||
       !aligned(w_packed, 16) || !aligned(w_scale, 4) || !aligned(y, 2))
     return fail(W8A8_ERR_ALIGN, "fp8b_grouped_gemm: misaligned buffer");
-  const int64_t need = w8a8::fp8b_sched_bytes(E);
+  const int64_t need = w8a8::fp8b_sched_bytes(R, E);
   if (!workspace || ws_bytes < need || !aligned(workspace, 256))
     return fail(W8A8_ERR_WORKSPACE, "fp8b_grouped_gemm: needs %lld workspace bytes (256-byte aligned), got %lld",
                 (long long)need, (long long)ws_bytes);
@@ -1241,6 +1247,9 @@ int w8a8_fp8b_grouped_gemm(const uint8_t* a, const float* a_scale, int64_t a_row
   p.group_list = group_list;
   p.E = E;
   p.ws = workspace;
+  p.exact = exact != 0;
+  const hipError_t err = w8a8::launch_fp8b_schedule(group_list, E, R, workspace, (hipStream_t)stream);
+  if (err != hipSuccess) return launched(err, "fp8b_grouped_gemm: schedule");
   return launched(w8a8::launch_fp8b_gemm(p, (hipStream_t)stream), "fp8b_grouped_gemm");
 }
 

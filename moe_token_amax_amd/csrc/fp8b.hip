@@ -19,6 +19,7 @@
 // the group's largest product per value, 1/32 of the half step of the BF16
 // output, and the price of twice the BF16 matrix rate.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.hpp"
 #include "fp8b.hpp"
@@ -182,81 +183,323 @@ hipError_t launch_fp8b_prepack(const uint8_t* w, int64_t E, int64_t N, int64_t K
 // ---------------------------------------------------------------------------
 // product
 // ---------------------------------------------------------------------------
-// 16 x 16 x 128: lane l holds 32 bytes of row (A) or column (B) l % 16; result
-// lane l holds column l % 16, rows 4 (l / 16) + {0..3}. Which 32 of the 128 k a
-// lane holds does not matter as long as A and B agree.
-__device__ __forceinline__ f32x4 mfma_fp8(const i32x8& a, const i32x8& b) {
-  const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, z, 0, 0, 0, 0, 0, 0);
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Eight E4M3 codes as BF16, exactly (an E4M3 value has 4 significant bits).
+__device__ __forceinline__ bf16x8 codes_to_bf16(int lo, int hi) {
+  const bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  const bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  const bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return __builtin_bit_cast(bf16x8, uint4{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1),
+                                          __builtin_bit_cast(uint32_t, p2), __builtin_bit_cast(uint32_t, p3)});
 }
 
-__device__ __forceinline__ i32x8 load_operand(const uint8_t* p0, const uint8_t* p1) {
-  const i32x4 x = *reinterpret_cast<const i32x4*>(p0);
-  const i32x4 y = *reinterpret_cast<const i32x4*>(p1);
+// Both MFMAs take the weight as the first operand: result lane l then holds
+// row m = l % 16 of the activation block and columns 4 (l / 16) + {0..3} of the
+// weight block, so that a lane has one activation scale per block and stores
+// four neighbouring outputs. Which k of a block a lane supplies does not matter
+// as long as both operands agree.
+__device__ __forceinline__ f32x4 mfma_fp8(const i32x8& w, const i32x8& a) {
+  const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, z, 0, 0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ i32x8 join(const i32x4& x, const i32x4& y) {
   return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// 16 rows x 64 columns a workgroup, one 16-column block a wavefront, operands
-// straight from global memory. The grouped form finds its (expert, 16-row tile)
-// in a schedule that every workgroup builds in LDS.
-__global__ __launch_bounds__(256) void fp8b_gemm_kernel(Fp8bGemm p) {
-  __shared__ int64_t row_off[kMaxExperts + 1];
-  __shared__ int tile_off[kMaxExperts + 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int NB = (int)((p.N + 15) / 16), NS = (int)((p.N + kFp8Block - 1) / kFp8Block);
-  int64_t row0 = (int64_t)blockIdx.x * 16, row_end = p.M;
-  int e = 0;
-  if (p.group_list) {
-    const int E = (int)p.E;
-    build_schedule<16>(p.group_list, E, row_off, tile_off);
-    const int t = blockIdx.x;
-    if (t >= tile_off[E]) return;
-    int lo = 0, hi = E - 1;  // last expert whose tiles start at or before t
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (tile_off[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    e = lo;
-    row0 = row_off[e] + (int64_t)(t - tile_off[e]) * 16;
-    row_end = min(row_off[e + 1], p.M);
-    if (row0 >= row_end) return;
-  }
-  const int nb = blockIdx.y * 4 + wave;
-  if (nb >= NB) return;
-  // rows past the tile's last read that row; they only feed rows never stored
-  const int64_t m = min(row0 + (lane & 15), row_end - 1);
-  int64_t ar = m;
-  if (p.row_index) ar = max((int64_t)0, min((int64_t)p.row_index[m], p.a_rows - 1));
-  const uint8_t* ap = p.a + ar * p.lda + (lane >> 4) * 16;
-  const uint8_t* wp = p.w + ((int64_t)e * NB + nb) * p.KB * kFp8BlockBytes + lane * 16;
-  const float* ws = p.w_scale + ((int64_t)e * NS + nb / 8) * p.KB;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t kb = 0; kb < p.KB; ++kb) {
-    const i32x8 a = load_operand(ap + kb * 128, ap + kb * 128 + 64);
-    const i32x8 b = load_operand(wp + kb * kFp8BlockBytes, wp + kb * kFp8BlockBytes + 1024);
-    const f32x4 part = mfma_fp8(a, b);
-    const float sx = p.a_scale[kb * p.a_rows + ar];  // of row lane % 16
-    const float sw = ws[kb];
+// Schedule of a grouped product: int32 count (256 bytes), then int4 {expert,
+// first row, rows, 0} for every tile of at most kTileRows rows of one expert,
+// in expert order.
+constexpr int kTileRows = 128;
+
+int64_t fp8b_max_tiles(int64_t R, int64_t E) { return R / kTileRows + std::min(R, E); }
+int64_t fp8b_sched_bytes(int64_t R, int64_t E) { return 256 + 16 * fp8b_max_tiles(R, E); }
+
+__global__ __launch_bounds__(1024) void fp8b_schedule_kernel(const int64_t* __restrict__ gl, int E, int64_t R,
+                                                             int* __restrict__ count, int4* __restrict__ tiles) {
+  __shared__ int64_t wrows[16];
+  __shared__ int wtiles[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // counts past R are a caller error: such rows own no tile
+  const int64_t n = tid < E ? min(max(gl[tid], (int64_t)0), R) : 0;
+  int64_t ri = n;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-      acc[t] = __builtin_fmaf(part[t], __shfl(sx, (lane >> 4) * 4 + t) * sw, acc[t]);
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t o = __shfl_up(ri, d, 64);
+    if (lane >= d) ri += o;
   }
-  const int64_t n = (int64_t)nb * 16 + (lane & 15);
-  if (n >= p.N) return;
-  const float b = p.bias ? bf16_to_f32(p.bias[n]) : 0.0f;
+  if (lane == 63) wrows[wave] = ri;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) ri += wrows[w];
+  const int64_t row0 = min(ri - n, R);
+  const int64_t rows = min(n, R - row0);
+  const int t = (int)((rows + kTileRows - 1) / kTileRows);
+  int ti = t;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int64_t r = row0 + (lane >> 4) * 4 + t;
-    if (r < row_end) p.y[r * p.ldy + n] = to_bf16(p.bias ? acc[t] + b : acc[t]);
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(ti, d, 64);
+    if (lane >= d) ti += o;
   }
+  if (lane == 63) wtiles[wave] = ti;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) ti += wtiles[w];
+  for (int i = 0; i < t; ++i)
+    tiles[ti - t + i] = int4{tid, (int)(row0 + (int64_t)i * kTileRows),
+                             (int)min((int64_t)kTileRows, rows - (int64_t)i * kTileRows), 0};
+  if (tid == 1023) *count = ti;
 }
 
-int64_t fp8b_sched_bytes(int64_t E) { return group_sched_bytes(E); }
+hipError_t launch_fp8b_schedule(const int64_t* group_list, int64_t E, int64_t R, void* ws, hipStream_t stream) {
+  hipLaunchKernelGGL(fp8b_schedule_kernel, dim3(1), dim3(1024), 0, stream, group_list, (int)E, R,
+                     reinterpret_cast<int*>(ws), reinterpret_cast<int4*>(reinterpret_cast<char*>(ws) + 256));
+  return hipGetLastError();
+}
 
-hipError_t launch_fp8b_gemm(const Fp8bGemm& p, hipStream_t stream) {
-  if (p.M == 0 || p.N == 0) return hipSuccess;
-  const int64_t mt = ceil_div(p.M, 16) + (p.group_list ? p.E : 0);
-  hipLaunchKernelGGL(fp8b_gemm_kernel, dim3((unsigned)mt, (unsigned)ceil_div(p.N, 64)), dim3(256), 0, stream, p);
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Streaming tile: up to 16 MB rows x 64 NBW columns over the whole K, four
+// wavefronts, two workgroups a CU. Wavefront w owns the NBW 16-column blocks
+// nb0 + NBW w + j and takes their weights from global memory straight into
+// registers (the packed layout is the operand layout), kAhead blocks of K
+// ahead: every weight byte of the tile is read once and never passes through
+// LDS. The activation codes, which all four share, go through LDS one block of
+// K at a time (two buffers, one barrier a block), widened to BF16 on the way if
+// EXACT. EXACT multiplies the codes as BF16 (16x16x32, every product exact, half
+// the matrix rate, which this tile does not run out of before the weights'
+// stream does); otherwise the FP8 MFMA.
+template <int MB, int NBW, bool EXACT>
+struct StreamTile {
+  static constexpr int kAhead = 3, kSets = kAhead + 1;
+  static constexpr int kStages = MB == 8 ? 1 : 2;                  // activation blocks in registers (MB 8: 16 registers each)
+  static constexpr int kPieces = (2 * MB + 3) / 4;                 // 16-byte pieces a thread stages per block of K
+  static constexpr int kABytes = MB * (EXACT ? 4096 : 2048);       // one buffer's codes
+  static constexpr int kBufBytes = kABytes + MB * 16 * 4;          // and its scales
+  static constexpr int kLdsBytes = 2 * kBufBytes;
+
+  struct Stage {
+    i32x4 a[kPieces];
+    float s;
+  };
+  using Weights = i32x4[NBW][2];
+
+  __device__ __forceinline__ static void run(const Fp8bGemm& p, uint8_t* smem, int e, int64_t row0, int rows, int nb0) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int NB = (int)((p.N + 15) / 16), NS = (int)((p.N + kFp8Block - 1) / kFp8Block);
+    const int KB = (int)p.KB;
+    const int nbw = nb0 + wave * NBW;
+    // sources of this thread's pieces: piece (m-block, half) = wave + 4 i, lane:
+    // row l % 16, 16 bytes at l / 16. Rows past the tile read its last row; they
+    // only feed outputs that are never stored.
+    const uint8_t* ap[kPieces];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int piece = wave + 4 * i;
+      const int r = min((piece >> 1) * 16 + (lane & 15), rows - 1);
+      int64_t src = row0 + r;
+      if (p.row_index) src = max((int64_t)0, min((int64_t)p.row_index[src], p.a_rows - 1));
+      ap[i] = p.a + src * p.lda + (piece & 1) * 64 + (lane >> 4) * 16;
+    }
+    const float* sp;
+    {
+      int64_t src = row0 + min(tid, rows - 1);
+      if (p.row_index) src = max((int64_t)0, min((int64_t)p.row_index[src], p.a_rows - 1));
+      sp = p.a_scale + src;
+    }
+    const uint8_t* wp[NBW];
+#pragma unroll
+    for (int j = 0; j < NBW; ++j)  // blocks past the last read it; their outputs are never stored
+      wp[j] = p.w + ((int64_t)e * NB + min(nbw + j, NB - 1)) * KB * kFp8BlockBytes;
+    const uint32_t l16 = lane * 16;
+    const float* wsp = p.w_scale + ((int64_t)e * NS + min(nbw, NB - 1) / 8) * KB;
+
+    auto load_w = [&](Weights& w, int kb) __attribute__((always_inline)) {
+      const int64_t k = min(kb, KB - 1);
+#pragma unroll
+      for (int j = 0; j < NBW; ++j) {
+        const uint8_t* b = wp[j] + k * kFp8BlockBytes;  // wave-uniform
+        w[j][0] = *reinterpret_cast<const i32x4*>(b + l16);
+        w[j][1] = *reinterpret_cast<const i32x4*>(b + l16 + 1024);
+      }
+    };
+    auto load_a = [&](Stage& st, int kb) __attribute__((always_inline)) {
+      const int64_t k = min(kb, KB - 1);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        if (wave + 4 * i < 2 * MB) st.a[i] = *reinterpret_cast<const i32x4*>(ap[i] + k * 128);
+      if (tid < 16 * MB) st.s = sp[k * p.a_rows];
+    };
+    auto store_a = [&](const Stage& st, uint8_t* buf) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) {
+        const int piece = wave + 4 * i;
+        if (piece < 2 * MB) {
+          if (EXACT) {
+            *reinterpret_cast<bf16x8*>(buf + (2 * piece) * 1024 + lane * 16) = codes_to_bf16(st.a[i][0], st.a[i][1]);
+            *reinterpret_cast<bf16x8*>(buf + (2 * piece + 1) * 1024 + lane * 16) = codes_to_bf16(st.a[i][2], st.a[i][3]);
+          } else {
+            *reinterpret_cast<i32x4*>(buf + piece * 1024 + lane * 16) = st.a[i];
+          }
+        }
+      }
+      if (tid < 16 * MB) *reinterpret_cast<float*>(buf + kABytes + tid * 4) = st.s;
+    };
+
+    f32x4 acc[MB][NBW];
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int j = 0; j < NBW; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    auto compute = [&](const Weights& w, const uint8_t* buf, float sw) __attribute__((always_inline)) {
+      bf16x8 wb[NBW][4];
+      if (EXACT) {
+#pragma unroll
+        for (int j = 0; j < NBW; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) wb[j][q] = codes_to_bf16(w[j][q >> 1][2 * (q & 1)], w[j][q >> 1][2 * (q & 1) + 1]);
+      }
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        const float s = *reinterpret_cast<const float*>(buf + kABytes + (m * 16 + (lane & 15)) * 4) * sw;
+        f32x4 part[NBW];
+        if (EXACT) {
+#pragma unroll
+          for (int j = 0; j < NBW; ++j) part[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const bf16x8 a = *reinterpret_cast<const bf16x8*>(buf + (m * 4 + q) * 1024 + lane * 16);
+#pragma unroll
+            for (int j = 0; j < NBW; ++j) part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][q], a, part[j], 0, 0, 0);
+          }
+        } else {
+          const i32x8 a = join(*reinterpret_cast<const i32x4*>(buf + m * 2048 + lane * 16),
+                               *reinterpret_cast<const i32x4*>(buf + m * 2048 + 1024 + lane * 16));
+#pragma unroll
+          for (int j = 0; j < NBW; ++j) part[j] = mfma_fp8(join(w[j][0], w[j][1]), a);
+        }
+#pragma unroll
+        for (int j = 0; j < NBW; ++j)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) acc[m][j][t] = __builtin_fmaf(part[j][t], s, acc[m][j][t]);
+      }
+    };
+
+    // Block kb: weights in set kb % kSets, activation in buffer kb % 2. In step
+    // kb the weights of kb + kAhead and the activation of kb + kStages are loaded, kb
+    // is multiplied, and the activation of kb + 1 goes to the other buffer (last
+    // read in step kb - 1, which every wavefront left through the barrier).
+    // Loads past the last block read it again.
+    Weights w[kSets];
+    Stage st[kStages];
+    load_a(st[0], 0);
+    if (kStages == 2) load_a(st[kStages - 1], 1);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load_w(w[i], i);
+    store_a(st[0], smem);
+    lds_barrier();
+    auto step = [&](int kb, auto SET) __attribute__((always_inline)) {
+      constexpr int set = decltype(SET)::value;
+      constexpr int cur = kStages == 2 ? set & 1 : 0, nxt = kStages == 2 ? cur ^ 1 : 0;
+      if (kStages == 2) load_a(st[cur], kb + 2);
+      else load_a(st[0], kb + 1);
+      load_w(w[(set + kAhead) % kSets], kb + kAhead);
+      __builtin_amdgcn_sched_barrier(0);
+      compute(w[set], smem + (set & 1) * kBufBytes, wsp[kb]);
+      store_a(st[nxt], smem + ((set & 1) ^ 1) * kBufBytes);
+      lds_barrier();
+    };
+    // one call site per register set: with a second one (a remainder loop) the
+    // compiler indexes the sets at run time, in scratch
+    for (int kb = 0; kb < KB; kb += kSets) {
+      step(kb, std::integral_constant<int, 0>{});
+      if (kb + 1 < KB) step(kb + 1, std::integral_constant<int, 1>{});
+      if (kb + 2 < KB) step(kb + 2, std::integral_constant<int, 2>{});
+      if (kb + 3 < KB) step(kb + 3, std::integral_constant<int, 3>{});
+    }
+
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      const int r = m * 16 + (lane & 15);
+      if (r < rows) {
+#pragma unroll
+        for (int j = 0; j < NBW; ++j) store4(p, row0 + r, (int64_t)(nbw + j) * 16 + (lane >> 4) * 4, acc[m][j]);
+      }
+    }
+  }
+
+  // four neighbouring outputs of one row
+  __device__ __forceinline__ static void store4(const Fp8bGemm& p, int64_t m, int64_t n, const f32x4& v) {
+    if (n >= p.N) return;
+    uint16_t* y = p.y + m * p.ldy + n;
+    uint16_t o[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      o[t] = to_bf16(p.bias ? v[t] + bf16_to_f32(p.bias[min(n + t, p.N - 1)]) : v[t]);
+    if (p.store_vec) {
+      *reinterpret_cast<uint2*>(y) = uint2{o[0] | ((uint32_t)o[1] << 16), o[2] | ((uint32_t)o[3] << 16)};
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (n + t < p.N) y[t] = o[t];
+    }
+  }
+};
+
+// tile height by the rows there are
+template <int NBW, bool EXACT>
+__device__ __forceinline__ void stream_tile(const Fp8bGemm& p, uint8_t* smem, int e, int64_t row0, int rows, int nb0) {
+  if (rows <= 16) StreamTile<1, NBW, EXACT>::run(p, smem, e, row0, rows, nb0);
+  else if (rows <= 32) StreamTile<2, NBW, EXACT>::run(p, smem, e, row0, rows, nb0);
+  else if (rows <= 64) StreamTile<4, NBW, EXACT>::run(p, smem, e, row0, rows, nb0);
+  else StreamTile<8, NBW, EXACT>::run(p, smem, e, row0, rows, nb0);
+}
+
+// Grouped: workgroup b takes column group b % NT of tile b / NT. NT (column
+// groups, rounded up to 8) keeps a column group on one XCD (b % 8), where the
+// tiles of an expert share its weights in L2.
+template <int NBW, bool EXACT>
+__global__ __launch_bounds__(256, 2) void fp8b_grouped_kernel(Fp8bGemm p, int NT) {
+  using T = StreamTile<8, NBW, EXACT>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
+  const int t = blockIdx.x / NT, c = blockIdx.x % NT;
+  if (t >= *reinterpret_cast<const int*>(p.ws)) return;
+  const int nb0 = c * 4 * NBW;
+  if ((int64_t)nb0 * 16 >= p.N) return;
+  const int4 tile = reinterpret_cast<const int4*>(reinterpret_cast<const char*>(p.ws) + 256)[t];
+  stream_tile<NBW, EXACT>(p, smem, __builtin_amdgcn_readfirstlane(tile.x), __builtin_amdgcn_readfirstlane(tile.y),
+                          __builtin_amdgcn_readfirstlane(tile.z), nb0);
+}
+
+// Dense: 128-row tiles.
+template <int NBW, bool EXACT>
+__global__ __launch_bounds__(256, 2) void fp8b_dense_kernel(Fp8bGemm p) {
+  using T = StreamTile<8, NBW, EXACT>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
+  const int64_t row0 = (int64_t)blockIdx.x * kTileRows;
+  stream_tile<NBW, EXACT>(p, smem, 0, row0, (int)min((int64_t)kTileRows, p.M - row0), blockIdx.y * 4 * NBW);
+}
+
+hipError_t launch_fp8b_gemm(const Fp8bGemm& args, hipStream_t stream) {
+  if (args.M == 0 || args.N == 0) return hipSuccess;
+  Fp8bGemm p = args;
+  p.store_vec = p.N % 4 == 0 && p.ldy % 4 == 0 && ((uintptr_t)p.y & 7) == 0;
+  constexpr int NBW = 2;
+  const int64_t nt = ceil_div(p.N, 64 * NBW);
+  if (!p.group_list) {
+    hipLaunchKernelGGL((fp8b_dense_kernel<NBW, false>), dim3((unsigned)ceil_div(p.M, kTileRows), (unsigned)nt), dim3(256),
+                       0, stream, p);
+    return hipGetLastError();
+  }
+  const int64_t NT = round_up(nt, 8);
+  const dim3 grid((unsigned)(fp8b_max_tiles(p.M, p.E) * NT));
+  if (p.exact) hipLaunchKernelGGL((fp8b_grouped_kernel<NBW, true>), grid, dim3(256), 0, stream, p, (int)NT);
+  else hipLaunchKernelGGL((fp8b_grouped_kernel<NBW, false>), grid, dim3(256), 0, stream, p, (int)NT);
   return hipGetLastError();
 }
 

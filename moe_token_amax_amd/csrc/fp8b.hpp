@@ -35,9 +35,14 @@ struct Fp8bGemm {
   int64_t ldy;
   const int64_t* group_list; // [E] or null
   int64_t E;
-  void* ws;                  // grouped: fp8b_sched_bytes(E) bytes, 256-byte aligned
+  int exact;                 // grouped: products of the codes as BF16, none of them cut
+  const void* ws;            // grouped: the schedule written by launch_fp8b_schedule
+  bool store_vec;            // set by the launcher: outputs in 8-byte pieces
 };
-int64_t fp8b_sched_bytes(int64_t E);
+// tiles of the rows of every expert; any number of products over one
+// group_list and R share a schedule
+int64_t fp8b_sched_bytes(int64_t R, int64_t E);
+hipError_t launch_fp8b_schedule(const int64_t* group_list, int64_t E, int64_t R, void* ws, hipStream_t stream);
 hipError_t launch_fp8b_gemm(const Fp8bGemm& p, hipStream_t stream);
 
 struct GateArgs {

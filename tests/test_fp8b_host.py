@@ -74,11 +74,12 @@ def test_linear_refusals(w, kw, status):
 
 
 def _grouped(L, a=P, s=P, rows=8, index=None, gl=P, R=8, E=4, N=16, K=64, wp=P, ws=P, y=P, room=P, n=1 << 20):
-    return L.w8a8_fp8b_grouped_gemm(a, s, rows, index, gl, R, E, N, K, wp, ws, y, room, n, None)
+    return L.w8a8_fp8b_grouped_gemm(a, s, rows, index, gl, R, E, N, K, wp, ws, y, 0, room, n, None)
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(R=-1), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), UNSUPPORTED), (dict(K=0), SHAPE), (dict(rows=7), SHAPE),
+    (dict(R=-1), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), UNSUPPORTED),
+    (dict(R=1 << 28, rows=1 << 28, N=1 << 14), UNSUPPORTED), (dict(K=0), SHAPE), (dict(rows=7), SHAPE),
     (dict(rows=0, index=P), SHAPE), (dict(gl=None), NULL), (dict(a=None), NULL), (dict(gl=ctypes.c_void_p(260)), ALIGN),
     (dict(a=ctypes.c_void_p(264)), ALIGN), (dict(index=ODD), ALIGN), (dict(n=8), WORKSPACE), (dict(room=None), WORKSPACE),
     (dict(R=0, a=None, gl=None), OK)])

@@ -44,12 +44,13 @@ def _weight(rng, *shape):
     return c, s.astype(np.float32)
 
 
-def _hold(got_bits, q, sx, cw, sw, bias_bits=None, what=""):
+def _hold(got_bits, q, sx, cw, sw, bias_bits=None, what="", exact=False):
+    """exact: products that are not cut, c = 0"""
     y = F.product64(q, sx, cw, sw, bias_bits)
     A = np.abs(F.dequant(q, sx)) @ np.abs(F.weight_dequant(cw, sw)).T
     if bias_bits is not None:
         A = A + np.abs(O.bf16_to_f32(bias_bits)).astype(np.float64)
-    d = F.cut_bound(q, sx, cw, sw) + (18 + F.blocks(cw.shape[1])) * 2.0 ** -23 * A
+    d = (0.0 if exact else F.cut_bound(q, sx, cw, sw)) + (18 + F.blocks(cw.shape[1])) * 2.0 ** -23 * A
     off = np.abs(O.bf16_to_f32(got_bits).astype(np.float64) - y)
     tol = 2.0 ** -8 * (np.abs(y) + d) + d + 1e-38
     bad = np.argwhere(~(off <= tol))
@@ -250,10 +251,11 @@ GROUPED = [  # counts, N, K
 ]
 
 
+@pytest.mark.parametrize("exact", [False, True])
 @pytest.mark.parametrize("indexed", [False, True])
 @pytest.mark.parametrize("counts,N,K", GROUPED)
-def test_grouped(w, counts, N, K, indexed):
-    show(f"grouped {counts if len(counts) < 9 else len(counts)} {N} x {K} indexed {indexed}")
+def test_grouped(w, counts, N, K, indexed, exact):
+    show(f"grouped {counts if len(counts) < 9 else len(counts)} {N} x {K} indexed {indexed} exact {exact}")
     rng = np.random.default_rng(len(counts) + N + K)
     g = np.array(counts, np.int64)
     used, E = int(g.sum()), len(g)
@@ -265,7 +267,7 @@ def test_grouped(w, counts, N, K, indexed):
     q, s = w.fp8b_quant(bf16_dev(x))
     y = torch.full((R, N), 7.0, dtype=torch.bfloat16, device=DEV)
     w.fp8b_grouped_gemm(q, s, dev(g), w.fp8b_prepack_weight(dev(cw)), dev(sw), N, K=K,
-                        row_index=dev(idx) if indexed else None, y=y)
+                        row_index=dev(idx) if indexed else None, y=y, exact=exact)
     sync()
     got = bf16_host(y)
     assert (y[used:] == 7).all()
@@ -274,7 +276,8 @@ def test_grouped(w, counts, N, K, indexed):
     for e in range(E):
         i = idx[r:r + g[e]]
         if len(i):
-            _hold(got[r:r + g[e]], qo[i], np.ascontiguousarray(so[:, i]), cw[e], sw[e], what=f"expert {e}")
+            _hold(got[r:r + g[e]], qo[i], np.ascontiguousarray(so[:, i]), cw[e], sw[e], what=f"expert {e}",
+                  exact=exact)
         r += int(g[e])
 
 
@@ -332,7 +335,7 @@ def test_chain(w, counts, H, I):
     q, s = w.fp8b_quant(xd)
     y2 = w.fp8b_moe_grouped(q, gl, *W, I, H=H, x_scale=s)
     # the chain equals its stages, and every stage is held on the GPU's own input
-    h = w.fp8b_grouped_gemm(q, s, gl, W[0], W[1], 2 * I, K=H)
+    h = w.fp8b_grouped_gemm(q, s, gl, W[0], W[1], 2 * I, K=H, exact=True)
     q2, sc2 = w.fp8b_quant(h, act=w.ACT_SWIGLU)
     y3 = w.fp8b_grouped_gemm(q2, sc2, gl, W[2], W[3], H, K=I)
     sync()
@@ -344,7 +347,8 @@ def test_chain(w, counts, H, I):
     for e in range(E):
         a, b = r, r + int(g[e])
         if b > a:
-            _hold(bf16_host(h)[a:b], qo[a:b], np.ascontiguousarray(so[:, a:b]), c13[e], s13[e], what=f"W13 {e}")
+            _hold(bf16_host(h)[a:b], qo[a:b], np.ascontiguousarray(so[:, a:b]), c13[e], s13[e], what=f"W13 {e}",
+                  exact=True)
             _hold(bf16_host(y)[a:b], q2o[a:b], np.ascontiguousarray(s2o[:, a:b]), c2[e], s2[e], what=f"W2 {e}")
         r = b
 
@@ -364,7 +368,7 @@ def test_router_to_layer(w, T, k, E, H, I, G, keep):
     out = w.fp8b_moe_layer(xd, ids, wts, *W, I)
     gl, rt, pr = w.moe_route(ids, E)
     q, s = w.fp8b_quant(xd)
-    h = w.fp8b_grouped_gemm(q, s, gl, W[0], W[1], 2 * I, K=H, row_index=rt)
+    h = w.fp8b_grouped_gemm(q, s, gl, W[0], W[1], 2 * I, K=H, row_index=rt, exact=True)
     q2, sc2 = w.fp8b_quant(h, act=w.ACT_SWIGLU)
     y = w.fp8b_grouped_gemm(q2, sc2, gl, W[2], W[3], H, K=I)
     out2 = w.moe_combine(y, pr, wts)
