@@ -262,12 +262,12 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// Streaming tile: up to 16 MB rows x 64 NBW columns over the whole K, four
-// wavefronts, two workgroups a CU. Wavefront w owns the NBW 16-column blocks
+// Streaming tile: up to 16 MB rows x 128 NBW columns over the whole K, eight
+// wavefronts, one workgroup a CU. Wavefront w owns the NBW 16-column blocks
 // nb0 + NBW w + j and takes their weights from global memory straight into
 // registers (the packed layout is the operand layout), kAhead blocks of K
 // ahead: every weight byte of the tile is read once and never passes through
-// LDS. The activation codes, which all four share, go through LDS one block of
+// LDS. The activation codes, which all eight share, go through LDS one block of
 // K at a time (two buffers, one barrier a block), widened to BF16 on the way if
 // EXACT. EXACT multiplies the codes as BF16 (16x16x32, every product exact, half
 // the matrix rate, which this tile does not run out of before the weights'
@@ -275,8 +275,8 @@ __device__ __forceinline__ void lds_barrier() {
 template <int MB, int NBW, bool EXACT>
 struct StreamTile {
   static constexpr int kAhead = 3, kSets = kAhead + 1;
-  static constexpr int kStages = MB == 8 ? 1 : 2;                  // activation blocks in registers (MB 8: 16 registers each)
-  static constexpr int kPieces = (2 * MB + 3) / 4;                 // 16-byte pieces a thread stages per block of K
+  static constexpr int kWaves = 8;
+  static constexpr int kPieces = (2 * MB + kWaves - 1) / kWaves;   // 16-byte pieces a thread stages per block of K
   static constexpr int kABytes = MB * (EXACT ? 4096 : 2048);       // one buffer's codes
   static constexpr int kBufBytes = kABytes + MB * 16 * 4;          // and its scales
   static constexpr int kLdsBytes = 2 * kBufBytes;
@@ -293,13 +293,13 @@ struct StreamTile {
     const int NB = (int)((p.N + 15) / 16), NS = (int)((p.N + kFp8Block - 1) / kFp8Block);
     const int KB = (int)p.KB;
     const int nbw = nb0 + wave * NBW;
-    // sources of this thread's pieces: piece (m-block, half) = wave + 4 i, lane:
+    // sources of this thread's pieces: piece (m-block, half) = wave + 8 i, lane:
     // row l % 16, 16 bytes at l / 16. Rows past the tile read its last row; they
     // only feed outputs that are never stored.
     const uint8_t* ap[kPieces];
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int piece = wave + 4 * i;
+      const int piece = wave + kWaves * i;
       const int r = min((piece >> 1) * 16 + (lane & 15), rows - 1);
       int64_t src = row0 + r;
       if (p.row_index) src = max((int64_t)0, min((int64_t)p.row_index[src], p.a_rows - 1));
@@ -331,13 +331,13 @@ struct StreamTile {
       const int64_t k = min(kb, KB - 1);
 #pragma unroll
       for (int i = 0; i < kPieces; ++i)
-        if (wave + 4 * i < 2 * MB) st.a[i] = *reinterpret_cast<const i32x4*>(ap[i] + k * 128);
+        if (wave + kWaves * i < 2 * MB) st.a[i] = *reinterpret_cast<const i32x4*>(ap[i] + k * 128);
       if (tid < 16 * MB) st.s = sp[k * p.a_rows];
     };
     auto store_a = [&](const Stage& st, uint8_t* buf) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        const int piece = wave + 4 * i;
+        const int piece = wave + kWaves * i;
         if (piece < 2 * MB) {
           if (EXACT) {
             *reinterpret_cast<bf16x8*>(buf + (2 * piece) * 1024 + lane * 16) = codes_to_bf16(st.a[i][0], st.a[i][1]);
@@ -391,27 +391,25 @@ struct StreamTile {
     };
 
     // Block kb: weights in set kb % kSets, activation in buffer kb % 2. In step
-    // kb the weights of kb + kAhead and the activation of kb + kStages are loaded, kb
+    // kb the weights of kb + kAhead and the activation of kb + 2 are loaded, kb
     // is multiplied, and the activation of kb + 1 goes to the other buffer (last
     // read in step kb - 1, which every wavefront left through the barrier).
     // Loads past the last block read it again.
     Weights w[kSets];
-    Stage st[kStages];
+    Stage st[2];
     load_a(st[0], 0);
-    if (kStages == 2) load_a(st[kStages - 1], 1);
+    load_a(st[1], 1);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) load_w(w[i], i);
     store_a(st[0], smem);
     lds_barrier();
     auto step = [&](int kb, auto SET) __attribute__((always_inline)) {
       constexpr int set = decltype(SET)::value;
-      constexpr int cur = kStages == 2 ? set & 1 : 0, nxt = kStages == 2 ? cur ^ 1 : 0;
-      if (kStages == 2) load_a(st[cur], kb + 2);
-      else load_a(st[0], kb + 1);
+      load_a(st[set & 1], kb + 2);
       load_w(w[(set + kAhead) % kSets], kb + kAhead);
       __builtin_amdgcn_sched_barrier(0);
       compute(w[set], smem + (set & 1) * kBufBytes, wsp[kb]);
-      store_a(st[nxt], smem + ((set & 1) ^ 1) * kBufBytes);
+      store_a(st[(set & 1) ^ 1], smem + ((set & 1) ^ 1) * kBufBytes);
       lds_barrier();
     };
     // one call site per register set: with a second one (a remainder loop) the
@@ -464,12 +462,12 @@ __device__ __forceinline__ void stream_tile(const Fp8bGemm& p, uint8_t* smem, in
 // groups, rounded up to 8) keeps a column group on one XCD (b % 8), where the
 // tiles of an expert share its weights in L2.
 template <int NBW, bool EXACT>
-__global__ __launch_bounds__(256, 2) void fp8b_grouped_kernel(Fp8bGemm p, int NT) {
+__global__ __launch_bounds__(512) void fp8b_grouped_kernel(Fp8bGemm p, int NT) {
   using T = StreamTile<8, NBW, EXACT>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
   const int t = blockIdx.x / NT, c = blockIdx.x % NT;
   if (t >= *reinterpret_cast<const int*>(p.ws)) return;
-  const int nb0 = c * 4 * NBW;
+  const int nb0 = c * 8 * NBW;
   if ((int64_t)nb0 * 16 >= p.N) return;
   const int4 tile = reinterpret_cast<const int4*>(reinterpret_cast<const char*>(p.ws) + 256)[t];
   stream_tile<NBW, EXACT>(p, smem, __builtin_amdgcn_readfirstlane(tile.x), __builtin_amdgcn_readfirstlane(tile.y),
@@ -478,11 +476,11 @@ __global__ __launch_bounds__(256, 2) void fp8b_grouped_kernel(Fp8bGemm p, int NT
 
 // Dense: 128-row tiles.
 template <int NBW, bool EXACT>
-__global__ __launch_bounds__(256, 2) void fp8b_dense_kernel(Fp8bGemm p) {
+__global__ __launch_bounds__(512) void fp8b_dense_kernel(Fp8bGemm p) {
   using T = StreamTile<8, NBW, EXACT>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
   const int64_t row0 = (int64_t)blockIdx.x * kTileRows;
-  stream_tile<NBW, EXACT>(p, smem, 0, row0, (int)min((int64_t)kTileRows, p.M - row0), blockIdx.y * 4 * NBW);
+  stream_tile<NBW, EXACT>(p, smem, 0, row0, (int)min((int64_t)kTileRows, p.M - row0), blockIdx.y * 8 * NBW);
 }
 
 hipError_t launch_fp8b_gemm(const Fp8bGemm& args, hipStream_t stream) {
@@ -490,16 +488,16 @@ hipError_t launch_fp8b_gemm(const Fp8bGemm& args, hipStream_t stream) {
   Fp8bGemm p = args;
   p.store_vec = p.N % 4 == 0 && p.ldy % 4 == 0 && ((uintptr_t)p.y & 7) == 0;
   constexpr int NBW = 2;
-  const int64_t nt = ceil_div(p.N, 64 * NBW);
+  const int64_t nt = ceil_div(p.N, 128 * NBW);
   if (!p.group_list) {
-    hipLaunchKernelGGL((fp8b_dense_kernel<NBW, false>), dim3((unsigned)ceil_div(p.M, kTileRows), (unsigned)nt), dim3(256),
+    hipLaunchKernelGGL((fp8b_dense_kernel<NBW, false>), dim3((unsigned)ceil_div(p.M, kTileRows), (unsigned)nt), dim3(512),
                        0, stream, p);
     return hipGetLastError();
   }
   const int64_t NT = round_up(nt, 8);
   const dim3 grid((unsigned)(fp8b_max_tiles(p.M, p.E) * NT));
-  if (p.exact) hipLaunchKernelGGL((fp8b_grouped_kernel<NBW, true>), grid, dim3(256), 0, stream, p, (int)NT);
-  else hipLaunchKernelGGL((fp8b_grouped_kernel<NBW, false>), grid, dim3(256), 0, stream, p, (int)NT);
+  if (p.exact) hipLaunchKernelGGL((fp8b_grouped_kernel<NBW, true>), grid, dim3(512), 0, stream, p, (int)NT);
+  else hipLaunchKernelGGL((fp8b_grouped_kernel<NBW, false>), grid, dim3(512), 0, stream, p, (int)NT);
   return hipGetLastError();
 }
 
