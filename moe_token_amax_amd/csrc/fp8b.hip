@@ -274,7 +274,9 @@ __device__ __forceinline__ void lds_barrier() {
 // stream does); otherwise the FP8 MFMA.
 template <int MB, int NBW, bool EXACT>
 struct StreamTile {
-  static constexpr int kAhead = 3, kSets = kAhead + 1;
+  // blocks of weights in flight: as many as the registers that exact rows leave
+  static constexpr int kAhead = EXACT && MB == 8 ? 1 : EXACT && MB == 6 ? 2 : 3, kSets = kAhead + 1;
+  static constexpr int kUnroll = kSets == 3 ? 6 : 4;
   static constexpr int kWaves = 8;
   static constexpr int kPieces = (2 * MB + kWaves - 1) / kWaves;   // 16-byte pieces a thread stages per block of K
   static constexpr int kABytes = MB * (EXACT ? 4096 : 2048);       // one buffer's codes
@@ -331,14 +333,14 @@ struct StreamTile {
       const int64_t k = min(kb, KB - 1);
 #pragma unroll
       for (int i = 0; i < kPieces; ++i)
-        if (wave + kWaves * i < 2 * MB) st.a[i] = *reinterpret_cast<const i32x4*>(ap[i] + k * 128);
+        if (2 * MB >= kWaves * (i + 1) || wave + kWaves * i < 2 * MB) st.a[i] = *reinterpret_cast<const i32x4*>(ap[i] + k * 128);
       if (tid < 16 * MB) st.s = sp[k * p.a_rows];
     };
     auto store_a = [&](const Stage& st, uint8_t* buf) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int piece = wave + kWaves * i;
-        if (piece < 2 * MB) {
+        if (2 * MB >= kWaves * (i + 1) || piece < 2 * MB) {
           if (EXACT) {
             *reinterpret_cast<bf16x8*>(buf + (2 * piece) * 1024 + lane * 16) = codes_to_bf16(st.a[i][0], st.a[i][1]);
             *reinterpret_cast<bf16x8*>(buf + (2 * piece + 1) * 1024 + lane * 16) = codes_to_bf16(st.a[i][2], st.a[i][3]);
@@ -356,7 +358,26 @@ struct StreamTile {
 #pragma unroll
       for (int j = 0; j < NBW; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+    // Operands come in pieces of two 16-byte registers: a 16-row block (FP8), or
+    // half of its K (EXACT).
+    constexpr int kH = EXACT ? 2 : 1;
+    struct Frag {
+      i32x4 v[2];
+    };
+    auto read_a = [&](Frag& f, const uint8_t* buf, int i) __attribute__((always_inline)) {
+      f.v[0] = *reinterpret_cast<const i32x4*>(buf + i * 2048 + l16);
+      f.v[1] = *reinterpret_cast<const i32x4*>(buf + i * 2048 + 1024 + l16);
+    };
+    // One block of K. Operands are read two pieces before their MFMAs, and the
+    // scaled sums of row block m - 1 follow the MFMAs of m; the scheduling barriers
+    // keep that order (left alone, the compiler reads each operand just before its
+    // use and keeps every partial product to the end, which spills).
     auto compute = [&](const Weights& w, const uint8_t* buf, float sw) __attribute__((always_inline)) {
+      Frag f[3];
+      f32x4 part[2][NBW];
+      float sc[2], sn = *reinterpret_cast<const float*>(buf + kABytes + (lane & 15) * 4);
+      read_a(f[0], buf, 0);
+      if (MB * kH > 1) read_a(f[1], buf, 1);
       bf16x8 wb[NBW][4];
       if (EXACT) {
 #pragma unroll
@@ -366,28 +387,41 @@ struct StreamTile {
       }
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
-        const float s = *reinterpret_cast<const float*>(buf + kABytes + (m * 16 + (lane & 15)) * 4) * sw;
-        f32x4 part[NBW];
-        if (EXACT) {
+        sc[m & 1] = sn * sw;
+        if (m + 1 < MB) sn = *reinterpret_cast<const float*>(buf + kABytes + ((m + 1) * 16 + (lane & 15)) * 4);
 #pragma unroll
-          for (int j = 0; j < NBW; ++j) part[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int h = 0; h < kH; ++h) {
+          const int i = m * kH + h;
+          if (i + 2 < MB * kH) read_a(f[(i + 2) % 3], buf, i + 2);
+          __builtin_amdgcn_sched_barrier(0);
+          const Frag& a = f[i % 3];
+          if (EXACT) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const bf16x8 a = *reinterpret_cast<const bf16x8*>(buf + (m * 4 + q) * 1024 + lane * 16);
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int j = 0; j < NBW; ++j) part[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][q], a, part[j], 0, 0, 0);
+              for (int j = 0; j < NBW; ++j)
+                part[m & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    wb[j][2 * h + q], __builtin_bit_cast(bf16x8, a.v[q]),
+                    h + q ? part[m & 1][j] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+          } else {
+#pragma unroll
+            for (int j = 0; j < NBW; ++j) part[m & 1][j] = mfma_fp8(join(w[j][0], w[j][1]), join(a.v[0], a.v[1]));
           }
-        } else {
-          const i32x8 a = join(*reinterpret_cast<const i32x4*>(buf + m * 2048 + lane * 16),
-                               *reinterpret_cast<const i32x4*>(buf + m * 2048 + 1024 + lane * 16));
+          if (h == 0 && m > 0) {
 #pragma unroll
-          for (int j = 0; j < NBW; ++j) part[j] = mfma_fp8(join(w[j][0], w[j][1]), a);
+            for (int j = 0; j < NBW; ++j)
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                acc[m - 1][j][t] = __builtin_fmaf(part[(m - 1) & 1][j][t], sc[(m - 1) & 1], acc[m - 1][j][t]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-#pragma unroll
-        for (int j = 0; j < NBW; ++j)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) acc[m][j][t] = __builtin_fmaf(part[j][t], s, acc[m][j][t]);
       }
+#pragma unroll
+      for (int j = 0; j < NBW; ++j)
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          acc[MB - 1][j][t] = __builtin_fmaf(part[(MB - 1) & 1][j][t], sc[(MB - 1) & 1], acc[MB - 1][j][t]);
     };
 
     // Block kb: weights in set kb % kSets, activation in buffer kb % 2. In step
@@ -403,22 +437,26 @@ struct StreamTile {
     for (int i = 0; i < kAhead; ++i) load_w(w[i], i);
     store_a(st[0], smem);
     lds_barrier();
-    auto step = [&](int kb, auto SET) __attribute__((always_inline)) {
-      constexpr int set = decltype(SET)::value;
-      load_a(st[set & 1], kb + 2);
+    auto step = [&](int kb, auto I) __attribute__((always_inline)) {
+      constexpr int i = decltype(I)::value, set = i % kSets, buf = i % 2;
+      load_a(st[buf], kb + 2);
       load_w(w[(set + kAhead) % kSets], kb + kAhead);
       __builtin_amdgcn_sched_barrier(0);
-      compute(w[set], smem + (set & 1) * kBufBytes, wsp[kb]);
-      store_a(st[(set & 1) ^ 1], smem + ((set & 1) ^ 1) * kBufBytes);
+      compute(w[set], smem + buf * kBufBytes, wsp[kb]);
+      store_a(st[buf ^ 1], smem + (buf ^ 1) * kBufBytes);
       lds_barrier();
     };
     // one call site per register set: with a second one (a remainder loop) the
     // compiler indexes the sets at run time, in scratch
-    for (int kb = 0; kb < KB; kb += kSets) {
+    for (int kb = 0; kb < KB; kb += kUnroll) {
       step(kb, std::integral_constant<int, 0>{});
       if (kb + 1 < KB) step(kb + 1, std::integral_constant<int, 1>{});
       if (kb + 2 < KB) step(kb + 2, std::integral_constant<int, 2>{});
       if (kb + 3 < KB) step(kb + 3, std::integral_constant<int, 3>{});
+      if constexpr (kUnroll == 6) {
+        if (kb + 4 < KB) step(kb + 4, std::integral_constant<int, 4>{});
+        if (kb + 5 < KB) step(kb + 5, std::integral_constant<int, 5>{});
+      }
     }
 
 #pragma unroll
@@ -455,6 +493,7 @@ __device__ __forceinline__ void stream_tile(const Fp8bGemm& p, uint8_t* smem, in
   if (rows <= 16) StreamTile<1, NBW, EXACT>::run(p, smem, e, row0, rows, nb0);
   else if (rows <= 32) StreamTile<2, NBW, EXACT>::run(p, smem, e, row0, rows, nb0);
   else if (rows <= 64) StreamTile<4, NBW, EXACT>::run(p, smem, e, row0, rows, nb0);
+  else if (rows <= 96) StreamTile<6, NBW, EXACT>::run(p, smem, e, row0, rows, nb0);
   else StreamTile<8, NBW, EXACT>::run(p, smem, e, row0, rows, nb0);
 }
 
