@@ -63,6 +63,20 @@ __device__ __forceinline__ float code_arg(float x, float s) {
   return fminf(fmaxf(t, -448.0f), 448.0f);
 }
 
+// Codes of this lane's 8 values of a block of 128 held by 16 lanes, and its scale.
+__device__ __forceinline__ uint2 quant_block(const float (&v)[8], int alg, float& s) {
+  uint32_t am = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) am = max(am, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  s = block_scale(row_max_u32(am), alg);
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(code_arg(v[0], s), code_arg(v[1], s), lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(code_arg(v[2], s), code_arg(v[3], s), lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(code_arg(v[4], s), code_arg(v[5], s), hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(code_arg(v[6], s), code_arg(v[7], s), hi, true);
+  return uint2{(uint32_t)lo, (uint32_t)hi};
+}
+
 template <bool VEC>
 __device__ __forceinline__ void load8(const uint16_t* src, int64_t n, float (&v)[8]) {
   if (VEC) {
@@ -104,17 +118,9 @@ __global__ __launch_bounds__(256) void fp8b_quant_kernel(const uint16_t* __restr
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = swiglu_fixed(v[j], u[j]);
     }
-    uint32_t am = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) am = max(am, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-    am = row_max_u32(am);
-    const float s = block_scale(am, alg);
-    int lo = 0, hi = 0;
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(code_arg(v[0], s), code_arg(v[1], s), lo, false);
-    lo = __builtin_amdgcn_cvt_pk_fp8_f32(code_arg(v[2], s), code_arg(v[3], s), lo, true);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(code_arg(v[4], s), code_arg(v[5], s), hi, false);
-    hi = __builtin_amdgcn_cvt_pk_fp8_f32(code_arg(v[6], s), code_arg(v[7], s), hi, true);
-    *reinterpret_cast<uint2*>(q + row * ((int64_t)KB * kFp8Block) + k0) = uint2{(uint32_t)lo, (uint32_t)hi};
+    float s;
+    const uint2 codes = quant_block(v, alg, s);
+    *reinterpret_cast<uint2*>(q + row * ((int64_t)KB * kFp8Block) + k0) = codes;
     if (sub == 0) scale[(int64_t)kb * M + row] = s;
   }
 }
@@ -260,6 +266,23 @@ hipError_t launch_fp8b_schedule(const int64_t* group_list, int64_t E, int64_t R,
 
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// four neighbouring outputs of one row
+__device__ __forceinline__ void store4(const Fp8bGemm& p, int64_t m, int64_t n, const f32x4& v) {
+  if (n >= p.N) return;
+  uint16_t* y = p.y + m * p.ldy + n;
+  uint16_t o[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+    o[t] = to_bf16(p.bias ? v[t] + bf16_to_f32(p.bias[min(n + t, p.N - 1)]) : v[t]);
+  if (p.store_vec) {
+    *reinterpret_cast<uint2*>(y) = uint2{o[0] | ((uint32_t)o[1] << 16), o[2] | ((uint32_t)o[3] << 16)};
+  } else {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+      if (n + t < p.N) y[t] = o[t];
+  }
 }
 
 // Streaming tile: up to 16 MB rows x 128 NBW columns over the whole K, eight
@@ -468,23 +491,6 @@ struct StreamTile {
       }
     }
   }
-
-  // four neighbouring outputs of one row
-  __device__ __forceinline__ static void store4(const Fp8bGemm& p, int64_t m, int64_t n, const f32x4& v) {
-    if (n >= p.N) return;
-    uint16_t* y = p.y + m * p.ldy + n;
-    uint16_t o[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      o[t] = to_bf16(p.bias ? v[t] + bf16_to_f32(p.bias[min(n + t, p.N - 1)]) : v[t]);
-    if (p.store_vec) {
-      *reinterpret_cast<uint2*>(y) = uint2{o[0] | ((uint32_t)o[1] << 16), o[2] | ((uint32_t)o[3] << 16)};
-    } else {
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-        if (n + t < p.N) y[t] = o[t];
-    }
-  }
 };
 
 // tile height by the rows there are
@@ -522,10 +528,160 @@ __global__ __launch_bounds__(512) void fp8b_dense_kernel(Fp8bGemm p) {
   stream_tile<NBW, EXACT>(p, smem, 0, row0, (int)min((int64_t)kTileRows, p.M - row0), blockIdx.y * 8 * NBW);
 }
 
+// Decode (dense, at most 64 rows): the weight's stream, split over K inside the
+// workgroup. A workgroup owns NBW 16-column blocks and 16 MB rows over the whole
+// K; its eight wavefronts take every eighth block of K, with U blocks of weights
+// and codes in flight each, straight from global memory into operand registers,
+// and their sums meet in LDS in a fixed order. FUSED (few rows): x is BF16, and
+// every workgroup quantizes the rows itself into LDS, behind its first weight
+// loads, which saves the quantizer's launch.
+constexpr int kDecodeWaves = 8;
+constexpr int64_t kFusedValues = 32768;  // M x K quantized by every workgroup, at most
+constexpr int64_t kFusedLds = 65536;     // their codes and scales
+
+template <int MB, int NBW, int U, bool FUSED>
+__global__ __launch_bounds__(kDecodeWaves * 64) void fp8b_decode_kernel(Fp8bGemm p) {
+  __shared__ f32x4 red[kDecodeWaves][MB * NBW][kWave];
+  extern __shared__ __attribute__((aligned(16))) uint8_t qlds[];  // FUSED: codes [M][128 KB], scales [KB][M]
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int NB = (int)((p.N + 15) / 16), KB = (int)p.KB, M = (int)p.M;
+  const int nb0 = blockIdx.x * NBW, m0 = blockIdx.y * MB * 16;
+  const uint32_t l16 = lane * 16;
+  const uint8_t* wp[NBW];
+#pragma unroll
+  for (int j = 0; j < NBW; ++j)  // blocks past the last read it; their outputs are never stored
+    wp[j] = p.w + (int64_t)min(nb0 + j, NB - 1) * KB * kFp8BlockBytes;
+  const float* wsp = p.w_scale + (int64_t)(nb0 / 8) * KB;  // NBW divides 8: one block of scales
+  int row[MB];  // rows past the last read it; they only feed outputs that are never stored
+#pragma unroll
+  for (int m = 0; m < MB; ++m) row[m] = min(m0 + m * 16 + (lane & 15), M - 1);
+
+  i32x4 w[U][NBW][2], a[U][MB][2];
+  float sx[U][MB], sw[U];
+  auto load_w = [&](int kb0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = min(kb0 + u * kDecodeWaves, KB - 1);
+#pragma unroll
+      for (int j = 0; j < NBW; ++j) {
+        const uint8_t* b = wp[j] + k * kFp8BlockBytes;
+        w[u][j][0] = *reinterpret_cast<const i32x4*>(b + l16);
+        w[u][j][1] = *reinterpret_cast<const i32x4*>(b + l16 + 1024);
+      }
+      sw[u] = wsp[k];
+    }
+  };
+  auto load_a = [&](int kb0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t k = min(kb0 + u * kDecodeWaves, KB - 1);
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        if (FUSED) {
+          const uint8_t* src = qlds + row[m] * (KB * 128) + k * 128 + (lane >> 4) * 16;
+          a[u][m][0] = *reinterpret_cast<const i32x4*>(src);
+          a[u][m][1] = *reinterpret_cast<const i32x4*>(src + 64);
+          sx[u][m] = reinterpret_cast<const float*>(qlds + M * (KB * 128))[k * M + row[m]];
+        } else {
+          const uint8_t* src = p.a + row[m] * p.lda + k * 128 + (lane >> 4) * 16;
+          a[u][m][0] = *reinterpret_cast<const i32x4*>(src);
+          a[u][m][1] = *reinterpret_cast<const i32x4*>(src + 64);
+          sx[u][m] = p.a_scale[k * p.a_rows + row[m]];
+        }
+      }
+    }
+  };
+
+  if (!FUSED) load_a(wave);
+  load_w(wave);
+  if constexpr (FUSED) {
+    __builtin_amdgcn_sched_barrier(0);
+    // as fp8b_quant_kernel: 16 lanes a (row, block)
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(p.a);
+    const int sub = tid & 15;
+    for (int b = tid >> 4; b < M * KB; b += kDecodeWaves * 4) {
+      const int r = b / KB, kb = b % KB;
+      const int64_t k0 = (int64_t)kb * kFp8Block + sub * 8;
+      float v[8];
+      load8<true>(x + r * p.lda + k0, p.K - k0, v);
+      float s;
+      const uint2 q = quant_block(v, p.scale_alg, s);
+      *reinterpret_cast<uint2*>(qlds + r * (KB * 128) + k0) = q;
+      if (sub == 0) reinterpret_cast<float*>(qlds + M * (KB * 128))[kb * M + r] = s;
+    }
+    __syncthreads();
+  }
+  f32x4 acc[MB][NBW];
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int j = 0; j < NBW; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int kb0 = wave; kb0 < KB; kb0 += kDecodeWaves * U) {
+    if (kb0 != wave) {
+      if (!FUSED) load_a(kb0);
+      load_w(kb0);
+    }
+    if (FUSED) load_a(kb0);
+    __builtin_amdgcn_sched_barrier(0);  // every load of the round in flight before the first product
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (kb0 + u * kDecodeWaves >= KB) break;  // wave-uniform: clamped blocks add nothing
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        const float s = sx[u][m] * sw[u];
+#pragma unroll
+        for (int j = 0; j < NBW; ++j) {
+          const f32x4 part = mfma_fp8(join(w[u][j][0], w[u][j][1]), join(a[u][m][0], a[u][m][1]));
+#pragma unroll
+          for (int t = 0; t < 4; ++t) acc[m][j][t] = __builtin_fmaf(part[t], s, acc[m][j][t]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int j = 0; j < NBW; ++j) red[wave][m * NBW + j][lane] = acc[m][j];
+  __syncthreads();
+  if (wave >= MB * NBW) return;
+  f32x4 sum = red[0][wave][lane];
+#pragma unroll
+  for (int v = 1; v < kDecodeWaves; ++v) sum += red[v][wave][lane];
+  const int r = m0 + (wave / NBW) * 16 + (lane & 15);
+  if (r < M) store4(p, r, (int64_t)(nb0 + wave % NBW) * 16 + (lane >> 4) * 4, sum);
+}
+
+// Whether a BF16 x of M rows is quantized inside the decode kernel: every
+// workgroup does all of it, which past kFusedValues costs more than a launch.
+bool fp8b_fused_ok(int64_t M, int64_t K, int64_t ldx, const void* x) {
+  const int64_t KB = ceil_div(K, kFp8Block);
+  return M >= 1 && M <= 16 && M * K <= kFusedValues && K % 8 == 0 && ldx % 8 == 0 && ((uintptr_t)x & 15) == 0 &&
+         M * KB * (kFp8Block + 4) <= kFusedLds;
+}
+
+hipError_t launch_fp8b_linear_fused(const Fp8bGemm& args, hipStream_t stream) {
+  Fp8bGemm p = args;
+  p.store_vec = p.N % 4 == 0 && p.ldy % 4 == 0 && ((uintptr_t)p.y & 7) == 0;
+  hipLaunchKernelGGL((fp8b_decode_kernel<1, 1, 7, true>), dim3((unsigned)ceil_div(p.N, 16)), dim3(kDecodeWaves * 64),
+                     (size_t)(p.M * p.KB * (kFp8Block + 4)), stream, p);
+  return hipGetLastError();
+}
+
 hipError_t launch_fp8b_gemm(const Fp8bGemm& args, hipStream_t stream) {
   if (args.M == 0 || args.N == 0) return hipSuccess;
   Fp8bGemm p = args;
   p.store_vec = p.N % 4 == 0 && p.ldy % 4 == 0 && ((uintptr_t)p.y & 7) == 0;
+  if (!p.group_list && p.M <= 64) {
+    // 33..64 rows as two groups of 32 on pairs of column blocks: a workgroup reads
+    // half the codes for twice the columns
+    const int nbw = p.M > 32 ? 2 : 1;
+    auto fn = p.M <= 16 ? fp8b_decode_kernel<1, 1, 7, false> : p.M <= 32 ? fp8b_decode_kernel<2, 1, 7, false>
+                                                                         : fp8b_decode_kernel<2, 2, 4, false>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)ceil_div(ceil_div(p.N, 16), nbw), (unsigned)ceil_div(p.M, 32)),
+                       dim3(kDecodeWaves * 64), 0, stream, p);
+    return hipGetLastError();
+  }
   constexpr int NBW = 2;
   const int64_t nt = ceil_div(p.N, 128 * NBW);
   if (!p.group_list) {

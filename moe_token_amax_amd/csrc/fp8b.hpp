@@ -37,6 +37,9 @@ struct Fp8bGemm {
   int64_t E;
   int exact;                 // grouped: products of the codes as BF16, none of them cut
   const void* ws;            // grouped: the schedule written by launch_fp8b_schedule
+  // BF16 input quantized inside (launch_fp8b_linear_fused): a = x, lda in elements
+  int64_t K;
+  int scale_alg;
   bool store_vec;            // set by the launcher: outputs in 8-byte pieces
 };
 // tiles of the rows of every expert; any number of products over one
@@ -44,6 +47,8 @@ struct Fp8bGemm {
 int64_t fp8b_sched_bytes(int64_t R, int64_t E);
 hipError_t launch_fp8b_schedule(const int64_t* group_list, int64_t E, int64_t R, void* ws, hipStream_t stream);
 hipError_t launch_fp8b_gemm(const Fp8bGemm& p, hipStream_t stream);
+bool fp8b_fused_ok(int64_t M, int64_t K, int64_t ldx, const void* x);
+hipError_t launch_fp8b_linear_fused(const Fp8bGemm& p, hipStream_t stream);
 
 struct GateArgs {
   const void* logits;  // [T, E], row stride ld

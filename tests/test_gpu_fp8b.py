@@ -131,6 +131,7 @@ def test_quant_non_finite_values_show_in_the_scale(w):
 # ------------------------------------------------------------------ linear
 LINEAR = [  # M, N, K
     (1, 16, 128), (1, 1, 1), (2, 17, 65), (4, 256, 1024), (16, 100, 300), (17, 128, 256), (33, 130, 2000),
+    (3, 40, 2048), (4, 48, 7168), (5, 48, 7168), (16, 64, 2048), (9, 33, 3000), (40, 40, 4200),
     (64, 512, 512), (65, 48, 384), (100, 333, 1000), (128, 256, 640), (200, 272, 128), (257, 300, 200), (300, 520, 1152),
 ]
 
