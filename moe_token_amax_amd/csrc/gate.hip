@@ -16,8 +16,8 @@
 //   that no expert fills get id -1 and weight 0. weight = score, divided by the
 //   sum of the k where asked (0 where that sum is 0), times a factor.
 //
-// Which of two close keys is larger decides an expert, so scores and keys are
-// doubles here and the weights are rounded once.
+// Which of two close keys is larger decides an expert: the result is that of
+// doubles (gate_exact), found with floats wherever they can tell (gate_fast).
 #include <hip/hip_fp16.h>
 
 #include "device_common.hpp"
@@ -37,12 +37,10 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 
 __device__ __forceinline__ double shfl_xor_d(double v, int m) { return __shfl_xor(v, m, kWave); }
 
-// One wavefront per token; lane l holds experts l + 64 i.
+// The definition itself, in doubles, by one wavefront; lane l holds experts
+// l + 64 i. Every lane of the wavefront takes part.
 template <int DT, int P>
-__global__ __launch_bounds__(256) void gate_kernel(GateArgs g) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (t >= g.T) return;
+__device__ void gate_exact(const GateArgs& g, int64_t t, int lane) {
   const int E = g.E;
   float l[P];
   bool in[P];
@@ -141,10 +139,262 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs g) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Fast form: one wavefront per token, lane l holds the P consecutive experts
+// P l + i, keys are floats. Where float rounding could change the choice the
+// wavefront falls back to gate_exact: it does so if two keys that have to be told
+// apart (neighbours among the k + 1 largest, the last group that stays and the
+// first that goes) are within kNear (1 + |a| + |b|) and do not come from the same
+// logit and bias. Scores are at most 1 and off by less than 2^-21: with d the
+// exponential's relative error, (1 + |l|) 2^-23 at most (one ulp, and the rounded
+// argument), a sigmoid is off by s (1 - s) d < 0.5 2^-23 and two roundings of s, a
+// softmax by s d and s times the sum's error, whose terms weigh d by e^-|l|. So keys
+// are off by 2^-21 + 2^-24 |key| and marks by twice that, and two of either by no
+// more than kNear (1 + |a| + |b|).
+// Without a bias the order of keys is the order of logits, which are compared as
+// they are; doubles saturate (1 from l = 37 on, 0 under -745), so logits past 36
+// or a selected one 700 under the maximum (softmax) or -700 (sigmoid) fall back
+// too. On random logits the fallback takes about 1 token in 2000.
+// The weights come from the selected logits alone, in doubles; only the sum of a
+// softmax that is not renormalized is a float sum.
+// ---------------------------------------------------------------------------
+constexpr float kNear = 0x1p-19f;
+
+// order-preserving map of finite floats and +inf to integers above 0 (0: out)
+__device__ __forceinline__ uint32_t key_bits(float f) {
+  const uint32_t u = __float_as_uint(f + 0.0f);  // -0 becomes +0: equal keys have equal bits
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+__device__ __forceinline__ float exp_f(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+
+__device__ __forceinline__ void merge2(float& a, float& b, float oa, float ob) {
+  b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+  a = fmaxf(a, oa);
+}
+
+// the two largest of `seg` consecutive lanes (aligned, a power of two), in all of them
+__device__ __forceinline__ void segment_top2(float& a, float& b, int seg) {
+  if (seg >= 2) merge2(a, b, dpp_f<0xB1>(a), dpp_f<0xB1>(b));    // lanes l ^ 1
+  if (seg >= 4) merge2(a, b, dpp_f<0x4E>(a), dpp_f<0x4E>(b));    // l ^ 2
+  if (seg >= 8) merge2(a, b, dpp_f<0x141>(a), dpp_f<0x141>(b));  // the other quad of 8
+  if (seg >= 16) merge2(a, b, dpp_f<0x140>(a), dpp_f<0x140>(b)); // the other half of 16
+  if (seg >= 32) merge2(a, b, __shfl_xor(a, 16, kWave), __shfl_xor(b, 16, kWave));
+  if (seg >= 64) merge2(a, b, __shfl_xor(a, 32, kWave), __shfl_xor(b, 32, kWave));
+}
+
+__device__ __forceinline__ float wave_sum_f(float v) {
+  v += dpp_f<0xB1>(v);
+  v += dpp_f<0x4E>(v);
+  v += dpp_f<0x141>(v);
+  v += dpp_f<0x140>(v);
+  v += __shfl_xor(v, 16, kWave);
+  return v + __shfl_xor(v, 32, kWave);
+}
+
+__device__ __forceinline__ float readlane_f(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+
+// the largest of the lanes' keys as a float; 0 if none is in
+__device__ __forceinline__ float wave_top(uint32_t kb) {
+  const uint32_t m = wave_max_u32(kb);
+  return m ? key_value(m) : 0.f;
+}
+
+template <int DT, int P>
+__device__ __forceinline__ void load_logits(const GateArgs& g, int64_t t, int lane, float (&l)[P]) {
+  const int e0 = lane * P;
+  const int64_t at = t * g.ld + e0;
+  if (P >= 4 && DT == 0 && g.vec) {
+#pragma unroll
+    for (int i = 0; i < P; i += 4) {
+      float4 v = {0.f, 0.f, 0.f, 0.f};
+      if (e0 + i < g.E) v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(g.logits) + at + i);
+      l[i] = v.x; l[i + 1] = v.y; l[i + 2] = v.z; l[i + 3] = v.w;
+    }
+  } else if (P >= 4 && DT != 0 && g.vec) {
+#pragma unroll
+    for (int i = 0; i < P; i += 4) {
+      uint2 v = {0u, 0u};
+      if (e0 + i < g.E) v = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(g.logits) + at + i);
+      const uint32_t h[4] = {v.x & 0xFFFFu, v.x >> 16, v.y & 0xFFFFu, v.y >> 16};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        l[i + j] = DT == 1 ? bf16_to_f32(h[j]) : __half2float(__builtin_bit_cast(__half, (uint16_t)h[j]));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) l[i] = e0 + i < g.E ? load_logit<DT>(g.logits, at + i) : 0.f;
+  }
+}
+
+// false: the choice is too close for floats
+template <int DT, int P>
+__device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane) {
+  const int E = g.E, k = g.top_k;
+  const bool sigmoid = g.scoring == 1, biased = g.bias != nullptr;
+  float l[P];
+  load_logits<DT, P>(g, t, lane, l);
+  bool in[P];
+  float top = -__builtin_huge_valf();
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    in[i] = lane * P + i < E && l[i] > -__builtin_huge_valf();  // false for NaN
+    l[i] = fminf(l[i], 3.402823466e38f);
+    if (in[i]) top = fmaxf(top, l[i]);
+  }
+  const bool need_scores = biased || g.n_group > 1 || (!sigmoid && !g.renormalize);
+  float s[P];
+  float total = 1.f;  // softmax: the sum of the exponentials
+  if (need_scores) {
+    if (sigmoid) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) s[i] = in[i] ? __builtin_amdgcn_rcpf(1.f + exp_f(-l[i])) : 0.f;
+    } else {
+      const uint32_t tb = wave_max_u32(top > -__builtin_huge_valf() ? key_bits(top) : 0u);
+      top = tb ? key_value(tb) : 0.f;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        s[i] = in[i] ? exp_f(l[i] - top) : 0.f;
+        sum += s[i];
+      }
+      total = wave_sum_f(sum);
+      const float r = total > 0.f ? 1.f / total : 0.f;
+#pragma unroll
+      for (int i = 0; i < P; ++i) s[i] *= r;
+    }
+  }
+  // keys as integers: logits without a bias, else scores + bias
+  uint32_t u[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    float key = l[i];
+    bool ok = in[i];
+    if (biased) {
+      key = s[i] + (in[i] ? g.bias[lane * P + i] : 0.f);
+      ok = ok && key > -__builtin_huge_valf();
+    }
+    u[i] = ok ? key_bits(key) : 0u;
+  }
+  bool close = false;
+  if (g.n_group > 1) {
+    const int per = E / g.n_group, seg = per / P;
+    float a = -__builtin_huge_valf(), b = a;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const float v = u[i] ? (biased ? key_value(u[i]) : s[i]) : -__builtin_huge_valf();
+      b = fmaxf(b, fminf(a, v));
+      a = fmaxf(a, v);
+    }
+    segment_top2(a, b, seg);
+    const float mark = b > -__builtin_huge_valf() ? a + b : a;
+    const int mine = lane / seg;
+    int rank = 0;
+    for (int h = 0; h < g.n_group; ++h) {
+      const float o = readlane_f(mark, h * seg);
+      rank += o > mark || (o == mark && h < mine);
+    }
+    const bool group = mine < g.n_group;
+    if (g.topk_group < g.n_group) {
+      // the last that stays and the first that goes
+      const uint64_t last = __ballot(group && rank == g.topk_group - 1), next = __ballot(group && rank == g.topk_group);
+      const float x = readlane_f(mark, __builtin_ctzll(last)), y = readlane_f(mark, __builtin_ctzll(next));
+      if (y > -__builtin_huge_valf()) close = !(x - y > kNear * (1.f + fabsf(x) + fabsf(y)));
+    }
+    if (!(group && rank < g.topk_group)) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) u[i] = 0u;
+    }
+  }
+  // top k (and the runner-up where keys are rounded): every step takes the
+  // largest key of the wavefront, of the lowest lane and index among equals
+  int id = -1;          // lane j: the j-th expert
+  uint32_t kb = 0u;     // and its key
+  const int steps = biased && k < kWave ? k + 1 : k;
+  for (int j = 0; j < steps; ++j) {
+    uint32_t m = u[0];
+#pragma unroll
+    for (int i = 1; i < P; ++i) m = max(m, u[i]);
+    const uint32_t best = wave_max_u32(m);
+    if (best == 0u) break;  // uniform: nothing is left
+    const int owner = __builtin_ctzll(__ballot(m == best));
+    int at = P - 1;
+#pragma unroll
+    for (int i = P - 2; i >= 0; --i)
+      if ((uint32_t)__builtin_amdgcn_readlane((int)u[i], owner) == best) at = i;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (at == i && lane == owner) u[i] = 0u;
+    if (lane == j) {
+      id = owner * P + at;
+      kb = best;
+    }
+  }
+  const float sel = id >= 0 ? fminf(load_logit<DT>(g.logits, t * g.ld + id), 3.402823466e38f) : 0.f;
+  if (biased) {
+    // lane j against lane j + 1, the runner-up included
+    const float v = key_value(kb), bj = id >= 0 ? g.bias[id] : 0.f;
+    const int n = __shfl_down(id, 1, kWave);
+    const float nv = __shfl_down(v, 1, kWave), nl = __shfl_down(sel, 1, kWave), nb = __shfl_down(bj, 1, kWave);
+    if (lane < k && lane + 1 < kWave && id >= 0 && n >= 0 && !(nl == sel && nb == bj))
+      close = close || !(v - nv > kNear * (1.f + fabsf(v) + fabsf(nv)));
+    if (k == kWave) close = true;  // no lane left for the runner-up
+  } else {
+    const float first = need_scores && !sigmoid ? top : readlane_f(sel, 0);
+    if (lane < k && id >= 0) close = close || (sigmoid ? sel > 36.f || sel < -700.f : sel - first < -700.f);
+  }
+  if (__ballot(close)) return false;
+  double w = 0.0;
+  const bool mine = lane < k && id >= 0;
+  if (sigmoid) {
+    if (mine) w = 1.0 / (1.0 + exp(-(double)sel));
+  } else {
+    // renormalized: the largest selected logit stands for the maximum
+    const float ref = g.renormalize ? wave_top(mine ? key_bits(sel) : 0u) : top;
+    if (mine) w = exp((double)sel - (double)ref);
+  }
+  if (g.renormalize) {
+    double sum = w;
+    for (int d = 1; d < k; d <<= 1) sum += shfl_xor_d(sum, d);  // lanes past k hold 0
+    w = sum > 0.0 ? w / sum : 0.0;
+  } else if (!sigmoid) {
+    w = total > 0.f ? w / (double)total : 0.0;
+  }
+  if (lane < k) {
+    g.ids[t * k + lane] = id;
+    g.weights[t * k + lane] = (float)(w * (double)g.scale);
+  }
+  return true;
+}
+
+template <int DT, int P>
+__global__ __launch_bounds__(256) void gate_kernel(GateArgs g) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= g.T) return;
+  if (!g.fast || !gate_fast<DT, P>(g, t, lane)) gate_exact<DT, P>(g, t, lane);  // uniform
+}
+
 template <int DT>
-static hipError_t launch_gate_dt(const GateArgs& p, hipStream_t stream) {
-  void (*fn)(GateArgs) = p.E <= 64 ? gate_kernel<DT, 1> : p.E <= 128 ? gate_kernel<DT, 2> : p.E <= 256 ? gate_kernel<DT, 4>
-                       : p.E <= 512 ? gate_kernel<DT, 8> : gate_kernel<DT, 16>;
+static hipError_t launch_gate_dt(const GateArgs& args, hipStream_t stream) {
+  GateArgs p = args;
+  const int P = p.E <= 64 ? 1 : p.E <= 128 ? 2 : p.E <= 256 ? 4 : p.E <= 512 ? 8 : 16;
+  const int per = p.E / p.n_group, seg = per / P;
+  // groups have to be whole aligned runs of a power of two of lanes
+  p.fast = p.n_group == 1 || (per % P == 0 && (seg & (seg - 1)) == 0);
+  p.vec = p.E % 4 == 0 && p.ld % 4 == 0 && ((uintptr_t)p.logits & (DT == 0 ? 15 : 7)) == 0;
+  void (*fn)(GateArgs) = P == 1 ? gate_kernel<DT, 1> : P == 2 ? gate_kernel<DT, 2> : P == 4 ? gate_kernel<DT, 4>
+                       : P == 8 ? gate_kernel<DT, 8> : gate_kernel<DT, 16>;
   hipLaunchKernelGGL(fn, dim3((unsigned)ceil_div(p.T, 4)), dim3(256), 0, stream, p);
   return hipGetLastError();
 }
