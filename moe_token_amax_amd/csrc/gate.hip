@@ -204,6 +204,19 @@ __device__ __forceinline__ float readlane_f(float v, int l) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
 }
 
+// wave_max_u32 with one readlane: the DPP broadcasts of row ends carry the
+// maximum to lane 63 (the scalar unit, shared by the CU's SIMDs, is what four
+// readlanes and their maxima ran out of)
+__device__ __forceinline__ uint32_t wave_max_last(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false));  // row_bcast15 into rows 1, 3
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false));  // row_bcast31 into rows 2, 3
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
 // the largest of the lanes' keys as a float; 0 if none is in
 __device__ __forceinline__ float wave_top(uint32_t kb) {
   const uint32_t m = wave_max_u32(kb);
@@ -325,18 +338,18 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
     uint32_t m = u[0];
 #pragma unroll
     for (int i = 1; i < P; ++i) m = max(m, u[i]);
-    const uint32_t best = wave_max_u32(m);
+    const uint32_t best = wave_max_last(m);
     if (best == 0u) break;  // uniform: nothing is left
+    int at = P - 1;  // this lane's lowest index of its maximum
+#pragma unroll
+    for (int i = P - 2; i >= 0; --i) at = u[i] == m ? i : at;
     const int owner = __builtin_ctzll(__ballot(m == best));
-    int at = P - 1;
+    const int e = owner * P + __builtin_amdgcn_readlane(at, owner);
+    at = lane == owner ? at : -1;
 #pragma unroll
-    for (int i = P - 2; i >= 0; --i)
-      if ((uint32_t)__builtin_amdgcn_readlane((int)u[i], owner) == best) at = i;
-#pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (at == i && lane == owner) u[i] = 0u;
+    for (int i = 0; i < P; ++i) u[i] = at == i ? 0u : u[i];
     if (lane == j) {
-      id = owner * P + at;
+      id = e;
       kb = best;
     }
   }
