@@ -230,7 +230,9 @@ def _check(status: int):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the raw handle of the current stream: torch.cuda.current_stream() builds a
+    # Stream object, 2.8 us of the 10 us that a small call spends on the host
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _ptr(t: torch.Tensor | None):
@@ -1117,12 +1119,28 @@ GATE_SOFTMAX, GATE_SIGMOID = 0, 1
 _LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
-def _here(*tensors):
-    """Every given tensor on the current device, whose stream the call uses."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+def _at(t: torch.Tensor | None, dtype, name: str, ndim: int):
+    """Address of a contiguous tensor on the current device, whose stream the call
+    uses (None for None). The checks of _need, each of which a small call feels."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.dim() == ndim and t.is_cuda and t.is_contiguous() and \
+                t.get_device() == torch._C._cuda_getDevice():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, dtype, name, ndim)
+    raise ValueError(f"{name} is on {t.device}, which is not the current device")
+
+
+def _rows_at(t: torch.Tensor, dtype, name: str):
+    """(address, row stride) of a 2-D tensor with contiguous rows on the current device."""
+    ld = t.shape[1] if isinstance(t, torch.Tensor) and t.dim() == 2 and t.is_contiguous() and t.is_cuda and \
+        t.dtype is dtype else _rows(t, dtype, name)
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return t.data_ptr(), ld
 
 
 def moe_gate(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None,
@@ -1135,32 +1153,42 @@ def moe_gate(logits: torch.Tensor, top_k: int, bias: torch.Tensor | None = None,
     ``bias`` (float32 [E]) moves the choice but not the weights; with n_group > 1
     only the topk_group best groups are chosen from. A logit of -inf switches an
     expert off for a token; slots that no expert fills get id -1, weight 0."""
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in _LOGIT_TYPES:
+    kind = _LOGIT_TYPES.get(logits.dtype) if isinstance(logits, torch.Tensor) else None
+    if kind is None:
         raise TypeError("logits must be a float32, bfloat16 or float16 tensor")
-    ld = _rows(logits, logits.dtype, "logits")
+    at, ld = _rows_at(logits, logits.dtype, "logits")
     T, E = logits.shape
     if ids is None:
         ids = torch.empty((T, max(top_k, 0)), dtype=torch.int32, device=logits.device)
     if weights is None:
         weights = torch.empty((T, max(top_k, 0)), dtype=torch.float32, device=logits.device)
-    _need(ids, torch.int32, "ids", 2)
-    _need(weights, torch.float32, "weights", 2)
-    if tuple(ids.shape) != (T, top_k) or tuple(weights.shape) != (T, top_k):
+    if ids.shape != (T, top_k) or weights.shape != (T, top_k):
         raise ValueError("ids / weights must be [T, top_k]")
-    if bias is not None:
-        _need(bias, torch.float32, "bias", 1)
-        if bias.shape[0] != E:
-            raise ValueError("bias must be [E]")
-    _here(logits, bias, ids, weights)
-    _check(lib.w8a8_moe_gate(_ptr(logits), _LOGIT_TYPES[logits.dtype], T, E, ld, _ptr(bias), scoring,
-                             n_group, topk_group, top_k, int(bool(renormalize)), scale, _ptr(ids),
-                             _ptr(weights), _stream()))
+    if bias is not None and bias.shape != (E,):
+        raise ValueError("bias must be [E]")
+    _check(lib.w8a8_moe_gate(at, kind, T, E, ld, _at(bias, torch.float32, "bias", 1), scoring, n_group, topk_group,
+                             top_k, 1 if renormalize else 0, scale, _at(ids, torch.int32, "ids", 2),
+                             _at(weights, torch.float32, "weights", 2), _stream()))
     return ids, weights
 
 
 # ---------------------------------------------------------------------------
 # block-scaled FP8
 # ---------------------------------------------------------------------------
+def _room(ws: torch.Tensor | None, device, nbytes, *sizes: int):
+    """(workspace, address, bytes); nbytes(*sizes) are allocated where none is given (the
+    library checks the size of a given one). The caller holds the tensor until its
+    launches are enqueued."""
+    if ws is None:
+        ws = torch.empty((max(nbytes(*sizes), 1),), dtype=torch.uint8, device=device)
+    return ws, _at(ws, torch.uint8, "workspace", 1), ws.numel()
+
+
+def _fp8_packed(E: int, N: int, K: int) -> int:
+    # fp8b_packed_bytes without the call into the library
+    return E * 16 * -(-N // 16) * 128 * _fp8_blocks(K)
+
+
 def _fp8_blocks(n: int) -> int:
     return -(-n // 128)
 
@@ -1170,7 +1198,7 @@ def fp8b_quant(x: torch.Tensor, act: int = ACT_NONE, scale_alg: int = 0, q: torc
     """BF16 [M, K], or [gate | up] [M, 2K] with act=ACT_SWIGLU (rows contiguous, a row
     stride is fine) -> (E4M3 codes uint8 [M, K rounded up to 128], float32 scales
     [ceil(K/128), M])."""
-    ldx = _rows(x, torch.bfloat16, "x")
+    at, ldx = _rows_at(x, torch.bfloat16, "x")
     M, K = x.shape
     if act == ACT_SWIGLU:
         if K % 2:
@@ -1181,12 +1209,10 @@ def fp8b_quant(x: torch.Tensor, act: int = ACT_NONE, scale_alg: int = 0, q: torc
         q = torch.empty((M, 128 * B), dtype=torch.uint8, device=x.device)
     if scale is None:
         scale = torch.empty((B, M), dtype=torch.float32, device=x.device)
-    _need(q, torch.uint8, "q", 2)
-    _need(scale, torch.float32, "scale", 2)
-    if tuple(q.shape) != (M, 128 * B) or tuple(scale.shape) != (B, M):
+    if q.shape != (M, 128 * B) or scale.shape != (B, M):
         raise ValueError("q must be [M, K rounded up to 128], scale [ceil(K/128), M]")
-    _here(x, q, scale)
-    _check(lib.w8a8_fp8b_quant(_ptr(x), M, K, ldx, act, scale_alg, _ptr(q), _ptr(scale), _stream()))
+    _check(lib.w8a8_fp8b_quant(at, M, K, ldx, act, scale_alg, _at(q, torch.uint8, "q", 2),
+                               _at(scale, torch.float32, "scale", 2), _stream()))
     return q, scale
 
 
@@ -1206,11 +1232,10 @@ def fp8b_prepack_weight(w_e4m3: torch.Tensor, out: torch.Tensor | None = None) -
     nbytes = fp8b_packed_bytes(E, N, K)
     if out is None:
         out = torch.empty((nbytes,), dtype=torch.uint8, device=w_e4m3.device)
-    _need(out, torch.uint8, "out", 1)
     if out.numel() < nbytes:
         raise ValueError(f"out needs {nbytes} bytes")
-    _here(w_e4m3, out)
-    _check(lib.w8a8_fp8b_prepack_weight(_ptr(w_e4m3), E, N, K, _ptr(out), _stream()))
+    _check(lib.w8a8_fp8b_prepack_weight(_at(w_e4m3, torch.uint8, "w_e4m3", w_e4m3.dim()), E, N, K,
+                                        _at(out, torch.uint8, "out", 1), _stream()))
     return out
 
 
@@ -1227,39 +1252,36 @@ def fp8b_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor, 
     of 128), times a packed E4M3 weight with w_scale float32 [ceil(N/128), ceil(K/128)]
     -> BF16 [M, N]. x and y may be row-strided."""
     if x_scale is None:
-        ldx = _rows(x, torch.bfloat16, "x")
+        at, ldx = _rows_at(x, torch.bfloat16, "x")
         M, Kx = x.shape
         if K is not None and K != Kx:
             raise ValueError("K must be the width of a BF16 x")
         K = Kx
     else:
-        ldx = _rows(x, torch.uint8, "x")
+        at, ldx = _rows_at(x, torch.uint8, "x")
         M = x.shape[0]
         K = x.shape[1] if K is None else K
         if x.shape[1] != 128 * _fp8_blocks(K):
             raise ValueError("E4M3 x must be [M, K rounded up to 128]")
-        _need(x_scale, torch.float32, "x_scale", 2)
-        if tuple(x_scale.shape) != (_fp8_blocks(K), M):
+        if x_scale.shape != (_fp8_blocks(K), M):
             raise ValueError("x_scale must be [ceil(K/128), M]")
-    _need(w_packed, torch.uint8, "w_packed", 1)
-    _need(w_scale, torch.float32, "w_scale", 2)
-    if w_packed.numel() < fp8b_packed_bytes(1, N, K):
+    wp = _at(w_packed, torch.uint8, "w_packed", 1)
+    if w_packed.numel() < _fp8_packed(1, N, K):
         raise ValueError("w_packed too small for [N, K]")
-    if tuple(w_scale.shape) != (_fp8_blocks(N), _fp8_blocks(K)):
+    if w_scale.shape != (_fp8_blocks(N), _fp8_blocks(K)):
         raise ValueError("w_scale must be [ceil(N/128), ceil(K/128)]")
-    if bias is not None:
-        _need(bias, torch.bfloat16, "bias", 1)
-        if bias.shape[0] != N:
-            raise ValueError("bias shape mismatch")
+    if bias is not None and bias.shape != (N,):
+        raise ValueError("bias shape mismatch")
     if y is None:
         y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    ldy = _rows(y, torch.bfloat16, "y")
-    if tuple(y.shape) != (M, N):
+    if y.shape != (M, N):
         raise ValueError("y shape mismatch")
-    ws, ws_n = _workspace(fp8b_linear_workspace_bytes(M, N, K) if x_scale is None else 0, x.device, workspace)
-    _here(x, x_scale, w_packed, w_scale, bias, y, ws)
-    _check(lib.w8a8_fp8b_linear(_ptr(x), ldx, _ptr(x_scale), M, K, _ptr(w_packed), _ptr(w_scale), N,
-                                _ptr(bias), _ptr(y), ldy, scale_alg, _ptr(ws), ws_n, _stream()))
+    yp, ldy = _rows_at(y, torch.bfloat16, "y")
+    room, ws, ws_n = (None, None, 0) if x_scale is not None else \
+        _room(workspace, x.device, fp8b_linear_workspace_bytes, M, N, K)
+    _check(lib.w8a8_fp8b_linear(at, ldx, _at(x_scale, torch.float32, "x_scale", 2), M, K, wp,
+                                _at(w_scale, torch.float32, "w_scale", 2), N, _at(bias, torch.bfloat16, "bias", 1),
+                                yp, ldy, scale_alg, ws, ws_n, _stream()))
     return y
 
 
@@ -1277,35 +1299,28 @@ def fp8b_grouped_gemm(a: torch.Tensor, a_scale: torch.Tensor, group_list: torch.
     ceil(K/128)]) -> BF16 [R, N]. Output row r reads row row_index[r] of a (int32 [R]), or
     row r without it (R = A). ``exact``: no product is cut, for an output that is quantized
     again (the chain's W13)."""
-    _need(a, torch.uint8, "a", 2)
-    _need(a_scale, torch.float32, "a_scale", 2)
-    _need(group_list, torch.int64, "group_list", 1)
-    _need(w_packed, torch.uint8, "w_packed", 1)
-    _need(w_scale, torch.float32, "w_scale", 3)
     A = a.shape[0]
     K = a.shape[1] if K is None else K
     E = group_list.shape[0]
     B = _fp8_blocks(K)
-    if a.shape[1] != 128 * B or tuple(a_scale.shape) != (B, A):
+    if a.shape != (A, 128 * B) or a_scale.shape != (B, A):
         raise ValueError("a must be [A, K rounded up to 128], a_scale [ceil(K/128), A]")
-    if tuple(w_scale.shape) != (E, _fp8_blocks(N), B):
+    if w_scale.shape != (E, _fp8_blocks(N), B):
         raise ValueError("w_scale must be [E, ceil(N/128), ceil(K/128)]")
-    if w_packed.numel() < fp8b_packed_bytes(E, N, K):
+    wp = _at(w_packed, torch.uint8, "w_packed", 1)
+    if w_packed.numel() < _fp8_packed(E, N, K):
         raise ValueError("w_packed too small for [E, N, K]")
-    R = A
-    if row_index is not None:
-        _need(row_index, torch.int32, "row_index", 1)
-        R = row_index.shape[0]
+    R = A if row_index is None else row_index.shape[0]
     if y is None:
         y = torch.empty((R, N), dtype=torch.bfloat16, device=a.device)
-    _need(y, torch.bfloat16, "y", 2)
-    if tuple(y.shape) != (R, N):
+    if y.shape != (R, N):
         raise ValueError("y shape mismatch")
-    ws, ws_n = _workspace(fp8b_grouped_workspace_bytes(R, E, N, K), a.device, workspace)
-    _here(a, a_scale, group_list, w_packed, w_scale, row_index, y, ws)
-    _check(lib.w8a8_fp8b_grouped_gemm(_ptr(a), _ptr(a_scale), A, _ptr(row_index), _ptr(group_list), R, E,
-                                      N, K, _ptr(w_packed), _ptr(w_scale), _ptr(y), int(bool(exact)),
-                                      _ptr(ws), ws_n, _stream()))
+    room, ws, ws_n = _room(workspace, a.device, fp8b_grouped_workspace_bytes, R, E, N, K)
+    _check(lib.w8a8_fp8b_grouped_gemm(_at(a, torch.uint8, "a", 2), _at(a_scale, torch.float32, "a_scale", 2), A,
+                                      _at(row_index, torch.int32, "row_index", 1),
+                                      _at(group_list, torch.int64, "group_list", 1), R, E, N, K, wp,
+                                      _at(w_scale, torch.float32, "w_scale", 3), _at(y, torch.bfloat16, "y", 2),
+                                      1 if exact else 0, ws, ws_n, _stream()))
     return y
 
 
@@ -1314,16 +1329,15 @@ def fp8b_moe_workspace_bytes(R: int, E: int, H: int, I: int) -> int:
 
 
 def _fp8b_experts(w13_packed, w13_scale, w2_packed, w2_scale, E: int, H: int, I: int):
-    for t, n in ((w13_packed, "w13_packed"), (w2_packed, "w2_packed")):
-        _need(t, torch.uint8, n, 1)
-    for t, n in ((w13_scale, "w13_scale"), (w2_scale, "w2_scale")):
-        _need(t, torch.float32, n, 3)
-    if tuple(w13_scale.shape) != (E, _fp8_blocks(2 * I), _fp8_blocks(H)) or \
-            tuple(w2_scale.shape) != (E, _fp8_blocks(H), _fp8_blocks(I)):
+    """Addresses of the experts' weights and scales."""
+    if w13_scale.shape != (E, _fp8_blocks(2 * I), _fp8_blocks(H)) or \
+            w2_scale.shape != (E, _fp8_blocks(H), _fp8_blocks(I)):
         raise ValueError("w13_scale must be [E, ceil(2I/128), ceil(H/128)], w2_scale [E, ceil(H/128), ceil(I/128)]")
-    if w13_packed.numel() < fp8b_packed_bytes(E, 2 * I, H) or \
-            w2_packed.numel() < fp8b_packed_bytes(E, H, I):
+    at = (_at(w13_packed, torch.uint8, "w13_packed", 1), _at(w13_scale, torch.float32, "w13_scale", 3),
+          _at(w2_packed, torch.uint8, "w2_packed", 1), _at(w2_scale, torch.float32, "w2_scale", 3))
+    if w13_packed.numel() < _fp8_packed(E, 2 * I, H) or w2_packed.numel() < _fp8_packed(E, H, I):
         raise ValueError("packed weights too small")
+    return at
 
 
 def fp8b_moe_grouped(x_rows: torch.Tensor, group_list: torch.Tensor, w13_packed: torch.Tensor,
@@ -1332,30 +1346,23 @@ def fp8b_moe_grouped(x_rows: torch.Tensor, group_list: torch.Tensor, w13_packed:
                      y: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Expert chain on expert-grouped rows, BF16 [R, H] or the codes and scales of
     fp8b_quant: W13 -> SwiGLU + quant -> W2 -> BF16 [R, H]. I: the width between."""
-    if x_scale is None:
-        _need(x_rows, torch.bfloat16, "x_rows", 2)
-    else:
-        _need(x_rows, torch.uint8, "x_rows", 2)
-        _need(x_scale, torch.float32, "x_scale", 2)
-    _need(group_list, torch.int64, "group_list", 1)
     R = x_rows.shape[0]
     H = x_rows.shape[1] if H is None else H
     E = group_list.shape[0]
-    if x_rows.shape[1] != (H if x_scale is None else 128 * _fp8_blocks(H)):
+    if x_rows.shape != (R, H if x_scale is None else 128 * _fp8_blocks(H)):
         raise ValueError("x_rows does not match H")
-    if x_scale is not None and tuple(x_scale.shape) != (_fp8_blocks(H), R):
+    if x_scale is not None and x_scale.shape != (_fp8_blocks(H), R):
         raise ValueError("x_scale must be [ceil(H/128), R]")
-    _fp8b_experts(w13_packed, w13_scale, w2_packed, w2_scale, E, H, I)
+    w13, s13, w2, s2 = _fp8b_experts(w13_packed, w13_scale, w2_packed, w2_scale, E, H, I)
     if y is None:
         y = torch.empty((R, H), dtype=torch.bfloat16, device=x_rows.device)
-    _need(y, torch.bfloat16, "y", 2)
-    if tuple(y.shape) != (R, H):
+    if y.shape != (R, H):
         raise ValueError("y shape mismatch")
-    ws, ws_n = _workspace(fp8b_moe_workspace_bytes(R, E, H, I), x_rows.device, workspace)
-    _here(x_rows, x_scale, group_list, w13_packed, w13_scale, w2_packed, w2_scale, y, ws)
-    _check(lib.w8a8_fp8b_moe_grouped(_ptr(x_rows), _ptr(x_scale), _ptr(group_list), R, E, H, I,
-                                     _ptr(w13_packed), _ptr(w13_scale), _ptr(w2_packed), _ptr(w2_scale),
-                                     scale_alg, _ptr(y), _ptr(ws), ws_n, _stream()))
+    room, ws, ws_n = _room(workspace, x_rows.device, fp8b_moe_workspace_bytes, R, E, H, I)
+    _check(lib.w8a8_fp8b_moe_grouped(_at(x_rows, torch.bfloat16 if x_scale is None else torch.uint8, "x_rows", 2),
+                                     _at(x_scale, torch.float32, "x_scale", 2),
+                                     _at(group_list, torch.int64, "group_list", 1), R, E, H, I, w13, s13, w2, s2,
+                                     scale_alg, _at(y, torch.bfloat16, "y", 2), ws, ws_n, _stream()))
     return y
 
 
@@ -1371,24 +1378,18 @@ def fp8b_moe_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.
     """Whole MoE layer on block-scaled FP8 experts: BF16 tokens [T, H] -> quantize once,
     route, W13 -> SwiGLU + quant -> W2, weighted combine -> BF16 [T, H]. topk_ids and
     topk_weights as moe_gate writes them. I: the width between."""
-    _need(x, torch.bfloat16, "x", 2)
-    _need(topk_ids, torch.int32, "topk_ids", 2)
-    _need(topk_weights, torch.float32, "topk_weights", 2)
-    _need(w13_scale, torch.float32, "w13_scale", 3)
     T, H = x.shape
     k = topk_ids.shape[1]
     E = w13_scale.shape[0]
-    if topk_ids.shape[0] != T or tuple(topk_weights.shape) != tuple(topk_ids.shape):
+    if topk_ids.shape != (T, k) or topk_weights.shape != (T, k):
         raise ValueError("topk_ids / topk_weights must be [T, top_k]")
-    _fp8b_experts(w13_packed, w13_scale, w2_packed, w2_scale, E, H, I)
+    w13, s13, w2, s2 = _fp8b_experts(w13_packed, w13_scale, w2_packed, w2_scale, E, H, I)
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    _need(out, torch.bfloat16, "out", 2)
-    if tuple(out.shape) != (T, H):
+    if out.shape != (T, H):
         raise ValueError("out shape mismatch")
-    ws, ws_n = _workspace(fp8b_moe_layer_workspace_bytes(T, k, E, H, I), x.device, workspace)
-    _here(x, topk_ids, topk_weights, w13_packed, w13_scale, w2_packed, w2_scale, out, ws)
-    _check(lib.w8a8_fp8b_moe_layer(_ptr(x), T, H, _ptr(topk_ids), _ptr(topk_weights), k, E, I,
-                                   _ptr(w13_packed), _ptr(w13_scale), _ptr(w2_packed), _ptr(w2_scale),
-                                   scale_alg, _ptr(out), _ptr(ws), ws_n, _stream()))
+    room, ws, ws_n = _room(workspace, x.device, fp8b_moe_layer_workspace_bytes, T, k, E, H, I)
+    _check(lib.w8a8_fp8b_moe_layer(_at(x, torch.bfloat16, "x", 2), T, H, _at(topk_ids, torch.int32, "topk_ids", 2),
+                                   _at(topk_weights, torch.float32, "topk_weights", 2), k, E, I, w13, s13, w2, s2,
+                                   scale_alg, _at(out, torch.bfloat16, "out", 2), ws, ws_n, _stream()))
     return out

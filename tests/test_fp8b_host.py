@@ -127,6 +127,13 @@ def test_binding_refusals_without_a_gpu(w):
         w.fp8b_quant(t)
     with pytest.raises(TypeError):
         w.fp8b_linear(t, t, t, 8)
+    b, u = t.to(torch.bfloat16), t.to(torch.uint8)
+    with pytest.raises(ValueError):
+        w.fp8b_quant(b)                                          # not on a GPU
+    with pytest.raises(ValueError):
+        w.fp8b_grouped_gemm(torch.zeros((4, 100), dtype=torch.uint8), t, torch.zeros(2, dtype=torch.int64), u, t, 8)
+    with pytest.raises(ValueError):
+        w.fp8b_moe_layer(b, torch.zeros((3, 2), dtype=torch.int32), torch.zeros((3, 2)), u, t[None], u, t[None], 32)
 
 
 @pytest.mark.skipif(_hipcc() is None, reason="hipcc not available")
