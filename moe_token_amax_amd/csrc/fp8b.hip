@@ -212,6 +212,15 @@ __device__ __forceinline__ f32x4 mfma_fp8(const i32x8& w, const i32x8& a) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, z, 0, 0, 0, 0, 0, 0);
 }
 
+// Scaled sum of one 16 x 16 block. The empty asm keeps the result where it is
+// computed: the compiler otherwise sinks the sums behind the next barrier and
+// keeps every partial product of the step in registers (or in scratch) till then.
+__device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& part, float s) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) acc[t] = __builtin_fmaf(part[t], s, acc[t]);
+  asm volatile("" : "+v"(acc));
+}
+
 __device__ __forceinline__ i32x8 join(const i32x4& x, const i32x4& y) {
   return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
 }
@@ -297,20 +306,22 @@ __device__ __forceinline__ void store4(const Fp8bGemm& p, int64_t m, int64_t n, 
 // stream does); otherwise the FP8 MFMA.
 template <int MB, int NBW, bool EXACT>
 struct StreamTile {
-  // blocks of weights in flight: as many as the registers that exact rows leave
-  static constexpr int kAhead = EXACT && MB == 8 ? 1 : EXACT && MB == 6 ? 2 : 3, kSets = kAhead + 1;
-  static constexpr int kUnroll = kSets == 3 ? 6 : 4;
+  static constexpr int kAhead = 3, kSets = kAhead + 1;  // blocks of weights in flight
   static constexpr int kWaves = 8;
   static constexpr int kPieces = (2 * MB + kWaves - 1) / kWaves;   // 16-byte pieces a thread stages per block of K
   static constexpr int kABytes = MB * (EXACT ? 4096 : 2048);       // one buffer's codes
   static constexpr int kBufBytes = kABytes + MB * 16 * 4;          // and its scales
-  static constexpr int kLdsBytes = 2 * kBufBytes;
+  static constexpr int kLdsBytes = 4 * kBufBytes;
 
   struct Stage {
     i32x4 a[kPieces];
     float s;
   };
-  using Weights = i32x4[NBW][2];
+  struct Weights {
+    i32x4 v[NBW][2];
+    float s;  // scale of the block (a load of its own kept in step: used in the step that
+              // issues it, it would wait for every weight load before it)
+  };
 
   __device__ __forceinline__ static void run(const Fp8bGemm& p, uint8_t* smem, int e, int64_t row0, int rows, int nb0) {
     const int tid = threadIdx.x, lane = tid & 63;
@@ -348,9 +359,10 @@ struct StreamTile {
 #pragma unroll
       for (int j = 0; j < NBW; ++j) {
         const uint8_t* b = wp[j] + k * kFp8BlockBytes;  // wave-uniform
-        w[j][0] = *reinterpret_cast<const i32x4*>(b + l16);
-        w[j][1] = *reinterpret_cast<const i32x4*>(b + l16 + 1024);
+        w.v[j][0] = *reinterpret_cast<const i32x4*>(b + l16);
+        w.v[j][1] = *reinterpret_cast<const i32x4*>(b + l16 + 1024);
       }
+      w.s = wsp[k];
     };
     auto load_a = [&](Stage& st, int kb) __attribute__((always_inline)) {
       const int64_t k = min(kb, KB - 1);
@@ -382,105 +394,114 @@ struct StreamTile {
       for (int j = 0; j < NBW; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     // Operands come in pieces of two 16-byte registers: a 16-row block (FP8), or
-    // half of its K (EXACT).
-    constexpr int kH = EXACT ? 2 : 1;
+    // half of its K (EXACT); kN pieces a step.
+    constexpr int kH = EXACT ? 2 : 1, kN = MB * kH, kD = kN < 2 ? kN : 2;
     struct Frag {
       i32x4 v[2];
     };
-    auto read_a = [&](Frag& f, const uint8_t* buf, int i) __attribute__((always_inline)) {
-      f.v[0] = *reinterpret_cast<const i32x4*>(buf + i * 2048 + l16);
-      f.v[1] = *reinterpret_cast<const i32x4*>(buf + i * 2048 + 1024 + l16);
+    Frag f[4];
+    auto read_a = [&](Frag& d, const uint8_t* buf, int i) __attribute__((always_inline)) {
+      d.v[0] = *reinterpret_cast<const i32x4*>(buf + i * 2048 + l16);
+      d.v[1] = *reinterpret_cast<const i32x4*>(buf + i * 2048 + 1024 + l16);
     };
-    // One block of K. Operands are read two pieces before their MFMAs, and the
-    // scaled sums of row block m - 1 follow the MFMAs of m; the scheduling barriers
-    // keep that order (left alone, the compiler reads each operand just before its
-    // use and keeps every partial product to the end, which spills).
-    auto compute = [&](const Weights& w, const uint8_t* buf, float sw) __attribute__((always_inline)) {
-      Frag f[3];
-      f32x4 part[2][NBW];
-      float sc[2], sn = *reinterpret_cast<const float*>(buf + kABytes + (lane & 15) * 4);
-      read_a(f[0], buf, 0);
-      if (MB * kH > 1) read_a(f[1], buf, 1);
-      bf16x8 wb[NBW][4];
-      if (EXACT) {
-#pragma unroll
-        for (int j = 0; j < NBW; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) wb[j][q] = codes_to_bf16(w[j][q >> 1][2 * (q & 1)], w[j][q >> 1][2 * (q & 1) + 1]);
-      }
-#pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        sc[m & 1] = sn * sw;
-        if (m + 1 < MB) sn = *reinterpret_cast<const float*>(buf + kABytes + ((m + 1) * 16 + (lane & 15)) * 4);
-#pragma unroll
-        for (int h = 0; h < kH; ++h) {
-          const int i = m * kH + h;
-          if (i + 2 < MB * kH) read_a(f[(i + 2) % 3], buf, i + 2);
-          __builtin_amdgcn_sched_barrier(0);
-          const Frag& a = f[i % 3];
-          if (EXACT) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int j = 0; j < NBW; ++j)
-                part[m & 1][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    wb[j][2 * h + q], __builtin_bit_cast(bf16x8, a.v[q]),
-                    h + q ? part[m & 1][j] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-          } else {
-#pragma unroll
-            for (int j = 0; j < NBW; ++j) part[m & 1][j] = mfma_fp8(join(w[j][0], w[j][1]), join(a.v[0], a.v[1]));
-          }
-          if (h == 0 && m > 0) {
-#pragma unroll
-            for (int j = 0; j < NBW; ++j)
-#pragma unroll
-              for (int t = 0; t < 4; ++t)
-                acc[m - 1][j][t] = __builtin_fmaf(part[(m - 1) & 1][j][t], sc[(m - 1) & 1], acc[m - 1][j][t]);
-          }
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < NBW; ++j)
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          acc[MB - 1][j][t] = __builtin_fmaf(part[(MB - 1) & 1][j][t], sc[(MB - 1) & 1], acc[MB - 1][j][t]);
+    auto read_s = [&](const uint8_t* buf, int m) __attribute__((always_inline)) {
+      return *reinterpret_cast<const float*>(buf + kABytes + (m * 16 + (lane & 15)) * 4);
     };
-
-    // Block kb: weights in set kb % kSets, activation in buffer kb % 2. In step
-    // kb the weights of kb + kAhead and the activation of kb + 2 are loaded, kb
-    // is multiplied, and the activation of kb + 1 goes to the other buffer (last
-    // read in step kb - 1, which every wavefront left through the barrier).
-    // Loads past the last block read it again.
+    // Step kb: weights in set kb % 4, activation in buffer kb % 4. The weights of
+    // kb + 3 and the activation of kb + 3 are loaded; kb is multiplied, each operand
+    // read kD pieces before its MFMAs (the first ones in the step before, so that no
+    // wavefront waits for LDS right behind the barrier) and the scaled sums of row
+    // block m - 1 after the MFMAs of m (the last block's in the next step); the
+    // activation of kb + 2 goes to its buffer, last read in step kb - 2, and is read
+    // from the end of step kb + 1 on, behind the barrier of step kb. Loads past the
+    // last block of K read it again.
     Weights w[kSets];
     Stage st[2];
+    f32x4 part[2][NBW];
+    float sc[2] = {0.f, 0.f}, sn;
+#pragma unroll
+    for (int j = 0; j < NBW; ++j) part[1][j] = part[0][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     load_a(st[0], 0);
     load_a(st[1], 1);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) load_w(w[i], i);
     store_a(st[0], smem);
+    load_a(st[0], 2);
+    store_a(st[1], smem + kBufBytes);
     lds_barrier();
-    auto step = [&](int kb, auto I) __attribute__((always_inline)) {
-      constexpr int i = decltype(I)::value, set = i % kSets, buf = i % 2;
-      load_a(st[buf], kb + 2);
-      load_w(w[(set + kAhead) % kSets], kb + kAhead);
-      __builtin_amdgcn_sched_barrier(0);
-      compute(w[set], smem + buf * kBufBytes, wsp[kb]);
-      store_a(st[buf ^ 1], smem + (buf ^ 1) * kBufBytes);
+#pragma unroll
+    for (int i = 0; i < kD; ++i) read_a(f[i], smem, i);
+    sn = read_s(smem, 0);
+    auto step = [&](int kb, auto STEP) __attribute__((always_inline)) {
+      constexpr int I = decltype(STEP)::value;
+      const uint8_t* buf = smem + I * kBufBytes;
+      const uint8_t* next = smem + ((I + 1) % 4) * kBufBytes;
+      load_a(st[(I + 1) & 1], kb + 3);
+      load_w(w[(I + kAhead) % kSets], kb + kAhead);
+      const auto& wk = w[I].v;
+      const float sw = w[I].s;
+      bf16x8 wb[NBW][4];
+      if (EXACT) {
+#pragma unroll
+        for (int j = 0; j < NBW; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            wb[j][q] = codes_to_bf16(wk[j][q >> 1][2 * (q & 1)], wk[j][q >> 1][2 * (q & 1) + 1]);
+      }
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        // MB row blocks a step: the partial sums alternate over the whole run
+        constexpr int odd = (I * MB) & 1;
+        f32x4 (&cur)[NBW] = part[(m + odd) & 1];
+        f32x4 (&old)[NBW] = part[(m + odd + 1) & 1];
+        float& sold = sc[(m + odd + 1) & 1];
+        sc[(m + odd) & 1] = sn * sw;
+        sn = m + 1 < MB ? read_s(buf, m + 1) : read_s(next, 0);
+#pragma unroll
+        for (int h = 0; h < kH; ++h) {
+          const int i = m * kH + h;
+          read_a(f[(I * kN + i + kD) % 4], i + kD < kN ? buf : next, (i + kD) % kN);
+          __builtin_amdgcn_sched_barrier(0);
+          const Frag& a = f[(I * kN + i) % 4];
+          if (EXACT) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int j = 0; j < NBW; ++j)
+                cur[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[j][2 * h + q], __builtin_bit_cast(bf16x8, a.v[q]),
+                                                                 h + q ? cur[j] : f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+          } else {
+#pragma unroll
+            for (int j = 0; j < NBW; ++j) cur[j] = mfma_fp8(join(wk[j][0], wk[j][1]), join(a.v[0], a.v[1]));
+          }
+          if (h == 0) {
+#pragma unroll
+            for (int j = 0; j < NBW; ++j) add_scaled(acc[(m + MB - 1) % MB][j], old[j], sold);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      store_a(st[I & 1], smem + ((I + 2) % 4) * kBufBytes);
       lds_barrier();
     };
-    // one call site per register set: with a second one (a remainder loop) the
-    // compiler indexes the sets at run time, in scratch
-    for (int kb = 0; kb < KB; kb += kUnroll) {
+    // One call site per register set (with a second one, a remainder loop, the
+    // compiler indexes the sets at run time, in scratch), and exits rather than
+    // skipped steps: a path that skips a step, though it cannot be taken, makes the
+    // compiler's waits let fewer loads be in flight.
+    for (int kb = 0;; kb += kSets) {
       step(kb, std::integral_constant<int, 0>{});
-      if (kb + 1 < KB) step(kb + 1, std::integral_constant<int, 1>{});
-      if (kb + 2 < KB) step(kb + 2, std::integral_constant<int, 2>{});
-      if (kb + 3 < KB) step(kb + 3, std::integral_constant<int, 3>{});
-      if constexpr (kUnroll == 6) {
-        if (kb + 4 < KB) step(kb + 4, std::integral_constant<int, 4>{});
-        if (kb + 5 < KB) step(kb + 5, std::integral_constant<int, 5>{});
-      }
+      if (kb + 1 >= KB) break;
+      step(kb + 1, std::integral_constant<int, 1>{});
+      if (kb + 2 >= KB) break;
+      step(kb + 2, std::integral_constant<int, 2>{});
+      if (kb + 3 >= KB) break;
+      step(kb + 3, std::integral_constant<int, 3>{});
+      if (kb + 4 >= KB) break;
     }
+    // the last row block's sums (MB odd: in the set that the last step left)
+    const int last = MB % 2 ? (KB - 1) & 1 : 1;
+#pragma unroll
+    for (int j = 0; j < NBW; ++j) add_scaled(acc[MB - 1][j], last ? part[1][j] : part[0][j], last ? sc[1] : sc[0]);
 
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
