@@ -156,6 +156,28 @@ def test_linear(w, M, N, K, bias):
     show(f"  share of the tolerance used: {_hold(got, *F.quant(x), cw, sw, b, f'{M}x{N}x{K}'):.3f}")
 
 
+@pytest.mark.parametrize("M,N,K", [(2100, 3900, 256), (3000, 2900, 130), (4096, 2048, 640), (2050, 4100, 1100)])
+def test_linear_many_tiles(w, M, N, K):
+    """Enough 256 x 256 tiles for the wide kernel, ragged on every side: every output of
+    sampled rows (all rows of the first, a middle and the last tile row's ends)."""
+    show(f"linear {M} x {N} x {K}")
+    rng = np.random.default_rng(M + N + K)
+    x = _acts(rng, M, K, 1.0)
+    cw, sw = _weight(rng, N, K)
+    b = O.f32_to_bf16(rng.standard_normal(N).astype(np.float32))
+    room = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    w.fp8b_linear(bf16_dev(x), w.fp8b_prepack_weight(dev(cw)), dev(sw), N, bias=bf16_dev(b), y=room[1:M + 1])
+    sync()
+    assert (room[0] == 7).all() and (room[M + 1] == 7).all()
+    pick = np.unique(np.r_[0:3, 14:18, 127:130, 254:258, 1000:1003, M - 3:M])
+    q, s = F.quant(x[pick])
+    _hold(bf16_host(room[1:M + 1])[pick], q, s, cw, sw, b)
+    # and the product of the codes is the same row by row as in a small call
+    y2 = w.fp8b_linear(bf16_dev(x)[M - 5:], w.fp8b_prepack_weight(dev(cw)), dev(sw), N, bias=bf16_dev(b))
+    sync()
+    _hold(bf16_host(y2), *F.quant(x[M - 5:]), cw, sw, b)
+
+
 @pytest.mark.parametrize("M", [1, 8, 40, 70, 300])
 def test_linear_rows_do_not_depend_on_the_batch(w, M):
     """Row 0 alone and inside a batch: held to the same tolerance, and rows past M stay as they are."""
@@ -206,17 +228,17 @@ def test_linear_exact_small_integers(w, M):
     assert np.array_equal(bf16_host(y), O.f32_to_bf16((xi @ wi.T).astype(np.float32)))
 
 
-@pytest.mark.parametrize("M", [1, 80, 260])
-def test_linear_every_scale_belongs_to_its_block(w, M):
+@pytest.mark.parametrize("M,N", [(1, 300), (80, 300), (260, 300), (5000, 2000)])
+def test_linear_every_scale_belongs_to_its_block(w, M, N):
     """One code per block, scales that are distinct powers of two: a scale of a wrong block shows."""
-    N, K = 300, 512
+    K = 512
     q = np.zeros((M, K), np.uint8)
     cw = np.zeros((N, K), np.uint8)
     for b in range(4):
         q[:, 128 * b + 17 * b] = 0x38
         cw[:, 128 * b + 17 * b] = 0x38
     s = 2.0 ** (np.arange(4)[:, None] + 4.0 * (np.arange(M) % 3)[None])
-    sw = 2.0 ** (-8.0 * np.arange(3)[:, None] + 2.0 * np.arange(4)[None])
+    sw = 2.0 ** (-8.0 * (np.arange(-(-N // 128)) % 3)[:, None] + 2.0 * np.arange(4)[None])
     s, sw = s.astype(np.float32), sw.astype(np.float32)
     y = w.fp8b_linear(dev(q), w.fp8b_prepack_weight(dev(cw)), dev(sw), N, x_scale=dev(s))
     sync()
