@@ -556,68 +556,92 @@ __global__ __launch_bounds__(512) void fp8b_dense_kernel(Fp8bGemm p) {
   stream_tile<NBW, EXACT>(p, smem, 0, row0, (int)min((int64_t)kTileRows, p.M - row0), blockIdx.y * 8 * NBW);
 }
 
-// Wide tile: 256 rows x 256 columns over the whole K on the FP8 MFMA, eight
-// wavefronts (2 x 4, each 128 x 64), both operands through LDS by DMA. What
-// bounds it is what the L2 hands a CU, about 32 bytes a clock: a block of K takes
-// 2 x 32 KB for 2048 clocks of MFMA, against 48 KB for 1024 in the streaming
-// tile, whose wavefronts also spend registers and issue on the copies.
+// Wide tiles: 256 rows x 256 columns over the whole K on the FP8 MFMA, eight
+// wavefronts (2 x 4, each 128 x 64), both operands through LDS by DMA. The L2 hands a
+// CU about 32 bytes a clock: a block of K takes 2 x 32 KB for 2048 clocks of MFMA,
+// against 48 KB for 1024 in the streaming tile, whose wavefronts also spend
+// registers and issue on the copies.
 //
 // LDS: two stages of one block of K, each 32 pieces of 8 activation rows x 128
 // bytes (whole cache lines; slot l of a piece holds row l / 8, 16-byte chunk
 // (l % 8) ^ (l / 8), so that the 16 rows of an operand lie in different banks), 32
-// pieces of packed weight and the rows' scales; and the tile's weight scales.
+// pieces of packed weight and the rows' scales; and the weight scales of two tiles.
 // Step kb: row blocks 0..5, then "own DMA of kb + 1 landed, own reads of kb done,
 // s_barrier", the DMA of kb + 2 into the stage of kb, row blocks 6 and 7 with the
 // first operands of kb + 1 read between them. So a stage's DMA has one whole step
-// to land, and one barrier a step serves both directions.
+// to land, and one barrier a step serves both directions. A workgroup walks over
+// its tiles without a gap: the last two steps of a tile load the first two blocks
+// of the next one, which land while the tile is stored.
+//
+// Measured on 8192 x 4096 x 7168: MFMAs alone (a copy of the kernel without copies,
+// reads and sums) 140 us on zeros, 169 on normal data (the clock gives way to the
+// power that the data takes), the sums 5 / 20, LDS reads 9 / 7, DMA 15 / 42, barriers
+// 27 / 17.
 struct WideTile {
-  static constexpr int BM = 256, BN = 256;
   static constexpr int kOperand = 32768;           // one operand of one stage
   static constexpr int kScaleBytes = 1280;         // 256 row scales (and what the last wavefront's DMA runs over)
   static constexpr int kStage = 2 * kOperand + kScaleBytes;
   static constexpr int kMaxKB = 1041;              // ceil(W8A8_MAX_K / 128)
-  static constexpr int kLdsBytes = 2 * kStage + 2 * kMaxKB * 4 + 24;
+  static constexpr int kLdsBytes = 2 * kStage + 4 * kMaxKB * 4;
 
-  __device__ __forceinline__ static void run(const Fp8bGemm& p, uint8_t* smem, int e, int64_t row0, int rows, int nb0) {
+  struct Where {
+    int e, rows, nb0;  // expert, rows, first column block; rows 0: no tile
+    int64_t row0;
+  };
+
+  // next(): this workgroup's next tile. KB >= 2.
+  template <class Next>
+  __device__ __forceinline__ static void run(const Fp8bGemm& p, uint8_t* smem, Next next) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3;
     const int NB = (int)((p.N + 15) / 16), NS = (int)((p.N + kFp8Block - 1) / kFp8Block);
     const int KB = (int)p.KB;
     const uint32_t l16 = lane * 16;
-    auto source = [&](int r) __attribute__((always_inline)) {  // row of a for tile row r; past the tile, its last
-      int64_t src = row0 + min(r, rows - 1);
-      if (p.row_index) src = max((int64_t)0, min((int64_t)p.row_index[src], p.a_rows - 1));
-      return src;
-    };
-    const uint8_t* ap[4];  // this wavefront's four activation pieces
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      ap[i] = p.a + source((wave * 4 + i) * 8 + (lane >> 3)) * p.lda + (((lane & 7) ^ (lane >> 3)) * 16);
-    const float* sp = p.a_scale + source(wave * 32 + lane);
-    const uint8_t* wp[2];  // its two weight blocks; past the last block, that one (never stored)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      wp[j] = p.w + ((int64_t)e * NB + min(nb0 + wave * 2 + j, NB - 1)) * KB * kFp8BlockBytes;
-    // weight scales of the tile's two 128-column blocks, [2][KB]
-    float* wsl = reinterpret_cast<float*>(smem + 2 * kStage);
-    for (int i = tid; i < 2 * KB; i += 512) {
-      const int b = i >= KB;
-      wsl[i] = p.w_scale[((int64_t)e * NS + min(nb0 / 8 + b, NS - 1)) * KB + (b ? i - KB : i)];
-    }
-    auto dma = [&](int kb, int stage) __attribute__((always_inline)) {
-      const int64_t k = min(kb, KB - 1);
-      W8A8_LDS uint8_t* dst = (W8A8_LDS uint8_t*)smem + stage * kStage;
+    float* const wscales = reinterpret_cast<float*>(smem + 2 * kStage);  // [2][2][KB]
+    uint32_t aoff[4], soff;  // this wavefront's four activation pieces and its rows' scales: bytes from a, a_scale
+    const uint8_t* wp[2];    // its two weight blocks
+    // Sources of tile t; its weight scales go to half `par` of wscales.
+    auto sources = [&](const Where& t, int par) __attribute__((always_inline)) {
+      auto source = [&](int r) __attribute__((always_inline)) {  // row of a for tile row r; past the tile, its last
+        int64_t src = t.row0 + min(r, t.rows - 1);
+        if (p.row_index) src = max((int64_t)0, min((int64_t)p.row_index[src], p.a_rows - 1));
+        return src;
+      };
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        __builtin_amdgcn_global_load_lds(ap[i] + k * 128, (W8A8_LDS void*)(dst + (wave * 4 + i) * 1024), 16, 0, 0);
+        aoff[i] = (uint32_t)(source((wave * 4 + i) * 8 + (lane >> 3)) * p.lda + (((lane & 7) ^ (lane >> 3)) * 16));
+      soff = (uint32_t)(source(wave * 32 + lane) * 4);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint8_t* b = wp[j] + k * kFp8BlockBytes;
-        __builtin_amdgcn_global_load_lds(b + l16, (W8A8_LDS void*)(dst + kOperand + (wave * 2 + j) * 2048), 16, 0, 0);
-        __builtin_amdgcn_global_load_lds(b + l16 + 1024, (W8A8_LDS void*)(dst + kOperand + (wave * 2 + j) * 2048 + 1024), 16, 0, 0);
+      for (int j = 0; j < 2; ++j)  // past the last block, that one (never stored)
+        wp[j] = p.w + ((int64_t)t.e * NB + min(t.nb0 + wave * 2 + j, NB - 1)) * KB * kFp8BlockBytes;
+      for (int i = tid; i < 2 * KB; i += 512) {
+        const int h = i >= KB;
+        wscales[par * 2 * KB + i] = p.w_scale[((int64_t)t.e * NS + min(t.nb0 / 8 + h, NS - 1)) * KB + (h ? i - KB : i)];
       }
-      __builtin_amdgcn_global_load_lds(sp + k * p.a_rows, (W8A8_LDS void*)(dst + 2 * kOperand + wave * 128), 4, 0, 0);
+    };
+    // Addresses are a wave-uniform base and a 32-bit lane offset; the empty asm keeps
+    // the compiler from hoisting their sums into register pairs.
+    auto dma = [&](int64_t k, int stage) __attribute__((always_inline)) {
+      W8A8_LDS uint8_t* dst = (W8A8_LDS uint8_t*)smem + stage * kStage;
+      const uint8_t* ab = p.a + k * 128;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o = aoff[i];
+        asm volatile("" : "+v"(o));
+        __builtin_amdgcn_global_load_lds(ab + o, (W8A8_LDS void*)(dst + (wave * 4 + i) * 1024), 16, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t o = l16;
+        asm volatile("" : "+v"(o));
+        const uint8_t* wb = wp[j >> 1] + k * kFp8BlockBytes + (j & 1) * 1024;
+        __builtin_amdgcn_global_load_lds(wb + o, (W8A8_LDS void*)(dst + kOperand + (wave * 4 + j) * 1024), 16, 0, 0);
+      }
+      uint32_t o = soff;
+      asm volatile("" : "+v"(o));
+      __builtin_amdgcn_global_load_lds(reinterpret_cast<const uint8_t*>(p.a_scale + k * p.a_rows) + o,
+                                       (W8A8_LDS void*)(dst + 2 * kOperand + wave * 128), 4, 0, 0);
     };
     // operand of row block m (16 rows) of this wavefront, and of its column block j
     const uint32_t arow = (wm * 128 + (lane & 15)) * 128 + (((lane >> 4) ^ (lane & 7)) * 16);
@@ -631,89 +655,118 @@ struct WideTile {
     auto read_s = [&](const uint8_t* st, int m) __attribute__((always_inline)) {
       return *reinterpret_cast<const float*>(st + 2 * kOperand + (wm * 128 + m * 16 + (lane & 15)) * 4);
     };
-    f32x4 acc[8][4];
-#pragma unroll
-    for (int m = 0; m < 8; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    f32x4 part[4];
-    i32x8 a[3], b[4];
-    float sc = 0.f, so = 0.f, sn;  // scales of this row block and the one before, and the next one's unscaled
-#pragma unroll
-    for (int j = 0; j < 4; ++j) part[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    Where cur = next();
+    if (!cur.rows) return;
+    sources(cur, 0);
     dma(0, 0);
     dma(1, 1);
     wait_vm_barrier<9>();  // stage 0 (and the scales) there
+    i32x8 a[3], b[4];
+    float sn;  // the next row block's scale, not yet times the weight's
 #pragma unroll
     for (int j = 0; j < 4; ++j) read_b(b[j], smem, j);
     read_a(a[0], smem, 0);
     read_a(a[1], smem, 1);
     sn = read_s(smem, 0);
-    const float* wsw = wsl + (wn >> 1) * KB;
-    for (int kb = 0; kb < KB; ++kb) {
-      const uint8_t* st = smem + (kb & 1) * kStage;
-      const uint8_t* nx = smem + ((kb & 1) ^ 1) * kStage;
-      const float sw = wsw[kb];
+    int stage = 0, par = 0;
+    for (;;) {
+      f32x4 acc[8][4], part[4];
+      float sc = 0.f, so = 0.f;  // scales of this row block and of the one before
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      Where after{0, 0, 0, 0};
+      const float* wsw = wscales + (par * 2 + (wn >> 1)) * KB;
+      // TAIL: the tile's last two steps, whose DMA is the next tile's first
+      auto step = [&](int kb, auto TAIL) __attribute__((always_inline)) {
+        const uint8_t* st = smem + stage * kStage;
+        const uint8_t* nx = smem + (stage ^ 1) * kStage;
+        const float sw = wsw[kb];
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          so = sc;
+          sc = sn * sw;  // before the next reads: behind them it would wait for them too
+          __builtin_amdgcn_sched_barrier(0);
+          if (m < 6) {
+            read_a(a[(m + 2) % 3], st, m + 2);
+            sn = read_s(st, m + 1);
+          } else if (m == 6) {
+            sn = read_s(st, 7);
+            // own reads of this stage done, own DMA of the next one landed, everyone
+            // there: the next stage may be read and this one refilled
+            wait_vm_barrier<0>();
+            if constexpr (decltype(TAIL)::value) {
+              if (after.rows) dma(kb + 2 - KB, stage);
+            } else {
+              dma(kb + 2, stage);
+            }
+            read_a(a[2], nx, 0);
+          } else {
+            sn = read_s(nx, 0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // the sums trail their MFMAs by three, and stay there: right behind its
+            // MFMA a sum waits for the whole latency, and so does the next MFMA
+            const int d = (j + 1) % 4;
+            add_scaled(acc[j < 3 ? (m + 7) % 8 : m][d], part[d], j < 3 ? so : sc);
+            part[j] = mfma_fp8(b[j], a[m % 3]);
+            if (m == 7) read_b(b[j], nx, j);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (m == 7) {
+            // row block 0 of the next step is in a[2]: rotate to a[0], a[1]
+            a[0] = a[2];
+            read_a(a[1], nx, 1);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        stage ^= 1;
+      };
+      for (int kb = 0; kb + 2 < KB; ++kb) step(kb, std::false_type{});
+      after = next();
+      if (after.rows) sources(after, par ^ 1);
+      for (int kb = KB - 2; kb < KB; ++kb) step(kb, std::true_type{});
+#pragma unroll
+      for (int j = 1; j < 4; ++j) add_scaled(acc[7][j], part[j], sc);
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
-        so = sc;
-        sc = sn * sw;
-        if (m < 6) {
-          read_a(a[(m + 2) % 3], st, m + 2);
-          sn = read_s(st, m + 1);
-        } else if (m == 6) {
-          sn = read_s(st, 7);
-          // own reads of this stage done, own DMA of the next one landed, everyone
-          // there: the next stage may be read and this one refilled
-          wait_vm_barrier<0>();
-          dma(kb + 2, kb & 1);
-          read_a(a[2], nx, 0);
-        } else {
-          sn = read_s(nx, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        const int r = wm * 128 + m * 16 + (lane & 15);
+        if (r < cur.rows) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // the sums trail their MFMAs by two
-          const int d = (j + 2) % 4;
-          if (j < 2) add_scaled(acc[(m + 7) % 8][d], part[d], so);
-          else add_scaled(acc[m][d], part[d], sc);
-          part[j] = mfma_fp8(b[j], a[m % 3]);
-          if (m == 7) read_b(b[j], nx, j);
+          for (int j = 0; j < 4; ++j) store4(p, cur.row0 + r, (int64_t)(cur.nb0 + wn * 4 + j) * 16 + (lane >> 4) * 4, acc[m][j]);
         }
-        if (m == 7) {
-          // row block 0 of the next step is in a[2]: rotate to a[0], a[1]
-          a[0] = a[2];
-          read_a(a[1], nx, 1);
-        }
-        __builtin_amdgcn_sched_barrier(0);
       }
-    }
-#pragma unroll
-    for (int j = 2; j < 4; ++j) add_scaled(acc[7][j], part[j], sc);
-    wait_vm_barrier<0>();  // DMA past the end landed before the LDS or the wavefront goes
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const int r = wm * 128 + m * 16 + (lane & 15);
-      if (r < rows) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) store4(p, row0 + r, (int64_t)(nb0 + wn * 4 + j) * 16 + (lane >> 4) * 4, acc[m][j]);
-      }
+      if (!after.rows) break;
+      cur = after;
+      par ^= 1;
     }
   }
 };
 
-// Dense: tiles go to the XCDs (workgroup w on XCD w % 8) in contiguous ranges, 8 rows
-// of tiles at a time, so that the tiles an XCD runs together share panels in its L2.
+// Dense: one workgroup a CU; XCD x (workgroups b with b % 8 == x) walks over its own
+// contiguous eighth of the tiles, 8 rows of tiles at a time, so that the tiles it
+// runs together share panels in its L2.
 __global__ __launch_bounds__(512) void fp8b_wide_kernel(Fp8bGemm p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[WideTile::kLdsBytes];
   const int64_t MT = (p.M + 255) / 256, NT = (p.N + 255) / 256, total = MT * NT;
-  const int64_t per = (total + 7) / 8;
-  const int64_t t = (blockIdx.x % 8) * per + blockIdx.x / 8;
-  if (blockIdx.x / 8 >= per || t >= total) return;
-  const int64_t group = t / (8 * NT), first = group * 8, gm = min((int64_t)8, MT - first), r = t % (8 * NT);
-  const int64_t row0 = (first + r % gm) * 256;
-  WideTile::run(p, smem, 0, row0, (int)min((int64_t)256, p.M - row0), (int)(r / gm) * 16);
+  const int64_t per = (total + 7) / 8, first = (blockIdx.x % 8) * per, end = min(first + per, total);
+  int64_t t = first + blockIdx.x / 8;
+  WideTile::run(p, smem, [&]() __attribute__((always_inline)) {
+    WideTile::Where w{0, 0, 0, 0};
+    if (t < end) {
+      const int64_t top = t / (8 * NT) * 8, gm = min((int64_t)8, MT - top), r = t % (8 * NT);
+      w.row0 = (top + r % gm) * 256;
+      w.rows = (int)min((int64_t)256, p.M - w.row0);
+      w.nb0 = (int)(r / gm) * 16;
+      t += gridDim.x / 8;
+    }
+    return w;
+  });
 }
 
 // Decode (dense, at most 64 rows): the weight's stream, split over K inside the
@@ -870,9 +923,9 @@ hipError_t launch_fp8b_gemm(const Fp8bGemm& args, hipStream_t stream) {
                        dim3(kDecodeWaves * 64), 0, stream, p);
     return hipGetLastError();
   }
-  if (!p.group_list && ceil_div(p.M, 256) * ceil_div(p.N, 256) >= 128) {
-    const int64_t tiles = ceil_div(p.M, 256) * ceil_div(p.N, 256);
-    hipLaunchKernelGGL(fp8b_wide_kernel, dim3((unsigned)round_up(tiles, 8)), dim3(512), 0, stream, p);
+  const int64_t wide = ceil_div(p.M, 256) * ceil_div(p.N, 256);
+  if (!p.group_list && wide >= 128 && p.KB >= 2 && p.a_rows * p.lda < (int64_t)1 << 32) {
+    hipLaunchKernelGGL(fp8b_wide_kernel, dim3((unsigned)std::min<int64_t>(256, round_up(wide, 8))), dim3(512), 0, stream, p);
     return hipGetLastError();
   }
   constexpr int NBW = 2;
