@@ -547,13 +547,13 @@ __global__ __launch_bounds__(512) void fp8b_grouped_kernel(Fp8bGemm p, int NT) {
                           __builtin_amdgcn_readfirstlane(tile.z), nb0);
 }
 
-// Dense: 128-row tiles.
-template <int NBW, bool EXACT>
+// Dense: tiles of one height.
+template <int MB, int NBW>
 __global__ __launch_bounds__(512) void fp8b_dense_kernel(Fp8bGemm p) {
-  using T = StreamTile<8, NBW, EXACT>;
+  using T = StreamTile<MB, NBW, false>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
-  const int64_t row0 = (int64_t)blockIdx.x * kTileRows;
-  stream_tile<NBW, EXACT>(p, smem, 0, row0, (int)min((int64_t)kTileRows, p.M - row0), blockIdx.y * 8 * NBW);
+  const int64_t row0 = (int64_t)blockIdx.x * (MB * 16);
+  T::run(p, smem, 0, row0, (int)min((int64_t)(MB * 16), p.M - row0), blockIdx.y * 8 * NBW);
 }
 
 // Wide tiles: 256 rows x 256 columns over the whole K on the FP8 MFMA, eight
@@ -909,33 +909,81 @@ hipError_t launch_fp8b_linear_fused(const Fp8bGemm& args, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Kernel of a dense product. Tall tiles read the weight less often, short ones give
+// every CU work; which wins is read off measured times (microseconds, 65 to 4096
+// rows by 1000 to 7168 columns, K 1000 to 7168): a launch, `first` a block of K while
+// there is at most a workgroup for every second CU, `full` a block of K for every
+// round of the chip (256 workgroups, or 512 where two fit a CU).
+enum DenseKernel { kDecode, kTile32, kTile64, kTile64x256, kTile128, kTile256 };
+
+static DenseKernel dense_kernel(const Fp8bGemm& p) {
+  if (p.M <= 64) return kDecode;
+  struct Cost {
+    DenseKernel kernel;
+    int rows, cols;
+    double launch, first, full;
+    bool two;  // workgroups fit a CU
+  };
+  // 1024 x 4096 x 7168: 176, 70, 53, 47, 71, 90 us; 128 rows: 25, 27, 32, 41, 70, 84
+  static const Cost kCosts[] = {{kDecode, 32, 32, 5.3, 0.0, 0.0, false},    {kTile32, 32, 128, 3.0, 0.42, 0.72, true},
+                                {kTile64, 64, 128, 3.0, 0.55, 0.95, true},  {kTile64x256, 64, 256, 3.0, 0.72, 0.80, false},
+                                {kTile128, 128, 256, 3.0, 1.20, 1.42, false}, {kTile256, 256, 256, 3.0, 1.60, 1.90, false}};
+  DenseKernel best = kTile128;
+  double least = 1e30;
+  for (const Cost& c : kCosts) {
+    // the wide tile's pipeline is two blocks deep and its row offsets have 32 bits
+    if (c.kernel == kTile256 && (p.KB < 2 || p.a_rows * p.lda >= (int64_t)1 << 32)) continue;
+    const int64_t n = ceil_div(p.M, c.rows) * ceil_div(p.N, c.cols);
+    const double rounds = c.two ? n / 512.0 : (double)ceil_div(n, 256);
+    const double us = c.kernel == kDecode ? rounds * (c.launch + 0.12 * p.KB)
+                                          : c.launch + p.KB * std::max(c.first, rounds * c.full);
+    if (us < least) {
+      least = us;
+      best = c.kernel;
+    }
+  }
+  return best;
+}
+
+template <int MB, int NBW>
+static void launch_dense_tiles(const Fp8bGemm& p, hipStream_t stream) {
+  hipLaunchKernelGGL((fp8b_dense_kernel<MB, NBW>),
+                     dim3((unsigned)ceil_div(p.M, MB * 16), (unsigned)ceil_div(p.N, 128 * NBW)), dim3(512), 0, stream, p);
+}
+
+static hipError_t launch_dense(const Fp8bGemm& p, hipStream_t stream) {
+  switch (dense_kernel(p)) {
+    case kDecode: {
+      // past 32 rows in groups of 32 on pairs of column blocks: a workgroup reads half
+      // the codes for twice the columns
+      const int nbw = p.M > 32 ? 2 : 1;
+      auto fn = p.M <= 16 ? fp8b_decode_kernel<1, 1, 7, false> : p.M <= 32 ? fp8b_decode_kernel<2, 1, 7, false>
+                                                                           : fp8b_decode_kernel<2, 2, 4, false>;
+      hipLaunchKernelGGL(fn, dim3((unsigned)ceil_div(ceil_div(p.N, 16), nbw), (unsigned)ceil_div(p.M, 32)),
+                         dim3(kDecodeWaves * 64), 0, stream, p);
+      break;
+    }
+    case kTile32: launch_dense_tiles<2, 1>(p, stream); break;
+    case kTile64: launch_dense_tiles<4, 1>(p, stream); break;
+    case kTile64x256: launch_dense_tiles<4, 2>(p, stream); break;
+    case kTile128: launch_dense_tiles<8, 2>(p, stream); break;
+    case kTile256: {
+      const int64_t tiles = ceil_div(p.M, 256) * ceil_div(p.N, 256);
+      hipLaunchKernelGGL(fp8b_wide_kernel, dim3((unsigned)std::min<int64_t>(256, round_up(tiles, 8))), dim3(512), 0,
+                         stream, p);
+      break;
+    }
+  }
+  return hipGetLastError();
+}
+
 hipError_t launch_fp8b_gemm(const Fp8bGemm& args, hipStream_t stream) {
   if (args.M == 0 || args.N == 0) return hipSuccess;
   Fp8bGemm p = args;
   p.store_vec = p.N % 4 == 0 && p.ldy % 4 == 0 && ((uintptr_t)p.y & 7) == 0;
-  if (!p.group_list && p.M <= 64) {
-    // 33..64 rows as two groups of 32 on pairs of column blocks: a workgroup reads
-    // half the codes for twice the columns
-    const int nbw = p.M > 32 ? 2 : 1;
-    auto fn = p.M <= 16 ? fp8b_decode_kernel<1, 1, 7, false> : p.M <= 32 ? fp8b_decode_kernel<2, 1, 7, false>
-                                                                         : fp8b_decode_kernel<2, 2, 4, false>;
-    hipLaunchKernelGGL(fn, dim3((unsigned)ceil_div(ceil_div(p.N, 16), nbw), (unsigned)ceil_div(p.M, 32)),
-                       dim3(kDecodeWaves * 64), 0, stream, p);
-    return hipGetLastError();
-  }
-  const int64_t wide = ceil_div(p.M, 256) * ceil_div(p.N, 256);
-  if (!p.group_list && wide >= 128 && p.KB >= 2 && p.a_rows * p.lda < (int64_t)1 << 32) {
-    hipLaunchKernelGGL(fp8b_wide_kernel, dim3((unsigned)std::min<int64_t>(256, round_up(wide, 8))), dim3(512), 0, stream, p);
-    return hipGetLastError();
-  }
+  if (!p.group_list) return launch_dense(p, stream);
   constexpr int NBW = 2;
-  const int64_t nt = ceil_div(p.N, 128 * NBW);
-  if (!p.group_list) {
-    hipLaunchKernelGGL((fp8b_dense_kernel<NBW, false>), dim3((unsigned)ceil_div(p.M, kTileRows), (unsigned)nt), dim3(512),
-                       0, stream, p);
-    return hipGetLastError();
-  }
-  const int64_t NT = round_up(nt, 8);
+  const int64_t NT = round_up(ceil_div(p.N, 128 * NBW), 8);
   const dim3 grid((unsigned)(fp8b_max_tiles(p.M, p.E) * NT));
   if (p.exact) hipLaunchKernelGGL((fp8b_grouped_kernel<NBW, true>), grid, dim3(512), 0, stream, p, (int)NT);
   else hipLaunchKernelGGL((fp8b_grouped_kernel<NBW, false>), grid, dim3(512), 0, stream, p, (int)NT);
