@@ -398,6 +398,227 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs g) {
   if (!g.fast || !gate_fast<DT, P>(g, t, lane)) gate_exact<DT, P>(g, t, lane);  // uniform
 }
 
+// ---------------------------------------------------------------------------
+// Many tokens: the fast form with four tokens a wavefront, 16 lanes each. Lane s
+// of a token holds experts P s .. P s + P - 1 (E <= 16 P), their keys also in LDS, the
+// maxima of its runs of four in registers: a step of the selection looks into one
+// run of the lane that owns the maximum instead of at every key. Vector
+// instructions bound this kernel (707 a token with a wavefront each; 16384 x 256,
+// sigmoid, 8 groups, bias, top 8: 32.3 us).
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
+}
+
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp_f<0xB1>(v);
+  v += dpp_f<0x4E>(v);
+  v += dpp_f<0x141>(v);
+  return v + dpp_f<0x140>(v);
+}
+
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+__device__ __forceinline__ double row_sum_d(double v) {
+  v += dpp_d<0xB1>(v);
+  v += dpp_d<0x4E>(v);
+  v += dpp_d<0x141>(v);
+  return v + dpp_d<0x140>(v);
+}
+
+// rank += "the mark of the lane N to the right in the row is better", N a rotation
+template <int N>
+__device__ __forceinline__ void rank_step(int& rank, float mark, int group, int seg) {
+  if (N % seg == 0) {  // uniform: one lane of every other group
+    const float o = dpp_f<0x120 + N>(mark);
+    const int og = __builtin_amdgcn_update_dpp(0, group, 0x120 + N, 0xF, 0xF, false);
+    rank += o > mark || (o == mark && og < group);
+  }
+}
+
+constexpr int kQuadWaves = 4;
+
+template <int DT, int P>
+__global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) {
+  constexpr int kRuns = P / 4, kPitch = P + 4;  // keys of a lane in LDS, padded against bank conflicts
+  __shared__ __attribute__((aligned(16))) uint32_t keys[kQuadWaves][64 * kPitch];
+  const int lane = threadIdx.x & 63, sub = lane & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t0 = ((int64_t)blockIdx.x * kQuadWaves + wave) * 4;
+  if (t0 >= g.T) return;
+  const bool live = t0 + (lane >> 4) < g.T;
+  const int64_t t = live ? t0 + (lane >> 4) : g.T - 1;
+  const int E = g.E, k = g.top_k, e0 = sub * P;
+  const bool sigmoid = g.scoring == 1, biased = g.bias != nullptr;
+  uint32_t* const mine = keys[wave] + lane * kPitch;
+
+  float l[P];
+  const int64_t at = t * g.ld + e0;
+#pragma unroll
+  for (int i = 0; i < P; i += 4) {
+    if (g.vec) {
+      if (DT == 0) {
+        float4 v = {0.f, 0.f, 0.f, 0.f};
+        if (e0 + i < E) v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(g.logits) + at + i);
+        l[i] = v.x; l[i + 1] = v.y; l[i + 2] = v.z; l[i + 3] = v.w;
+      } else {
+        uint2 v = {0u, 0u};
+        if (e0 + i < E) v = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(g.logits) + at + i);
+        const uint32_t h[4] = {v.x & 0xFFFFu, v.x >> 16, v.y & 0xFFFFu, v.y >> 16};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          l[i + j] = DT == 1 ? bf16_to_f32(h[j]) : __half2float(__builtin_bit_cast(__half, (uint16_t)h[j]));
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) l[i + j] = e0 + i + j < E ? load_logit<DT>(g.logits, at + i + j) : 0.f;
+    }
+  }
+  const float low = -__builtin_huge_valf();
+  float top = low;
+  uint32_t in = 0u;  // bit i: expert e0 + i takes part
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const bool ok = e0 + i < E && l[i] > low;  // false for NaN
+    in |= ok ? 1u << i : 0u;
+    l[i] = fminf(l[i], 3.402823466e38f);
+    if (ok) top = fmaxf(top, l[i]);
+  }
+  const bool need_scores = biased || g.n_group > 1 || (!sigmoid && !g.renormalize);
+  float total = 1.f, r = 1.f;
+  if (need_scores && !sigmoid) {
+    const uint32_t tb = row_max(top > low ? key_bits(top) : 0u);
+    top = tb ? key_value(tb) : 0.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < P; ++i) sum += (in >> i) & 1 ? exp_f(l[i] - top) : 0.f;
+    total = row_sum(sum);
+    r = total > 0.f ? 1.f / total : 0.f;
+  }
+  // scores; keys as integers; the lane's two largest values for its group's mark
+  uint32_t u[P];
+  float a = low, b = low;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    float v = l[i], key = l[i];
+    bool ok = (in >> i) & 1;
+    if (need_scores) v = sigmoid ? __builtin_amdgcn_rcpf(1.f + exp_f(-l[i])) : exp_f(l[i] - top) * r;
+    if (biased) {
+      v = v + (e0 + i < E ? g.bias[e0 + i] : 0.f);
+      key = v;
+      ok = ok && key > low;
+    }
+    u[i] = ok ? key_bits(key) : 0u;
+    v = ok ? v : low;
+    b = fmaxf(b, fminf(a, v));
+    a = fmaxf(a, v);
+  }
+  bool close = false;
+  if (g.n_group > 1) {
+    const int seg = E / g.n_group / P;  // lanes of a group
+    segment_top2(a, b, seg);
+    const float mark = b > low ? a + b : a;
+    const int group = sub / seg;
+    int rank = 0;
+    rank_step<1>(rank, mark, group, seg); rank_step<2>(rank, mark, group, seg); rank_step<3>(rank, mark, group, seg);
+    rank_step<4>(rank, mark, group, seg); rank_step<5>(rank, mark, group, seg); rank_step<6>(rank, mark, group, seg);
+    rank_step<7>(rank, mark, group, seg); rank_step<8>(rank, mark, group, seg); rank_step<9>(rank, mark, group, seg);
+    rank_step<10>(rank, mark, group, seg); rank_step<11>(rank, mark, group, seg); rank_step<12>(rank, mark, group, seg);
+    rank_step<13>(rank, mark, group, seg); rank_step<14>(rank, mark, group, seg); rank_step<15>(rank, mark, group, seg);
+    const bool real = group < g.n_group;
+    if (g.topk_group < g.n_group) {
+      // the last group that stays and the first that goes
+      const uint32_t xb = row_max(real && rank == g.topk_group - 1 && mark > low ? key_bits(mark) : 0u);
+      const uint32_t yb = row_max(real && rank == g.topk_group && mark > low ? key_bits(mark) : 0u);
+      const float x = key_value(xb), y = key_value(yb);
+      if (yb) close = !(x - y > kNear * (1.f + fabsf(x) + fabsf(y)));
+    }
+    const bool stays = real && rank < g.topk_group;
+#pragma unroll
+    for (int i = 0; i < P; ++i) u[i] = stays ? u[i] : 0u;
+  }
+  uint32_t run[kRuns];  // maxima of four
+#pragma unroll
+  for (int q = 0; q < kRuns; ++q) {
+    *reinterpret_cast<uint4*>(mine + 4 * q) = uint4{u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]};
+    run[q] = max(max(u[4 * q], u[4 * q + 1]), max(u[4 * q + 2], u[4 * q + 3]));
+  }
+  int id = -1;       // lane j of a token: its j-th expert
+  uint32_t kb = 0u;  // and that one's key
+  const int steps = biased ? k + 1 : k;  // at most 16
+  for (int j = 0; j < steps; ++j) {
+    uint32_t m = run[0];
+#pragma unroll
+    for (int q = 1; q < kRuns; ++q) m = max(m, run[q]);
+    const uint32_t best = row_max(m);
+    const uint32_t same = (uint32_t)(__ballot(m == best) >> (lane & 48)) & 0xFFFFu;
+    const int owner = __builtin_ctz(same);
+    int q = kRuns - 1;
+#pragma unroll
+    for (int i = kRuns - 2; i >= 0; --i) q = run[i] == m ? i : q;
+    const uint4 v = *reinterpret_cast<const uint4*>(mine + 4 * q);
+    const int i = v.x == m ? 0 : v.y == m ? 1 : v.z == m ? 2 : 3;
+    const int e = __shfl(e0 + 4 * q + i, (lane & 48) | owner, kWave);
+    if (sub == j && best != 0u) {
+      id = e;
+      kb = best;
+    }
+    if (sub == owner && best != 0u) {
+      mine[4 * q + i] = 0u;
+      const uint32_t left = max(max(i == 0 ? 0u : v.x, i == 1 ? 0u : v.y), max(i == 2 ? 0u : v.z, i == 3 ? 0u : v.w));
+#pragma unroll
+      for (int n = 0; n < kRuns; ++n) run[n] = n == q ? left : run[n];
+    }
+  }
+  const float sel = id >= 0 ? fminf(load_logit<DT>(g.logits, t * g.ld + id), 3.402823466e38f) : 0.f;
+  if (biased) {
+    // lane j against lane j + 1 of the token, the runner-up included
+    const float v = key_value(kb), bj = id >= 0 ? g.bias[id] : 0.f;
+    const int n = __shfl_down(id, 1, 16);
+    const float nv = __shfl_down(v, 1, 16), nl = __shfl_down(sel, 1, 16), nb = __shfl_down(bj, 1, 16);
+    if (sub < k && sub < 15 && id >= 0 && n >= 0 && !(nl == sel && nb == bj))
+      close = close || !(v - nv > kNear * (1.f + fabsf(v) + fabsf(nv)));
+  } else {
+    const float first = need_scores && !sigmoid ? top : __shfl(sel, lane & 48, kWave);
+    if (sub < k && id >= 0) close = close || (sigmoid ? sel > 36.f || sel < -700.f : sel - first < -700.f);
+  }
+  double w = 0.0;
+  const bool chosen = sub < k && id >= 0;
+  if (sigmoid) {
+    if (chosen) w = 1.0 / (1.0 + exp(-(double)sel));
+  } else {
+    const uint32_t tb = row_max(chosen ? key_bits(sel) : 0u);
+    const float ref = g.renormalize ? (tb ? key_value(tb) : 0.f) : top;
+    if (chosen) w = exp((double)sel - (double)ref);
+  }
+  if (g.renormalize) {
+    const double sum = row_sum_d(w);
+    w = sum > 0.0 ? w / sum : 0.0;
+  } else if (!sigmoid) {
+    w = total > 0.f ? w / (double)total : 0.0;
+  }
+  const uint64_t again = __ballot(close && live);
+  if (live && sub < k && ((again >> (lane & 48)) & 0xFFFFu) == 0u) {
+    g.ids[t * k + sub] = id;
+    g.weights[t * k + sub] = (float)(w * (double)g.scale);
+  }
+  // tokens too close for floats, one after the other (uniform)
+  for (int q = 0; q < 4; ++q)
+    if ((again >> (16 * q)) & 0xFFFFu) gate_exact<DT, (P * 16 + 63) / 64>(g, t0 + q, lane);
+}
+
+// from here on four tokens a wavefront beat one (2048 tokens: see the launcher's figures)
+constexpr int64_t kQuadTokens = 1024;
+
 template <int DT>
 static hipError_t launch_gate_dt(const GateArgs& args, hipStream_t stream) {
   GateArgs p = args;
@@ -406,6 +627,13 @@ static hipError_t launch_gate_dt(const GateArgs& args, hipStream_t stream) {
   // groups have to be whole aligned runs of a power of two of lanes
   p.fast = p.n_group == 1 || (per % P == 0 && (seg & (seg - 1)) == 0);
   p.vec = p.E % 4 == 0 && p.ld % 4 == 0 && ((uintptr_t)p.logits & (DT == 0 ? 15 : 7)) == 0;
+  const int Q = p.E <= 64 ? 4 : p.E <= 128 ? 8 : 16, qseg = per / Q;
+  if (p.T >= kQuadTokens && p.E <= 256 && p.top_k + (p.bias ? 1 : 0) <= 16 &&
+      (p.n_group == 1 || (per % Q == 0 && (qseg & (qseg - 1)) == 0))) {
+    auto fn = Q == 4 ? gate_quad_kernel<DT, 4> : Q == 8 ? gate_quad_kernel<DT, 8> : gate_quad_kernel<DT, 16>;
+    hipLaunchKernelGGL(fn, dim3((unsigned)ceil_div(p.T, 4 * kQuadWaves)), dim3(kQuadWaves * 64), 0, stream, p);
+    return hipGetLastError();
+  }
   void (*fn)(GateArgs) = P == 1 ? gate_kernel<DT, 1> : P == 2 ? gate_kernel<DT, 2> : P == 4 ? gate_kernel<DT, 4>
                        : P == 8 ? gate_kernel<DT, 8> : gate_kernel<DT, 16>;
   hipLaunchKernelGGL(fn, dim3((unsigned)ceil_div(p.T, 4)), dim3(256), 0, stream, p);

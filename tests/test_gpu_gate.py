@@ -123,6 +123,36 @@ def test_gate_close_keys(w, scoring, G, keep):
     _check(w, torch.from_numpy(l2), 8, b, scoring, G, keep)
 
 
+MANY = [  # T, E, k, scoring, groups, keep, dtype, bias: four tokens a wavefront
+    (1025, 256, 8, "sigmoid", 8, 4, torch.float32, True), (1030, 256, 8, "sigmoid", 8, 4, torch.bfloat16, True),
+    (1024, 64, 6, "softmax", 1, 1, torch.bfloat16, False), (1027, 160, 6, "softmax", 10, 3, torch.float32, False),
+    (1101, 99, 6, "softmax", 1, 1, torch.bfloat16, False), (1026, 128, 15, "sigmoid", 4, 2, torch.float16, True),
+    (1099, 256, 16, "softmax", 16, 5, torch.float32, False), (1040, 32, 4, "sigmoid", 8, 3, torch.float32, False),
+    (1033, 17, 5, "softmax", 1, 1, torch.float32, True), (1029, 256, 8, "sigmoid", 2, 1, torch.float32, False),
+    (1025, 3, 2, "sigmoid", 1, 1, torch.float32, True),
+]
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,k,scoring,G,keep,dtype,with_bias", MANY)
+def test_gate_four_tokens_a_wavefront(w, T, E, k, scoring, G, keep, dtype, with_bias, renorm):
+    """Random tokens, and among them ties, masks, specials and keys that are too close
+    for floats, so that a wavefront holds tokens of every kind."""
+    rng = np.random.default_rng(T)
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    b = 0.1 * rng.standard_normal(E).astype(np.float32)
+    l[0::7] = rng.integers(0, 3, l[0::7].shape)                      # ties
+    l[1::9] = np.where(rng.random(l[1::9].shape) < 0.5, -np.inf, l[1::9])
+    l[2::11] = -np.inf
+    l[3::13, 0] = np.nan
+    l[4::17] = _nudge(np.float32(2.5) + 0 * l[4::17], rng.integers(-3, 4, l[4::17].shape))
+    l[5::19] *= 300.0
+    l[6::23, -1] = np.inf
+    if E > 1:
+        b[1] = -np.inf
+    _check(w, torch.from_numpy(l).to(dtype), k, b if with_bias else None, scoring, G, keep, renorm, 1.5)
+
+
 def test_gate_many_tokens(w):
     # more tokens than one pass of the chip; every token exact against the oracle on a sample
     T, E, k = 9001, 256, 8
