@@ -37,43 +37,95 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 
 __device__ __forceinline__ double shfl_xor_d(double v, int m) { return __shfl_xor(v, m, kWave); }
 
-// The definition itself, in doubles, by one wavefront; lane l holds experts
-// l + 64 i. Every lane of the wavefront takes part.
+// v of another lane by DPP; lanes of rows outside ROWS keep their own
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ double dpp_d(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const int lo = (int)(uint32_t)u, hi = (int)(uint32_t)(u >> 32);
+  const uint32_t l = (uint32_t)__builtin_amdgcn_update_dpp(lo, lo, CTRL, ROWS, 0xF, false);
+  const uint32_t h = (uint32_t)__builtin_amdgcn_update_dpp(hi, hi, CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, ((uint64_t)h << 32) | l);
+}
+
+__device__ __forceinline__ double readlane_d(double v, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, l);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// maximum and sum over the wavefront, in every lane
+__device__ __forceinline__ double wave_max_d(double v) {
+  v = fmax(v, dpp_d<0xB1>(v));
+  v = fmax(v, dpp_d<0x4E>(v));
+  v = fmax(v, dpp_d<0x141>(v));
+  v = fmax(v, dpp_d<0x140>(v));
+  v = fmax(v, dpp_d<0x142, 0xA>(v));  // the ends of rows 0 and 2 into rows 1 and 3
+  v = fmax(v, dpp_d<0x143, 0xC>(v));  // and of the first half into the second
+  return readlane_d(v, 63);
+}
+
+__device__ __forceinline__ double wave_sum_d(double v) {
+  v += dpp_d<0xB1>(v);
+  v += dpp_d<0x4E>(v);
+  v += dpp_d<0x141>(v);
+  v += dpp_d<0x140>(v);
+  return (readlane_d(v, 0) + readlane_d(v, 16)) + (readlane_d(v, 32) + readlane_d(v, 48));
+}
+
+__device__ __forceinline__ void merge2_d(double& a, double& b, double oa, double ob) {
+  b = fmax(fmin(a, oa), fmax(b, ob));
+  a = fmax(a, oa);
+}
+
+// The definition itself, in doubles, by one wavefront; lane l holds the experts
+// P l + i. Every lane of the wavefront takes part. A launch lasts as long as its
+// slowest wavefront and this code is cold when it runs, so it has no LDS latency in
+// its loops and one copy of the exponential (unrolled and with shuffles, one such
+// token added 10 us to a launch).
 template <int DT, int P>
 __device__ void gate_exact(const GateArgs& g, int64_t t, int lane) {
-  const int E = g.E;
+  const int E = g.E, e0 = lane * P;
   float l[P];
   bool in[P];
-  float top = -__builtin_huge_valf();
+  double top = kOut;
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const int e = lane + 64 * i;
-    l[i] = e < E ? load_logit<DT>(g.logits, t * g.ld + e) : -__builtin_huge_valf();
+    l[i] = e0 + i < E ? load_logit<DT>(g.logits, t * g.ld + e0 + i) : -__builtin_huge_valf();
     in[i] = l[i] > -__builtin_huge_valf();  // false for NaN
     l[i] = fminf(l[i], 3.402823466e38f);
-    if (in[i]) top = fmaxf(top, l[i]);
+    if (in[i]) top = fmax(top, (double)l[i]);
   }
   double score[P], key[P];
-  if (g.scoring == 1) {
+  const bool sigmoid = g.scoring == 1;
+  if (!sigmoid) top = wave_max_d(top);
+  double sum = 0.0;
 #pragma unroll
-    for (int i = 0; i < P; ++i) score[i] = in[i] ? 1.0 / (1.0 + exp(-(double)l[i])) : 0.0;
-  } else {
+  for (int i = 0; i < P; ++i) score[i] = 0.0;
+#pragma nounroll
+  for (int n = 0; n < P; ++n) {  // one copy of the exponential's code
+    float x = l[0];
+    bool ok = in[0];
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      score[i] = in[i] ? exp((double)l[i] - (double)top) : 0.0;
-      sum += score[i];
+    for (int i = 1; i < P; ++i) {
+      x = n == i ? l[i] : x;
+      ok = n == i ? in[i] : ok;
     }
+    double v = exp(sigmoid ? -(double)x : (double)x - top);
+    if (sigmoid) v = 1.0 / (1.0 + v);
+    v = ok ? v : 0.0;
+    sum += v;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) sum += shfl_xor_d(sum, d);
+    for (int i = 0; i < P; ++i) score[i] = n == i ? v : score[i];
+  }
+  if (!sigmoid) {
+    sum = wave_sum_d(sum);
 #pragma unroll
     for (int i = 0; i < P; ++i) score[i] = sum > 0.0 ? score[i] / sum : 0.0;
   }
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    const double k = g.bias && in[i] ? score[i] + (double)g.bias[lane + 64 * i] : score[i];
+    const double k = g.bias && in[i] ? score[i] + (double)g.bias[e0 + i] : score[i];
     key[i] = in[i] && k > kOut ? k : kOut;
   }
   if (g.n_group > 1) {
@@ -83,53 +135,54 @@ __device__ void gate_exact(const GateArgs& g, int64_t t, int lane) {
       double a = kOut, b = kOut;  // the group's two largest keys
 #pragma unroll
       for (int i = 0; i < P; ++i) {
-        const int e = lane + 64 * i;
+        const int e = e0 + i;
         if (e >= h * per && e < (h + 1) * per) {
           b = fmax(b, fmin(a, key[i]));
           a = fmax(a, key[i]);
         }
       }
+      merge2_d(a, b, dpp_d<0xB1>(a), dpp_d<0xB1>(b));
+      merge2_d(a, b, dpp_d<0x4E>(a), dpp_d<0x4E>(b));
+      merge2_d(a, b, dpp_d<0x141>(a), dpp_d<0x141>(b));
+      merge2_d(a, b, dpp_d<0x140>(a), dpp_d<0x140>(b));
+      double x = readlane_d(a, 0), y = readlane_d(b, 0);  // the four rows of 16 lanes
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const double oa = shfl_xor_d(a, d), ob = shfl_xor_d(b, d);
-        b = fmax(fmin(a, oa), fmax(b, ob));
-        a = fmax(a, oa);
-      }
-      if (lane == h) mark = b > kOut ? a + b : a;
+      for (int q = 16; q < kWave; q += 16) merge2_d(x, y, readlane_d(a, q), readlane_d(b, q));
+      if (lane == h) mark = y > kOut ? x + y : x;
     }
     int rank = 0;
     for (int h = 0; h < g.n_group; ++h) {
-      const double o = __shfl(mark, h, kWave);
+      const double o = readlane_d(mark, h);
       rank += o > mark || (o == mark && h < lane);
     }
     const uint64_t stays = __ballot(lane < g.n_group && rank < g.topk_group);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int e = lane + 64 * i;
-      if (e < E && !((stays >> (e / per)) & 1)) key[i] = kOut;
-    }
+    for (int i = 0; i < P; ++i)
+      if (e0 + i < E && !((stays >> ((e0 + i) / per)) & 1)) key[i] = kOut;
   }
   int id = -1;        // lane j: the j-th expert
   double w = 0.0;
   double total = 0.0;
   for (int j = 0; j < g.top_k; ++j) {
-    double best = kOut;
-    int be = 1 << 30;
-    double bs = 0.0;
+    double m = key[0];
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (key[i] > best) { best = key[i]; be = lane + 64 * i; bs = score[i]; }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double ok = shfl_xor_d(best, d), os = shfl_xor_d(bs, d);
-      const int oe = __shfl_xor(be, d, kWave);
-      if (ok > best || (ok == best && oe < be)) { best = ok; be = oe; bs = os; }
-    }
+    for (int i = 1; i < P; ++i) m = fmax(m, key[i]);
+    const double best = wave_max_d(m);
     if (!(best > kOut)) break;  // uniform: nothing is left
+    int at = P - 1;  // this lane's lowest index of its maximum, and that one's score
+    double s = score[P - 1];
 #pragma unroll
-    for (int i = 0; i < P; ++i)
-      if (be == lane + 64 * i) key[i] = kOut;
-    if (lane == j) { id = be; w = bs; }
+    for (int i = P - 2; i >= 0; --i) {
+      at = key[i] == m ? i : at;
+      s = key[i] == m ? score[i] : s;
+    }
+    const int owner = __builtin_ctzll(__ballot(m == best));
+    const int e = owner * P + __builtin_amdgcn_readlane(at, owner);
+    const double bs = readlane_d(s, owner);
+    at = lane == owner ? at : -1;
+#pragma unroll
+    for (int i = 0; i < P; ++i) key[i] = at == i ? kOut : key[i];
+    if (lane == j) { id = e; w = bs; }
     total += bs;
   }
   if (lane < g.top_k) {
@@ -143,22 +196,28 @@ __device__ void gate_exact(const GateArgs& g, int64_t t, int lane) {
 // Fast form: one wavefront per token, lane l holds the P consecutive experts
 // P l + i, keys are floats. Where float rounding could change the choice the
 // wavefront falls back to gate_exact: it does so if two keys that have to be told
-// apart (neighbours among the k + 1 largest, the last group that stays and the
-// first that goes) are within kNear (1 + |a| + |b|) and do not come from the same
-// logit and bias. Scores are at most 1 and off by less than 2^-21: with d the
-// exponential's relative error, (1 + |l|) 2^-23 at most (one ulp, and the rounded
-// argument), a sigmoid is off by s (1 - s) d < 0.5 2^-23 and two roundings of s, a
-// softmax by s d and s times the sum's error, whose terms weigh d by e^-|l|. So keys
-// are off by 2^-21 + 2^-24 |key| and marks by twice that, and two of either by no
-// more than kNear (1 + |a| + |b|).
+// apart (neighbours among the k + 1 largest, unless equal logits and biases place
+// them both inside the list; the last group that stays and the first that goes) are
+// within 2^-20 or 2^-19 times (1 + |a| + |b|). With d the exponential's relative error, (1 + |x|) 2^-23 at most
+// (one ulp, and the rounded argument):
+// - a sigmoid is off by s (1 - s) d <= 0.48 2^-23, a rounding of 1 + e and an ulp of
+//   the reciprocal, together less than 2^-22; keys by 2^-24 |key| more and marks
+//   by twice that. Two of either are compared with 2^-20 (1 + |a| + |b|);
+// - a softmax by s d <= 2^-23 and an ulp of the division, and all scores of a token
+//   by the error of their sum, at most 2^-23 times 2.4 / s (its terms' d; s the
+//   largest score) + 5 (its roundings, a tree of 10). Two sums of two scores
+//   differ by less than 2^-19 for that; compared with 2^-19 (1 + |a| + |b|).
+// Close neighbours among the selected are then put in order by the doubles that
+// their weights need anyway (sigmoid scores); what is left, a group at the border
+// or a chain of close keys that leaves the list, falls back.
 // Without a bias the order of keys is the order of logits, which are compared as
 // they are; doubles saturate (1 from l = 37 on, 0 under -745), so logits past 36
 // or a selected one 700 under the maximum (softmax) or -700 (sigmoid) fall back
-// too. On random logits the fallback takes about 1 token in 2000.
+// too. On random logits the fallback takes about 1 token in 7000.
 // The weights come from the selected logits alone, in doubles; only the sum of a
 // softmax that is not renormalized is a float sum.
 // ---------------------------------------------------------------------------
-constexpr float kNear = 0x1p-19f;
+constexpr float kNearSigmoid = 0x1p-20f, kNearSoftmax = 0x1p-19f;
 
 // order-preserving map of finite floats and +inf to integers above 0 (0: out)
 __device__ __forceinline__ uint32_t key_bits(float f) {
@@ -189,6 +248,20 @@ __device__ __forceinline__ void segment_top2(float& a, float& b, int seg) {
   if (seg >= 16) merge2(a, b, dpp_f<0x140>(a), dpp_f<0x140>(b)); // the other half of 16
   if (seg >= 32) merge2(a, b, __shfl_xor(a, 16, kWave), __shfl_xor(b, 16, kWave));
   if (seg >= 64) merge2(a, b, __shfl_xor(a, 32, kWave), __shfl_xor(b, 32, kWave));
+}
+
+// sum of P floats (a power of two) with log2 P roundings
+template <int P>
+__device__ __forceinline__ float tree_sum(const float (&v)[P]) {
+  float t[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) t[i] = v[i];
+#pragma unroll
+  for (int h = P / 2; h > 0; h >>= 1) {
+#pragma unroll
+    for (int i = 0; i < h; ++i) t[i] += t[i + h];
+  }
+  return t[0];
 }
 
 __device__ __forceinline__ float wave_sum_f(float v) {
@@ -250,11 +323,39 @@ __device__ __forceinline__ void load_logits(const GateArgs& g, int64_t t, int la
   }
 }
 
+// Order of the k + 1 entries of a row of 16 lanes (lane j: expert id of double key
+// `key`, weight w) by those keys, lowest index first among equals. The entries fill
+// the row from lane 0; others stay where they are. Every lane takes part.
+template <int N>
+__device__ __forceinline__ void settle_step(int& rank, int id, double key, bool entry) {
+  const double ok = dpp_d<0x120 + N>(key);
+  const int oid = __builtin_amdgcn_update_dpp(0, id, 0x120 + N, 0xF, 0xF, false);
+  const int oe = __builtin_amdgcn_update_dpp(0, (int)entry, 0x120 + N, 0xF, 0xF, false);
+  rank += oe && (ok > key || (ok == key && oid < id));
+}
+
+__device__ __forceinline__ void settle_row(int& id, double& w, double key, int k, int lane) {
+  const bool entry = (lane & 15) <= k && id >= 0;
+  int rank = 0;
+  settle_step<1>(rank, id, key, entry); settle_step<2>(rank, id, key, entry); settle_step<3>(rank, id, key, entry);
+  settle_step<4>(rank, id, key, entry); settle_step<5>(rank, id, key, entry); settle_step<6>(rank, id, key, entry);
+  settle_step<7>(rank, id, key, entry); settle_step<8>(rank, id, key, entry); settle_step<9>(rank, id, key, entry);
+  settle_step<10>(rank, id, key, entry); settle_step<11>(rank, id, key, entry); settle_step<12>(rank, id, key, entry);
+  settle_step<13>(rank, id, key, entry); settle_step<14>(rank, id, key, entry); settle_step<15>(rank, id, key, entry);
+  const int to = 4 * (entry ? (lane & 48) + rank : lane);
+  const uint64_t u = __builtin_bit_cast(uint64_t, w);
+  id = __builtin_amdgcn_ds_permute(to, id);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_permute(to, (int)(uint32_t)u);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_permute(to, (int)(uint32_t)(u >> 32));
+  w = __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
 // false: the choice is too close for floats
 template <int DT, int P>
 __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane) {
   const int E = g.E, k = g.top_k;
   const bool sigmoid = g.scoring == 1, biased = g.bias != nullptr;
+  const float near = sigmoid ? kNearSigmoid : kNearSoftmax;
   float l[P];
   load_logits<DT, P>(g, t, lane, l);
   bool in[P];
@@ -275,13 +376,9 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
     } else {
       const uint32_t tb = wave_max_u32(top > -__builtin_huge_valf() ? key_bits(top) : 0u);
       top = tb ? key_value(tb) : 0.f;
-      float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        s[i] = in[i] ? exp_f(l[i] - top) : 0.f;
-        sum += s[i];
-      }
-      total = wave_sum_f(sum);
+      for (int i = 0; i < P; ++i) s[i] = in[i] ? exp_f(l[i] - top) : 0.f;
+      total = wave_sum_f(tree_sum<P>(s));
       const float r = total > 0.f ? 1.f / total : 0.f;
 #pragma unroll
       for (int i = 0; i < P; ++i) s[i] *= r;
@@ -322,7 +419,7 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
       // the last that stays and the first that goes
       const uint64_t last = __ballot(group && rank == g.topk_group - 1), next = __ballot(group && rank == g.topk_group);
       const float x = readlane_f(mark, __builtin_ctzll(last)), y = readlane_f(mark, __builtin_ctzll(next));
-      if (y > -__builtin_huge_valf()) close = !(x - y > kNear * (1.f + fabsf(x) + fabsf(y)));
+      if (y > -__builtin_huge_valf()) close = !(x - y > near * (1.f + fabsf(x) + fabsf(y)));
     }
     if (!(group && rank < g.topk_group)) {
 #pragma unroll
@@ -333,7 +430,9 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
   // largest key of the wavefront, of the lowest lane and index among equals
   int id = -1;          // lane j: the j-th expert
   uint32_t kb = 0u;     // and its key
-  const int steps = biased && k < kWave ? k + 1 : k;
+  // with a bias two more than asked, as far as there are lanes: the runner-up and the
+  // one after it
+  const int steps = biased ? min(k + 2, kWave) : k;
   for (int j = 0; j < steps; ++j) {
     uint32_t m = u[0];
 #pragma unroll
@@ -354,25 +453,32 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
     }
   }
   const float sel = id >= 0 ? fminf(load_logit<DT>(g.logits, t * g.ld + id), 3.402823466e38f) : 0.f;
+  const float bj = biased && id >= 0 ? g.bias[id] : 0.f;
+  bool swap = false;  // lane j: too close to lane j + 1, other than equal inside the list
   if (biased) {
-    // lane j against lane j + 1, the runner-up included
-    const float v = key_value(kb), bj = id >= 0 ? g.bias[id] : 0.f;
+    const float v = key_value(kb);
     const int n = __shfl_down(id, 1, kWave);
     const float nv = __shfl_down(v, 1, kWave), nl = __shfl_down(sel, 1, kWave), nb = __shfl_down(bj, 1, kWave);
-    if (lane < k && lane + 1 < kWave && id >= 0 && n >= 0 && !(nl == sel && nb == bj))
-      close = close || !(v - nv > kNear * (1.f + fabsf(v) + fabsf(nv)));
-    if (k == kWave) close = true;  // no lane left for the runner-up
+    if (lane <= k && lane + 1 < kWave && id >= 0 && n >= 0 && !(lane < k - 1 && nl == sel && nb == bj))
+      swap = !(v - nv > near * (1.f + fabsf(v) + fabsf(nv)));
+    if (k > 14 && (lane < k || k == kWave)) close = close || swap || k == kWave;  // past a row of lanes
+    if (!sigmoid && lane < k) close = close || swap;
   } else {
     const float first = need_scores && !sigmoid ? top : readlane_f(sel, 0);
     if (lane < k && id >= 0) close = close || (sigmoid ? sel > 36.f || sel < -700.f : sel - first < -700.f);
   }
-  if (__ballot(close)) return false;
+  const uint64_t pairs = __ballot(swap);
+  const bool order = biased && sigmoid && k <= 14 && (pairs & ((1ull << k) - 1)) != 0;  // uniform
+  // close to the last of the list, which is close to one outside of it
+  if (__ballot(close) || (order && (pairs >> (k - 1) & 3) == 3)) return false;
   double w = 0.0;
-  const bool mine = lane < k && id >= 0;
   if (sigmoid) {
-    if (mine) w = 1.0 / (1.0 + exp(-(double)sel));
+    if (lane <= k && id >= 0) w = 1.0 / (1.0 + exp(-(double)sel));
+    if (order) settle_row(id, w, w + (double)bj, k, lane);
+    if (!(lane < k && id >= 0)) w = 0.0;
   } else {
     // renormalized: the largest selected logit stands for the maximum
+    const bool mine = lane < k && id >= 0;
     const float ref = g.renormalize ? wave_top(mine ? key_bits(sel) : 0u) : top;
     if (mine) w = exp((double)sel - (double)ref);
   }
@@ -403,8 +509,8 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs g) {
 // of a token holds experts P s .. P s + P - 1 (E <= 16 P), their keys also in LDS, the
 // maxima of its runs of four in registers: a step of the selection looks into one
 // run of the lane that owns the maximum instead of at every key. Vector
-// instructions bound this kernel (707 a token with a wavefront each; 16384 x 256,
-// sigmoid, 8 groups, bias, top 8: 32.3 us).
+// instructions bound this kernel: 16384 x 256, sigmoid, 8 groups, bias, top 8 take
+// 17.9 us without a fallback and 21.7 with one, the logits' bytes 4.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
@@ -418,14 +524,6 @@ __device__ __forceinline__ float row_sum(float v) {
   v += dpp_f<0x4E>(v);
   v += dpp_f<0x141>(v);
   return v + dpp_f<0x140>(v);
-}
-
-template <int CTRL>
-__device__ __forceinline__ double dpp_d(double v) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xF, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
-  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
 __device__ __forceinline__ double row_sum_d(double v) {
@@ -459,6 +557,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
   const int64_t t = live ? t0 + (lane >> 4) : g.T - 1;
   const int E = g.E, k = g.top_k, e0 = sub * P;
   const bool sigmoid = g.scoring == 1, biased = g.bias != nullptr;
+  const float near = sigmoid ? kNearSigmoid : kNearSoftmax;
   uint32_t* const mine = keys[wave] + lane * kPitch;
 
   float l[P];
@@ -498,10 +597,10 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
   if (need_scores && !sigmoid) {
     const uint32_t tb = row_max(top > low ? key_bits(top) : 0u);
     top = tb ? key_value(tb) : 0.f;
-    float sum = 0.f;
+    float part[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) sum += (in >> i) & 1 ? exp_f(l[i] - top) : 0.f;
-    total = row_sum(sum);
+    for (int i = 0; i < P; ++i) part[i] = (in >> i) & 1 ? exp_f(l[i] - top) : 0.f;
+    total = row_sum(tree_sum<P>(part));
     r = total > 0.f ? 1.f / total : 0.f;
   }
   // scores; keys as integers; the lane's two largest values for its group's mark
@@ -540,7 +639,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
       const uint32_t xb = row_max(real && rank == g.topk_group - 1 && mark > low ? key_bits(mark) : 0u);
       const uint32_t yb = row_max(real && rank == g.topk_group && mark > low ? key_bits(mark) : 0u);
       const float x = key_value(xb), y = key_value(yb);
-      if (yb) close = !(x - y > kNear * (1.f + fabsf(x) + fabsf(y)));
+      if (yb) close = !(x - y > near * (1.f + fabsf(x) + fabsf(y)));
     }
     const bool stays = real && rank < g.topk_group;
 #pragma unroll
@@ -554,7 +653,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
   }
   int id = -1;       // lane j of a token: its j-th expert
   uint32_t kb = 0u;  // and that one's key
-  const int steps = biased ? k + 1 : k;  // at most 16
+  const int steps = biased ? k + 2 : k;  // at most 16: the runner-up and the one after it
   for (int j = 0; j < steps; ++j) {
     uint32_t m = run[0];
 #pragma unroll
@@ -580,21 +679,31 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     }
   }
   const float sel = id >= 0 ? fminf(load_logit<DT>(g.logits, t * g.ld + id), 3.402823466e38f) : 0.f;
+  const float bj = biased && id >= 0 ? g.bias[id] : 0.f;
+  bool swap = false;  // lane j: too close to lane j + 1 of the token, other than equal inside the list
   if (biased) {
-    // lane j against lane j + 1 of the token, the runner-up included
-    const float v = key_value(kb), bj = id >= 0 ? g.bias[id] : 0.f;
+    const float v = key_value(kb);
     const int n = __shfl_down(id, 1, 16);
     const float nv = __shfl_down(v, 1, 16), nl = __shfl_down(sel, 1, 16), nb = __shfl_down(bj, 1, 16);
-    if (sub < k && sub < 15 && id >= 0 && n >= 0 && !(nl == sel && nb == bj))
-      close = close || !(v - nv > kNear * (1.f + fabsf(v) + fabsf(nv)));
+    if (sub <= k && id >= 0 && n >= 0 && !(sub < k - 1 && nl == sel && nb == bj))
+      swap = !(v - nv > near * (1.f + fabsf(v) + fabsf(nv)));
+    if (!sigmoid && sub < k) close = close || swap;
   } else {
     const float first = need_scores && !sigmoid ? top : __shfl(sel, lane & 48, kWave);
     if (sub < k && id >= 0) close = close || (sigmoid ? sel > 36.f || sel < -700.f : sel - first < -700.f);
   }
+  const uint64_t all = __ballot(swap);
+  if (sigmoid && biased) {
+    // close to the last of the list, which is close to one outside of it
+    const uint32_t pairs = (uint32_t)(all >> (lane & 48)) & 0xFFFFu;
+    close = close || (pairs >> (k - 1) & 3) == 3;
+  }
   double w = 0.0;
   const bool chosen = sub < k && id >= 0;
   if (sigmoid) {
-    if (chosen) w = 1.0 / (1.0 + exp(-(double)sel));
+    if (sub <= k && id >= 0) w = 1.0 / (1.0 + exp(-(double)sel));
+    if (biased && all) settle_row(id, w, w + (double)bj, k, lane);  // uniform
+    if (!(sub < k && id >= 0)) w = 0.0;
   } else {
     const uint32_t tb = row_max(chosen ? key_bits(sel) : 0u);
     const float ref = g.renormalize ? (tb ? key_value(tb) : 0.f) : top;
@@ -616,8 +725,14 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     if ((again >> (16 * q)) & 0xFFFFu) gate_exact<DT, (P * 16 + 63) / 64>(g, t0 + q, lane);
 }
 
-// from here on four tokens a wavefront beat one (2048 tokens: see the launcher's figures)
-constexpr int64_t kQuadTokens = 1024;
+// From here on (five wavefronts a SIMD) four tokens a wavefront beat one; us a call,
+// 256 experts, one / four:  sigmoid, 8 groups, bias, top 8   softmax, bf16, top 8
+//                   1024 tokens    6.9 /  9.5                   4.6 / 6.3
+//                   4096          13.7 / 10.4 to 15.9           6.0 / 6.5
+//                   8192          13.8 to 17.8 / 17.3           8.6 / 7.1
+//                  16384          23.6 to 26.8 / 21.7          14.0 / 9.4
+// (a launch in which a token falls back takes 5 us more).
+constexpr int64_t kQuadTokens = 5120;
 
 template <int DT>
 static hipError_t launch_gate_dt(const GateArgs& args, hipStream_t stream) {
@@ -628,7 +743,7 @@ static hipError_t launch_gate_dt(const GateArgs& args, hipStream_t stream) {
   p.fast = p.n_group == 1 || (per % P == 0 && (seg & (seg - 1)) == 0);
   p.vec = p.E % 4 == 0 && p.ld % 4 == 0 && ((uintptr_t)p.logits & (DT == 0 ? 15 : 7)) == 0;
   const int Q = p.E <= 64 ? 4 : p.E <= 128 ? 8 : 16, qseg = per / Q;
-  if (p.T >= kQuadTokens && p.E <= 256 && p.top_k + (p.bias ? 1 : 0) <= 16 &&
+  if (p.T >= kQuadTokens && p.E <= 256 && p.top_k + (p.bias ? 2 : 0) <= 16 &&
       (p.n_group == 1 || (per % Q == 0 && (qseg & (qseg - 1)) == 0))) {
     auto fn = Q == 4 ? gate_quad_kernel<DT, 4> : Q == 8 ? gate_quad_kernel<DT, 8> : gate_quad_kernel<DT, 16>;
     hipLaunchKernelGGL(fn, dim3((unsigned)ceil_div(p.T, 4 * kQuadWaves)), dim3(kQuadWaves * 64), 0, stream, p);

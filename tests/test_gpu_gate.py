@@ -124,12 +124,12 @@ def test_gate_close_keys(w, scoring, G, keep):
 
 
 MANY = [  # T, E, k, scoring, groups, keep, dtype, bias: four tokens a wavefront
-    (1025, 256, 8, "sigmoid", 8, 4, torch.float32, True), (1030, 256, 8, "sigmoid", 8, 4, torch.bfloat16, True),
-    (1024, 64, 6, "softmax", 1, 1, torch.bfloat16, False), (1027, 160, 6, "softmax", 10, 3, torch.float32, False),
-    (1101, 99, 6, "softmax", 1, 1, torch.bfloat16, False), (1026, 128, 15, "sigmoid", 4, 2, torch.float16, True),
-    (1099, 256, 16, "softmax", 16, 5, torch.float32, False), (1040, 32, 4, "sigmoid", 8, 3, torch.float32, False),
-    (1033, 17, 5, "softmax", 1, 1, torch.float32, True), (1029, 256, 8, "sigmoid", 2, 1, torch.float32, False),
-    (1025, 3, 2, "sigmoid", 1, 1, torch.float32, True),
+    (5121, 256, 8, "sigmoid", 8, 4, torch.float32, True), (5126, 256, 8, "sigmoid", 8, 4, torch.bfloat16, True),
+    (5120, 64, 6, "softmax", 1, 1, torch.bfloat16, False), (5123, 160, 6, "softmax", 10, 3, torch.float32, False),
+    (5197, 99, 6, "softmax", 1, 1, torch.bfloat16, False), (5122, 128, 15, "sigmoid", 4, 2, torch.float16, True),
+    (5195, 256, 16, "softmax", 16, 5, torch.float32, False), (5136, 32, 4, "sigmoid", 8, 3, torch.float32, False),
+    (5129, 17, 5, "softmax", 1, 1, torch.float32, True), (5125, 256, 8, "sigmoid", 2, 1, torch.float32, False),
+    (5121, 3, 2, "sigmoid", 1, 1, torch.float32, True),
 ]
 
 
@@ -145,12 +145,53 @@ def test_gate_four_tokens_a_wavefront(w, T, E, k, scoring, G, keep, dtype, with_
     l[1::9] = np.where(rng.random(l[1::9].shape) < 0.5, -np.inf, l[1::9])
     l[2::11] = -np.inf
     l[3::13, 0] = np.nan
-    l[4::17] = _nudge(np.float32(2.5) + 0 * l[4::17], rng.integers(-3, 4, l[4::17].shape))
+    l[4::17] = _nudge(np.full_like(l[4::17], 2.5), rng.integers(-3, 4, l[4::17].shape))
     l[5::19] *= 300.0
     l[6::23, -1] = np.inf
     if E > 1:
         b[1] = -np.inf
     _check(w, torch.from_numpy(l).to(dtype), k, b if with_bias else None, scoring, G, keep, renorm, 1.5)
+
+
+@pytest.mark.parametrize("T", [64, 5200])
+@pytest.mark.parametrize("k", [1, 2, 8, 13, 14, 20])
+def test_gate_pairs_in_float_order_and_double_order_differ(w, T, k):
+    """Keys that agree in about 22 bits: pairs that floats put in the wrong order, at every
+    place of the list and across its end, singly and in chains."""
+    rng = np.random.default_rng(k)
+    E = 64
+    l = rng.uniform(-2.0, 2.0, (T, E))
+    b = rng.uniform(-0.2, 0.2, E)
+    # bias of expert e + 32 such that its key is within some 2^-24 of expert e's in token 0's logits
+    s = 1 / (1 + np.exp(-l.astype(np.float32).astype(np.float64)))
+    for t in range(T):
+        n = rng.integers(1, 4)
+        top = np.argsort(-(s[t] + b))[rng.integers(0, min(k + 2, 12))]
+        for j in range(n):
+            e = (top + 7 * (j + 1)) % E
+            want = s[t, top] + b[top] - b[e] + rng.integers(-8, 9) * 2.0 ** -26
+            if 0.01 < want < 0.99:
+                l[t, e] = np.log(want / (1 - want))
+    _check(w, torch.from_numpy(l.astype(np.float32)), k, b, "sigmoid", 1, 1, True, 1.0)
+
+
+@pytest.mark.parametrize("T", [64, 5200])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("k", [1, 2, 5, 8, 14, 17])
+def test_gate_equal_pairs_next_to_a_closer_one(w, T, scoring, k):
+    """Two experts of one logit and bias at the end of the list, and a third, of another
+    logit and bias, within some 2^-24 of both: on either side of them in doubles."""
+    rng = np.random.default_rng(100 + k)
+    E, h = 64, 16
+    l = rng.uniform(-2.0, 2.0, (T, E))
+    b = rng.uniform(-0.2, 0.2, E)
+    l[:, h:2 * h], b[h:2 * h] = l[:, :h], b[:h]
+    if scoring == "sigmoid":
+        s = 1 / (1 + np.exp(-l[:, :h].astype(np.float32).astype(np.float64)))
+        want = np.clip(s + b[:h] - b[2 * h:3 * h] + rng.integers(-6, 7, (T, h)) * 2.0 ** -26, 0.01, 0.99)
+        l[:, 2 * h:3 * h] = np.log(want / (1 - want))
+    l[:, 3 * h:] = -9.0
+    _check(w, torch.from_numpy(l.astype(np.float32)), k, b, scoring, 1, 1, True, 1.0)
 
 
 def test_gate_many_tokens(w):
