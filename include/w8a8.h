@@ -597,9 +597,10 @@ int w8a8_w4a16_moe_grouped(int fmt, const uint16_t* x_rows, const int64_t* group
  * equals; a slot that no expert fills gets id -1 (w8a8_moe_route drops it) and
  * weight 0. The weight of an expert is its score, divided by the sum of the
  * selected scores if renormalize (0 if that sum is 0), times scale. Keys are
- * compared as doubles, weights rounded once to float.
+ * compared as doubles, weights rounded once to float; only the sum of a softmax
+ * that is not renormalized is one of floats.
  * 1 <= E <= 1024, n_group <= 64 dividing E, top_k <= 64 and no more than the
- * experts of topk_group groups, T * top_k < 2^31, scale finite.
+ * experts of topk_group groups, T < 2^26, T * top_k < 2^31, scale finite.
  */
 typedef enum {
   W8A8_DT_F32 = 0,
@@ -666,7 +667,8 @@ int w8a8_moe_gate(const void* logits, int dtype, int64_t T, int64_t E, int64_t l
  *   once, route (w8a8_moe_route), the chain with the tokens' rows read through
  *   the routing, combine (w8a8_moe_combine). topk_ids, topk_weights as
  *   w8a8_moe_gate writes them.
- * 1 <= K, H, I <= W8A8_MAX_K, N, 2I <= 2^22, M, R, T * top_k < 2^30. Workspaces
+ * 1 <= K, H, I <= W8A8_MAX_K, N, 2I <= 2^22, M, R, T * top_k < 2^28, T < 2^24 (layer), and a
+ * grouped product of at most 2^23 tiles of 128 rows x 256 columns. Workspaces
  * 256-byte aligned and rewritten by every call: two calls that may overlap
  * need two.
  */

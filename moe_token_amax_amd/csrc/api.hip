@@ -1000,8 +1000,9 @@ int w8a8_w4a16_linear(const uint16_t* x, int64_t M, int64_t K, const void* w_pac
 int w8a8_moe_gate(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int scoring,
                   int64_t n_group, int64_t topk_group, int64_t top_k, int renormalize, float scale,
                   int32_t* topk_ids, float* topk_weights, void* stream) {
-  if (T < 0 || E < 1 || top_k < 1 || T * top_k >= kMaxDim || ld < E || T >= kMaxDim)
-    return fail(W8A8_ERR_SHAPE, "moe_gate: need T >= 0, E >= 1, ld >= E, top_k >= 1 and T * top_k < 2^31");
+  // 64 threads a token of a launch of fewer than 2^32
+  if (T < 0 || T >= (int64_t)1 << 26 || E < 1 || top_k < 1 || ld < E)
+    return fail(W8A8_ERR_SHAPE, "moe_gate: need 0 <= T < 2^26, E >= 1, ld >= E and top_k >= 1");
   if (dtype != W8A8_DT_F32 && dtype != W8A8_DT_BF16 && dtype != W8A8_DT_F16)
     return fail(W8A8_ERR_UNSUPPORTED, "moe_gate: unknown logit type %d", dtype);
   if (scoring != W8A8_GATE_SOFTMAX && scoring != W8A8_GATE_SIGMOID)
@@ -1011,8 +1012,9 @@ int w8a8_moe_gate(const void* logits, int dtype, int64_t T, int64_t E, int64_t l
     return fail(W8A8_ERR_SHAPE,
                 "moe_gate: need 1 <= n_group <= 64 dividing E and 1 <= topk_group <= n_group (E=%lld n_group=%lld "
                 "topk_group=%lld)", (long long)E, (long long)n_group, (long long)topk_group);
-  if (top_k > 64 || top_k > topk_group * (E / n_group))
-    return fail(W8A8_ERR_SHAPE, "moe_gate: top_k = %lld is past 64 or past the experts of topk_group groups",
+  if (top_k > 64 || top_k > topk_group * (E / n_group) || T * top_k >= kMaxDim)
+    return fail(W8A8_ERR_SHAPE,
+                "moe_gate: top_k = %lld is past 64 or past the experts of topk_group groups, or T * top_k past 2^31",
                 (long long)top_k);
   if (!std::isfinite(scale)) return fail(W8A8_ERR_SHAPE, "moe_gate: scale must be finite");
   if (T == 0) return ok();
@@ -1048,9 +1050,11 @@ constexpr int64_t kFp8MaxN = (int64_t)1 << 22;  // columns: the tile grids stay 
 int64_t fp8b_pad(int64_t K) { return w8a8::round_up(K, w8a8::kFp8Block); }
 int64_t fp8b_kb(int64_t K) { return w8a8::ceil_div(K, w8a8::kFp8Block); }
 
+constexpr int64_t kFp8MaxM = (int64_t)1 << 28;  // rows: launches of fewer than 2^32 threads, at most 16 a row
+
 int check_fp8b(const char* who, int64_t M, int64_t N, int64_t K) {
-  if (M < 0 || N < 1 || K < 1 || M >= kMaxDim / 2 || N > kFp8MaxN || K > W8A8_MAX_K)
-    return fail(W8A8_ERR_SHAPE, "%s: need 0 <= M < 2^30, 1 <= N <= 2^22 and 1 <= K <= %d (M=%lld N=%lld K=%lld)", who,
+  if (M < 0 || N < 1 || K < 1 || M >= kFp8MaxM || N > kFp8MaxN || K > W8A8_MAX_K)
+    return fail(W8A8_ERR_SHAPE, "%s: need 0 <= M < 2^28, 1 <= N <= 2^22 and 1 <= K <= %d (M=%lld N=%lld K=%lld)", who,
                 W8A8_MAX_K, (long long)M, (long long)N, (long long)K);
   return W8A8_OK;
 }
@@ -1060,7 +1064,7 @@ int check_fp8b_grouped(const char* who, int64_t R, int64_t E, int64_t N, int64_t
   if (st) return st;
   if (E < 1) return fail(W8A8_ERR_SHAPE, "%s: need E >= 1", who);
   if (E > kMaxExperts) return fail(W8A8_ERR_UNSUPPORTED, "%s: at most %lld experts", who, (long long)kMaxExperts);
-  if ((R / 128 + E) * w8a8::ceil_div(N, 64) > (int64_t)1 << 23)
+  if (w8a8::fp8b_grid_tiles(R, E, N) >= (int64_t)1 << 23)  // of 512 threads
     return fail(W8A8_ERR_UNSUPPORTED, "%s: R = %lld rows of N = %lld columns are past one launch", who, (long long)R,
                 (long long)N);
   return W8A8_OK;
@@ -1236,7 +1240,7 @@ int w8a8_fp8b_grouped_gemm(const uint8_t* a, const float* a_scale, int64_t a_row
   int st = check_fp8b_grouped("fp8b_grouped_gemm", R, E, N, K);
   if (st) return st;
   if (R == 0) return ok();
-  if (a_rows < 1 || a_rows >= kMaxDim / 2 || (!row_index && a_rows < R))
+  if (a_rows < 1 || a_rows >= kFp8MaxM || (!row_index && a_rows < R))
     return fail(W8A8_ERR_SHAPE, "fp8b_grouped_gemm: a_rows = %lld rows do not cover R = %lld", (long long)a_rows,
                 (long long)R);
   if (!a || !a_scale || !group_list || !w_packed || !w_scale || !y)
@@ -1339,6 +1343,8 @@ int w8a8_fp8b_moe_layer(const uint16_t* x, int64_t T, int64_t H, const int32_t* 
                         int64_t ws_bytes, void* stream) {
   int st = check_route("fp8b_moe_layer", T, top_k, E);
   if (st) return st;
+  if (T >= (int64_t)1 << 24)  // the combine's workgroups of 256 threads
+    return fail(W8A8_ERR_SHAPE, "fp8b_moe_layer: need T < 2^24, got %lld", (long long)T);
   const int64_t P = T * top_k;
   st = check_fp8b_grouped("fp8b_moe_layer", P, E, 2 * I, H);
   if (st) return st;

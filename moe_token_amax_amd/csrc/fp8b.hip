@@ -254,6 +254,10 @@ constexpr int kTileRows = 128;
 
 int64_t fp8b_max_tiles(int64_t R, int64_t E) { return R / kTileRows + std::min(R, E); }
 int64_t fp8b_sched_bytes(int64_t R, int64_t E) { return 256 + 16 * fp8b_max_tiles(R, E); }
+// column groups of a row tile, whole rounds of the XCDs
+constexpr int kGroupedNBW = 2;
+static int64_t grouped_columns(int64_t N) { return round_up(ceil_div(N, 128 * kGroupedNBW), 8); }
+int64_t fp8b_grid_tiles(int64_t R, int64_t E, int64_t N) { return fp8b_max_tiles(R, E) * grouped_columns(N); }
 
 __global__ __launch_bounds__(1024) void fp8b_schedule_kernel(const int64_t* __restrict__ gl, int E, int64_t R,
                                                              int* __restrict__ count, int4* __restrict__ tiles) {
@@ -607,7 +611,7 @@ struct WideTile {
   static constexpr int kLdsBytes = 2 * kStage + 4 * kMaxKB * 4;
 
   struct Where {
-    int e, rows, nb0;  // expert, rows, first column block; rows 0: no tile
+    int rows, nb0;  // rows, first column block; rows 0: no tile
     int64_t row0;
   };
 
@@ -621,25 +625,25 @@ struct WideTile {
     const int KB = (int)p.KB;
     const uint32_t l16 = lane * 16;
     float* const wscales = reinterpret_cast<float*>(smem + 2 * kStage);  // [2][2][KB]
-    uint32_t aoff[4], soff;  // this wavefront's four activation pieces and its rows' scales: bytes from a, a_scale
+    uint32_t aoff[4];        // this wavefront's four activation pieces: bytes from a
+    const float* sbase;      // its rows' scales of block 0, the last of them
+    int slast;
     const uint8_t* wp[2];    // its two weight blocks
     // Sources of tile t; its weight scales go to half `par` of wscales.
     auto sources = [&](const Where& t, int par) __attribute__((always_inline)) {
-      auto source = [&](int r) __attribute__((always_inline)) {  // row of a for tile row r; past the tile, its last
-        int64_t src = t.row0 + min(r, t.rows - 1);
-        if (p.row_index) src = max((int64_t)0, min((int64_t)p.row_index[src], p.a_rows - 1));
-        return src;
-      };
+      // rows past the tile read its last
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        aoff[i] = (uint32_t)(source((wave * 4 + i) * 8 + (lane >> 3)) * p.lda + (((lane & 7) ^ (lane >> 3)) * 16));
-      soff = (uint32_t)(source(wave * 32 + lane) * 4);
+        aoff[i] = (uint32_t)((t.row0 + min((wave * 4 + i) * 8 + (lane >> 3), t.rows - 1)) * p.lda +
+                             (((lane & 7) ^ (lane >> 3)) * 16));
+      sbase = p.a_scale + t.row0 + min(wave * 32, t.rows - 1);
+      slast = max(t.rows - 1 - wave * 32, 0);
 #pragma unroll
       for (int j = 0; j < 2; ++j)  // past the last block, that one (never stored)
-        wp[j] = p.w + ((int64_t)t.e * NB + min(t.nb0 + wave * 2 + j, NB - 1)) * KB * kFp8BlockBytes;
+        wp[j] = p.w + (int64_t)min(t.nb0 + wave * 2 + j, NB - 1) * KB * kFp8BlockBytes;
       for (int i = tid; i < 2 * KB; i += 512) {
         const int h = i >= KB;
-        wscales[par * 2 * KB + i] = p.w_scale[((int64_t)t.e * NS + min(t.nb0 / 8 + h, NS - 1)) * KB + (h ? i - KB : i)];
+        wscales[par * 2 * KB + i] = p.w_scale[(int64_t)min(t.nb0 / 8 + h, NS - 1) * KB + (h ? i - KB : i)];
       }
     };
     // Addresses are a wave-uniform base and a 32-bit lane offset; the empty asm keeps
@@ -660,9 +664,9 @@ struct WideTile {
         const uint8_t* wb = wp[j >> 1] + k * kFp8BlockBytes + (j & 1) * 1024;
         __builtin_amdgcn_global_load_lds(wb + o, (W8A8_LDS void*)(dst + kOperand + (wave * 4 + j) * 1024), 16, 0, 0);
       }
-      uint32_t o = soff;
+      uint32_t o = min(lane, slast) * 4;
       asm volatile("" : "+v"(o));
-      __builtin_amdgcn_global_load_lds(reinterpret_cast<const uint8_t*>(p.a_scale + k * p.a_rows) + o,
+      __builtin_amdgcn_global_load_lds(reinterpret_cast<const uint8_t*>(sbase + k * p.a_rows) + o,
                                        (W8A8_LDS void*)(dst + 2 * kOperand + wave * 128), 4, 0, 0);
     };
     // operand of row block m (16 rows) of this wavefront, and of its column block j
@@ -700,7 +704,7 @@ struct WideTile {
         for (int j = 0; j < 4; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < 4; ++j) part[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      Where after{0, 0, 0, 0};
+      Where after{0, 0, 0};
       const float* wsw = wscales + (par * 2 + (wn >> 1)) * KB;
       // TAIL: the tile's last two steps, whose DMA is the next tile's first
       auto step = [&](int kb, auto TAIL) __attribute__((always_inline)) {
@@ -779,7 +783,7 @@ __global__ __launch_bounds__(512) void fp8b_wide_kernel(Fp8bGemm p) {
   const int64_t per = (total + 7) / 8, first = (blockIdx.x % 8) * per, end = min(first + per, total);
   int64_t t = first + blockIdx.x / 8;
   WideTile::run(p, smem, [&]() __attribute__((always_inline)) {
-    WideTile::Where w{0, 0, 0, 0};
+    WideTile::Where w{0, 0, 0};
     if (t < end) {
       const int64_t top = t / (8 * NT) * 8, gm = min((int64_t)8, MT - top), r = t % (8 * NT);
       w.row0 = (top + r % gm) * 256;
@@ -1004,9 +1008,9 @@ hipError_t launch_fp8b_gemm(const Fp8bGemm& args, hipStream_t stream) {
   Fp8bGemm p = args;
   p.store_vec = p.N % 4 == 0 && p.ldy % 4 == 0 && ((uintptr_t)p.y & 7) == 0;
   if (!p.group_list) return launch_dense(p, stream);
-  constexpr int NBW = 2;
-  const int64_t NT = round_up(ceil_div(p.N, 128 * NBW), 8);
-  const dim3 grid((unsigned)(fp8b_max_tiles(p.M, p.E) * NT));
+  constexpr int NBW = kGroupedNBW;
+  const int64_t NT = grouped_columns(p.N);
+  const dim3 grid((unsigned)fp8b_grid_tiles(p.M, p.E, p.N));
   if (p.exact) hipLaunchKernelGGL((fp8b_grouped_kernel<NBW, true>), grid, dim3(512), 0, stream, p, (int)NT);
   else hipLaunchKernelGGL((fp8b_grouped_kernel<NBW, false>), grid, dim3(512), 0, stream, p, (int)NT);
   return hipGetLastError();

@@ -33,7 +33,7 @@ def _gate(L, logits=P, dtype=0, T=4, E=64, ld=64, bias=None, scoring=1, n_group=
 
 @pytest.mark.parametrize("kw,status", [
     (dict(T=-1), SHAPE), (dict(E=0), SHAPE), (dict(ld=63), SHAPE), (dict(top_k=0), SHAPE),
-    (dict(T=1 << 30, top_k=2), SHAPE), (dict(dtype=3), UNSUPPORTED), (dict(scoring=2), UNSUPPORTED),
+    (dict(T=1 << 30, top_k=2), SHAPE), (dict(T=1 << 26), SHAPE), (dict(T=1 << 25, top_k=64, E=64), SHAPE), (dict(dtype=3), UNSUPPORTED), (dict(scoring=2), UNSUPPORTED),
     (dict(E=1025, ld=1025), UNSUPPORTED), (dict(n_group=0), SHAPE), (dict(n_group=3), SHAPE),
     (dict(E=130, ld=130, n_group=65), SHAPE), (dict(n_group=4, topk_group=5), SHAPE), (dict(topk_group=0), SHAPE),
     (dict(top_k=65, E=128, ld=128), SHAPE), (dict(n_group=8, topk_group=1, top_k=9), SHAPE),
@@ -50,7 +50,7 @@ def _quant(L, x=P, M=4, K=64, ldx=64, act=0, alg=0, q=P, s=P):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(M=-1), SHAPE), (dict(K=0), SHAPE), (dict(K=200000, ldx=200000), SHAPE), (dict(M=1 << 30), SHAPE),
+    (dict(M=-1), SHAPE), (dict(K=0), SHAPE), (dict(K=200000, ldx=200000), SHAPE), (dict(M=1 << 30), SHAPE), (dict(M=1 << 28), SHAPE),
     (dict(ldx=63), SHAPE), (dict(act=1, ldx=127), SHAPE), (dict(act=2), UNSUPPORTED), (dict(alg=2), UNSUPPORTED),
     (dict(x=None), NULL), (dict(q=None), NULL), (dict(s=None), NULL), (dict(x=ODD), ALIGN),
     (dict(q=ctypes.c_void_p(264)), ALIGN), (dict(s=ODD), ALIGN), (dict(M=0, x=None, q=None, s=None), OK)])
@@ -63,7 +63,7 @@ def _linear(L, x=P, ldx=64, xs=None, M=4, K=64, wp=P, ws=P, N=8, bias=None, y=P,
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(M=-1), SHAPE), (dict(N=0), SHAPE), (dict(N=(1 << 22) + 1, ldy=1 << 23), SHAPE), (dict(ldx=63), SHAPE),
+    (dict(M=-1), SHAPE), (dict(M=1 << 28), SHAPE), (dict(N=0), SHAPE), (dict(N=(1 << 22) + 1, ldy=1 << 23), SHAPE), (dict(ldx=63), SHAPE),
     (dict(ldy=7), SHAPE), (dict(xs=P, ldx=64), SHAPE), (dict(alg=-1), UNSUPPORTED), (dict(x=None), NULL),
     (dict(wp=None), NULL), (dict(ws=None), NULL), (dict(y=None), NULL), (dict(wp=ctypes.c_void_p(264)), ALIGN),
     (dict(x=ODD), ALIGN), (dict(bias=ODD), ALIGN), (dict(xs=P, ldx=136), ALIGN),
@@ -79,7 +79,8 @@ def _grouped(L, a=P, s=P, rows=8, index=None, gl=P, R=8, E=4, N=16, K=64, wp=P, 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(R=-1), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), UNSUPPORTED),
-    (dict(R=1 << 28, rows=1 << 28, N=1 << 14), UNSUPPORTED), (dict(K=0), SHAPE), (dict(rows=7), SHAPE),
+    (dict(R=1 << 28, rows=1 << 28, N=1 << 14), SHAPE),
+    (dict(R=1 << 27, rows=1 << 27, N=1 << 14), UNSUPPORTED), (dict(R=1 << 27, rows=1 << 27, N=1), UNSUPPORTED), (dict(K=0), SHAPE), (dict(rows=7), SHAPE),
     (dict(rows=0, index=P), SHAPE), (dict(gl=None), NULL), (dict(a=None), NULL), (dict(gl=ctypes.c_void_p(260)), ALIGN),
     (dict(a=ctypes.c_void_p(264)), ALIGN), (dict(index=ODD), ALIGN), (dict(n=8), WORKSPACE), (dict(room=None), WORKSPACE),
     (dict(R=0, a=None, gl=None), OK)])
@@ -100,6 +101,7 @@ def test_chain_and_layer_refusals(w):
     assert chain(alg=7) == UNSUPPORTED and chain(x=None) == NULL and chain(wp=ctypes.c_void_p(264)) == ALIGN
     assert chain(xs=P, x=ctypes.c_void_p(264)) == ALIGN and chain(n=64) == WORKSPACE and chain(room=None) == WORKSPACE
     assert chain(R=0, x=None) == OK
+    assert layer(T=1 << 24, k=1) == SHAPE
     assert layer(T=-1) == SHAPE and layer(k=0) == SHAPE and layer(E=1025) == UNSUPPORTED and layer(H=0) == SHAPE
     assert layer(alg=2) == UNSUPPORTED and layer(ids=None) == NULL and layer(out=ODD) == ALIGN
     assert layer(n=64) == WORKSPACE and layer(room=ODD) == WORKSPACE and layer(T=0, x=None) == OK
