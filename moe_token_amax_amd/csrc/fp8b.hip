@@ -99,12 +99,26 @@ __device__ __forceinline__ uint2 quant_block(const float (&v)[8], int alg, float
   return pack_codes(t);
 }
 
-template <bool VEC>
+// 8 values from src, n of them in the row (0 past it), by loads of VEC values:
+// every address and n are multiples of VEC
+template <int VEC>
 __device__ __forceinline__ void load8(const uint16_t* src, int64_t n, float (&v)[8]) {
-  if (VEC) {
-    uint4 u = {0u, 0u, 0u, 0u};
-    if (n >= 8) u = *reinterpret_cast<const uint4*>(src);  // VEC: the row's end is a multiple of 8
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  if (VEC >= 4) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (VEC == 8) {
+      if (n >= 8) {
+        const uint4 u = *reinterpret_cast<const uint4*>(src);
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (n >= 4 * (h + 1)) {
+          const uint2 u = *reinterpret_cast<const uint2*>(src + 4 * h);
+          w[2 * h] = u.x; w[2 * h + 1] = u.y;
+        }
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       v[2 * j] = __uint_as_float(w[j] << 16);
@@ -121,7 +135,7 @@ __device__ __forceinline__ void load8(const uint16_t* src, int64_t n, float (&v)
 // one 64-byte piece of its [M] line.
 constexpr int kQuantRows = 16;
 
-template <int ACT, bool VEC>
+template <int ACT, int VEC>
 __global__ __launch_bounds__(256) void fp8b_quant_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
                                                          int64_t ldx, int alg, int KB, int per,
                                                          uint8_t* __restrict__ q, float* __restrict__ scale) {
@@ -151,14 +165,16 @@ hipError_t launch_fp8b_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ld
                              uint8_t* q, float* scale, hipStream_t stream) {
   if (M == 0) return hipSuccess;
   const int KB = (int)ceil_div(K, kFp8Block);
-  const bool vec = K % 8 == 0 && ldx % 8 == 0 && ((uintptr_t)x & 15) == 0;
+  auto whole = [&](int64_t v) { return K % v == 0 && ldx % v == 0 && (uintptr_t)x % (2 * v) == 0; };
+  // 1237 rows of 2 x 1412, SwiGLU: 8.0 us in single values, 5.0 by fours
+  const int vec = whole(8) ? 8 : whole(4) ? 4 : 1;
   const int64_t gx = ceil_div(M, kQuantRows);
   // enough workgroups to fill the chip, each with as many blocks as that leaves
   const int64_t gy = std::min<int64_t>(KB, std::max<int64_t>(1, ceil_div(2048, gx)));
   const int per = (int)ceil_div(KB, gy);
   const dim3 grid((unsigned)gx, (unsigned)ceil_div(KB, per));
-  auto fn = act ? (vec ? fp8b_quant_kernel<1, true> : fp8b_quant_kernel<1, false>)
-                : (vec ? fp8b_quant_kernel<0, true> : fp8b_quant_kernel<0, false>);
+  auto fn = act ? (vec == 8 ? fp8b_quant_kernel<1, 8> : vec == 4 ? fp8b_quant_kernel<1, 4> : fp8b_quant_kernel<1, 1>)
+                : (vec == 8 ? fp8b_quant_kernel<0, 8> : vec == 4 ? fp8b_quant_kernel<0, 4> : fp8b_quant_kernel<0, 1>);
   hipLaunchKernelGGL(fn, grid, dim3(256), 0, stream, x, M, K, ldx, scale_alg, KB, per, q, scale);
   return hipGetLastError();
 }
@@ -826,42 +842,40 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fp8b_decode_kernel(Fp8bGemm
 
   i32x4 w[U][NBW][2], a[U][MB][2];
   float sx[U][MB], sw[U];
-  auto load_w = [&](int kb0) __attribute__((always_inline)) {
+  // block k (clamped) into set u
+  auto load_w = [&](int u, int kb) __attribute__((always_inline)) {
+    const int64_t k = min(kb, KB - 1);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t k = min(kb0 + u * kDecodeWaves, KB - 1);
-#pragma unroll
-      for (int j = 0; j < NBW; ++j) {
-        const uint8_t* b = wp[j] + k * kFp8BlockBytes;
-        w[u][j][0] = *reinterpret_cast<const i32x4*>(b + l16);
-        w[u][j][1] = *reinterpret_cast<const i32x4*>(b + l16 + 1024);
-      }
-      sw[u] = wsp[k];
+    for (int j = 0; j < NBW; ++j) {
+      const uint8_t* b = wp[j] + k * kFp8BlockBytes;
+      w[u][j][0] = *reinterpret_cast<const i32x4*>(b + l16);
+      w[u][j][1] = *reinterpret_cast<const i32x4*>(b + l16 + 1024);
     }
+    sw[u] = wsp[k];
   };
-  auto load_a = [&](int kb0) __attribute__((always_inline)) {
+  auto load_a = [&](int u, int kb) __attribute__((always_inline)) {
+    const int64_t k = min(kb, KB - 1);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t k = min(kb0 + u * kDecodeWaves, KB - 1);
-#pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        if (FUSED) {
-          const uint8_t* src = qlds + row[m] * (KB * 128) + k * 128 + (lane >> 4) * 16;
-          a[u][m][0] = *reinterpret_cast<const i32x4*>(src);
-          a[u][m][1] = *reinterpret_cast<const i32x4*>(src + 64);
-          sx[u][m] = reinterpret_cast<const float*>(qlds + M * (KB * 128))[k * M + row[m]];
-        } else {
-          const uint8_t* src = p.a + row[m] * p.lda + k * 128 + (lane >> 4) * 16;
-          a[u][m][0] = *reinterpret_cast<const i32x4*>(src);
-          a[u][m][1] = *reinterpret_cast<const i32x4*>(src + 64);
-          sx[u][m] = p.a_scale[k * p.a_rows + row[m]];
-        }
+    for (int m = 0; m < MB; ++m) {
+      if (FUSED) {
+        const uint8_t* src = qlds + row[m] * (KB * 128) + k * 128 + (lane >> 4) * 16;
+        a[u][m][0] = *reinterpret_cast<const i32x4*>(src);
+        a[u][m][1] = *reinterpret_cast<const i32x4*>(src + 64);
+        sx[u][m] = reinterpret_cast<const float*>(qlds + M * (KB * 128))[k * M + row[m]];
+      } else {
+        const uint8_t* src = p.a + row[m] * p.lda + k * 128 + (lane >> 4) * 16;
+        a[u][m][0] = *reinterpret_cast<const i32x4*>(src);
+        a[u][m][1] = *reinterpret_cast<const i32x4*>(src + 64);
+        sx[u][m] = p.a_scale[k * p.a_rows + row[m]];
       }
     }
   };
 
-  if (!FUSED) load_a(wave);
-  load_w(wave);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (!FUSED) load_a(u, wave + u * kDecodeWaves);
+    load_w(u, wave + u * kDecodeWaves);
+  }
   if constexpr (FUSED) {
     __builtin_amdgcn_sched_barrier(0);
     // as fp8b_quant_kernel: 16 lanes a (row, block)
@@ -871,7 +885,7 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fp8b_decode_kernel(Fp8bGemm
       const int r = b / KB, kb = b % KB;
       const int64_t k0 = (int64_t)kb * kFp8Block + sub * 8;
       float v[8];
-      load8<true>(x + r * p.lda + k0, p.K - k0, v);
+      load8<8>(x + r * p.lda + k0, p.K - k0, v);
       float s;
       const uint2 q = quant_block(v, p.scale_alg, s);
       *reinterpret_cast<uint2*>(qlds + r * (KB * 128) + k0) = q;
@@ -884,26 +898,41 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fp8b_decode_kernel(Fp8bGemm
   for (int m = 0; m < MB; ++m)
 #pragma unroll
     for (int j = 0; j < NBW; ++j) acc[m][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int kb0 = wave; kb0 < KB; kb0 += kDecodeWaves * U) {
-    if (kb0 != wave) {
-      if (!FUSED) load_a(kb0);
-      load_w(kb0);
+  auto mul = [&](int u) __attribute__((always_inline)) {
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      const float s = sx[u][m] * sw[u];
+#pragma unroll
+      for (int j = 0; j < NBW; ++j) {
+        const f32x4 part = mfma_fp8(join(w[u][j][0], w[u][j][1]), join(a[u][m][0], a[u][m][1]));
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[m][j][t] = __builtin_fmaf(part[t], s, acc[m][j][t]);
+      }
     }
-    if (FUSED) load_a(kb0);
-    __builtin_amdgcn_sched_barrier(0);  // every load of the round in flight before the first product
+  };
+  __builtin_amdgcn_sched_barrier(0);  // every first load in flight before the first product
+  int kb0 = wave;
+  // a set is refilled as soon as it is multiplied
+  for (; kb0 + kDecodeWaves * U < KB; kb0 += kDecodeWaves * U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (FUSED) load_a(u, kb0 + u * kDecodeWaves);
+      mul(u);
+      if (!FUSED) load_a(u, kb0 + (u + U) * kDecodeWaves);
+      load_w(u, kb0 + (u + U) * kDecodeWaves);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  if (kb0 < KB) {
+    if (FUSED) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_a(u, kb0 + u * kDecodeWaves);
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (kb0 + u * kDecodeWaves >= KB) break;  // wave-uniform: clamped blocks add nothing
-#pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        const float s = sx[u][m] * sw[u];
-#pragma unroll
-        for (int j = 0; j < NBW; ++j) {
-          const f32x4 part = mfma_fp8(join(w[u][j][0], w[u][j][1]), join(a[u][m][0], a[u][m][1]));
-#pragma unroll
-          for (int t = 0; t < 4; ++t) acc[m][j][t] = __builtin_fmaf(part[t], s, acc[m][j][t]);
-        }
-      }
+      mul(u);
     }
   }
 #pragma unroll
