@@ -811,16 +811,18 @@ __global__ __launch_bounds__(512) void fp8b_wide_kernel(Fp8bGemm p) {
   });
 }
 
-// Decode (dense, at most 64 rows): the weight's stream, split over K inside the
-// workgroup. A workgroup owns NBW 16-column blocks and 16 MB rows over the whole
-// K; its eight wavefronts take every eighth block of K, with U blocks of weights
-// and codes in flight each, straight from global memory into operand registers,
-// and their sums meet in LDS in a fixed order. FUSED (few rows): x is BF16, and
-// every workgroup quantizes the rows itself into LDS, behind its first weight
-// loads, which saves the quantizer's launch.
+// Decode (dense, few rows): the weight's stream, split over K inside the workgroup.
+// A workgroup owns NBW 16-column blocks and 16 MB rows over the whole K; its eight
+// wavefronts take every eighth block of K, with U blocks of weights and codes in
+// flight each, straight from global memory into operand registers and each set
+// refilled as soon as it is multiplied, and their sums meet in LDS in a fixed
+// order. FUSED (few rows): x is BF16, and every workgroup quantizes the rows itself
+// into LDS, behind its first weight loads, which saves the quantizer's launch.
+// Bound by the weights' stream: 1 x 16384 x 7168 23.0 us (5.1 TB/s), 16 rows 24.7; with
+// 64 rows by the L2's stream into the CUs, 32 bytes a clock, of the codes that every
+// workgroup reads again (64 x 4096 x 7168 13.8 us).
 constexpr int kDecodeWaves = 8;
-constexpr int64_t kFusedValues = 32768;  // M x K quantized by every workgroup, at most
-constexpr int64_t kFusedLds = 65536;     // their codes and scales
+constexpr int64_t kFusedValues = 8192;  // M x K quantized by every workgroup, at most
 
 template <int MB, int NBW, int U, bool FUSED>
 __global__ __launch_bounds__(kDecodeWaves * 64) void fp8b_decode_kernel(Fp8bGemm p) {
@@ -949,49 +951,69 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fp8b_decode_kernel(Fp8bGemm
 }
 
 // Whether a BF16 x of M rows is quantized inside the decode kernel: every
-// workgroup does all of it, which past kFusedValues costs more than a launch.
+// workgroup does all of it, which past kFusedValues costs more than the
+// quantizer's launch (us in a graph, inside / launched: 1 x 7168 x 2048 5.3 / 6.9,
+// 1 x 4096 x 7168 9.0 / 9.9, 2 x 7168 x 7168 14.4 / 14.4, 4 x 7168 x 7168 17.2 / 14.4).
 bool fp8b_fused_ok(int64_t M, int64_t K, int64_t ldx, const void* x) {
-  const int64_t KB = ceil_div(K, kFp8Block);
-  return M >= 1 && M <= 16 && M * K <= kFusedValues && K % 8 == 0 && ldx % 8 == 0 && ((uintptr_t)x & 15) == 0 &&
-         M * KB * (kFp8Block + 4) <= kFusedLds;
+  return M >= 1 && M <= 16 && M * K <= kFusedValues && K % 8 == 0 && ldx % 8 == 0 && ((uintptr_t)x & 15) == 0;
+}
+
+// U: a wavefront's blocks of K, at most as many as registers hold (sets without a
+// block of their own load the last one again)
+template <int MB, int NBW, bool FUSED>
+static void launch_decode(const Fp8bGemm& p, hipStream_t stream) {
+  constexpr int kMost = MB * NBW >= 8 ? 2 : MB * NBW >= 4 ? 4 : 8;
+  const int64_t blocks = ceil_div(p.KB, kDecodeWaves);
+  auto fn = blocks <= 2 ? fp8b_decode_kernel<MB, NBW, 2, FUSED>
+          : blocks <= 4 ? fp8b_decode_kernel<MB, NBW, std::min(4, kMost), FUSED> : fp8b_decode_kernel<MB, NBW, kMost, FUSED>;
+  hipLaunchKernelGGL(fn, dim3((unsigned)ceil_div(ceil_div(p.N, 16), NBW), (unsigned)ceil_div(p.M, 16 * MB)),
+                     dim3(kDecodeWaves * 64), FUSED ? (size_t)(p.M * p.KB * (kFp8Block + 4)) : 0, stream, p);
 }
 
 hipError_t launch_fp8b_linear_fused(const Fp8bGemm& args, hipStream_t stream) {
   Fp8bGemm p = args;
   p.store_vec = p.N % 4 == 0 && p.ldy % 4 == 0 && ((uintptr_t)p.y & 7) == 0;
-  hipLaunchKernelGGL((fp8b_decode_kernel<1, 1, 7, true>), dim3((unsigned)ceil_div(p.N, 16)), dim3(kDecodeWaves * 64),
-                     (size_t)(p.M * p.KB * (kFp8Block + 4)), stream, p);
+  // a workgroup a CU at most, if pairs of column blocks reach that
+  // (1 x 16384 x 7168: 28.9 us one by one, 26.7 in pairs)
+  if (ceil_div(p.N, 16) <= 256) launch_decode<1, 1, true>(p, stream);
+  else launch_decode<1, 2, true>(p, stream);
   return hipGetLastError();
 }
 
-// Kernel of a dense product. Tall tiles read the weight less often, short ones give
-// every CU work; which wins is read off measured times (microseconds, 65 to 4096
-// rows by 1000 to 7168 columns, K 1000 to 7168): a launch, `first` a block of K while
-// there is at most a workgroup for every second CU, `full` a block of K for every
-// round of the chip (256 workgroups, or 512 where two fit a CU).
-enum DenseKernel { kDecode, kTile32, kTile64, kTile64x256, kTile128, kTile256 };
+// Kernel of a dense product. Tall and wide tiles read operands less often, small ones
+// give every CU work; which wins is read off measured times (microseconds; weights
+// from memory; 1 to 1024 rows by 256 to 32768 columns, K 512 to 16384): a launch,
+// `round` for every round of the chip (256 workgroups; 512 where two fit a CU) and
+// per block of K `full` a round, but at least `first`. Over these sizes the choice
+// is 1 % slower than the best kernel of each size in the mean, 26 % at worst.
+//   us, best of the decode kernels / of the others:
+//     rows x columns, K 7168:  1 x 4096 7.9 / 30   64 x 4096 14 / 33   64 x 16384 43 / 42
+//                              333 x 1000 18 / 25  1024 x 4096 141 / 71
+//     K 512:                   1 x 4096 3.1 / 4.3  64 x 4096 4.8 / 5.0  64 x 16384 12 / 6.3
+enum DenseKernel { kDecode16, kDecode16x32, kDecode32, kDecode64, kTile32, kTile64, kTile64x256, kTile128, kTile256 };
 
 static DenseKernel dense_kernel(const Fp8bGemm& p) {
-  if (p.M <= 64) return kDecode;
   struct Cost {
     DenseKernel kernel;
     int rows, cols;
-    double launch, first, full;
+    double launch, round, first, full;
     bool two;  // workgroups fit a CU
   };
-  // 1024 x 4096 x 7168: 176, 70, 53, 47, 71, 90 us; 128 rows: 25, 27, 32, 41, 70, 84
-  static const Cost kCosts[] = {{kDecode, 32, 32, 5.3, 0.0, 0.0, false},    {kTile32, 32, 128, 3.0, 0.42, 0.72, true},
-                                {kTile64, 64, 128, 3.0, 0.55, 0.95, true},  {kTile64x256, 64, 256, 3.0, 0.72, 0.80, false},
-                                {kTile128, 128, 256, 3.0, 1.20, 1.42, false}, {kTile256, 256, 256, 3.0, 1.60, 1.90, false}};
+  static const Cost kCosts[] = {
+      {kDecode16, 16, 16, 1.2, 1.7, 0.08, 0.09, false},    {kDecode16x32, 16, 32, 1.9, 1.0, 0.08, 0.12, false},
+      {kDecode32, 32, 32, 1.5, 1.4, 0.14, 0.20, false},    {kDecode64, 64, 32, 2.4, 2.7, 0.24, 0.28, false},
+      {kTile32, 32, 128, 3.9, 0.0, 0.46, 1.37, true},      {kTile64, 64, 128, 4.1, 0.0, 0.54, 1.55, true},
+      {kTile64x256, 64, 256, 0.0, 4.5, 0.09, 0.77, false}, {kTile128, 128, 256, 5.3, 4.6, 1.08, 0.85, false},
+      {kTile256, 256, 256, 13.0, 1.2, 0.09, 1.44, false}};
   DenseKernel best = kTile128;
   double least = 1e30;
   for (const Cost& c : kCosts) {
     // the wide tile's pipeline is two blocks deep and its row offsets have 32 bits
     if (c.kernel == kTile256 && (p.KB < 2 || p.a_rows * p.lda >= (int64_t)1 << 32)) continue;
+    if (c.kernel < kTile32 && p.M > 65535 * 16) continue;  // their rows are the grid's second dimension
     const int64_t n = ceil_div(p.M, c.rows) * ceil_div(p.N, c.cols);
     const double rounds = c.two ? n / 512.0 : (double)ceil_div(n, 256);
-    const double us = c.kernel == kDecode ? rounds * (c.launch + 0.12 * p.KB)
-                                          : c.launch + p.KB * std::max(c.first, rounds * c.full);
+    const double us = c.launch + rounds * c.round + p.KB * std::max(c.first, rounds * c.full);
     if (us < least) {
       least = us;
       best = c.kernel;
@@ -1008,16 +1030,10 @@ static void launch_dense_tiles(const Fp8bGemm& p, hipStream_t stream) {
 
 static hipError_t launch_dense(const Fp8bGemm& p, hipStream_t stream) {
   switch (dense_kernel(p)) {
-    case kDecode: {
-      // past 32 rows in groups of 32 on pairs of column blocks: a workgroup reads half
-      // the codes for twice the columns
-      const int nbw = p.M > 32 ? 2 : 1;
-      auto fn = p.M <= 16 ? fp8b_decode_kernel<1, 1, 7, false> : p.M <= 32 ? fp8b_decode_kernel<2, 1, 7, false>
-                                                                           : fp8b_decode_kernel<2, 2, 4, false>;
-      hipLaunchKernelGGL(fn, dim3((unsigned)ceil_div(ceil_div(p.N, 16), nbw), (unsigned)ceil_div(p.M, 32)),
-                         dim3(kDecodeWaves * 64), 0, stream, p);
-      break;
-    }
+    case kDecode16: launch_decode<1, 1, false>(p, stream); break;
+    case kDecode16x32: launch_decode<1, 2, false>(p, stream); break;
+    case kDecode32: launch_decode<2, 2, false>(p, stream); break;
+    case kDecode64: launch_decode<4, 2, false>(p, stream); break;
     case kTile32: launch_dense_tiles<2, 1>(p, stream); break;
     case kTile64: launch_dense_tiles<4, 1>(p, stream); break;
     case kTile64x256: launch_dense_tiles<4, 2>(p, stream); break;
