@@ -133,6 +133,9 @@ LINEAR = [  # M, N, K
     (1, 16, 128), (1, 1, 1), (2, 17, 65), (4, 256, 1024), (16, 100, 300), (17, 128, 256), (33, 130, 2000),
     (3, 40, 2048), (4, 48, 7168), (5, 48, 7168), (16, 64, 2048), (9, 33, 3000), (40, 40, 4200),
     (64, 512, 512), (65, 48, 384), (100, 333, 1000), (128, 256, 640), (200, 272, 128), (257, 300, 200), (300, 520, 1152),
+    (1, 47, 3000), (1, 47, 8000), (1, 4200, 200), (1, 4101, 2600), (1, 4101, 6000), (5, 4200, 200), (16, 4200, 2100),
+    (7, 4101, 5000), (64, 4000, 300), (64, 4000, 1500), (64, 4090, 3000), (33, 2100, 3900), (70, 2100, 1300),
+    (64, 5000, 1500), (50, 7100, 2100), (100, 4100, 700), (5, 16400, 100), (100, 9000, 100), (130, 16400, 100),
 ]
 
 
@@ -158,7 +161,7 @@ def test_linear(w, M, N, K, bias):
 
 @pytest.mark.parametrize("M,N,K", [(2100, 3900, 256), (3000, 2900, 130), (4096, 2048, 640), (2050, 4100, 1100),
                                    (1024, 4000, 1024), (600, 4000, 1024), (150, 4096, 2000), (150, 200, 7000),
-                                   (4100, 4100, 128)])
+                                   (4100, 4100, 128), (333, 16400, 600), (2000, 300, 2000)])
 def test_linear_many_tiles(w, M, N, K):
     """Sizes of every tile height, ragged on every side: every output of sampled rows."""
     show(f"linear {M} x {N} x {K}")
