@@ -63,7 +63,8 @@ struct GateArgs {
   float scale;
   int32_t* ids;        // [T, top_k]
   float* weights;      // [T, top_k]
-  bool fast, vec;      // set by the launcher: floats first; 4 logits per load
+  // set by the launcher: floats first; 4 logits per load; 4 biases per load
+  bool fast, vec, bias_vec;
 };
 hipError_t launch_gate(const GateArgs& p, hipStream_t stream);
 

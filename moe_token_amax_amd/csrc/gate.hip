@@ -207,13 +207,16 @@ __device__ void gate_exact(const GateArgs& g, int64_t t, int lane) {
 //   by the error of their sum, at most 2^-23 times 2.4 / s (its terms' d; s the
 //   largest score) + 5 (its roundings, a tree of 10). Two sums of two scores
 //   differ by less than 2^-19 for that; compared with 2^-19 (1 + |a| + |b|).
-// Close neighbours among the selected are then put in order by the doubles that
-// their weights need anyway (sigmoid scores); what is left, a group at the border
-// or a chain of close keys that leaves the list, falls back.
+// What only two candidates decide is settled in place (sigmoid scores with a bias):
+// two groups at the border by their marks in doubles, close neighbours among the
+// selected and the runner-up by the doubles that their weights need anyway. What is
+// left, a third group or a chain of close keys that leaves the list, falls back
+// (a launch lasts as long as its slowest wavefront: with every close choice left to
+// gate_exact, 2048 tokens took 15.8 us instead of 7.2 and 16384 took 21.7, not 15.8).
 // Without a bias the order of keys is the order of logits, which are compared as
 // they are; doubles saturate (1 from l = 37 on, 0 under -745), so logits past 36
 // or a selected one 700 under the maximum (softmax) or -700 (sigmoid) fall back
-// too. On random logits the fallback takes about 1 token in 7000.
+// too.
 // The weights come from the selected logits alone, in doubles; only the sum of a
 // softmax that is not renormalized is a float sum.
 // ---------------------------------------------------------------------------
@@ -323,6 +326,26 @@ __device__ __forceinline__ void load_logits(const GateArgs& g, int64_t t, int la
   }
 }
 
+// biases of experts e0 .. e0 + P - 1; 0 without one and past the last expert
+template <int P>
+__device__ __forceinline__ void load_bias(const GateArgs& g, int e0, float (&b)[P]) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) b[i] = 0.f;
+  if (!g.bias) return;
+  if (P >= 4 && g.bias_vec) {
+#pragma unroll
+    for (int i = 0; i + 4 <= P; i += 4) {
+      if (e0 + i < g.E) {
+        const float4 v = *reinterpret_cast<const float4*>(g.bias + e0 + i);
+        b[i] = v.x; b[i + 1] = v.y; b[i + 2] = v.z; b[i + 3] = v.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < P; ++i) b[i] = e0 + i < g.E ? g.bias[e0 + i] : 0.f;
+  }
+}
+
 // Order of the k + 1 entries of a row of 16 lanes (lane j: expert id of double key
 // `key`, weight w) by those keys, lowest index first among equals. The entries fill
 // the row from lane 0; others stay where they are. Every lane takes part.
@@ -384,6 +407,8 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
       for (int i = 0; i < P; ++i) s[i] *= r;
     }
   }
+  float bias[P];
+  load_bias<P>(g, lane * P, bias);
   // keys as integers: logits without a bias, else scores + bias
   uint32_t u[P];
 #pragma unroll
@@ -391,7 +416,7 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
     float key = l[i];
     bool ok = in[i];
     if (biased) {
-      key = s[i] + (in[i] ? g.bias[lane * P + i] : 0.f);
+      key = s[i] + bias[i];
       ok = ok && key > -__builtin_huge_valf();
     }
     u[i] = ok ? key_bits(key) : 0u;
@@ -417,9 +442,45 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
     const bool group = mine < g.n_group;
     if (g.topk_group < g.n_group) {
       // the last that stays and the first that goes
-      const uint64_t last = __ballot(group && rank == g.topk_group - 1), next = __ballot(group && rank == g.topk_group);
-      const float x = readlane_f(mark, __builtin_ctzll(last)), y = readlane_f(mark, __builtin_ctzll(next));
+      const int last = __builtin_ctzll(__ballot(group && rank == g.topk_group - 1));
+      const int next = __builtin_ctzll(__ballot(group && rank == g.topk_group));
+      const float x = readlane_f(mark, last), y = readlane_f(mark, next);
       if (y > -__builtin_huge_valf()) close = !(x - y > near * (1.f + fabsf(x) + fabsf(y)));
+      if (close && sigmoid && biased) {  // uniform
+        // their marks in doubles, if no third group is close to either
+        const uint64_t before = __ballot(group && rank == g.topk_group - 2), past = __ballot(group && rank == g.topk_group + 1);
+        const float px = before ? readlane_f(mark, __builtin_ctzll(before)) : 0.f;
+        const float py = past ? readlane_f(mark, __builtin_ctzll(past)) : -__builtin_huge_valf();
+        const bool pair = (!before || px - x > near * (1.f + fabsf(px) + fabsf(x))) &&
+                          (!(py > -__builtin_huge_valf()) || y - py > near * (1.f + fabsf(y) + fabsf(py)));
+        if (pair) {  // uniform
+          const bool border = group && (rank == g.topk_group - 1 || rank == g.topk_group);
+          double first = kOut, second = kOut;
+#pragma nounroll
+          for (int n = 0; n < P; ++n) {
+            uint32_t un = u[0];
+            float ln = l[0];
+#pragma unroll
+            for (int i = 1; i < P; ++i) {
+              un = n == i ? u[i] : un;
+              ln = n == i ? l[i] : ln;
+            }
+            // keys that may be among the group's two largest
+            const bool cand = border && un && !(key_value(un) < b - near * (1.f + 2.f * fabsf(b)));
+            if (!__ballot(cand)) continue;
+            const double v = 1.0 / (1.0 + exp(-(double)ln));
+            if (cand) merge2_d(first, second, v + (double)g.bias[lane * P + n], kOut);
+          }
+          for (int d = 1; d < seg; d <<= 1) {
+            const double o1 = shfl_xor_d(first, d), o2 = shfl_xor_d(second, d);
+            merge2_d(first, second, o1, o2);
+          }
+          const double dm = second > kOut ? first + second : first;
+          const double dx = readlane_d(dm, last), dy = readlane_d(dm, next);
+          if (border && (dy > dx || (dy == dx && next < last))) rank = 2 * g.topk_group - 1 - rank;
+          close = false;
+        }
+      }
     }
     if (!(group && rank < g.topk_group)) {
 #pragma unroll
@@ -509,8 +570,9 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs g) {
 // of a token holds experts P s .. P s + P - 1 (E <= 16 P), their keys also in LDS, the
 // maxima of its runs of four in registers: a step of the selection looks into one
 // run of the lane that owns the maximum instead of at every key. Vector
-// instructions bound this kernel: 16384 x 256, sigmoid, 8 groups, bias, top 8 take
-// 17.9 us without a fallback and 21.7 with one, the logits' bytes 4.
+// instructions (1430 a wavefront, 9.5 us at 16384 tokens) and the selection's
+// dependent steps bound this kernel: 16384 x 256, sigmoid, 8 groups, bias, top 8
+// take 15.8 us, the logits' bytes 4.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
@@ -524,6 +586,13 @@ __device__ __forceinline__ float row_sum(float v) {
   v += dpp_f<0x4E>(v);
   v += dpp_f<0x141>(v);
   return v + dpp_f<0x140>(v);
+}
+
+__device__ __forceinline__ double row_max_d(double v) {
+  v = fmax(v, dpp_d<0xB1>(v));
+  v = fmax(v, dpp_d<0x4E>(v));
+  v = fmax(v, dpp_d<0x141>(v));
+  return fmax(v, dpp_d<0x140>(v));
 }
 
 __device__ __forceinline__ double row_sum_d(double v) {
@@ -603,6 +672,8 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     total = row_sum(tree_sum<P>(part));
     r = total > 0.f ? 1.f / total : 0.f;
   }
+  float bias[P];
+  load_bias<P>(g, e0, bias);
   // scores; keys as integers; the lane's two largest values for its group's mark
   uint32_t u[P];
   float a = low, b = low;
@@ -612,7 +683,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     bool ok = (in >> i) & 1;
     if (need_scores) v = sigmoid ? __builtin_amdgcn_rcpf(1.f + exp_f(-l[i])) : exp_f(l[i] - top) * r;
     if (biased) {
-      v = v + (e0 + i < E ? g.bias[e0 + i] : 0.f);
+      v = v + bias[i];
       key = v;
       ok = ok && key > low;
     }
@@ -640,6 +711,41 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
       const uint32_t yb = row_max(real && rank == g.topk_group && mark > low ? key_bits(mark) : 0u);
       const float x = key_value(xb), y = key_value(yb);
       if (yb) close = !(x - y > near * (1.f + fabsf(x) + fabsf(y)));
+      if (sigmoid && biased && __ballot(close)) {  // uniform
+        // their marks in doubles, if no third group is close to either
+        const uint32_t pb = row_max(real && rank == g.topk_group - 2 && mark > low ? key_bits(mark) : 0u);
+        const uint32_t nb = row_max(real && rank == g.topk_group + 1 && mark > low ? key_bits(mark) : 0u);
+        const float prev = key_value(pb), next = key_value(nb);
+        const bool pair = close && !(pb && !(prev - x > near * (1.f + fabsf(prev) + fabsf(x)))) &&
+                          !(nb && !(y - next > near * (1.f + fabsf(y) + fabsf(next))));
+        const bool border = pair && real && (rank == g.topk_group - 1 || rank == g.topk_group);
+        // the keys that may be among the group's two largest
+        const float from = b - near * (1.f + 2.f * fabsf(b));
+        uint32_t cand = 0u;
+#pragma unroll
+        for (int i = 0; i < P; ++i) cand |= border && u[i] && !(key_value(u[i]) < from) ? 1u << i : 0u;
+        double first = kOut, second = kOut;
+        while (__ballot(cand != 0u)) {
+          const int n = cand ? __builtin_ctz(cand) : 0;
+          float x1 = l[0];
+#pragma unroll
+          for (int i = 1; i < P; ++i) x1 = n == i ? l[i] : x1;
+          double v = 1.0 / (1.0 + exp(-(double)x1));
+          if (cand) merge2_d(first, second, v + (double)g.bias[e0 + n], kOut);
+          cand &= cand - 1u;  // 0 stays 0
+        }
+        for (int d = 1; d < seg; d <<= 1) {
+          const double o1 = shfl_xor_d(first, d), o2 = shfl_xor_d(second, d);
+          merge2_d(first, second, o1, o2);
+        }
+        const double dm = second > kOut ? first + second : first;
+        const double dx = row_max_d(border && rank == g.topk_group - 1 ? dm : kOut);
+        const double dy = row_max_d(border && rank == g.topk_group ? dm : kOut);
+        const uint32_t gx = row_max(border && rank == g.topk_group - 1 ? (uint32_t)group : 0u);
+        const uint32_t gy = row_max(border && rank == g.topk_group ? (uint32_t)group : 0u);
+        if (border && (dy > dx || (dy == dx && gy < gx))) rank = 2 * g.topk_group - 1 - rank;
+        close = close && !pair;
+      }
     }
     const bool stays = real && rank < g.topk_group;
 #pragma unroll
@@ -727,11 +833,11 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
 
 // From here on (five wavefronts a SIMD) four tokens a wavefront beat one; us a call,
 // 256 experts, one / four:  sigmoid, 8 groups, bias, top 8   softmax, bf16, top 8
-//                   1024 tokens    6.9 /  9.5                   4.6 / 6.3
-//                   4096          13.7 / 10.4 to 15.9           6.0 / 6.5
-//                   8192          13.8 to 17.8 / 17.3           8.6 / 7.1
-//                  16384          23.6 to 26.8 / 21.7          14.0 / 9.4
-// (a launch in which a token falls back takes 5 us more).
+//                   1024 tokens    7.0 /  9.3                   4.8 / 6.3
+//                   4096           9.3 / 10.4                   6.3 / 6.5
+//                   5120          10.5 / 10.8                   7.1 / 7.4
+//                   8192          13.5 / 11.1                   9.0 / 7.1
+//                  16384          22.3 / 15.8                  14.9 / 9.6
 constexpr int64_t kQuadTokens = 5120;
 
 template <int DT>
@@ -741,6 +847,7 @@ static hipError_t launch_gate_dt(const GateArgs& args, hipStream_t stream) {
   const int per = p.E / p.n_group, seg = per / P;
   // groups have to be whole aligned runs of a power of two of lanes
   p.fast = p.n_group == 1 || (per % P == 0 && (seg & (seg - 1)) == 0);
+  p.bias_vec = p.E % 4 == 0 && ((uintptr_t)p.bias & 15) == 0;
   p.vec = p.E % 4 == 0 && p.ld % 4 == 0 && ((uintptr_t)p.logits & (DT == 0 ? 15 : 7)) == 0;
   const int Q = p.E <= 64 ? 4 : p.E <= 128 ? 8 : 16, qseg = per / Q;
   if (p.T >= kQuadTokens && p.E <= 256 && p.top_k + (p.bias ? 2 : 0) <= 16 &&

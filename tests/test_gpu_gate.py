@@ -194,6 +194,31 @@ def test_gate_equal_pairs_next_to_a_closer_one(w, T, scoring, k):
     _check(w, torch.from_numpy(l.astype(np.float32)), k, b, scoring, 1, 1, True, 1.0)
 
 
+@pytest.mark.parametrize("T", [64, 5200])
+@pytest.mark.parametrize("E,G,keep,third", [(256, 8, 4, False), (256, 8, 4, True), (128, 16, 1, False), (64, 2, 1, False),
+                                            (96, 3, 2, False), (256, 4, 3, True)])
+def test_gate_groups_whose_marks_nearly_tie(w, T, E, G, keep, third):
+    """The last group that stays and the first that goes (and one more) have marks that agree
+    in some 24 bits, from other logits and biases."""
+    rng = np.random.default_rng(E + G + T)
+    per = E // G
+    l = rng.uniform(-2.0, 2.0, (T, E))
+    b = rng.uniform(-0.1, 0.1, E)
+    s = 1 / (1 + np.exp(-l.astype(np.float32).astype(np.float64)))
+    key = (s + b).reshape(T, G, per)
+    top = np.argsort(-key, axis=2)[:, :, :2]
+    order = np.argsort(-np.take_along_axis(key, top, 2).sum(2), axis=1)
+    t = np.arange(T)
+    a = order[:, keep - 1]
+    for o in [keep] + ([keep + 1] if third and keep + 1 < G else []):
+        c = order[:, o]
+        for j in range(2):
+            e_a, e_c = a * per + top[t, a, j], c * per + top[t, c, j]
+            want = s[t, e_a] + b[e_a] - b[e_c] + rng.integers(-6, 7, T) * 2.0 ** -26
+            l[t, e_c] = np.log(np.clip(want, 0.01, 0.99) / (1 - np.clip(want, 0.01, 0.99)))
+    _check(w, torch.from_numpy(l.astype(np.float32)), 6, b, "sigmoid", G, keep, True, 1.0)
+
+
 def test_gate_many_tokens(w):
     # more tokens than one pass of the chip; every token exact against the oracle on a sample
     T, E, k = 9001, 256, 8
