@@ -1206,7 +1206,7 @@ int w8a8_fp8b_linear(const void* x, int64_t ldx, const float* x_scale, int64_t M
     if (!workspace || ws_bytes < need || !aligned(workspace, 256))
       return fail(W8A8_ERR_WORKSPACE, "fp8b_linear: BF16 input needs %lld workspace bytes (256-byte aligned), got %lld",
                   (long long)need, (long long)ws_bytes);
-    if (w8a8::fp8b_fused_ok(M, K, ldx, x)) {
+    if (w8a8::fp8b_fused_ok(M, K)) {
       w8a8::Fp8bGemm p = fp8b_args(a, ldx, nullptr, M, M, K, w_packed, w_scale, N, y);
       p.bias = bias;
       p.ldy = ldy;

@@ -99,30 +99,25 @@ __device__ __forceinline__ uint2 quant_block(const float (&v)[8], int alg, float
   return pack_codes(t);
 }
 
-// 8 values from src, n of them in the row (0 past it), by loads of VEC values:
-// every address and n are multiples of VEC
-template <int VEC>
+// 16 and 8 bytes at any BF16 address: gfx950 loads and stores them in one
+// instruction, at full rate where they happen to be aligned, so odd widths need no
+// path of their own (in single values the quantizer took 20.3 us for 4096 x 4097,
+// now 10.1, and a product's outputs 52 us for 5366 x 4089 x 197, now 34)
+struct __attribute__((packed, aligned(2))) Bytes16 {
+  uint32_t w[4];
+};
+struct __attribute__((packed, aligned(2))) Bytes8 {
+  uint32_t w[2];
+};
+
+// 8 values from src, n of them in the row (0 past it)
 __device__ __forceinline__ void load8(const uint16_t* src, int64_t n, float (&v)[8]) {
-  if (VEC >= 4) {
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (VEC == 8) {
-      if (n >= 8) {
-        const uint4 u = *reinterpret_cast<const uint4*>(src);
-        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-      }
-    } else {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        if (n >= 4 * (h + 1)) {
-          const uint2 u = *reinterpret_cast<const uint2*>(src + 4 * h);
-          w[2 * h] = u.x; w[2 * h + 1] = u.y;
-        }
-      }
-    }
+  if (n >= 8) {
+    const Bytes16 u = *reinterpret_cast<const Bytes16*>(src);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      v[2 * j] = __uint_as_float(u.w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(u.w[j] & 0xFFFF0000u);
     }
   } else {
 #pragma unroll
@@ -135,7 +130,7 @@ __device__ __forceinline__ void load8(const uint16_t* src, int64_t n, float (&v)
 // one 64-byte piece of its [M] line.
 constexpr int kQuantRows = 16;
 
-template <int ACT, int VEC>
+template <int ACT>
 __global__ __launch_bounds__(256) void fp8b_quant_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
                                                          int64_t ldx, int alg, int KB, int per,
                                                          uint8_t* __restrict__ q, float* __restrict__ scale) {
@@ -147,10 +142,10 @@ __global__ __launch_bounds__(256) void fp8b_quant_kernel(const uint16_t* __restr
     const int64_t k0 = (int64_t)kb * kFp8Block + sub * 8;
     const uint16_t* src = x + row * ldx + k0;
     float v[8];
-    load8<VEC>(src, K - k0, v);
+    load8(src, K - k0, v);
     if (ACT == 1) {
       float u[8];
-      load8<VEC>(src + K, K - k0, u);
+      load8(src + K, K - k0, u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = swiglu_fixed(v[j], u[j]);
     }
@@ -165,16 +160,12 @@ hipError_t launch_fp8b_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ld
                              uint8_t* q, float* scale, hipStream_t stream) {
   if (M == 0) return hipSuccess;
   const int KB = (int)ceil_div(K, kFp8Block);
-  auto whole = [&](int64_t v) { return K % v == 0 && ldx % v == 0 && (uintptr_t)x % (2 * v) == 0; };
-  // 1237 rows of 2 x 1412, SwiGLU: 8.0 us in single values, 5.0 by fours
-  const int vec = whole(8) ? 8 : whole(4) ? 4 : 1;
   const int64_t gx = ceil_div(M, kQuantRows);
   // enough workgroups to fill the chip, each with as many blocks as that leaves
   const int64_t gy = std::min<int64_t>(KB, std::max<int64_t>(1, ceil_div(2048, gx)));
   const int per = (int)ceil_div(KB, gy);
   const dim3 grid((unsigned)gx, (unsigned)ceil_div(KB, per));
-  auto fn = act ? (vec == 8 ? fp8b_quant_kernel<1, 8> : vec == 4 ? fp8b_quant_kernel<1, 4> : fp8b_quant_kernel<1, 1>)
-                : (vec == 8 ? fp8b_quant_kernel<0, 8> : vec == 4 ? fp8b_quant_kernel<0, 4> : fp8b_quant_kernel<0, 1>);
+  auto fn = act ? fp8b_quant_kernel<1> : fp8b_quant_kernel<0>;
   hipLaunchKernelGGL(fn, grid, dim3(256), 0, stream, x, M, K, ldx, scale_alg, KB, per, q, scale);
   return hipGetLastError();
 }
@@ -330,16 +321,24 @@ __device__ __forceinline__ void lds_barrier() {
 __device__ __forceinline__ void store4(const Fp8bGemm& p, int64_t m, int64_t n, const f32x4& v) {
   if (n >= p.N) return;
   uint16_t* y = p.y + m * p.ldy + n;
-  uint16_t o[4];
+  if (n + 4 <= p.N) {
+    float b[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.bias) {
+      const Bytes8 u = *reinterpret_cast<const Bytes8*>(p.bias + n);
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
-    o[t] = to_bf16(p.bias ? v[t] + bf16_to_f32(p.bias[min(n + t, p.N - 1)]) : v[t]);
-  if (p.store_vec) {
-    *reinterpret_cast<uint2*>(y) = uint2{o[0] | ((uint32_t)o[1] << 16), o[2] | ((uint32_t)o[3] << 16)};
+      for (int t = 0; t < 2; ++t) {
+        b[2 * t] = __uint_as_float(u.w[t] << 16);
+        b[2 * t + 1] = __uint_as_float(u.w[t] & 0xFFFF0000u);
+      }
+    }
+    uint16_t o[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) o[t] = to_bf16(p.bias ? v[t] + b[t] : v[t]);
+    *reinterpret_cast<Bytes8*>(y) = Bytes8{{o[0] | ((uint32_t)o[1] << 16), o[2] | ((uint32_t)o[3] << 16)}};
   } else {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
-      if (n + t < p.N) y[t] = o[t];
+      if (n + t < p.N) y[t] = to_bf16(p.bias ? v[t] + bf16_to_f32(p.bias[n + t]) : v[t]);
   }
 }
 
@@ -887,7 +886,7 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fp8b_decode_kernel(Fp8bGemm
       const int r = b / KB, kb = b % KB;
       const int64_t k0 = (int64_t)kb * kFp8Block + sub * 8;
       float v[8];
-      load8<8>(x + r * p.lda + k0, p.K - k0, v);
+      load8(x + r * p.lda + k0, p.K - k0, v);
       float s;
       const uint2 q = quant_block(v, p.scale_alg, s);
       *reinterpret_cast<uint2*>(qlds + r * (KB * 128) + k0) = q;
@@ -954,8 +953,8 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fp8b_decode_kernel(Fp8bGemm
 // workgroup does all of it, which past kFusedValues costs more than the
 // quantizer's launch (us in a graph, inside / launched: 1 x 7168 x 2048 5.3 / 6.9,
 // 1 x 4096 x 7168 9.0 / 9.9, 2 x 7168 x 7168 14.4 / 14.4, 4 x 7168 x 7168 17.2 / 14.4).
-bool fp8b_fused_ok(int64_t M, int64_t K, int64_t ldx, const void* x) {
-  return M >= 1 && M <= 16 && M * K <= kFusedValues && K % 8 == 0 && ldx % 8 == 0 && ((uintptr_t)x & 15) == 0;
+bool fp8b_fused_ok(int64_t M, int64_t K) {
+  return M >= 1 && M <= 16 && M * K <= kFusedValues;
 }
 
 // U: a wavefront's blocks of K, at most as many as registers hold (sets without a
@@ -970,9 +969,7 @@ static void launch_decode(const Fp8bGemm& p, hipStream_t stream) {
                      dim3(kDecodeWaves * 64), FUSED ? (size_t)(p.M * p.KB * (kFp8Block + 4)) : 0, stream, p);
 }
 
-hipError_t launch_fp8b_linear_fused(const Fp8bGemm& args, hipStream_t stream) {
-  Fp8bGemm p = args;
-  p.store_vec = p.N % 4 == 0 && p.ldy % 4 == 0 && ((uintptr_t)p.y & 7) == 0;
+hipError_t launch_fp8b_linear_fused(const Fp8bGemm& p, hipStream_t stream) {
   // a workgroup a CU at most, if pairs of column blocks reach that
   // (1 x 16384 x 7168: 28.9 us one by one, 26.7 in pairs)
   if (ceil_div(p.N, 16) <= 256) launch_decode<1, 1, true>(p, stream);
@@ -1048,10 +1045,8 @@ static hipError_t launch_dense(const Fp8bGemm& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-hipError_t launch_fp8b_gemm(const Fp8bGemm& args, hipStream_t stream) {
-  if (args.M == 0 || args.N == 0) return hipSuccess;
-  Fp8bGemm p = args;
-  p.store_vec = p.N % 4 == 0 && p.ldy % 4 == 0 && ((uintptr_t)p.y & 7) == 0;
+hipError_t launch_fp8b_gemm(const Fp8bGemm& p, hipStream_t stream) {
+  if (p.M == 0 || p.N == 0) return hipSuccess;
   if (!p.group_list) return launch_dense(p, stream);
   constexpr int NBW = kGroupedNBW;
   const int64_t NT = grouped_columns(p.N);

@@ -40,7 +40,6 @@ struct Fp8bGemm {
   // BF16 input quantized inside (launch_fp8b_linear_fused): a = x, lda in elements
   int64_t K;
   int scale_alg;
-  bool store_vec;            // set by the launcher: outputs in 8-byte pieces
 };
 // tiles of the rows of every expert; any number of products over one
 // group_list and R share a schedule
@@ -48,7 +47,7 @@ int64_t fp8b_sched_bytes(int64_t R, int64_t E);
 int64_t fp8b_grid_tiles(int64_t R, int64_t E, int64_t N);  // workgroups of a grouped product's launch
 hipError_t launch_fp8b_schedule(const int64_t* group_list, int64_t E, int64_t R, void* ws, hipStream_t stream);
 hipError_t launch_fp8b_gemm(const Fp8bGemm& p, hipStream_t stream);
-bool fp8b_fused_ok(int64_t M, int64_t K, int64_t ldx, const void* x);
+bool fp8b_fused_ok(int64_t M, int64_t K);
 hipError_t launch_fp8b_linear_fused(const Fp8bGemm& p, hipStream_t stream);
 
 struct GateArgs {
