@@ -261,10 +261,11 @@ constexpr int kTileRows = 128;
 
 int64_t fp8b_max_tiles(int64_t R, int64_t E) { return R / kTileRows + std::min(R, E); }
 int64_t fp8b_sched_bytes(int64_t R, int64_t E) { return 256 + 16 * fp8b_max_tiles(R, E); }
-// column groups of a row tile, whole rounds of the XCDs
-constexpr int kGroupedNBW = 2;
-static int64_t grouped_columns(int64_t N) { return round_up(ceil_div(N, 128 * kGroupedNBW), 8); }
-int64_t fp8b_grid_tiles(int64_t R, int64_t E, int64_t N) { return fp8b_max_tiles(R, E) * grouped_columns(N); }
+constexpr int kGroupedNBW = 2, kSpreadTiles = 64;
+static int64_t grouped_columns(int64_t N) { return ceil_div(N, 128 * kGroupedNBW); }
+int64_t fp8b_grid_tiles(int64_t R, int64_t E, int64_t N) {
+  return round_up(fp8b_max_tiles(R, E), 8) * grouped_columns(N);
+}
 
 __global__ __launch_bounds__(1024) void fp8b_schedule_kernel(const int64_t* __restrict__ gl, int E, int64_t R,
                                                              int* __restrict__ count, int4* __restrict__ tiles) {
@@ -572,17 +573,29 @@ __device__ __forceinline__ void stream_tile(const Fp8bGemm& p, uint8_t* smem, in
   else StreamTile<8, NBW, EXACT>::run(p, smem, e, row0, rows, nb0);
 }
 
-// Grouped: workgroup b takes column group b % NT of tile b / NT. NT (column
-// groups, rounded up to 8) keeps a column group on one XCD (b % 8), where the
-// tiles of an expert share its weights in L2.
+// Grouped: every row tile times NT column groups; workgroup b runs on XCD b % 8.
+// Few tiles: in order, so that every XCD has its share. From kSpreadTiles on a tile's
+// column groups go to two XCDs (one if NT is odd), whose L2 they read the tile's codes
+// through, 4 or 8 tiles at a time; us of a layer of 256 experts of 4096 x 2048, top 8,
+// on 8 / 4 / 2 / 1 XCDs a tile: 16 tokens 392 / 383 / 370 / 362, 2048 tokens 1519 / 1500 /
+// 1499 / 1514; 8 experts, 4096 tokens, top 2: 534 / 521 / 541 / 564.
 template <int NBW, bool EXACT>
 __global__ __launch_bounds__(512) void fp8b_grouped_kernel(Fp8bGemm p, int NT) {
   using T = StreamTile<8, NBW, EXACT>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
-  const int t = blockIdx.x / NT, c = blockIdx.x % NT;
-  if (t >= *reinterpret_cast<const int*>(p.ws)) return;
+  const int count = *reinterpret_cast<const int*>(p.ws);
+  int t, c;
+  if (count >= kSpreadTiles) {
+    const int spread = NT % 2 ? 1 : 2;
+    const int x = blockIdx.x % 8, j = blockIdx.x / 8, per = NT / spread;
+    t = j / per * (8 / spread) + x / spread;
+    c = x % spread + j % per * spread;
+  } else {
+    t = blockIdx.x / NT;
+    c = blockIdx.x % NT;
+  }
+  if (t >= count) return;
   const int nb0 = c * 8 * NBW;
-  if ((int64_t)nb0 * 16 >= p.N) return;
   const int4 tile = reinterpret_cast<const int4*>(reinterpret_cast<const char*>(p.ws) + 256)[t];
   stream_tile<NBW, EXACT>(p, smem, __builtin_amdgcn_readfirstlane(tile.x), __builtin_amdgcn_readfirstlane(tile.y),
                           __builtin_amdgcn_readfirstlane(tile.z), nb0);

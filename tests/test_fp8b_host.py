@@ -80,7 +80,7 @@ def _grouped(L, a=P, s=P, rows=8, index=None, gl=P, R=8, E=4, N=16, K=64, wp=P, 
 @pytest.mark.parametrize("kw,status", [
     (dict(R=-1), SHAPE), (dict(E=0), SHAPE), (dict(E=1025), UNSUPPORTED),
     (dict(R=1 << 28, rows=1 << 28, N=1 << 14), SHAPE),
-    (dict(R=1 << 27, rows=1 << 27, N=1 << 14), UNSUPPORTED), (dict(R=1 << 27, rows=1 << 27, N=1), UNSUPPORTED), (dict(K=0), SHAPE), (dict(rows=7), SHAPE),
+    (dict(R=1 << 27, rows=1 << 27, N=1 << 14), UNSUPPORTED), (dict(R=1 << 27, rows=1 << 27, N=1 << 12), UNSUPPORTED), (dict(K=0), SHAPE), (dict(rows=7), SHAPE),
     (dict(rows=0, index=P), SHAPE), (dict(gl=None), NULL), (dict(a=None), NULL), (dict(gl=ctypes.c_void_p(260)), ALIGN),
     (dict(a=ctypes.c_void_p(264)), ALIGN), (dict(index=ODD), ALIGN), (dict(n=8), WORKSPACE), (dict(room=None), WORKSPACE),
     (dict(R=0, a=None, gl=None), OK)])

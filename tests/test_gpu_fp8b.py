@@ -276,6 +276,8 @@ def test_linear_non_finite_values_stay_in_their_row_and_column(w):
 GROUPED = [  # counts, N, K
     ([12, 7, 0, 19], 64, 64), ([1], 16, 128), ([0, 0, 5, 0], 130, 300), ([64, 65, 1, 0, 16, 17], 272, 256),
     ([129, 0, 300, 3], 144, 384), ([1] * 40, 48, 200), ([0] * 31 + [70], 80, 128), ([256, 257, 511], 520, 640),
+    # 64 tiles and more, of one, two and three column groups; 63
+    ([2] * 70, 130, 200), ([3, 0, 1] * 33, 272, 128), ([1, 129] * 22, 600, 130), ([1] * 63, 272, 128), ([1] * 64, 530, 100),
 ]
 
 
