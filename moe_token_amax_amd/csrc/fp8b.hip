@@ -16,8 +16,9 @@
 // 8-byte operand group after cutting each, towards zero, to a multiple of
 // 2^(E - 13), E the largest sum of the two operands' exponents in the group
 // (measured with in-bounds probes; groups add in fp32). That is below 2^-13 of
-// the group's largest product per value, 1/32 of the half step of the BF16
-// output, and the price of twice the BF16 matrix rate.
+// the group's largest product per value, which a BF16 output does not feel; where
+// the output is quantized again (an expert's W13), its error grows to 1.6 times that
+// of exact products, so EXACT tiles multiply the codes as BF16, at half the rate.
 #include <algorithm>
 #include <type_traits>
 
