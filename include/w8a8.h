@@ -667,10 +667,10 @@ int w8a8_moe_gate(const void* logits, int dtype, int64_t T, int64_t E, int64_t l
  *   once, route (w8a8_moe_route), the chain with the tokens' rows read through
  *   the routing, combine (w8a8_moe_combine). topk_ids, topk_weights as
  *   w8a8_moe_gate writes them.
- * 1 <= K, H, I <= W8A8_MAX_K, N, 2I <= 2^22, M, R, T * top_k < 2^28, T < 2^24 (layer), and a
- * grouped product of at most 2^23 tiles of 128 rows x 256 columns. Workspaces
- * 256-byte aligned and rewritten by every call: two calls that may overlap
- * need two.
+ * 1 <= K, H, I <= W8A8_MAX_K, N, 2I <= 2^22, M, R, T * top_k < 2^28 - 16, T <
+ * 2^24 (layer), and a grouped product of fewer than 2^23 tiles of 128 rows x 256
+ * columns. Workspaces 256-byte aligned and rewritten by every call: two calls
+ * that may overlap need two.
  */
 int w8a8_fp8b_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int act, int scale_alg, uint8_t* q,
                     float* scale, void* stream);

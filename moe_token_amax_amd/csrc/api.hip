@@ -1050,11 +1050,12 @@ constexpr int64_t kFp8MaxN = (int64_t)1 << 22;  // columns: the tile grids stay 
 int64_t fp8b_pad(int64_t K) { return w8a8::round_up(K, w8a8::kFp8Block); }
 int64_t fp8b_kb(int64_t K) { return w8a8::ceil_div(K, w8a8::kFp8Block); }
 
-constexpr int64_t kFp8MaxM = (int64_t)1 << 28;  // rows: launches of fewer than 2^32 threads, at most 16 a row
+// rows: launches of fewer than 2^32 threads, at most 16 a row and a workgroup more
+constexpr int64_t kFp8MaxM = ((int64_t)1 << 28) - 16;
 
 int check_fp8b(const char* who, int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 1 || K < 1 || M >= kFp8MaxM || N > kFp8MaxN || K > W8A8_MAX_K)
-    return fail(W8A8_ERR_SHAPE, "%s: need 0 <= M < 2^28, 1 <= N <= 2^22 and 1 <= K <= %d (M=%lld N=%lld K=%lld)", who,
+    return fail(W8A8_ERR_SHAPE, "%s: need 0 <= M < 2^28 - 16, 1 <= N <= 2^22 and 1 <= K <= %d (M=%lld N=%lld K=%lld)", who,
                 W8A8_MAX_K, (long long)M, (long long)N, (long long)K);
   return W8A8_OK;
 }
@@ -1115,7 +1116,8 @@ w8a8::Fp8bGemm fp8b_args(const uint8_t* a, int64_t lda, const float* a_scale, in
 }
 
 // W13 -> SwiGLU + quant -> W2 on quantized rows: `a` [a_rows][H padded] with
-// scales [KB][a_rows], read at row_index (null: row r itself)
+// scales [KB][a_rows], read at row_index (null: row r itself); the schedule stands in
+// ws + L.sched
 hipError_t fp8b_chain(const uint8_t* a, const float* a_scale, int64_t a_rows, const int32_t* row_index,
                       const int64_t* group_list, int64_t R, int64_t E, int64_t H, int64_t I, const void* w13,
                       const float* w13_scale, const void* w2, const float* w2_scale, int alg, uint16_t* y, char* ws,
@@ -1129,9 +1131,7 @@ hipError_t fp8b_chain(const uint8_t* a, const float* a_scale, int64_t a_rows, co
   p.E = E;
   p.ws = ws + L.sched;
   p.exact = 1;  // its output is quantized again, which would amplify the cuts of the FP8 products
-  hipError_t err = w8a8::launch_fp8b_schedule(group_list, E, R, ws + L.sched, s);
-  if (err != hipSuccess) return err;
-  err = w8a8::launch_fp8b_gemm(p, s);
+  hipError_t err = w8a8::launch_fp8b_gemm(p, s);
   if (err != hipSuccess) return err;
   err = w8a8::launch_fp8b_quant(h, R, I, 2 * I, 1, alg, q2, s2, s);
   if (err != hipSuccess) return err;
@@ -1300,10 +1300,14 @@ int w8a8_fp8b_moe_grouped(const void* x_rows, const float* x_scale, const int64_
   if (!x_scale) {
     uint8_t* q = reinterpret_cast<uint8_t*>(ws + L.q1);
     float* sc = reinterpret_cast<float*>(ws + L.s1);
-    hipError_t err = w8a8::launch_fp8b_quant(reinterpret_cast<const uint16_t*>(x_rows), R, H, H, 0, scale_alg, q, sc, s);
+    hipError_t err = w8a8::launch_fp8b_quant_schedule(reinterpret_cast<const uint16_t*>(x_rows), R, H, H, scale_alg, q,
+                                                      sc, group_list, E, R, ws + L.sched, s);
     if (err != hipSuccess) return launched(err, "fp8b_moe_grouped: quant");
     a = q;
     as = sc;
+  } else {
+    hipError_t err = w8a8::launch_fp8b_schedule(group_list, E, R, ws + L.sched, s);
+    if (err != hipSuccess) return launched(err, "fp8b_moe_grouped: schedule");
   }
   return launched(fp8b_chain(a, as, R, nullptr, group_list, R, E, H, I, w13_packed, w13_scale, w2_packed, w2_scale,
                              scale_alg, y, ws, L, s),
@@ -1372,10 +1376,10 @@ int w8a8_fp8b_moe_layer(const uint16_t* x, int64_t T, int64_t H, const int32_t* 
   const Fp8bMoeWs C = fp8b_moe_layout(T, P, E, H, I);
   uint8_t* q = reinterpret_cast<uint8_t*>(chain + C.q1);
   float* sc = reinterpret_cast<float*>(chain + C.s1);
-  hipError_t err = w8a8::launch_fp8b_quant(x, T, H, H, 0, scale_alg, q, sc, s);
-  if (err != hipSuccess) return launched(err, "fp8b_moe_layer: quant");
-  err = w8a8::launch_route(topk_ids, T, top_k, E, gl, rt, pr, s);
+  hipError_t err = w8a8::launch_route(topk_ids, T, top_k, E, gl, rt, pr, s);
   if (err != hipSuccess) return launched(err, "fp8b_moe_layer: route");
+  err = w8a8::launch_fp8b_quant_schedule(x, T, H, H, scale_alg, q, sc, gl, E, P, chain + C.sched, s);
+  if (err != hipSuccess) return launched(err, "fp8b_moe_layer: quant");
   err = fp8b_chain(q, sc, T, rt, gl, P, E, H, I, w13_packed, w13_scale, w2_packed, w2_scale, scale_alg, y, chain, C,
                    s);
   if (err != hipSuccess) return launched(err, "fp8b_moe_layer: experts");

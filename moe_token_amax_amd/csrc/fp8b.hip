@@ -40,6 +40,90 @@ __device__ __forceinline__ uint16_t to_bf16(float f) {
 }
 
 // ---------------------------------------------------------------------------
+// Schedule of a grouped product: int32 count (256 bytes), then int4 {expert,
+// first row, rows, 0} for every tile of at most kTileRows rows of one expert,
+// in expert order.
+// ---------------------------------------------------------------------------
+constexpr int kTileRows = 128;
+
+int64_t fp8b_max_tiles(int64_t R, int64_t E) { return R / kTileRows + std::min(R, E); }
+int64_t fp8b_sched_bytes(int64_t R, int64_t E) { return 256 + 16 * fp8b_max_tiles(R, E); }
+// column groups of a row tile
+constexpr int kGroupedNBW = 2, kSpreadTiles = 64;
+static int64_t grouped_columns(int64_t N) { return ceil_div(N, 128 * kGroupedNBW); }
+int64_t fp8b_grid_tiles(int64_t R, int64_t E, int64_t N) {
+  return round_up(fp8b_max_tiles(R, E), 8) * grouped_columns(N);
+}
+
+struct Schedule {
+  const int64_t* group_list;
+  int E;  // at most 1024
+  int64_t R;
+  int* count;
+  int4* tiles;
+};
+
+static Schedule schedule_of(const int64_t* group_list, int64_t E, int64_t R, void* ws) {
+  return Schedule{group_list, (int)E, R, reinterpret_cast<int*>(ws),
+                  reinterpret_cast<int4*>(reinterpret_cast<char*>(ws) + 256)};
+}
+
+// by a workgroup of 256 threads, four experts each
+__device__ __forceinline__ void write_schedule(const Schedule& p) {
+  __shared__ int64_t wrows[4];
+  __shared__ int wtiles[4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // counts past R are a caller error: such rows own no tile
+  int64_t n[4], sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    n[i] = 4 * tid + i < p.E ? min(max(p.group_list[4 * tid + i], (int64_t)0), p.R) : 0;
+    sum += n[i];
+  }
+  int64_t ri = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t o = __shfl_up(ri, d, 64);
+    if (lane >= d) ri += o;
+  }
+  if (lane == 63) wrows[wave] = ri;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) ri += wrows[w];
+  ri -= sum;
+  int64_t row0[4];
+  int t = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    row0[i] = min(ri, p.R);
+    ri += n[i];
+    n[i] = min(n[i], p.R - row0[i]);
+    t += (int)((n[i] + kTileRows - 1) / kTileRows);
+  }
+  int ti = t;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(ti, d, 64);
+    if (lane >= d) ti += o;
+  }
+  if (lane == 63) wtiles[wave] = ti;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) ti += wtiles[w];
+  if (tid == 255) *p.count = ti;
+  ti -= t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    for (int64_t r = 0; r < n[i]; r += kTileRows)
+      p.tiles[ti++] = int4{4 * tid + i, (int)(row0[i] + r), (int)min((int64_t)kTileRows, n[i] - r), 0};
+}
+
+__global__ __launch_bounds__(256) void fp8b_schedule_kernel(Schedule p) { write_schedule(p); }
+
+hipError_t launch_fp8b_schedule(const int64_t* group_list, int64_t E, int64_t R, void* ws, hipStream_t stream) {
+  hipLaunchKernelGGL(fp8b_schedule_kernel, dim3(1), dim3(256), 0, stream, schedule_of(group_list, E, R, ws));
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
 // quant
 // ---------------------------------------------------------------------------
 // max over the 16 lanes of a DPP row, in every lane
@@ -131,12 +215,19 @@ __device__ __forceinline__ void load8(const uint16_t* src, int64_t n, float (&v)
 // one 64-byte piece of its [M] line.
 constexpr int kQuantRows = 16;
 
-template <int ACT>
+// SCHED: the first workgroup column writes a grouped product's schedule instead, which
+// saves that launch where both have to run.
+template <int ACT, bool SCHED>
 __global__ __launch_bounds__(256) void fp8b_quant_kernel(const uint16_t* __restrict__ x, int64_t M, int64_t K,
                                                          int64_t ldx, int alg, int KB, int per,
-                                                         uint8_t* __restrict__ q, float* __restrict__ scale) {
+                                                         uint8_t* __restrict__ q, float* __restrict__ scale,
+                                                         Schedule sched) {
+  if (SCHED && blockIdx.x == 0) {
+    if (blockIdx.y == 0) write_schedule(sched);
+    return;
+  }
   const int sub = threadIdx.x & 15;
-  const int64_t row = (int64_t)blockIdx.x * kQuantRows + (threadIdx.x >> 4);
+  const int64_t row = ((int64_t)blockIdx.x - SCHED) * kQuantRows + (threadIdx.x >> 4);
   if (row >= M) return;  // whole 16-lane rows leave together
   const int kb1 = min(KB, ((int)blockIdx.y + 1) * per);
   for (int kb = blockIdx.y * per; kb < kb1; ++kb) {
@@ -157,18 +248,30 @@ __global__ __launch_bounds__(256) void fp8b_quant_kernel(const uint16_t* __restr
   }
 }
 
-hipError_t launch_fp8b_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int act, int scale_alg,
-                             uint8_t* q, float* scale, hipStream_t stream) {
-  if (M == 0) return hipSuccess;
+template <int ACT, bool SCHED>
+static hipError_t launch_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int scale_alg, uint8_t* q,
+                               float* scale, const Schedule& sched, hipStream_t stream) {
   const int KB = (int)ceil_div(K, kFp8Block);
   const int64_t gx = ceil_div(M, kQuantRows);
   // enough workgroups to fill the chip, each with as many blocks as that leaves
   const int64_t gy = std::min<int64_t>(KB, std::max<int64_t>(1, ceil_div(2048, gx)));
   const int per = (int)ceil_div(KB, gy);
-  const dim3 grid((unsigned)gx, (unsigned)ceil_div(KB, per));
-  auto fn = act ? fp8b_quant_kernel<1> : fp8b_quant_kernel<0>;
-  hipLaunchKernelGGL(fn, grid, dim3(256), 0, stream, x, M, K, ldx, scale_alg, KB, per, q, scale);
+  hipLaunchKernelGGL((fp8b_quant_kernel<ACT, SCHED>), dim3((unsigned)(gx + SCHED), (unsigned)ceil_div(KB, per)),
+                     dim3(256), 0, stream, x, M, K, ldx, scale_alg, KB, per, q, scale, sched);
   return hipGetLastError();
+}
+
+hipError_t launch_fp8b_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int act, int scale_alg,
+                             uint8_t* q, float* scale, hipStream_t stream) {
+  if (M == 0) return hipSuccess;
+  return act ? launch_quant<1, false>(x, M, K, ldx, scale_alg, q, scale, Schedule{}, stream)
+             : launch_quant<0, false>(x, M, K, ldx, scale_alg, q, scale, Schedule{}, stream);
+}
+
+hipError_t launch_fp8b_quant_schedule(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int scale_alg, uint8_t* q,
+                                      float* scale, const int64_t* group_list, int64_t E, int64_t R, void* ws,
+                                      hipStream_t stream) {
+  return launch_quant<0, true>(x, M, K, ldx, scale_alg, q, scale, schedule_of(group_list, E, R, ws), stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -253,59 +356,6 @@ __device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& part, float 
 
 __device__ __forceinline__ i32x8 join(const i32x4& x, const i32x4& y) {
   return __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-// Schedule of a grouped product: int32 count (256 bytes), then int4 {expert,
-// first row, rows, 0} for every tile of at most kTileRows rows of one expert,
-// in expert order.
-constexpr int kTileRows = 128;
-
-int64_t fp8b_max_tiles(int64_t R, int64_t E) { return R / kTileRows + std::min(R, E); }
-int64_t fp8b_sched_bytes(int64_t R, int64_t E) { return 256 + 16 * fp8b_max_tiles(R, E); }
-constexpr int kGroupedNBW = 2, kSpreadTiles = 64;
-static int64_t grouped_columns(int64_t N) { return ceil_div(N, 128 * kGroupedNBW); }
-int64_t fp8b_grid_tiles(int64_t R, int64_t E, int64_t N) {
-  return round_up(fp8b_max_tiles(R, E), 8) * grouped_columns(N);
-}
-
-__global__ __launch_bounds__(1024) void fp8b_schedule_kernel(const int64_t* __restrict__ gl, int E, int64_t R,
-                                                             int* __restrict__ count, int4* __restrict__ tiles) {
-  __shared__ int64_t wrows[16];
-  __shared__ int wtiles[16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  // counts past R are a caller error: such rows own no tile
-  const int64_t n = tid < E ? min(max(gl[tid], (int64_t)0), R) : 0;
-  int64_t ri = n;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t o = __shfl_up(ri, d, 64);
-    if (lane >= d) ri += o;
-  }
-  if (lane == 63) wrows[wave] = ri;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) ri += wrows[w];
-  const int64_t row0 = min(ri - n, R);
-  const int64_t rows = min(n, R - row0);
-  const int t = (int)((rows + kTileRows - 1) / kTileRows);
-  int ti = t;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(ti, d, 64);
-    if (lane >= d) ti += o;
-  }
-  if (lane == 63) wtiles[wave] = ti;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) ti += wtiles[w];
-  for (int i = 0; i < t; ++i)
-    tiles[ti - t + i] = int4{tid, (int)(row0 + (int64_t)i * kTileRows),
-                             (int)min((int64_t)kTileRows, rows - (int64_t)i * kTileRows), 0};
-  if (tid == 1023) *count = ti;
-}
-
-hipError_t launch_fp8b_schedule(const int64_t* group_list, int64_t E, int64_t R, void* ws, hipStream_t stream) {
-  hipLaunchKernelGGL(fp8b_schedule_kernel, dim3(1), dim3(1024), 0, stream, group_list, (int)E, R,
-                     reinterpret_cast<int*>(ws), reinterpret_cast<int4*>(reinterpret_cast<char*>(ws) + 256));
-  return hipGetLastError();
 }
 
 #define W8A8_LDS __attribute__((address_space(3)))

@@ -46,6 +46,10 @@ struct Fp8bGemm {
 int64_t fp8b_sched_bytes(int64_t R, int64_t E);
 int64_t fp8b_grid_tiles(int64_t R, int64_t E, int64_t N);  // workgroups of a grouped product's launch
 hipError_t launch_fp8b_schedule(const int64_t* group_list, int64_t E, int64_t R, void* ws, hipStream_t stream);
+// launch_fp8b_quant (act 0) of M >= 1 rows and launch_fp8b_schedule in one launch
+hipError_t launch_fp8b_quant_schedule(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int scale_alg, uint8_t* q,
+                                      float* scale, const int64_t* group_list, int64_t E, int64_t R, void* ws,
+                                      hipStream_t stream);
 hipError_t launch_fp8b_gemm(const Fp8bGemm& p, hipStream_t stream);
 bool fp8b_fused_ok(int64_t M, int64_t K);
 hipError_t launch_fp8b_linear_fused(const Fp8bGemm& p, hipStream_t stream);

@@ -50,7 +50,7 @@ def _quant(L, x=P, M=4, K=64, ldx=64, act=0, alg=0, q=P, s=P):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(M=-1), SHAPE), (dict(K=0), SHAPE), (dict(K=200000, ldx=200000), SHAPE), (dict(M=1 << 30), SHAPE), (dict(M=1 << 28), SHAPE),
+    (dict(M=-1), SHAPE), (dict(K=0), SHAPE), (dict(K=200000, ldx=200000), SHAPE), (dict(M=1 << 30), SHAPE), (dict(M=(1 << 28) - 16), SHAPE),
     (dict(ldx=63), SHAPE), (dict(act=1, ldx=127), SHAPE), (dict(act=2), UNSUPPORTED), (dict(alg=2), UNSUPPORTED),
     (dict(x=None), NULL), (dict(q=None), NULL), (dict(s=None), NULL), (dict(x=ODD), ALIGN),
     (dict(q=ctypes.c_void_p(264)), ALIGN), (dict(s=ODD), ALIGN), (dict(M=0, x=None, q=None, s=None), OK)])
