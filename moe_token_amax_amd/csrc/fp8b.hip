@@ -195,18 +195,31 @@ struct __attribute__((packed, aligned(2))) Bytes8 {
   uint32_t w[2];
 };
 
-// 8 values from src, n of them in the row (0 past it)
-__device__ __forceinline__ void load8(const uint16_t* src, int64_t n, float (&v)[8]) {
+// 8 values from src, n of them in the row (0 past it), and with PAIR 8 more from
+// src + next (under one branch, so that both loads are in flight together)
+template <bool PAIR>
+__device__ __forceinline__ void load8(const uint16_t* src, int64_t next, int64_t n, float (&v)[8], float (&u)[8]) {
+  Bytes16 a{}, b{};
   if (n >= 8) {
-    const Bytes16 u = *reinterpret_cast<const Bytes16*>(src);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(u.w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(u.w[j] & 0xFFFF0000u);
-    }
+    a = *reinterpret_cast<const Bytes16*>(src);
+    if (PAIR) b = *reinterpret_cast<const Bytes16*>(src + next);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? bf16_to_f32(src[j]) : 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      if (j < n) {
+        a.w[j / 2] |= (uint32_t)src[j] << (16 * (j & 1));
+        if (PAIR) b.w[j / 2] |= (uint32_t)src[next + j] << (16 * (j & 1));
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(a.w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(a.w[j] & 0xFFFF0000u);
+    if (PAIR) {
+      u[2 * j] = __uint_as_float(b.w[j] << 16);
+      u[2 * j + 1] = __uint_as_float(b.w[j] & 0xFFFF0000u);
+    }
   }
 }
 
@@ -233,11 +246,9 @@ __global__ __launch_bounds__(256) void fp8b_quant_kernel(const uint16_t* __restr
   for (int kb = blockIdx.y * per; kb < kb1; ++kb) {
     const int64_t k0 = (int64_t)kb * kFp8Block + sub * 8;
     const uint16_t* src = x + row * ldx + k0;
-    float v[8];
-    load8(src, K - k0, v);
+    float v[8], u[8];
+    load8<ACT == 1>(src, K, K - k0, v, u);
     if (ACT == 1) {
-      float u[8];
-      load8(src + K, K - k0, u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = swiglu_fixed(v[j], u[j]);
     }
@@ -951,8 +962,8 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fp8b_decode_kernel(Fp8bGemm
     for (int b = tid >> 4; b < M * KB; b += kDecodeWaves * 4) {
       const int r = b / KB, kb = b % KB;
       const int64_t k0 = (int64_t)kb * kFp8Block + sub * 8;
-      float v[8];
-      load8(x + r * p.lda + k0, p.K - k0, v);
+      float v[8], none[8];
+      load8<false>(x + r * p.lda + k0, 0, p.K - k0, v, none);
       float s;
       const uint2 q = quant_block(v, p.scale_alg, s);
       *reinterpret_cast<uint2*>(qlds + r * (KB * 128) + k0) = q;
