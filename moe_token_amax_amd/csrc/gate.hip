@@ -214,13 +214,30 @@ __device__ void gate_exact(const GateArgs& g, int64_t t, int lane) {
 // (a launch lasts as long as its slowest wavefront: with every close choice left to
 // gate_exact, 2048 tokens took 15.8 us instead of 7.2 and 16384 took 21.7, not 15.8).
 // Without a bias the order of keys is the order of logits, which are compared as
-// they are; doubles saturate (1 from l = 37 on, 0 under -745), so logits past 36
-// or a selected one 700 under the maximum (softmax) or -700 (sigmoid) fall back
-// too.
+// they are, as far as doubles tell the keys of distinct logits apart (unsure_logit);
+// a selected one 700 under the maximum (softmax) or under -700 (sigmoid), where
+// doubles run out, falls back.
 // The weights come from the selected logits alone, in doubles; only the sum of a
 // softmax that is not renormalized is a float sum.
 // ---------------------------------------------------------------------------
 constexpr float kNearSigmoid = 0x1p-20f, kNearSoftmax = 0x1p-19f;
+
+// Whether doubles may give logit x the key of another logit, so that the lower index
+// would win and not the larger logit. Sigmoids: logits d apart have scores at least
+// d exp(-x) / 4 apart (x >= 0) or a share of d / 2 (x < 0). Distinct floats of magnitude
+// 2^-16 and more are 2^-40 apart and more, from 8 on 2^-20, from 16 on 2^-19, so up to
+// x = 20 scores are 2^-50 apart, eight steps of doubles under 1; from 23 on neighbours
+// meet. Softmax: l - max, above -700 (below: see there), is rounded by 2^-44 at most,
+// and so distinct floats of magnitude 2^-16 and more keep scores that differ by a share
+// of 2^-41; those next to 0 may be absorbed.
+__device__ __forceinline__ bool unsure_logit(float x, bool sigmoid) {
+  return (sigmoid && x > 20.f) || fabsf(x) < 0x1p-16f;
+}
+// a > b, a unsure: whether doubles tell their keys apart all the same (sigmoids of 19
+// and of anything past 20 differ by 2^-29; 2^-30 next to 0 is 2^-32 in the scores)
+__device__ __forceinline__ bool keys_apart(float a, float b, bool sigmoid) {
+  return sigmoid && a > 20.f ? b <= 19.f : a - b > 0x1p-30f;
+}
 
 // order-preserving map of finite floats and +inf to integers above 0 (0: out)
 __device__ __forceinline__ uint32_t key_bits(float f) {
@@ -526,7 +543,23 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
     if (!sigmoid && lane < k) close = close || swap;
   } else {
     const float first = need_scores && !sigmoid ? top : readlane_f(sel, 0);
-    if (lane < k && id >= 0) close = close || (sigmoid ? sel > 36.f || sel < -700.f : sel - first < -700.f);
+    const bool chosen = lane < k && id >= 0;
+    if (chosen) close = close || (sigmoid ? sel < -700.f : sel - first < -700.f);
+    const bool unsure = chosen && unsure_logit(sel, sigmoid);
+    const uint64_t any = __ballot(unsure);
+    if (any) {  // uniform
+      const int n = __shfl_down(id, 1, kWave);
+      const float nl = __shfl_down(sel, 1, kWave);
+      if (unsure && lane < k - 1 && n >= 0 && nl != sel && !keys_apart(sel, nl, sigmoid)) close = true;
+      if (any >> (k - 1) & 1) {  // the last of the list against what is left
+        const float last = readlane_f(sel, k - 1);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          const float v = key_value(u[i]);
+          if (u[i] && v != last && !keys_apart(last, v, sigmoid)) close = true;
+        }
+      }
+    }
   }
   const uint64_t pairs = __ballot(swap);
   const bool order = biased && sigmoid && k <= 14 && (pairs & ((1ull << k) - 1)) != 0;  // uniform
@@ -786,6 +819,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
   }
   const float sel = id >= 0 ? fminf(load_logit<DT>(g.logits, t * g.ld + id), 3.402823466e38f) : 0.f;
   const float bj = biased && id >= 0 ? g.bias[id] : 0.f;
+  const bool chosen = sub < k && id >= 0;
   bool swap = false;  // lane j: too close to lane j + 1 of the token, other than equal inside the list
   if (biased) {
     const float v = key_value(kb);
@@ -796,7 +830,23 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     if (!sigmoid && sub < k) close = close || swap;
   } else {
     const float first = need_scores && !sigmoid ? top : __shfl(sel, lane & 48, kWave);
-    if (sub < k && id >= 0) close = close || (sigmoid ? sel > 36.f || sel < -700.f : sel - first < -700.f);
+    if (chosen) close = close || (sigmoid ? sel < -700.f : sel - first < -700.f);
+    const bool unsure = chosen && unsure_logit(sel, sigmoid);
+    const uint64_t any = __ballot(unsure);
+    if (any) {  // uniform
+      const int n = __shfl_down(id, 1, 16);
+      const float nl = __shfl_down(sel, 1, 16);
+      if (unsure && sub < k - 1 && n >= 0 && nl != sel && !keys_apart(sel, nl, sigmoid)) close = true;
+      // the last of the list against what is left of the token
+      const float last = __shfl(sel, (lane & 48) + k - 1, kWave);
+      if (any >> ((lane & 48) + k - 1) & 1) {
+        for (int i = 0; i < P; ++i) {
+          const uint32_t left = mine[i];
+          const float v = key_value(left);
+          if (left && v != last && !keys_apart(last, v, sigmoid)) close = true;
+        }
+      }
+    }
   }
   const uint64_t all = __ballot(swap);
   if (sigmoid && biased) {
@@ -805,7 +855,6 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     close = close || (pairs >> (k - 1) & 3) == 3;
   }
   double w = 0.0;
-  const bool chosen = sub < k && id >= 0;
   if (sigmoid) {
     if (sub <= k && id >= 0) w = 1.0 / (1.0 + exp(-(double)sel));
     if (biased && all) settle_row(id, w, w + (double)bj, k, lane);  // uniform

@@ -254,3 +254,73 @@ def test_gate_on_another_stream(w):
         b = w.moe_gate(l, 8, scoring=w.GATE_SIGMOID, n_group=8, topk_group=4)
     sync()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# ------------------------------------------------------------------ logits that doubles cannot tell apart
+TINY = np.array([0.0, -0.0, 1e-17, -1e-17, 2e-17, 3e-18, -5e-20, 1e-30, 1.4e-45])  # 1 + exp(-x) = 2 for each
+
+
+@pytest.mark.parametrize("T", [64, 5200])
+@pytest.mark.parametrize("G,keep", [(1, 1), (4, 2), (4, 4)])
+@pytest.mark.parametrize("k", [1, 2, 8, 16])
+def test_gate_distinct_logits_of_equal_sigmoids(w, T, k, G, keep):
+    """Without a bias the order of keys is that of the logits only as far as doubles tell
+    their sigmoids apart: past 23 or so, and next to 0, distinct logits have equal scores,
+    which go to the lower index, inside the list and across its end."""
+    rng = np.random.default_rng(1000 * k + G + keep)
+    E = 64
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    for r in range(T):
+        n = int(rng.integers(1, E + 1))
+        at = rng.permutation(E)[:n]
+        kind = r % 6
+        if kind == 0:                                    # anywhere in the range where they start to meet
+            l[r, at] = rng.uniform(18.0, 38.0, n)
+        elif kind == 1:                                  # neighbours of one value
+            l[r, at] = _nudge(np.full(n, rng.uniform(19.0, 37.0), np.float32), rng.integers(-4, 5, n))
+        elif kind == 2:                                  # steps of BF16 in that range
+            l[r, at] = 30.0 + 0.25 * rng.integers(0, 28, n)
+        elif kind == 3:                                  # one alone, the rest far below
+            l[r, at[0]] = rng.uniform(20.0, 40.0)
+        elif kind == 4:                                  # next to 0, everything else below
+            l[r] = -1.0 - np.abs(l[r])
+            l[r, at] = rng.choice(TINY, n)
+        else:                                            # next to 0 below a few others
+            l[r, at] = rng.choice(TINY, n)
+    _check(w, torch.from_numpy(l), k, None, "sigmoid", G, keep)
+    _check(w, torch.from_numpy(l), k, None, "sigmoid", G, keep, False, 2.5)
+    _check(w, torch.from_numpy(l).to(torch.bfloat16), k, None, "sigmoid", G, keep)
+
+
+@pytest.mark.parametrize("T", [64, 5200])
+@pytest.mark.parametrize("G,keep", [(1, 1), (4, 2)])
+@pytest.mark.parametrize("k", [1, 2, 8, 16])
+def test_gate_distinct_logits_of_equal_softmax_scores(w, T, k, G, keep):
+    """Logits that the difference to the maximum absorbs, as the maximum and below it."""
+    rng = np.random.default_rng(2000 * k + G)
+    E = 64
+    l = -1.0 - np.abs(rng.standard_normal((T, E))).astype(np.float32)
+    for r in range(T):
+        n = int(rng.integers(1, E + 1))
+        at = rng.permutation(E)[:n]
+        l[r, at] = rng.choice(TINY, n)
+        if r % 3 == 1:
+            l[r, at[0]] = rng.uniform(1.0, 90.0)
+        if r % 3 == 2:
+            l[r] = np.where(np.isin(np.arange(E), at), l[r], -np.inf)
+    for renorm in (True, False):
+        _check(w, torch.from_numpy(l), k, None, "softmax", G, keep, renorm)
+    _check(w, torch.from_numpy(l).to(torch.bfloat16), k, None, "softmax", G, keep)
+
+
+@pytest.mark.parametrize("T", [1, 5120])
+def test_gate_saturated_pair_goes_to_the_lower_index(w, T):
+    """sigmoid(34) and sigmoid(34.01) are one double: expert 3, whatever else decides the path taken."""
+    l = np.full((T, 64), -1.0, np.float32)
+    l[:, 3], l[:, 7] = 34.0, 34.01
+    for k in (1, 2):
+        ids, wts = w.moe_gate(dev(l), k, scoring=w.GATE_SIGMOID)
+        zero, _ = w.moe_gate(dev(l), k, scoring=w.GATE_SIGMOID, bias=torch.zeros(64, device=DEV))
+        sync()
+        assert (host(ids) == np.array([3, 7])[:k]).all() and torch.equal(ids, zero)
+        assert (host(wts) == np.float32(1.0 / k)).all()
