@@ -270,6 +270,14 @@ __device__ __forceinline__ void segment_top2(float& a, float& b, int seg) {
   if (seg >= 64) merge2(a, b, __shfl_xor(a, 32, kWave), __shfl_xor(b, 32, kWave));
 }
 
+// A group's mark from its two largest keys: their sum, the one that is in, or out. Lost:
+// both are in and the sum is below the floats; it then stands with the groups that are out.
+// Which of those stay takes doubles, unless only marks clear of that range do.
+__device__ __forceinline__ bool mark_lost(float mark, float b) {
+  return b > -__builtin_huge_valf() && mark == -__builtin_huge_valf();
+}
+__device__ __forceinline__ bool mark_clear(float last_that_stays) { return last_that_stays > -1e38f; }
+
 // sum of P floats (a power of two) with log2 P roundings
 template <int P>
 __device__ __forceinline__ float tree_sum(const float (&v)[P]) {
@@ -498,6 +506,7 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
           close = false;
         }
       }
+      if (mark_lost(mark, b) && !mark_clear(x)) close = true;
     }
     if (!(group && rank < g.topk_group)) {
 #pragma unroll
@@ -779,6 +788,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
         if (border && (dy > dx || (dy == dx && gy < gx))) rank = 2 * g.topk_group - 1 - rank;
         close = close && !pair;
       }
+      if (mark_lost(mark, b) && !mark_clear(x)) close = true;  // x NaN: fewer marks than groups that stay
     }
     const bool stays = real && rank < g.topk_group;
 #pragma unroll

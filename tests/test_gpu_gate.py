@@ -324,3 +324,21 @@ def test_gate_saturated_pair_goes_to_the_lower_index(w, T):
         sync()
         assert (host(ids) == np.array([3, 7])[:k]).all() and torch.equal(ids, zero)
         assert (host(wts) == np.float32(1.0 / k)).all()
+
+
+@pytest.mark.parametrize("T", [64, 5200])
+@pytest.mark.parametrize("keep", [1, 2, 3])
+@pytest.mark.parametrize("scoring", ["sigmoid", "softmax"])
+def test_gate_group_marks_past_the_float_range(w, T, scoring, keep):
+    """Two keys whose sum a float does not hold: a group of them is in, below groups whose
+    sum is larger and above groups that have no expert."""
+    rng = np.random.default_rng(keep)
+    E, G, per = 64, 4, 16
+    low = float(np.finfo(np.float32).min)
+    for order in ([-3e38, -2e38, low, 0.0], [low, low, -3e38, -2.5e38], [0.0, low, -2e38, -3e38], [-2e38, 3e38, low, 3e38]):
+        b = np.repeat(np.array(order), per)
+        l = rng.standard_normal((T, E)).astype(np.float32)
+        for g in range(G):                               # groups without an expert, and with one
+            l[g::7, g * per:(g + 1) * per] = -np.inf
+            l[g + 1::9, g * per:(g + 1) * per - 1] = -np.inf
+        _check(w, torch.from_numpy(l), 5, b, scoring, G, keep)
