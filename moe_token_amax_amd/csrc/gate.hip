@@ -216,7 +216,7 @@ __device__ void gate_exact(const GateArgs& g, int64_t t, int lane) {
 // Without a bias the order of keys is the order of logits, which are compared as
 // they are, as far as doubles tell the keys of distinct logits apart (unsure_logit);
 // a selected one 700 under the maximum (softmax) or under -700 (sigmoid), where
-// doubles run out, falls back.
+// doubles run out, falls back, and with a bias a softmax whose selected are all there.
 // The weights come from the selected logits alone, in doubles; only the sum of a
 // softmax that is not renormalized is a float sum.
 // ---------------------------------------------------------------------------
@@ -238,6 +238,11 @@ __device__ __forceinline__ bool unsure_logit(float x, bool sigmoid) {
 __device__ __forceinline__ bool keys_apart(float a, float b, bool sigmoid) {
   return sigmoid && a > 20.f ? b <= 19.f : a - b > 0x1p-30f;
 }
+
+// The scores of a softmax whose logits are all at most ref, 700 under the maximum, run out
+// of doubles: their sum may be 0, and then so are the weights. (Chosen by the bias; without
+// one the order of keys is in doubt there as well.)
+__device__ __forceinline__ bool scores_vanish(float ref, float top) { return ref - top < -700.f; }
 
 // order-preserving map of finite floats and +inf to integers above 0 (0: out)
 __device__ __forceinline__ uint32_t key_bits(float f) {
@@ -553,7 +558,7 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
   } else {
     const float first = need_scores && !sigmoid ? top : readlane_f(sel, 0);
     const bool chosen = lane < k && id >= 0;
-    if (chosen) close = close || (sigmoid ? sel < -700.f : sel - first < -700.f);
+    if (chosen) close = close || (sigmoid ? sel < -700.f : scores_vanish(sel, first));
     const bool unsure = chosen && unsure_logit(sel, sigmoid);
     const uint64_t any = __ballot(unsure);
     if (any) {  // uniform
@@ -583,6 +588,7 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
     // renormalized: the largest selected logit stands for the maximum
     const bool mine = lane < k && id >= 0;
     const float ref = g.renormalize ? wave_top(mine ? key_bits(sel) : 0u) : top;
+    if (biased && scores_vanish(ref, top)) return false;  // uniform
     if (mine) w = exp((double)sel - (double)ref);
   }
   if (g.renormalize) {
@@ -840,7 +846,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     if (!sigmoid && sub < k) close = close || swap;
   } else {
     const float first = need_scores && !sigmoid ? top : __shfl(sel, lane & 48, kWave);
-    if (chosen) close = close || (sigmoid ? sel < -700.f : sel - first < -700.f);
+    if (chosen) close = close || (sigmoid ? sel < -700.f : scores_vanish(sel, first));
     const bool unsure = chosen && unsure_logit(sel, sigmoid);
     const uint64_t any = __ballot(unsure);
     if (any) {  // uniform
@@ -872,6 +878,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
   } else {
     const uint32_t tb = row_max(chosen ? key_bits(sel) : 0u);
     const float ref = g.renormalize ? (tb ? key_value(tb) : 0.f) : top;
+    if (biased && scores_vanish(ref, top)) close = true;
     if (chosen) w = exp((double)sel - (double)ref);
   }
   if (g.renormalize) {

@@ -342,3 +342,20 @@ def test_gate_group_marks_past_the_float_range(w, T, scoring, keep):
             l[g::7, g * per:(g + 1) * per] = -np.inf
             l[g + 1::9, g * per:(g + 1) * per - 1] = -np.inf
         _check(w, torch.from_numpy(l), 5, b, scoring, G, keep)
+
+
+@pytest.mark.parametrize("T", [64, 5200])
+@pytest.mark.parametrize("G,keep", [(1, 1), (4, 2)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gate_softmax_chosen_by_the_bias_far_below_the_maximum(w, T, G, keep, renorm):
+    """The bias moves the choice to experts whose scores are 0 or next to it: their sum is 0, and
+    so are the weights."""
+    rng = np.random.default_rng(G)
+    E, k = 64, 4
+    l = rng.standard_normal((T, E)).astype(np.float32)
+    b = 0.1 * rng.standard_normal(E)
+    b[5] = -9.0
+    for r, top in enumerate((600.0, 695.0, 700.5, 710.0, 722.0, 760.0, 1000.0, 3e38)):
+        l[r::9, 5] = top
+    b[E // 4:] -= 1.0                                    # the group of expert 5 is chosen
+    _check(w, torch.from_numpy(l), k, b, "softmax", G, keep, renorm)
