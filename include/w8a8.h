@@ -630,8 +630,10 @@ int w8a8_moe_gate(const void* logits, int dtype, int64_t T, int64_t E, int64_t l
  *   w8a8_swiglu_quant; scale = max|v| / 448 over the block, the code is E4M3
  *   (half to even, saturating at 448) of v / scale, both one IEEE fp32
  *   division; a block of zeros gets scale 0 and codes 0. scale_alg 1 takes the
- *   smallest power of two (at least 2^-126) not below max|v| / 448 instead. A
- *   NaN or infinity in a block makes its scale NaN or infinite.
+ *   smallest power of two (at least 2^-126) not below max|v| / 448 instead. An
+ *   infinity in a block makes its scale infinite, its own code NaN (0x7F or
+ *   0xFF) and the codes of finite values 0; a NaN makes the scale NaN and every
+ *   code of the block 0. Either way every product with the block is NaN.
  * w8a8_fp8b_packed_bytes / w8a8_fp8b_prepack_weight: E4M3 codes w [E, N, K] ->
  *   the load-time layout of the products: 2 KB blocks [e][n/16][k/128] of two
  *   1 KB pieces, byte 16 l + j of piece h = w[16 (n/16) + l % 16][128 (k/128) +

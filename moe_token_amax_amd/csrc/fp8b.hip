@@ -179,7 +179,11 @@ __device__ __forceinline__ uint2 quant_block(const float (&v)[8], int alg, float
     for (int j = 0; j < 8; ++j) t[j] = quotient(v[j], s, y);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = s > 0.0f ? fminf(fmaxf(v[j] / s, -448.0f), 448.0f) : 0.0f;
+    for (int j = 0; j < 8; ++j) {
+      t[j] = s > 0.0f ? v[j] / s : 0.0f;  // s NaN: 0
+      // an infinity over its infinite scale stays NaN (the limits alone would make it -448)
+      if (!__builtin_isnan(t[j])) t[j] = fminf(fmaxf(t[j], -448.0f), 448.0f);
+    }
   }
   return pack_codes(t);
 }

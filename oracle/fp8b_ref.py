@@ -8,8 +8,8 @@ of the activations, the sum over blocks and the router are this library's own
 definitions (parity unpinned beyond them).
 
   quant    per row and 128 columns: s = fl32(amax / 448), code = E4M3(fl32(v / s)),
-           half to even, saturating; zeros for s = 0. scale_alg 1: s rounded up to a
-           power of two, at least 2^-126.
+           half to even, saturating, NaN of NaN; zeros for s = 0 and s NaN.
+           scale_alg 1: a finite s rounded up to a power of two, at least 2^-126.
   product  float64: sum over blocks of s_x s_w times the exact sum of code products.
   gate     see ``gate``; everything in float64.
 
@@ -51,11 +51,13 @@ def quant(x_bits, act: int = 0, scale_alg: int = 0):
     if scale_alg == 1:
         m, e = np.frexp(s.astype(np.float64))            # s = m 2^e, m in [0.5, 1)
         e = np.where(m == 0.5, e - 1, e)
-        s = np.where(s > 0, np.ldexp(1.0, np.maximum(e, -126)), 0.0).astype(np.float32)
+        up = np.where(s > 0, np.ldexp(1.0, np.maximum(e, -126)), 0.0).astype(np.float32)
+        s = np.where(np.isfinite(s), up, s)
     with np.errstate(divide="ignore", invalid="ignore"):
         t = (full / s[..., None]).astype(np.float32)
     t = np.where(s[..., None] > 0, t, np.float32(0.0))
-    return e4m3_encode(t).reshape(M, B * BLOCK), np.ascontiguousarray(s.T)
+    codes = np.where(np.isnan(t), np.uint8(0x7F), e4m3_encode(t))   # an infinity over its infinite scale
+    return codes.reshape(M, B * BLOCK), np.ascontiguousarray(s.T)
 
 
 def dequant(q, s):

@@ -520,3 +520,49 @@ def test_two_streams_with_their_own_workspaces(w):
     sync()
     for i in range(2):
         assert all(torch.equal(want[i], g) for g in got[i])
+
+
+# ------------------------------------------------------------------ infinities
+@pytest.mark.parametrize("alg", [0, 1])
+@pytest.mark.parametrize("sign", [0x0000, 0x8000])
+def test_quant_infinity_is_a_nan_code(w, sign, alg):
+    """An infinite value makes its block's scale infinite: v / scale is NaN for it and 0 for the
+    finite values of the block. A block with a NaN has scale NaN and codes 0."""
+    rng = np.random.default_rng(7)
+    x = _acts(rng, 5, 300)
+    x[1, 130] = 0x7F80 | sign
+    x[2, [0, 9]] = 0x7F80 | sign
+    x[3, 299] = 0x7FC0 | sign
+    for act, xs in ((0, x), (1, np.concatenate([x, np.full((5, 300), 0x3F80, np.uint16)], 1))):
+        q, s = w.fp8b_quant(bf16_dev(xs), act=act, scale_alg=alg)
+        sync()
+        q, s = host(q), host(s)
+        qo, so = F.quant(xs, act, alg)
+        if not (act and sign):                           # silu(-inf) is NaN in the fixed sequence
+            assert np.isinf(s[1, 1]) and (q[1, 130] & 0x7F) == 0x7F and not (np.delete(q[1, 128:256], 2) & 0x7F).any()
+            assert np.isinf(s[0, 2]) and (q[2, [0, 9]] & 0x7F == 0x7F).all() and not (q[2, 1:9] & 0x7F).any()
+        assert np.isnan(s[2, 3]) and not (q[3, 256:] & 0x7F).any()
+        nan = (qo & 0x7F) == 0x7F
+        assert np.array_equal(s, so, equal_nan=True) and np.array_equal((q & 0x7F) == 0x7F, nan)
+        assert np.array_equal(q[~nan], qo[~nan])
+
+
+@pytest.mark.parametrize("M", [5, 40, 300])
+def test_linear_infinite_activation_gives_nan(w, M):
+    """The codes of an infinity are NaN, and so is every output of its row; no other row feels it."""
+    rng = np.random.default_rng(M)
+    x = _acts(rng, M, 256)
+    cw, sw = _weight(rng, 40, 256)
+    wp, swd = w.fp8b_prepack_weight(dev(cw)), dev(sw)
+    clean = w.fp8b_linear(bf16_dev(x), wp, swd, 40)
+    x[3, 10], x[4, 200] = 0x7F80, 0xFF80
+    y = w.fp8b_linear(bf16_dev(x), wp, swd, 40)
+    q, s = w.fp8b_quant(bf16_dev(x))
+    z = w.fp8b_grouped_gemm(q, s, dev(np.array([M], np.int64)), wp, swd[None], 40, exact=True)
+    sync()
+    for v in (y, z):
+        v = v.float().cpu().numpy()
+        assert np.isnan(v[[3, 4]]).all()
+        assert np.isfinite(np.delete(v, [3, 4], 0)).all()
+    keep = np.delete(np.arange(M), [3, 4])
+    assert np.array_equal(bf16_host(y)[keep], bf16_host(clean)[keep])

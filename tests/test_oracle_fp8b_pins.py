@@ -97,3 +97,14 @@ def test_gate_against_torch():
     assert np.array_equal(top.numpy(), ids)
     p = s.gather(1, top)
     assert np.allclose((p / p.sum(1, keepdim=True)).numpy(), w, rtol=1e-14)
+
+
+def test_quant_infinity_and_nan():
+    x = np.zeros((3, 128), np.uint16)
+    x[0, :3] = [0x7F80, 0x3F80, 0xBF80]                       # inf, 1, -1
+    x[1, :2] = [0x3F80, 0xFF80]
+    x[2, :2] = [0x7FC0, 0x3F80]
+    for alg in (0, 1):
+        q, s = F.quant(x, 0, alg)
+        assert np.isinf(s[0, :2]).all() and np.isnan(s[0, 2])
+        assert q[0, 0] == 0x7F and q[1, 1] == 0x7F and not (q[0, 1:] & 0x7F).any() and not q[1, 0] and not q[2].any()
