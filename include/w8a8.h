@@ -600,7 +600,7 @@ int w8a8_w4a16_moe_grouped(int fmt, const uint16_t* x_rows, const int64_t* group
  * compared as doubles, weights rounded once to float; only the sum of a softmax
  * that is not renormalized is one of floats.
  * 1 <= E <= 1024, n_group <= 64 dividing E, top_k <= 64 and no more than the
- * experts of topk_group groups, T < 2^26, T * top_k < 2^31, scale finite.
+ * experts of topk_group groups, T <= 2^26 - 4, T * top_k < 2^31, scale finite.
  */
 typedef enum {
   W8A8_DT_F32 = 0,
@@ -669,10 +669,11 @@ int w8a8_moe_gate(const void* logits, int dtype, int64_t T, int64_t E, int64_t l
  *   once, route (w8a8_moe_route), the chain with the tokens' rows read through
  *   the routing, combine (w8a8_moe_combine). topk_ids, topk_weights as
  *   w8a8_moe_gate writes them.
- * 1 <= K, H, I <= W8A8_MAX_K, N, 2I <= 2^22, M, R, T * top_k < 2^28 - 16, T <
- * 2^24 (layer), and a grouped product of fewer than 2^23 tiles of 128 rows x 256
- * columns. Workspaces 256-byte aligned and rewritten by every call: two calls
- * that may overlap need two.
+ * 1 <= K, H, I <= W8A8_MAX_K, N, 2I <= 2^22, M, R, T * top_k < 2^28 - 16 (R <=
+ * 2^28 - 32 for BF16 rows through the chain), T < 2^24 (layer), and a grouped
+ * product of fewer than 2^23 tiles of 128 rows x 256 columns. Workspaces
+ * 256-byte aligned and rewritten by every call: two calls that may overlap need
+ * two.
  */
 int w8a8_fp8b_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int act, int scale_alg, uint8_t* q,
                     float* scale, void* stream);

@@ -1000,9 +1000,9 @@ int w8a8_w4a16_linear(const uint16_t* x, int64_t M, int64_t K, const void* w_pac
 int w8a8_moe_gate(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int scoring,
                   int64_t n_group, int64_t topk_group, int64_t top_k, int renormalize, float scale,
                   int32_t* topk_ids, float* topk_weights, void* stream) {
-  // 64 threads a token of a launch of fewer than 2^32
-  if (T < 0 || T >= (int64_t)1 << 26 || E < 1 || top_k < 1 || ld < E)
-    return fail(W8A8_ERR_SHAPE, "moe_gate: need 0 <= T < 2^26, E >= 1, ld >= E and top_k >= 1");
+  // workgroups of 256 threads, four tokens each, in a launch of fewer than 2^32 threads
+  if (T < 0 || T > ((int64_t)1 << 26) - 4 || E < 1 || top_k < 1 || ld < E)
+    return fail(W8A8_ERR_SHAPE, "moe_gate: need 0 <= T <= 2^26 - 4, E >= 1, ld >= E and top_k >= 1");
   if (dtype != W8A8_DT_F32 && dtype != W8A8_DT_BF16 && dtype != W8A8_DT_F16)
     return fail(W8A8_ERR_UNSUPPORTED, "moe_gate: unknown logit type %d", dtype);
   if (scoring != W8A8_GATE_SOFTMAX && scoring != W8A8_GATE_SIGMOID)
@@ -1050,7 +1050,7 @@ constexpr int64_t kFp8MaxN = (int64_t)1 << 22;  // columns: the tile grids stay 
 int64_t fp8b_pad(int64_t K) { return w8a8::round_up(K, w8a8::kFp8Block); }
 int64_t fp8b_kb(int64_t K) { return w8a8::ceil_div(K, w8a8::kFp8Block); }
 
-// rows: launches of fewer than 2^32 threads, at most 16 a row and a workgroup more
+// rows: launches of fewer than 2^32 threads, at most 16 a row in workgroups of 256
 constexpr int64_t kFp8MaxM = ((int64_t)1 << 28) - 16;
 
 int check_fp8b(const char* who, int64_t M, int64_t N, int64_t K) {
@@ -1278,6 +1278,8 @@ int w8a8_fp8b_moe_grouped(const void* x_rows, const float* x_scale, const int64_
   if (st) return st;
   st = check_fp8b_grouped("fp8b_moe_grouped", R, E, H, I);
   if (st) return st;
+  if (!x_scale && R > kFp8MaxM - 16)  // the quantizer's launch has a workgroup more, for the tile list
+    return fail(W8A8_ERR_SHAPE, "fp8b_moe_grouped: need R <= 2^28 - 32 BF16 rows, got %lld", (long long)R);
   st = check_scale_alg("fp8b_moe_grouped", scale_alg);
   if (st) return st;
   if (R == 0) return ok();

@@ -155,3 +155,17 @@ def test_kernels_keep_out_of_scratch(src, tmp_path):
         loops = _innermost_mfma_loops(lines)
         assert loops
         assert not [1 for a, b in loops for x in lines[a:b + 1] if "scratch_" in x]
+
+
+def test_one_workgroup_too_many_is_refused(w):
+    """Sizes whose launch would have exactly 2^32 threads; one less passes this check (and fails a
+    later one: nothing is launched here)."""
+    assert _gate(w.lib, T=(1 << 26) - 3, logits=None) == SHAPE and _gate(w.lib, T=(1 << 26) - 1, logits=None) == SHAPE
+    assert _gate(w.lib, T=(1 << 26) - 4, logits=None) == NULL
+
+    def chain(R, xs=None):
+        return w.lib.w8a8_fp8b_moe_grouped(P, xs, P, R, 4, 64, 32, P, P, P, P, 0, P, P, 64, None)
+
+    assert chain((1 << 28) - 17) == SHAPE and chain((1 << 28) - 31) == SHAPE
+    assert chain((1 << 28) - 32) == WORKSPACE and chain((1 << 28) - 17, xs=P) == WORKSPACE
+    assert _quant(w.lib, M=(1 << 28) - 17, q=None) == NULL
