@@ -169,3 +169,56 @@ def test_one_workgroup_too_many_is_refused(w):
     assert chain((1 << 28) - 17) == SHAPE and chain((1 << 28) - 31) == SHAPE
     assert chain((1 << 28) - 32) == WORKSPACE and chain((1 << 28) - 17, xs=P) == WORKSPACE
     assert _quant(w.lib, M=(1 << 28) - 17, q=None) == NULL
+
+
+# ------------------------------------------------------------------ which kernel a linear's sizes take
+def _costs():
+    """The table of dense_kernel, as the source has it."""
+    with open(os.path.join(CSRC, "fp8b.hip")) as f:
+        src = f.read()
+    rows = re.findall(r"\{(k\w+), (\d+), (\d+), ([\d.]+), ([\d.]+), ([\d.]+), ([\d.]+), (true|false)\}", src)
+    names = re.search(r"enum DenseKernel \{([^}]*)\}", src).group(1).replace(",", " ").split()
+    assert [r[0] for r in rows] == names
+    return rows
+
+
+def _dense_kernel(M, N, K):
+    KB, best, least = -(-K // 128), None, 1e30
+    for name, rows, cols, launch, per, first, full, two in _costs():
+        rows, cols, launch, per, first, full = int(rows), int(cols), float(launch), float(per), float(first), float(full)
+        if (name == "kTile256" and KB < 2) or ("Decode" in name and M > 65535 * 16):
+            continue
+        n = -(-M // rows) * -(-N // cols)
+        rounds = n / 512.0 if two == "true" else float(-(-n // 256))
+        us = launch + rounds * per + KB * max(first, rounds * full)
+        if us < least:
+            best, least = name, us
+    return best
+
+
+def _decode_sets(M, N, K):
+    """Register sets of a decode kernel, None for a tile."""
+    most = {"kDecode16": 8, "kDecode16x32": 8, "kDecode32": 4, "kDecode64": 2}.get(_dense_kernel(M, N, K))
+    blocks = -(-(-(-K // 128)) // 8)
+    return most and (min(2, most) if blocks <= 2 else min(4, most) if blocks <= 4 else most)
+
+
+def test_linear_tests_reach_every_kernel():
+    from tests import test_gpu_fp8b as g
+    many = next(m for m in g.test_linear_many_tiles.pytestmark if m.name == "parametrize").args[1]
+    sizes = [*g.LINEAR, *many, *g.WIDE]
+    got = {}
+    for s in sizes:
+        got.setdefault((_dense_kernel(*s), _decode_sets(*s)), []).append(s)
+    want = {("kDecode16", 2), ("kDecode16", 4), ("kDecode16", 8), ("kDecode16x32", 2), ("kDecode16x32", 4),
+            ("kDecode16x32", 8), ("kDecode32", 2), ("kDecode32", 4), ("kDecode64", 2), ("kTile32", None), ("kTile64", None),
+            ("kTile64x256", None), ("kTile128", None), ("kTile256", None)}
+    assert set(got) == want, (want - set(got), set(got) - want)
+
+
+def test_wide_tests_walk_over_several_tiles():
+    """256 workgroups share the tiles: past 512 some have three, at two blocks of K and more."""
+    from tests import test_gpu_fp8b as g
+    for M, N, K in [*g.WIDE, (8200, 8200, 400)]:
+        assert _dense_kernel(M, N, K) == "kTile256" and -(-M // 256) * -(-N // 256) > 512
+    assert {-(-K // 128) for _, _, K in g.WIDE} >= {2, 3, 4}

@@ -566,3 +566,52 @@ def test_linear_infinite_activation_gives_nan(w, M):
         assert np.isfinite(np.delete(v, [3, 4], 0)).all()
     keep = np.delete(np.arange(M), [3, 4])
     assert np.array_equal(bf16_host(y)[keep], bf16_host(clean)[keep])
+
+
+# ------------------------------------------------------------------ the wide tiles' walk
+WIDE = [(8192, 8192, 256), (8200, 8100, 384), (12300, 8192, 200), (9000, 12300, 512)]  # M, N, K
+
+
+@pytest.mark.parametrize("M,N,K", WIDE)
+def test_linear_wide_tiles_one_after_the_other(w, M, N, K):
+    """More 256 x 256 tiles than workgroups, so that each walks over two or three, at two to four
+    blocks of K: one code per block and scales that are powers of two, different from tile to
+    tile, so that a block, scale or row of another tile shows. Every output is exact."""
+    show(f"linear {M} x {N} x {K}")
+    B = -(-K // 128)
+    q = torch.zeros((M, 128 * B), dtype=torch.uint8, device=DEV)
+    cw = torch.zeros((N, K), dtype=torch.uint8, device=DEV)
+    for b in range(B):
+        # 1.0 on one column of the block for the rows, on the same one for the columns
+        q[:, 128 * b + 17 * b] = 0x38
+        cw[:, 128 * b + 17 * b] = 0x38
+    m = torch.arange(M, device=DEV)
+    n = torch.arange(-(-N // 128), device=DEV)
+    b = torch.arange(B, device=DEV)
+    # exponents of the blocks' terms lie within the 8 bits of a BF16, and move with the row, the
+    # row's tile, the column's block and the block of K
+    ea = (b[:, None] + (m % 7 + m // 256 % 5)[None]) % 4
+    eb = 2 * ((b[None] + n[:, None]) % 2) + (n // 2 % 3)[:, None] * 8
+    s, sw = (2.0 ** ea).float().contiguous(), (2.0 ** eb).float().contiguous()
+    y = torch.full((M + 1, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    w.fp8b_linear(q, w.fp8b_prepack_weight(cw), sw, N, x_scale=s, K=K, y=y[:M])
+    sync()
+    want = s.t() @ sw.t()                                # exact in float32
+    want = want.repeat_interleave(128, 1)[:, :N].to(torch.bfloat16)
+    bad = (y[:M] != want).nonzero()
+    assert bad.numel() == 0, (len(bad), bad[:4].tolist())
+    assert (y[M] == 7).all()
+
+
+def test_linear_wide_tiles_of_random_values(w):
+    """Two tiles a workgroup, ragged on every side: every output of two rows of every row of tiles."""
+    M, N, K = 8200, 8200, 400
+    rng = np.random.default_rng(1)
+    x = _acts(rng, M, K, 1.0)
+    cw, sw = _weight(rng, N, K)
+    b = O.f32_to_bf16(rng.standard_normal(N).astype(np.float32))
+    y = w.fp8b_linear(bf16_dev(x), w.fp8b_prepack_weight(dev(cw)), dev(sw), N, bias=bf16_dev(b))
+    sync()
+    first = np.arange(0, M, 256)
+    pick = np.unique(np.r_[first + rng.integers(0, 8, len(first)), np.minimum(first + rng.integers(8, 256, len(first)), M - 1)])
+    _hold(bf16_host(y)[pick], *F.quant(x[pick]), cw, sw, b)
