@@ -126,15 +126,6 @@ hipError_t launch_fp8b_schedule(const int64_t* group_list, int64_t E, int64_t R,
 // ---------------------------------------------------------------------------
 // quant
 // ---------------------------------------------------------------------------
-// max over the 16 lanes of a DPP row, in every lane
-__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));   // quad_perm [1,0,3,2]
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));   // quad_perm [2,3,0,1]
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));  // row_half_mirror
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));  // row_mirror
-  return v;
-}
-
 // Scale of a block from the bits of its largest magnitude. alg 1: the smallest
 // power of two (at least 2^-126) not below amax / 448. NaN stays NaN.
 __device__ __forceinline__ float block_scale(uint32_t amax_bits, int alg) {

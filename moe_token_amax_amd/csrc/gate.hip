@@ -222,6 +222,11 @@ __device__ void gate_exact(const GateArgs& g, int64_t t, int lane) {
 // ---------------------------------------------------------------------------
 constexpr float kNearSigmoid = 0x1p-20f, kNearSoftmax = 0x1p-19f;
 
+// a >= b: whether float rounding could have put two keys or marks in this order (NaN: yes)
+__device__ __forceinline__ bool too_close(float a, float b, float near) {
+  return !(a - b > near * (1.f + fabsf(a) + fabsf(b)));
+}
+
 // Whether doubles may give logit x the key of another logit, so that the lower index
 // would win and not the larger logit. Sigmoids: logits d apart have scores at least
 // d exp(-x) / 4 apart (x >= 0) or a share of d / 2 (x < 0). Distinct floats of magnitude
@@ -329,6 +334,7 @@ __device__ __forceinline__ float wave_top(uint32_t kb) {
   return m ? key_value(m) : 0.f;
 }
 
+// logits of experts P lane .. P lane + P - 1 of token t (0 past the last)
 template <int DT, int P>
 __device__ __forceinline__ void load_logits(const GateArgs& g, int64_t t, int lane, float (&l)[P]) {
   const int e0 = lane * P;
@@ -475,14 +481,13 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
       const int last = __builtin_ctzll(__ballot(group && rank == g.topk_group - 1));
       const int next = __builtin_ctzll(__ballot(group && rank == g.topk_group));
       const float x = readlane_f(mark, last), y = readlane_f(mark, next);
-      if (y > -__builtin_huge_valf()) close = !(x - y > near * (1.f + fabsf(x) + fabsf(y)));
+      if (y > -__builtin_huge_valf()) close = too_close(x, y, near);
       if (close && sigmoid && biased) {  // uniform
         // their marks in doubles, if no third group is close to either
         const uint64_t before = __ballot(group && rank == g.topk_group - 2), past = __ballot(group && rank == g.topk_group + 1);
         const float px = before ? readlane_f(mark, __builtin_ctzll(before)) : 0.f;
         const float py = past ? readlane_f(mark, __builtin_ctzll(past)) : -__builtin_huge_valf();
-        const bool pair = (!before || px - x > near * (1.f + fabsf(px) + fabsf(x))) &&
-                          (!(py > -__builtin_huge_valf()) || y - py > near * (1.f + fabsf(y) + fabsf(py)));
+        const bool pair = !(before && too_close(px, x, near)) && !(py > -__builtin_huge_valf() && too_close(y, py, near));
         if (pair) {  // uniform
           const bool border = group && (rank == g.topk_group - 1 || rank == g.topk_group);
           double first = kOut, second = kOut;
@@ -552,7 +557,7 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
     const int n = __shfl_down(id, 1, kWave);
     const float nv = __shfl_down(v, 1, kWave), nl = __shfl_down(sel, 1, kWave), nb = __shfl_down(bj, 1, kWave);
     if (lane <= k && lane + 1 < kWave && id >= 0 && n >= 0 && !(lane < k - 1 && nl == sel && nb == bj))
-      swap = !(v - nv > near * (1.f + fabsf(v) + fabsf(nv)));
+      swap = too_close(v, nv, near);
     if (k > 14 && (lane < k || k == kWave)) close = close || swap || k == kWave;  // past a row of lanes
     if (!sigmoid && lane < k) close = close || swap;
   } else {
@@ -622,13 +627,6 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs g) {
 // dependent steps bound this kernel: 16384 x 256, sigmoid, 8 groups, bias, top 8
 // take 15.8 us, the logits' bytes 4.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));
-  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));
-}
-
 __device__ __forceinline__ float row_sum(float v) {
   v += dpp_f<0xB1>(v);
   v += dpp_f<0x4E>(v);
@@ -678,27 +676,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
   uint32_t* const mine = keys[wave] + lane * kPitch;
 
   float l[P];
-  const int64_t at = t * g.ld + e0;
-#pragma unroll
-  for (int i = 0; i < P; i += 4) {
-    if (g.vec) {
-      if (DT == 0) {
-        float4 v = {0.f, 0.f, 0.f, 0.f};
-        if (e0 + i < E) v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(g.logits) + at + i);
-        l[i] = v.x; l[i + 1] = v.y; l[i + 2] = v.z; l[i + 3] = v.w;
-      } else {
-        uint2 v = {0u, 0u};
-        if (e0 + i < E) v = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(g.logits) + at + i);
-        const uint32_t h[4] = {v.x & 0xFFFFu, v.x >> 16, v.y & 0xFFFFu, v.y >> 16};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          l[i + j] = DT == 1 ? bf16_to_f32(h[j]) : __half2float(__builtin_bit_cast(__half, (uint16_t)h[j]));
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) l[i + j] = e0 + i + j < E ? load_logit<DT>(g.logits, at + i + j) : 0.f;
-    }
-  }
+  load_logits<DT, P>(g, t, sub, l);
   const float low = -__builtin_huge_valf();
   float top = low;
   uint32_t in = 0u;  // bit i: expert e0 + i takes part
@@ -712,7 +690,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
   const bool need_scores = biased || g.n_group > 1 || (!sigmoid && !g.renormalize);
   float total = 1.f, r = 1.f;
   if (need_scores && !sigmoid) {
-    const uint32_t tb = row_max(top > low ? key_bits(top) : 0u);
+    const uint32_t tb = row_max_u32(top > low ? key_bits(top) : 0u);
     top = tb ? key_value(tb) : 0.f;
     float part[P];
 #pragma unroll
@@ -755,17 +733,16 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     const bool real = group < g.n_group;
     if (g.topk_group < g.n_group) {
       // the last group that stays and the first that goes
-      const uint32_t xb = row_max(real && rank == g.topk_group - 1 && mark > low ? key_bits(mark) : 0u);
-      const uint32_t yb = row_max(real && rank == g.topk_group && mark > low ? key_bits(mark) : 0u);
+      const uint32_t xb = row_max_u32(real && rank == g.topk_group - 1 && mark > low ? key_bits(mark) : 0u);
+      const uint32_t yb = row_max_u32(real && rank == g.topk_group && mark > low ? key_bits(mark) : 0u);
       const float x = key_value(xb), y = key_value(yb);
-      if (yb) close = !(x - y > near * (1.f + fabsf(x) + fabsf(y)));
+      if (yb) close = too_close(x, y, near);
       if (sigmoid && biased && __ballot(close)) {  // uniform
         // their marks in doubles, if no third group is close to either
-        const uint32_t pb = row_max(real && rank == g.topk_group - 2 && mark > low ? key_bits(mark) : 0u);
-        const uint32_t nb = row_max(real && rank == g.topk_group + 1 && mark > low ? key_bits(mark) : 0u);
+        const uint32_t pb = row_max_u32(real && rank == g.topk_group - 2 && mark > low ? key_bits(mark) : 0u);
+        const uint32_t nb = row_max_u32(real && rank == g.topk_group + 1 && mark > low ? key_bits(mark) : 0u);
         const float prev = key_value(pb), next = key_value(nb);
-        const bool pair = close && !(pb && !(prev - x > near * (1.f + fabsf(prev) + fabsf(x)))) &&
-                          !(nb && !(y - next > near * (1.f + fabsf(y) + fabsf(next))));
+        const bool pair = close && !(pb && too_close(prev, x, near)) && !(nb && too_close(y, next, near));
         const bool border = pair && real && (rank == g.topk_group - 1 || rank == g.topk_group);
         // the keys that may be among the group's two largest
         const float from = b - near * (1.f + 2.f * fabsf(b));
@@ -789,8 +766,8 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
         const double dm = second > kOut ? first + second : first;
         const double dx = row_max_d(border && rank == g.topk_group - 1 ? dm : kOut);
         const double dy = row_max_d(border && rank == g.topk_group ? dm : kOut);
-        const uint32_t gx = row_max(border && rank == g.topk_group - 1 ? (uint32_t)group : 0u);
-        const uint32_t gy = row_max(border && rank == g.topk_group ? (uint32_t)group : 0u);
+        const uint32_t gx = row_max_u32(border && rank == g.topk_group - 1 ? (uint32_t)group : 0u);
+        const uint32_t gy = row_max_u32(border && rank == g.topk_group ? (uint32_t)group : 0u);
         if (border && (dy > dx || (dy == dx && gy < gx))) rank = 2 * g.topk_group - 1 - rank;
         close = close && !pair;
       }
@@ -813,7 +790,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     uint32_t m = run[0];
 #pragma unroll
     for (int q = 1; q < kRuns; ++q) m = max(m, run[q]);
-    const uint32_t best = row_max(m);
+    const uint32_t best = row_max_u32(m);
     const uint32_t same = (uint32_t)(__ballot(m == best) >> (lane & 48)) & 0xFFFFu;
     const int owner = __builtin_ctz(same);
     int q = kRuns - 1;
@@ -842,7 +819,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     const int n = __shfl_down(id, 1, 16);
     const float nv = __shfl_down(v, 1, 16), nl = __shfl_down(sel, 1, 16), nb = __shfl_down(bj, 1, 16);
     if (sub <= k && id >= 0 && n >= 0 && !(sub < k - 1 && nl == sel && nb == bj))
-      swap = !(v - nv > near * (1.f + fabsf(v) + fabsf(nv)));
+      swap = too_close(v, nv, near);
     if (!sigmoid && sub < k) close = close || swap;
   } else {
     const float first = need_scores && !sigmoid ? top : __shfl(sel, lane & 48, kWave);
@@ -876,7 +853,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     if (biased && all) settle_row(id, w, w + (double)bj, k, lane);  // uniform
     if (!(sub < k && id >= 0)) w = 0.0;
   } else {
-    const uint32_t tb = row_max(chosen ? key_bits(sel) : 0u);
+    const uint32_t tb = row_max_u32(chosen ? key_bits(sel) : 0u);
     const float ref = g.renormalize ? (tb ? key_value(tb) : 0.f) : top;
     if (biased && scores_vanish(ref, top)) close = true;
     if (chosen) w = exp((double)sel - (double)ref);
