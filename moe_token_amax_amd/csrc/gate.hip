@@ -559,7 +559,10 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
     if (lane <= k && lane + 1 < kWave && id >= 0 && n >= 0 && !(lane < k - 1 && nl == sel && nb == bj))
       swap = too_close(v, nv, near);
     if (k > 14 && (lane < k || k == kWave)) close = close || swap || k == kWave;  // past a row of lanes
-    if (!sigmoid && lane < k) close = close || swap;
+    if (!sigmoid) {
+      if (lane < k) close = close || swap;
+      if (g.renormalize && scores_vanish(wave_top(lane < k && id >= 0 ? key_bits(sel) : 0u), top)) close = true;
+    }
   } else {
     const float first = need_scores && !sigmoid ? top : readlane_f(sel, 0);
     const bool chosen = lane < k && id >= 0;
@@ -593,7 +596,6 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
     // renormalized: the largest selected logit stands for the maximum
     const bool mine = lane < k && id >= 0;
     const float ref = g.renormalize ? wave_top(mine ? key_bits(sel) : 0u) : top;
-    if (biased && scores_vanish(ref, top)) return false;  // uniform
     if (mine) w = exp((double)sel - (double)ref);
   }
   if (g.renormalize) {
