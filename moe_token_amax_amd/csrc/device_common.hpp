@@ -30,15 +30,6 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float f) {
   return u >> 16;
 }
 
-// Unsigned max over the 16 lanes of a DPP row, in every lane.
-__device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));   // quad_perm [1,0,3,2]
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));   // quad_perm [2,3,0,1]
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));  // row_half_mirror
-  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));  // row_mirror
-  return v;
-}
-
 // ---------------------------------------------------------------------------
 // Wave-wide max of a non-negative quantity held as uint32 bit patterns.
 // Non-negative IEEE floats (and |BF16| bit patterns) order like unsigned ints,
@@ -47,7 +38,10 @@ __device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
 // into scalars and combined. Every lane returns the wave result.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-  v = row_max_u32(v);
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, false));   // quad_perm [1,0,3,2]
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, false));   // quad_perm [2,3,0,1]
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xF, 0xF, false));  // row_half_mirror
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xF, 0xF, false));  // row_mirror
   uint32_t a = (uint32_t)__builtin_amdgcn_readlane((int)v, 0);
   uint32_t b = (uint32_t)__builtin_amdgcn_readlane((int)v, 16);
   uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)v, 32);

@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "device_common.hpp"
+#include "dpp_row.hpp"
 #include "fp8b.hpp"
 #include "launch.hpp"
 

@@ -21,6 +21,7 @@
 #include <hip/hip_fp16.h>
 
 #include "device_common.hpp"
+#include "dpp_row.hpp"
 #include "fp8b.hpp"
 #include "launch.hpp"
 
