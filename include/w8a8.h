@@ -591,8 +591,9 @@ int w8a8_w4a16_moe_grouped(int fmt, const uint16_t* x_rows, const int64_t* group
  * NaN or -inf, or whose key is NaN or -inf, is out (a mask of -inf switches
  * experts off for a token); a logit of +inf counts as the largest float.
  * n_group > 1: the mark of a group of E / n_group consecutive experts is the
- * sum of its two largest keys (the key if one is in); only the topk_group
- * groups of largest mark stay, lowest index first among equals. The top_k
+ * sum of its two largest keys (the key if one is in), also without a bias;
+ * only the topk_group groups of largest mark stay, lowest index first among
+ * equals. The top_k
  * experts of largest key follow in that order, lowest index first among
  * equals; a slot that no expert fills gets id -1 (w8a8_moe_route drops it) and
  * weight 0. The weight of an expert is its score, divided by the sum of the

@@ -219,6 +219,12 @@ __device__ __forceinline__ void load8(const uint16_t* src, int64_t next, int64_t
   }
 }
 
+// ACT 1 quantizes swiglu_fixed, the INT8 quantizer's sequence of single roundings (its
+// exponential is within 1.2 ulp): one SwiGLU for both, whose codes can be pinned bit by
+// bit. It keeps the vector unit busy without a pause (16384 x 2048: 49 to 52 us, HBM 35).
+// Of 10^8 codes 134 fall to the other side of a tie than 64 bits have them, with torch's
+// exponential and division 136.
+//
 // 16 lanes own one (row, block): 8 values a lane. A 256-thread workgroup takes
 // 16 rows of one block at a time, so that the 16 scales of a block go out as
 // one 64-byte piece of its [M] line.
@@ -409,10 +415,10 @@ __device__ __forceinline__ void store4(const Fp8bGemm& p, int64_t m, int64_t n, 
 // LDS. The activation codes, which all eight share, go through LDS one block of
 // K at a time (four buffers, one barrier a block), widened to BF16 on the way if
 // EXACT. EXACT multiplies the codes as BF16 (16x16x32, every product exact, half
-// the matrix rate); otherwise the FP8 MFMA. Up to 64 rows the weights' stream hides
+// the matrix rate); otherwise the FP8 MFMA. Up to 32 rows the weights' stream hides
 // the difference, past that the LDS carries as much as the MFMAs take: 256 experts of
-// 4096 x 4096, 2 / 32 / 64 / 128 rows each, exact 710 / 760 / 876 / 1380 us, else 705 /
-// 755 / 800 / 970 (6.0 to 4.4 TB/s).
+// 4096 x 4096, 2 / 32 / 64 / 128 rows each, exact 699 / 752 / 839 / 1282 us, else 695 /
+// 748 / 788 / 931 (6.2 to 4.6 TB/s).
 template <int MB, int NBW, bool EXACT>
 struct StreamTile {
   static constexpr int kAhead = 3, kSets = kAhead + 1;  // blocks of weights in flight
@@ -890,9 +896,11 @@ __global__ __launch_bounds__(512) void fp8b_wide_kernel(Fp8bGemm p) {
 // refilled as soon as it is multiplied, and their sums meet in LDS in a fixed
 // order. FUSED (few rows): x is BF16, and every workgroup quantizes the rows itself
 // into LDS, behind its first weight loads, which saves the quantizer's launch.
-// Bound by the weights' stream: 1 x 16384 x 7168 23.0 us (5.1 TB/s), 16 rows 24.7; with
-// 64 rows by the L2's stream into the CUs, 32 bytes a clock, of the codes that every
-// workgroup reads again (64 x 4096 x 7168 13.8 us).
+// Bound by the weights' stream (us in a graph): 1 x 16384 x 7168 22.2 of codes (5.3 TB/s),
+// 25.4 with the quantizer inside; 16 rows 23.1. With tens of rows by the L1: the 16 lanes
+// of a quarter of a code load lie in 16 rows, a look-up for every 16 bytes; 64 x 4096 x
+// 7168 take 21246 look-ups a CU, 8.9 us at one a clock, of 11.4 (its lines from the L2, at
+// 32 bytes a clock, 6.2).
 constexpr int kDecodeWaves = 8;
 constexpr int64_t kFusedValues = 8192;  // M x K quantized by every workgroup, at most
 

@@ -213,7 +213,7 @@ __device__ void gate_exact(const GateArgs& g, int64_t t, int lane) {
 // selected and the runner-up by the doubles that their weights need anyway. What is
 // left, a third group or a chain of close keys that leaves the list, falls back
 // (a launch lasts as long as its slowest wavefront: with every close choice left to
-// gate_exact, 2048 tokens took 15.8 us instead of 7.2 and 16384 took 21.7, not 15.8).
+// gate_exact, 2048 tokens took 15.8 us in a graph instead of 7.1, and 16384 took 5.9 more).
 // Without a bias the order of keys is the order of logits, which are compared as
 // they are, as far as doubles tell the keys of distinct logits apart (unsure_logit);
 // a selected one 700 under the maximum (softmax) or under -700 (sigmoid), where
@@ -626,9 +626,9 @@ __global__ __launch_bounds__(256) void gate_kernel(GateArgs g) {
 // of a token holds experts P s .. P s + P - 1 (E <= 16 P), their keys also in LDS, the
 // maxima of its runs of four in registers: a step of the selection looks into one
 // run of the lane that owns the maximum instead of at every key. Vector
-// instructions (1430 a wavefront, 9.5 us at 16384 tokens) and the selection's
+// instructions (1476 a wavefront, 9.8 us at 16384 tokens) and the selection's
 // dependent steps bound this kernel: 16384 x 256, sigmoid, 8 groups, bias, top 8
-// take 15.8 us, the logits' bytes 4.
+// take 14.2 to 14.5 us in a graph, the logits' bytes 4.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float row_sum(float v) {
   v += dpp_f<0xB1>(v);
@@ -877,13 +877,14 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     if ((again >> (16 * q)) & 0xFFFFu) gate_exact<DT, (P * 16 + 63) / 64>(g, t0 + q, lane);
 }
 
-// From here on (five wavefronts a SIMD) four tokens a wavefront beat one; us a call,
-// 256 experts, one / four:  sigmoid, 8 groups, bias, top 8   softmax, bf16, top 8
-//                   1024 tokens    7.0 /  9.3                   4.8 / 6.3
-//                   4096           9.3 / 10.4                   6.3 / 6.5
-//                   5120          10.5 / 10.8                   7.1 / 7.4
-//                   8192          13.5 / 11.1                   9.0 / 7.1
-//                  16384          22.3 / 15.8                  14.9 / 9.6
+// From about here on (five wavefronts a SIMD) four tokens a wavefront beat one; us a
+// call in a graph, 256 experts, one / four:
+//                             sigmoid, 8 groups, bias, top 8   softmax, bf16, top 8
+//                   1024 tokens    6.7 /  9.1                   4.5 / 6.0
+//                   4096           8.4 /  9.5                   6.0 / 6.1
+//                   5120          10.0 / 10.5                   6.7 / 6.7
+//                   8192          13.0 / 10.6                   8.8 / 6.7
+//                  16384          22.3 / 14.5                  14.6 / 8.8
 constexpr int64_t kQuadTokens = 5120;
 
 template <int DT>

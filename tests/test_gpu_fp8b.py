@@ -574,7 +574,7 @@ WIDE = [(8192, 8192, 256), (8200, 8100, 384), (12300, 8192, 200), (9000, 12300, 
 
 @pytest.mark.parametrize("M,N,K", WIDE)
 def test_linear_wide_tiles_one_after_the_other(w, M, N, K):
-    """More 256 x 256 tiles than workgroups, so that each walks over two or three, at two to four
+    """More 256 x 256 tiles than workgroups, so that each walks over four to seven, at two to four
     blocks of K: one code per block and scales that are powers of two, different from tile to
     tile, so that a block, scale or row of another tile shows. Every output is exact."""
     show(f"linear {M} x {N} x {K}")
@@ -604,7 +604,7 @@ def test_linear_wide_tiles_one_after_the_other(w, M, N, K):
 
 
 def test_linear_wide_tiles_of_random_values(w):
-    """Two tiles a workgroup, ragged on every side: every output of two rows of every row of tiles."""
+    """Four tiles a workgroup, ragged on every side: every output of two rows of every row of tiles."""
     M, N, K = 8200, 8200, 400
     rng = np.random.default_rng(1)
     x = _acts(rng, M, K, 1.0)
