@@ -598,8 +598,9 @@ int w8a8_w4a16_moe_grouped(int fmt, const uint16_t* x_rows, const int64_t* group
  * equals; a slot that no expert fills gets id -1 (w8a8_moe_route drops it) and
  * weight 0. The weight of an expert is its score, divided by the sum of the
  * selected scores if renormalize (0 if that sum is 0), times scale. Keys are
- * compared as doubles, weights rounded once to float; only the sum of a softmax
- * that is not renormalized is one of floats.
+ * compared as doubles (softmax keys within a rounding of their sum of each other
+ * may be told apart or not), weights rounded once to float; only the sum of a
+ * softmax that is not renormalized is one of floats.
  * 1 <= E <= 1024, n_group <= 64 dividing E, top_k <= 64 and no more than the
  * experts of topk_group groups, T <= 2^26 - 4, T * top_k < 2^31, scale finite.
  */

@@ -217,7 +217,7 @@ __device__ void gate_exact(const GateArgs& g, int64_t t, int lane) {
 // Without a bias the order of keys is the order of logits, which are compared as
 // they are, as far as doubles tell the keys of distinct logits apart (unsure_logit);
 // a selected one 700 under the maximum (softmax) or under -700 (sigmoid), where
-// doubles run out, falls back, and with a bias a softmax whose selected are all there.
+// doubles run out, falls back, and with a bias a softmax whose selected are all 600 under.
 // The weights come from the selected logits alone, in doubles; only the sum of a
 // softmax that is not renormalized is a float sum.
 // ---------------------------------------------------------------------------
@@ -245,10 +245,10 @@ __device__ __forceinline__ bool keys_apart(float a, float b, bool sigmoid) {
   return sigmoid && a > 20.f ? b <= 19.f : a - b > 0x1p-30f;
 }
 
-// The scores of a softmax whose logits are all at most ref, 700 under the maximum, run out
-// of doubles: their sum may be 0, and then so are the weights. (Chosen by the bias; without
-// one the order of keys is in doubt there as well.)
-__device__ __forceinline__ bool scores_vanish(float ref, float top) { return ref - top < -700.f; }
+// Softmax scores run out of doubles under e^-708 of the maximum's. Where the selected
+// are all at most e^-600 (chosen by the bias) their sum may be 0, and then so are the
+// weights, or hold few bits of those 103 under the largest, which floats still have.
+__device__ __forceinline__ bool scores_vanish(float largest, float top) { return largest - top < -600.f; }
 
 // order-preserving map of finite floats and +inf to integers above 0 (0: out)
 __device__ __forceinline__ uint32_t key_bits(float f) {
@@ -567,7 +567,7 @@ __device__ __forceinline__ bool gate_fast(const GateArgs& g, int64_t t, int lane
   } else {
     const float first = need_scores && !sigmoid ? top : readlane_f(sel, 0);
     const bool chosen = lane < k && id >= 0;
-    if (chosen) close = close || (sigmoid ? sel < -700.f : scores_vanish(sel, first));
+    if (chosen) close = close || (sigmoid ? sel < -700.f : sel - first < -700.f);
     const bool unsure = chosen && unsure_logit(sel, sigmoid);
     const uint64_t any = __ballot(unsure);
     if (any) {  // uniform
@@ -826,7 +826,7 @@ __global__ __launch_bounds__(kQuadWaves * 64) void gate_quad_kernel(GateArgs g) 
     if (!sigmoid && sub < k) close = close || swap;
   } else {
     const float first = need_scores && !sigmoid ? top : __shfl(sel, lane & 48, kWave);
-    if (chosen) close = close || (sigmoid ? sel < -700.f : scores_vanish(sel, first));
+    if (chosen) close = close || (sigmoid ? sel < -700.f : sel - first < -700.f);
     const bool unsure = chosen && unsure_logit(sel, sigmoid);
     const uint64_t any = __ballot(unsure);
     if (any) {  // uniform

@@ -359,3 +359,18 @@ def test_gate_softmax_chosen_by_the_bias_far_below_the_maximum(w, T, G, keep, re
         l[r::9, 5] = top
     b[E // 4:] -= 1.0                                    # the group of expert 5 is chosen
     _check(w, torch.from_numpy(l), k, b, "softmax", G, keep, renorm)
+
+
+@pytest.mark.parametrize("T", [64, 5200])
+@pytest.mark.parametrize("far", [600.0, 650.0, 690.0])
+def test_gate_softmax_scores_that_a_double_holds_in_part(w, T, far):
+    """Chosen by the bias: one score e^-far of the maximum's, others 45 under that, which a double
+    holds with a few bits. The weights are those of the scores as doubles."""
+    rng = np.random.default_rng(int(far))
+    E, k = 64, 4
+    l = rng.uniform(-1.0, 1.0, (T, E)).astype(np.float32)
+    l[:, 5] = far + 45.0
+    l[:, 9] = 45.0
+    b = 0.1 * rng.standard_normal(E)
+    b[5], b[9] = -9.0, 0.5
+    _check(w, torch.from_numpy(l), k, b, "softmax")
