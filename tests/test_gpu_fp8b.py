@@ -615,3 +615,25 @@ def test_linear_wide_tiles_of_random_values(w):
     first = np.arange(0, M, 256)
     pick = np.unique(np.r_[first + rng.integers(0, 8, len(first)), np.minimum(first + rng.integers(8, 256, len(first)), M - 1)])
     _hold(bf16_host(y)[pick], *F.quant(x[pick]), cw, sw, b)
+
+
+# ------------------------------------------------------------------ offsets past 32 bits
+def test_quant_and_linear_past_32_bit_offsets(w):
+    """More than 2^32 bytes of codes and elements of x: rows on either side of every 2^32."""
+    M, N, K = 1 << 19 | 4097, 40, 8200
+    g = torch.Generator(device=DEV).manual_seed(0)
+    x = torch.randn((M, K), generator=g, device=DEV, dtype=torch.bfloat16)
+    cw, sw = _weight(np.random.default_rng(0), N, K)
+    wp, swd = w.fp8b_prepack_weight(dev(cw)), dev(sw)
+    Kp = 128 * F.blocks(K)
+    pick = np.unique([0, 1, (1 << 31) // K, (1 << 32) // K, (1 << 32) // K + 1, (1 << 32) // Kp, (1 << 32) // Kp + 1, M - 2, M - 1])
+    rows = torch.from_numpy(pick).to(DEV)
+    xh = bf16_host(x[rows])
+    y = w.fp8b_linear(x, wp, swd, N)
+    q, s = w.fp8b_quant(x)
+    z = w.fp8b_linear(q, wp, swd, N, x_scale=s, K=K)
+    sync()
+    qo, so = F.quant(xh)
+    assert np.array_equal(host(q[rows]), qo) and np.array_equal(host(s[:, rows]), so)
+    _hold(bf16_host(y[rows]), qo, so, cw, sw)
+    assert torch.equal(y, z)

@@ -374,3 +374,18 @@ def test_gate_softmax_scores_that_a_double_holds_in_part(w, T, far):
     b = 0.1 * rng.standard_normal(E)
     b[5], b[9] = -9.0, 0.5
     _check(w, torch.from_numpy(l), k, b, "softmax")
+
+
+def test_gate_past_32_bit_offsets(w):
+    """The most tokens a call takes: 2^32 logits and more, the tokens on either side of 2^31 and 2^32
+    logits and the last ones."""
+    T, E, k = (1 << 26) - 4, 68, 2
+    g = torch.Generator(device=DEV).manual_seed(1)
+    l = torch.randn((T, E), generator=g, device=DEV, dtype=torch.bfloat16)
+    ids, wts = w.moe_gate(l, k, scoring=w.GATE_SIGMOID)
+    sync()
+    at = np.r_[0:4, (1 << 31) // E - 2:(1 << 31) // E + 3, (1 << 32) // E - 2:(1 << 32) // E + 3, T - 5:T]
+    rows = torch.from_numpy(at).to(DEV)
+    want, ww = O.fp8b.gate(l[rows].double().cpu().numpy(), k, None, "sigmoid")
+    assert np.array_equal(host(ids[rows]), want)
+    assert np.abs(host(wts[rows]) - ww).max() <= 2.0 ** -23
