@@ -53,7 +53,8 @@ typedef enum {
 
 typedef enum {
   W8A8_OUT_BF16 = 0,  /* epilogue output: BF16 bits, uint16_t */
-  W8A8_OUT_I32 = 1    /* raw INT32 accumulator (no epilogue), int32_t */
+  W8A8_OUT_I32 = 1,   /* raw INT32 accumulator (no epilogue), int32_t */
+  W8A8_OUT_F32 = 2    /* float (w8a8_bf16_linear) */
 } w8a8_out;
 
 /* Flag OR-ed into the `out` argument of w8a8_linear: q is in the packed block
@@ -61,10 +62,15 @@ typedef enum {
 #define W8A8_A_PACKED 4
 
 /* Input of w8a8_mx_grouped_gemm: the rows themselves, or the SwiGLU of
- * [gate | up] rows rounded to BF16. */
+ * [gate | up] rows rounded to BF16. The others are activations of the fused
+ * epilogues (w8a8_linear_fused and the calls beside it). */
 typedef enum {
   W8A8_ACT_NONE = 0,
-  W8A8_ACT_SWIGLU = 1
+  W8A8_ACT_SWIGLU = 1,
+  W8A8_ACT_RELU = 2,
+  W8A8_ACT_SILU = 3,
+  W8A8_ACT_GELU = 4,      /* v Phi(v) */
+  W8A8_ACT_GELU_TANH = 5  /* v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) */
 } w8a8_act;
 
 /* Largest K (reduction length) accepted: K * 127 * 127 stays below 2^31. */
@@ -700,6 +706,99 @@ int w8a8_fp8b_moe_layer(const uint16_t* x, int64_t T, int64_t H, const int32_t* 
                         int64_t top_k, int64_t E, int64_t I, const void* w13_packed, const float* w13_scale,
                         const void* w2_packed, const float* w2_scale, int scale_alg, uint16_t* out, void* workspace,
                         int64_t ws_bytes, void* stream);
+
+/*
+ * RMS norm of the residual stream, with the 8-bit output that the quantized
+ * products take.  [DSV4 §二 quantizes the activation that a linear is given; the
+ * norm in front of it is not on the page, its definition is this library's.]
+ *   x        device, BF16 [M, K], row stride ldx
+ *   residual device, BF16 [M, K], row stride ldr, or NULL; then h receives the
+ *            sum, BF16 [M, K], row stride ldh (h may be the residual itself, or
+ *            x; without a residual it is not written and may be NULL)
+ *   weight   device, BF16 [K], or NULL for 1
+ *   y        device, BF16 [M, K], row stride ldy: the norm in BF16, or NULL
+ *            (w8a8_rms_norm needs it)
+ * h = BF16(fl32(x + residual)) or x; r = fl32(1 / sqrt(sum of h^2 / K + eps)), the
+ * sum in doubles; n = fl32(fl32(h r) weight); y = BF16(n). The codes are of n, with
+ * no rounding to BF16 between:
+ *   w8a8_rms_norm_quant: scale float [M], q int8 [M, K] with row stride ldq, as
+ *     w8a8_dynamic_quant
+ *   w8a8_fp8b_rms_norm_quant: q uint8 [M, Kp] (Kp: K rounded up to 128, 16-byte
+ *     aligned, written whole), scale float [ceil(K/128), M], as w8a8_fp8b_quant
+ *   w8a8_mx_rms_norm_quant: e4m3 [M, K] (8-byte aligned), e8m0 [M, K/32], the rule of
+ *     w8a8_mx_quant; K % 32 == 0, else W8A8_ERR_UNSUPPORTED. A group with an infinity
+ *     or NaN gets the byte 255 and codes NaN.
+ * An infinity or NaN in a row makes the row's norm NaN: scale NaN, codes 0 (INT8,
+ * blocks that hold one). 1 <= K <= W8A8_MAX_K, M < 2^31, eps >= 0 and finite.
+ */
+int w8a8_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, uint16_t* h, int64_t ldh,
+                  const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* y, int64_t ldy, void* stream);
+int w8a8_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, uint16_t* h, int64_t ldh,
+                        const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* y, int64_t ldy, int8_t* q,
+                        int64_t ldq, float* scale, void* stream);
+int w8a8_fp8b_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, uint16_t* h,
+                             int64_t ldh, const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* y,
+                             int64_t ldy, int scale_alg, uint8_t* q, float* scale, void* stream);
+int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, uint16_t* h,
+                           int64_t ldh, const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* y,
+                           int64_t ldy, int scale_alg, uint8_t* e4m3, uint8_t* e8m0, void* stream);
+
+/*
+ * Products with bias, activation and residual in their epilogue: y = out(act(v) +
+ * residual), v the fp32 value in front of the output's rounding (the only one).
+ *   act       w8a8_act; evaluated in fp32 with the hardware's exponential (a few
+ *             2^-24 relative; GELU within 2^-21 |v|). W8A8_ACT_SWIGLU only on BF16
+ *             weights prepacked for it
+ *   residual  device, BF16 [M, outputs], row stride ldr, or NULL; may be y itself
+ *   bias      device, BF16 [N] or NULL
+ *   workspace the call's workspace_bytes, 256-byte aligned, rewritten; needed only
+ *             for rows that are not 16-byte aligned whole 16-byte pieces, of many
+ *             rows or of fewer than 16 bytes (else NULL / 0 is fine)
+ *
+ * w8a8_linear_fused [DSV4 §二 npu_quant_matmul]: INT8 codes q [M, K], row stride ldq,
+ *   x_scale float [M] (from w8a8_dynamic_quant_ld or w8a8_rms_norm_quant), a weight
+ *   from w8a8_prepack_weight (E = 1) with w_scale float [N]; v = fl32(fl32(fp32(acc)
+ *   x_scale[m]) w_scale[n]) (+ bias, fl32), acc exact. Without activation and
+ *   residual bit for bit w8a8_linear.
+ * w8a8_fp8b_linear_fused: w8a8_fp8b_linear with the epilogue; the same arguments,
+ *   workspace and products.
+ * w8a8_bf16_linear: BF16 x [M, K], row stride ldx, times a BF16 weight, for the
+ *   layers that a recipe leaves unquantized [DSV4 §一]: exact products, fp32 sums.
+ *   out W8A8_OUT_BF16 or W8A8_OUT_F32 (router logits for w8a8_moe_gate).
+ * w8a8_bf16_prepack_weight (load time): w BF16 [E, N, K] -> 1 KB blocks [e][n-block]
+ *   [64 bytes of k], byte 16 l + j of a block holding bytes 16 (l / 16) + j of the 64
+ *   of row l % 16; N zero-padded to 32, K to 64; w8a8_bf16_packed_bytes(E, N, K) bytes,
+ *   16-byte aligned. act W8A8_ACT_SWIGLU: the rows are [gate | up] (N even) and n-blocks
+ *   alternate, 16 gate rows then their 16 up rows; the products then take act
+ *   W8A8_ACT_SWIGLU and give N / 2 outputs silu(gate) up; any other act: rows in order.
+ * w8a8_bf16_grouped_gemm [DSV4 §三 npu_grouped_matmul]: the rows of every expert times
+ *   that expert's BF16 weight. group_list as for w8a8_grouped_gemm; output row r reads
+ *   row row_index[r] of x (clamped to [0, x_rows)), or row r if row_index is NULL; y
+ *   BF16 [R, outputs]; no bias, no residual. Rows past the counts are left as they
+ *   are. workspace: w8a8_bf16_grouped_workspace_bytes(R, E, N, K) bytes, 256-byte
+ *   aligned (the tile list). E <= 1024, K >= 8.
+ * 1 <= K <= W8A8_MAX_K, N <= 2^22, M, R < 2^28 - 16, a grouped product of fewer than
+ * 2^23 tiles of 128 rows x 256 columns. Workspaces are rewritten by every call: two
+ * calls that may overlap need two.
+ */
+int64_t w8a8_linear_fused_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int w8a8_linear_fused(const int8_t* q, int64_t ldq, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
+                      const float* w_scale, int64_t N, const uint16_t* bias, int act, const uint16_t* residual,
+                      int64_t ldr, uint16_t* y, int64_t ldy, void* workspace, int64_t ws_bytes, void* stream);
+int w8a8_fp8b_linear_fused(const void* x, int64_t ldx, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
+                           const float* w_scale, int64_t N, const uint16_t* bias, int act, const uint16_t* residual,
+                           int64_t ldr, uint16_t* y, int64_t ldy, int scale_alg, void* workspace, int64_t ws_bytes,
+                           void* stream);
+int64_t w8a8_bf16_packed_bytes(int64_t E, int64_t N, int64_t K);
+int w8a8_bf16_prepack_weight(const uint16_t* w, int64_t E, int64_t N, int64_t K, int act, void* w_packed, void* stream);
+int64_t w8a8_bf16_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int w8a8_bf16_linear(const uint16_t* x, int64_t ldx, int64_t M, int64_t K, const void* w_packed, int64_t N,
+                     const uint16_t* bias, int act, const uint16_t* residual, int64_t ldr, void* y, int64_t ldy, int out,
+                     void* workspace, int64_t ws_bytes, void* stream);
+int64_t w8a8_bf16_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K);
+int w8a8_bf16_grouped_gemm(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_t* row_index,
+                           const int64_t* group_list, int64_t R, int64_t E, int64_t N, int64_t K, const void* w_packed,
+                           int act, uint16_t* y, void* workspace, int64_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

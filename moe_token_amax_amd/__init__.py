@@ -90,12 +90,31 @@ __all__ = [
     "fp8b_moe_grouped",
     "fp8b_moe_layer_workspace_bytes",
     "fp8b_moe_layer",
+    "OUT_F32",
+    "ACT_RELU",
+    "ACT_SILU",
+    "ACT_GELU",
+    "ACT_GELU_TANH",
+    "rms_norm",
+    "rms_norm_quant",
+    "fp8b_rms_norm_quant",
+    "mx_rms_norm_quant",
+    "linear_fused_workspace_bytes",
+    "linear_fused",
+    "fp8b_linear_fused",
+    "bf16_packed_bytes",
+    "bf16_prepack_weight",
+    "bf16_linear_workspace_bytes",
+    "bf16_linear",
+    "bf16_grouped_workspace_bytes",
+    "bf16_grouped_gemm",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw8a8.so")
 
 OUT_BF16 = 0
 OUT_I32 = 1
+OUT_F32 = 2    # bf16_linear
 A_PACKED = 4   # flag for linear's `out`: q in the packed block layout
 
 _c_i64 = ctypes.c_int64
@@ -213,6 +232,30 @@ def _load():
         "w8a8_fp8b_moe_layer": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_i64,
                                                _c_p, _c_p, _c_p, _c_p, ctypes.c_int, _c_p, _c_p, _c_i64,
                                                _c_p]),
+        "w8a8_rms_norm": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p, ctypes.c_double, _c_i64,
+                                         _c_i64, _c_p, _c_i64, _c_p]),
+        "w8a8_rms_norm_quant": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p, ctypes.c_double,
+                                               _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_p]),
+        "w8a8_fp8b_rms_norm_quant": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p,
+                                                    ctypes.c_double, _c_i64, _c_i64, _c_p, _c_i64, ctypes.c_int,
+                                                    _c_p, _c_p, _c_p]),
+        "w8a8_mx_rms_norm_quant": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p,
+                                                  ctypes.c_double, _c_i64, _c_i64, _c_p, _c_i64, ctypes.c_int,
+                                                  _c_p, _c_p, _c_p]),
+        "w8a8_linear_fused_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64]),
+        "w8a8_linear_fused": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p,
+                                             ctypes.c_int, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p]),
+        "w8a8_fp8b_linear_fused": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p,
+                                                  ctypes.c_int, _c_p, _c_i64, _c_p, _c_i64, ctypes.c_int, _c_p,
+                                                  _c_i64, _c_p]),
+        "w8a8_bf16_packed_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64]),
+        "w8a8_bf16_prepack_weight": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, ctypes.c_int, _c_p, _c_p]),
+        "w8a8_bf16_linear_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64]),
+        "w8a8_bf16_linear": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, ctypes.c_int, _c_p,
+                                            _c_i64, _c_p, _c_i64, ctypes.c_int, _c_p, _c_i64, _c_p]),
+        "w8a8_bf16_grouped_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_i64]),
+        "w8a8_bf16_grouped_gemm": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_i64,
+                                                  _c_i64, _c_p, ctypes.c_int, _c_p, _c_p, _c_i64, _c_p]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -1243,6 +1286,15 @@ def fp8b_linear_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(lib.w8a8_fp8b_linear_workspace_bytes(M, N, K))
 
 
+def _residual(t: torch.Tensor | None, shape):
+    """(address, row stride) of a residual; (None, 0) without one."""
+    if t is None:
+        return None, 0
+    if t.shape != shape:
+        raise ValueError("residual shape mismatch")
+    return _rows_at(t, torch.bfloat16, "residual")
+
+
 def fp8b_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor, N: int,
                 x_scale: torch.Tensor | None = None, K: int | None = None,
                 bias: torch.Tensor | None = None, scale_alg: int = 0, y: torch.Tensor | None = None,
@@ -1251,6 +1303,17 @@ def fp8b_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor, 
     of fp8b_quant (x uint8 [M, K rounded up to 128], x_scale; K if it is not a multiple
     of 128), times a packed E4M3 weight with w_scale float32 [ceil(N/128), ceil(K/128)]
     -> BF16 [M, N]. x and y may be row-strided."""
+    return fp8b_linear_fused(x, w_packed, w_scale, N, x_scale, K, bias, ACT_NONE, None, scale_alg, y, workspace)
+
+
+def fp8b_linear_fused(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor, N: int,
+                      x_scale: torch.Tensor | None = None, K: int | None = None,
+                      bias: torch.Tensor | None = None, act: int = ACT_NONE,
+                      residual: torch.Tensor | None = None, scale_alg: int = 0,
+                      y: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """fp8b_linear with an activation (ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH) and a
+    BF16 residual [M, N] (rows contiguous; may be y) in its epilogue: BF16(act(v) +
+    residual)."""
     if x_scale is None:
         at, ldx = _rows_at(x, torch.bfloat16, "x")
         M, Kx = x.shape
@@ -1277,11 +1340,13 @@ def fp8b_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor, 
     if y.shape != (M, N):
         raise ValueError("y shape mismatch")
     yp, ldy = _rows_at(y, torch.bfloat16, "y")
+    rp, ldr = _residual(residual, (M, N))
     room, ws, ws_n = (None, None, 0) if x_scale is not None else \
         _room(workspace, x.device, fp8b_linear_workspace_bytes, M, N, K)
-    _check(lib.w8a8_fp8b_linear(at, ldx, _at(x_scale, torch.float32, "x_scale", 2), M, K, wp,
-                                _at(w_scale, torch.float32, "w_scale", 2), N, _at(bias, torch.bfloat16, "bias", 1),
-                                yp, ldy, scale_alg, ws, ws_n, _stream()))
+    _check(lib.w8a8_fp8b_linear_fused(at, ldx, _at(x_scale, torch.float32, "x_scale", 2), M, K, wp,
+                                      _at(w_scale, torch.float32, "w_scale", 2), N,
+                                      _at(bias, torch.bfloat16, "bias", 1), act, rp, ldr, yp, ldy, scale_alg, ws, ws_n,
+                                      _stream()))
     return y
 
 
@@ -1393,3 +1458,233 @@ def fp8b_moe_layer(x: torch.Tensor, topk_ids: torch.Tensor, topk_weights: torch.
                                    _at(topk_weights, torch.float32, "topk_weights", 2), k, E, I, w13, s13, w2, s2,
                                    scale_alg, _at(out, torch.bfloat16, "out", 2), ws, ws_n, _stream()))
     return out
+
+
+# ---------------------------------------------------------------------------
+# RMS norm
+# ---------------------------------------------------------------------------
+def _norm_args(x, weight, eps, residual, h, y):
+    """(M, K, the leading arguments of the norms). Without h the residual takes the sum."""
+    at, ldx = _rows_at(x, torch.bfloat16, "x")
+    M, K = x.shape
+    if weight is not None and weight.shape != (K,):
+        raise ValueError("weight must be [K]")
+    rp, ldr = _residual(residual, (M, K))
+    if residual is None:
+        if h is not None:
+            raise ValueError("h without a residual")
+        hp, ldh = None, 0
+    else:
+        if h is None:
+            h = residual
+        if h.shape != (M, K):
+            raise ValueError("h shape mismatch")
+        hp, ldh = _rows_at(h, torch.bfloat16, "h")
+    yp, ldy = None, 0
+    if y is not None:
+        if y.shape != (M, K):
+            raise ValueError("y shape mismatch")
+        yp, ldy = _rows_at(y, torch.bfloat16, "y")
+    return M, K, (at, ldx, rp, ldr, hp, ldh, _at(weight, torch.bfloat16, "weight", 1), eps, M, K, yp, ldy)
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6, residual: torch.Tensor | None = None,
+             h: torch.Tensor | None = None, y: torch.Tensor | None = None) -> torch.Tensor:
+    """BF16 [M, K] -> its RMS norm times ``weight`` (BF16 [K] or None), BF16 [M, K]. With a
+    residual (BF16 [M, K]) the norm of x + residual; the sum goes to ``h``, or into the
+    residual itself. All rows may be strided."""
+    if y is None:
+        y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    _, _, args = _norm_args(x, weight, eps, residual, h, y)
+    _check(lib.w8a8_rms_norm(*args, _stream()))
+    return y
+
+
+def rms_norm_quant(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6,
+                   residual: torch.Tensor | None = None, h: torch.Tensor | None = None,
+                   y: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                   scale: torch.Tensor | None = None):
+    """rms_norm with the INT8 codes and scales of linear and linear_fused: (int8 [M, K],
+    float32 [M]) of the norm in fp32; ``y`` (BF16 [M, K]) takes the norm too where given."""
+    M, K, args = _norm_args(x, weight, eps, residual, h, y)
+    if q is None:
+        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty((M,), dtype=torch.float32, device=x.device)
+    if q.shape != (M, K) or scale.shape != (M,):
+        raise ValueError("q must be [M, K], scale [M]")
+    qp, ldq = _rows_at(q, torch.int8, "q")
+    _check(lib.w8a8_rms_norm_quant(*args, qp, ldq, _at(scale, torch.float32, "scale", 1), _stream()))
+    return q, scale
+
+
+def fp8b_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6,
+                        residual: torch.Tensor | None = None, h: torch.Tensor | None = None,
+                        y: torch.Tensor | None = None, scale_alg: int = 0, q: torch.Tensor | None = None,
+                        scale: torch.Tensor | None = None):
+    """rms_norm with the codes and scales of fp8b_linear: (uint8 [M, K rounded up to 128],
+    float32 [ceil(K/128), M])."""
+    M, K, args = _norm_args(x, weight, eps, residual, h, y)
+    B = _fp8_blocks(K)
+    if q is None:
+        q = torch.empty((M, 128 * B), dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = torch.empty((B, M), dtype=torch.float32, device=x.device)
+    if q.shape != (M, 128 * B) or scale.shape != (B, M):
+        raise ValueError("q must be [M, K rounded up to 128], scale [ceil(K/128), M]")
+    _check(lib.w8a8_fp8b_rms_norm_quant(*args, scale_alg, _at(q, torch.uint8, "q", 2),
+                                        _at(scale, torch.float32, "scale", 2), _stream()))
+    return q, scale
+
+
+def mx_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor | None, eps: float = 1e-6,
+                      residual: torch.Tensor | None = None, h: torch.Tensor | None = None,
+                      y: torch.Tensor | None = None, scale_alg: int = 0, q: torch.Tensor | None = None,
+                      scale: torch.Tensor | None = None):
+    """rms_norm with the payload and scales of mx_linear: (uint8 [M, K], uint8 [M, K/32]);
+    K a multiple of 32."""
+    M, K, args = _norm_args(x, weight, eps, residual, h, y)
+    if q is None:
+        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = torch.empty((M, K // 32), dtype=torch.uint8, device=x.device)
+    if q.shape != (M, K) or scale.shape != (M, K // 32):
+        raise ValueError("q must be [M, K], scale [M, K/32]")
+    _check(lib.w8a8_mx_rms_norm_quant(*args, scale_alg, _at(q, torch.uint8, "q", 2),
+                                      _at(scale, torch.uint8, "scale", 2), _stream()))
+    return q, scale
+
+
+# ---------------------------------------------------------------------------
+# products with a fused epilogue
+# ---------------------------------------------------------------------------
+ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 2, 3, 4, 5
+
+
+def linear_fused_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib.w8a8_linear_fused_workspace_bytes(M, N, K))
+
+
+def linear_fused(q: torch.Tensor, x_scale: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor, N: int,
+                 bias: torch.Tensor | None = None, act: int = ACT_NONE, residual: torch.Tensor | None = None,
+                 y: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """INT8 linear with bias, activation (ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH) and a
+    BF16 residual [M, N] (may be y) in its epilogue: int8 [M, K] codes with x_scale float32
+    [M], a weight from prepack_weight with w_scale float32 [N] -> BF16 [M, N]. q, residual
+    and y may be row-strided."""
+    at, ldq = _rows_at(q, torch.int8, "q")
+    M, K = q.shape
+    wp = _at(w_packed, torch.uint8, "w_packed", 1)
+    if w_packed.numel() < 16 * -(-N // 16) * 64 * -(-K // 64):
+        raise ValueError("w_packed too small for [N, K]")
+    if x_scale.shape != (M,) or w_scale.shape != (N,):
+        raise ValueError("x_scale must be [M], w_scale [N]")
+    if bias is not None and bias.shape != (N,):
+        raise ValueError("bias shape mismatch")
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=q.device)
+    if y.shape != (M, N):
+        raise ValueError("y shape mismatch")
+    yp, ldy = _rows_at(y, torch.bfloat16, "y")
+    rp, ldr = _residual(residual, (M, N))
+    aligned = at % 16 == 0 and ldq % 16 == 0 and K % 16 == 0  # no copy, no workspace
+    room, ws, ws_n = (None, None, 0) if aligned and workspace is None else \
+        _room(workspace, q.device, linear_fused_workspace_bytes, M, N, K)
+    _check(lib.w8a8_linear_fused(at, ldq, _at(x_scale, torch.float32, "x_scale", 1), M, K, wp,
+                                 _at(w_scale, torch.float32, "w_scale", 1), N, _at(bias, torch.bfloat16, "bias", 1), act,
+                                 rp, ldr, yp, ldy, ws, ws_n, _stream()))
+    return y
+
+
+def _bf16_packed(E: int, N: int, K: int) -> int:
+    # bf16_packed_bytes without the call into the library
+    return E * 32 * -(-N // 32) * 128 * -(-K // 64)
+
+
+def bf16_packed_bytes(E: int, N: int, K: int) -> int:
+    return int(lib.w8a8_bf16_packed_bytes(E, N, K))
+
+
+def bf16_prepack_weight(w: torch.Tensor, act: int = ACT_NONE, out: torch.Tensor | None = None) -> torch.Tensor:
+    """BF16 [N, K] or [E, N, K] -> packed uint8 buffer (stable, caller-owned). act=ACT_SWIGLU
+    for rows [gate | up] that are multiplied with act=ACT_SWIGLU."""
+    _need(w, torch.bfloat16, "w")
+    if w.dim() == 2:
+        E, (N, K) = 1, w.shape
+    elif w.dim() == 3:
+        E, N, K = w.shape
+    else:
+        raise ValueError("w must be [N, K] or [E, N, K]")
+    nbytes = bf16_packed_bytes(E, N, K)
+    if out is None:
+        out = torch.empty((nbytes,), dtype=torch.uint8, device=w.device)
+    if out.numel() < nbytes:
+        raise ValueError(f"out needs {nbytes} bytes")
+    _check(lib.w8a8_bf16_prepack_weight(_at(w, torch.bfloat16, "w", w.dim()), E, N, K, act,
+                                        _at(out, torch.uint8, "out", 1), _stream()))
+    return out
+
+
+def bf16_linear_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(lib.w8a8_bf16_linear_workspace_bytes(M, N, K))
+
+
+def bf16_linear(x: torch.Tensor, w_packed: torch.Tensor, N: int, bias: torch.Tensor | None = None,
+                act: int = ACT_NONE, residual: torch.Tensor | None = None, out: int = OUT_BF16,
+                y: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """BF16 linear for layers that stay unquantized: x [M, K] times a weight [N, K] from
+    bf16_prepack_weight, with bias (BF16 [N]), activation and BF16 residual in the
+    epilogue -> [M, N] (ACT_SWIGLU: [M, N/2], silu(gate) * up) in BF16, or float32 with
+    out=OUT_F32 or a float32 y. x, residual and y may be row-strided."""
+    at, ldx = _rows_at(x, torch.bfloat16, "x")
+    M, K = x.shape
+    wp = _at(w_packed, torch.uint8, "w_packed", 1)
+    if w_packed.numel() < _bf16_packed(1, N, K):
+        raise ValueError("w_packed too small for [N, K]")
+    if bias is not None and bias.shape != (N,):
+        raise ValueError("bias shape mismatch")
+    width = N // 2 if act == ACT_SWIGLU else N
+    if y is None:
+        y = torch.empty((M, width), dtype=torch.float32 if out == OUT_F32 else torch.bfloat16, device=x.device)
+    elif y.dtype is torch.float32:
+        out = OUT_F32
+    if y.shape != (M, width):
+        raise ValueError("y shape mismatch")
+    yp, ldy = _rows_at(y, torch.float32 if out == OUT_F32 else torch.bfloat16, "y")
+    rp, ldr = _residual(residual, (M, width))
+    aligned = at % 16 == 0 and ldx % 8 == 0 and K % 8 == 0  # no copy, no workspace
+    room, ws, ws_n = (None, None, 0) if aligned and workspace is None else \
+        _room(workspace, x.device, bf16_linear_workspace_bytes, M, N, K)
+    _check(lib.w8a8_bf16_linear(at, ldx, M, K, wp, N, _at(bias, torch.bfloat16, "bias", 1), act, rp, ldr, yp, ldy, out,
+                                ws, ws_n, _stream()))
+    return y
+
+
+def bf16_grouped_workspace_bytes(R: int, E: int, N: int, K: int) -> int:
+    return int(lib.w8a8_bf16_grouped_workspace_bytes(R, E, N, K))
+
+
+def bf16_grouped_gemm(x: torch.Tensor, group_list: torch.Tensor, w_packed: torch.Tensor, N: int, act: int = ACT_NONE,
+                      row_index: torch.Tensor | None = None, y: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows grouped by expert (group_list int64 [E]) times each expert's BF16 weight [N, K]
+    (bf16_prepack_weight of [E, N, K]) -> BF16 [R, N], or [R, N/2] with act=ACT_SWIGLU. Output
+    row r reads row row_index[r] of x (int32 [R]), or row r without it. x may be
+    row-strided."""
+    at, ldx = _rows_at(x, torch.bfloat16, "x")
+    A, K = x.shape
+    gl = _at(group_list, torch.int64, "group_list", 1)
+    E = group_list.shape[0]
+    wp = _at(w_packed, torch.uint8, "w_packed", 1)
+    if w_packed.numel() < _bf16_packed(E, N, K):
+        raise ValueError("w_packed too small for [E, N, K]")
+    R = A if row_index is None else row_index.shape[0]
+    width = N // 2 if act == ACT_SWIGLU else N
+    if y is None:
+        y = torch.empty((R, width), dtype=torch.bfloat16, device=x.device)
+    if y.shape != (R, width):
+        raise ValueError("y shape mismatch")
+    room, ws, ws_n = _room(workspace, x.device, bf16_grouped_workspace_bytes, R, E, N, K)
+    _check(lib.w8a8_bf16_grouped_gemm(at, ldx, A, _at(row_index, torch.int32, "row_index", 1), gl, R, E, N, K, wp, act,
+                                      _at(y, torch.bfloat16, "y", 2), ws, ws_n, _stream()))
+    return y

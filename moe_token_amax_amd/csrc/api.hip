@@ -12,8 +12,10 @@
 
 #include "../../include/w8a8.h"
 #include "fp8b.hpp"
+#include "fused.hpp"
 #include "launch.hpp"
 #include "mx.hpp"
+#include "norm.hpp"
 #include "w4.hpp"
 
 namespace {
@@ -1181,19 +1183,31 @@ int64_t w8a8_fp8b_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return fp8b_codes_bytes(M, K) + fp8b_scales_bytes(M, K);
 }
 
-int w8a8_fp8b_linear(const void* x, int64_t ldx, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
-                     const float* w_scale, int64_t N, const uint16_t* bias, uint16_t* y, int64_t ldy, int scale_alg,
-                     void* workspace, int64_t ws_bytes, void* stream) {
+// the activations of a fused epilogue; SwiGLU only where the weight's halves are paired
+static int check_act(const char* who, int act, bool swiglu) {
+  if (act < W8A8_ACT_NONE || act > W8A8_ACT_GELU_TANH || (act == W8A8_ACT_SWIGLU && !swiglu))
+    return fail(W8A8_ERR_UNSUPPORTED, "%s: unknown act %d", who, act);
+  return W8A8_OK;
+}
+
+int w8a8_fp8b_linear_fused(const void* x, int64_t ldx, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
+                           const float* w_scale, int64_t N, const uint16_t* bias, int act, const uint16_t* residual,
+                           int64_t ldr, uint16_t* y, int64_t ldy, int scale_alg, void* workspace, int64_t ws_bytes,
+                           void* stream) {
   int st = check_fp8b("fp8b_linear", M, N, K);
   if (st) return st;
   st = check_scale_alg("fp8b_linear", scale_alg);
   if (st) return st;
+  st = check_act("fp8b_linear", act, false);
+  if (st) return st;
+  if (residual && ldr < N)
+    return fail(W8A8_ERR_SHAPE, "fp8b_linear: ldr = %lld is below the row width", (long long)ldr);
   if (ldy < N || ldx < (x_scale ? fp8b_pad(K) : K))
     return fail(W8A8_ERR_SHAPE, "fp8b_linear: ldx = %lld or ldy = %lld is below the row width", (long long)ldx,
                 (long long)ldy);
   if (M == 0) return ok();
   if (!x || !w_packed || !w_scale || !y) return fail(W8A8_ERR_NULL, "fp8b_linear: null pointer");
-  if (!aligned(w_packed, 16) || !aligned(w_scale, 4) || !aligned(bias, 2) || !aligned(y, 2) ||
+  if (!aligned(w_packed, 16) || !aligned(w_scale, 4) || !aligned(bias, 2) || !aligned(residual, 2) || !aligned(y, 2) ||
       !aligned(x_scale, 4) || !aligned(x, x_scale ? 16 : 2) || (x_scale && ldx % 16))
     return fail(W8A8_ERR_ALIGN, "fp8b_linear: w_packed and E4M3 rows need 16-byte, scales 4-byte, BF16 2-byte "
                                 "alignment");
@@ -1209,6 +1223,9 @@ int w8a8_fp8b_linear(const void* x, int64_t ldx, const float* x_scale, int64_t M
     if (w8a8::fp8b_fused_ok(M, K)) {
       w8a8::Fp8bGemm p = fp8b_args(a, ldx, nullptr, M, M, K, w_packed, w_scale, N, y);
       p.bias = bias;
+      p.act = act;
+      p.residual = residual;
+      p.ldr = ldr;
       p.ldy = ldy;
       p.K = K;
       p.scale_alg = scale_alg;
@@ -1224,8 +1241,18 @@ int w8a8_fp8b_linear(const void* x, int64_t ldx, const float* x_scale, int64_t M
   }
   w8a8::Fp8bGemm p = fp8b_args(a, lda, as, M, M, K, w_packed, w_scale, N, y);
   p.bias = bias;
+  p.act = act;
+  p.residual = residual;
+  p.ldr = ldr;
   p.ldy = ldy;
   return launched(w8a8::launch_fp8b_gemm(p, s), "fp8b_linear");
+}
+
+int w8a8_fp8b_linear(const void* x, int64_t ldx, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
+                     const float* w_scale, int64_t N, const uint16_t* bias, uint16_t* y, int64_t ldy, int scale_alg,
+                     void* workspace, int64_t ws_bytes, void* stream) {
+  return w8a8_fp8b_linear_fused(x, ldx, x_scale, M, K, w_packed, w_scale, N, bias, W8A8_ACT_NONE, nullptr, 0, y, ldy,
+                                scale_alg, workspace, ws_bytes, stream);
 }
 
 int64_t w8a8_fp8b_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K) {
@@ -1386,6 +1413,280 @@ int w8a8_fp8b_moe_layer(const uint16_t* x, int64_t T, int64_t H, const int32_t* 
                    s);
   if (err != hipSuccess) return launched(err, "fp8b_moe_layer: experts");
   return launched(w8a8::launch_combine(y, pr, topk_weights, T, top_k, P, H, out, s), "fp8b_moe_layer: combine");
+}
+
+// ---------------------------------------------------------------------------
+// RMS norm
+// ---------------------------------------------------------------------------
+static int rms_norm(const char* who, int format, const w8a8::NormArgs& p, void* stream) {
+  if (p.M < 0 || p.K < 1 || p.M >= kMaxDim || p.K > W8A8_MAX_K)
+    return fail(W8A8_ERR_SHAPE, "%s: need M >= 0 and 1 <= K <= %d (M=%lld K=%lld)", who, W8A8_MAX_K, (long long)p.M,
+                (long long)p.K);
+  if (!(p.eps >= 0.0) || std::isinf(p.eps)) return fail(W8A8_ERR_SHAPE, "%s: eps must be finite and at least 0", who);
+  if (format == w8a8::kNormMx && p.K % 32)
+    return fail(W8A8_ERR_UNSUPPORTED, "%s: needs K %% 32 == 0 (K=%lld)", who, (long long)p.K);
+  if (p.scale_alg != 0 && p.scale_alg != 1) return fail(W8A8_ERR_UNSUPPORTED, "%s: scale_alg must be 0 or 1", who);
+  if (p.ldx < p.K || (p.residual && (p.ldr < p.K || p.ldh < p.K)) || (p.y && p.ldy < p.K) ||
+      (format == w8a8::kNormInt8 && p.ldq < p.K))
+    return fail(W8A8_ERR_SHAPE, "%s: a row stride is below the row width %lld", who, (long long)p.K);
+  if (p.M == 0) return ok();
+  if (!p.x || (p.residual && !p.h) || (format == w8a8::kNormBf16 ? !p.y : !p.q || !p.scale))
+    return fail(W8A8_ERR_NULL, "%s: null pointer", who);
+  if (!aligned(p.x, 2) || !aligned(p.residual, 2) || !aligned(p.h, 2) || !aligned(p.weight, 2) || !aligned(p.y, 2) ||
+      (format == w8a8::kNormFp8b && !aligned(p.q, 16)) || (format == w8a8::kNormMx && !aligned(p.q, 8)) ||
+      (format != w8a8::kNormMx && !aligned(p.scale, 4)))
+    return fail(W8A8_ERR_ALIGN, "%s: BF16 buffers need 2-byte, float scales 4-byte, E4M3 codes 16-byte (MX: 8-byte) "
+                                "alignment", who);
+  return launched(w8a8::launch_rms_norm(format, p, (hipStream_t)stream), who);
+}
+
+static w8a8::NormArgs norm_args(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, uint16_t* h,
+                                int64_t ldh, const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* y,
+                                int64_t ldy) {
+  w8a8::NormArgs p{};
+  p.x = x;
+  p.ldx = ldx;
+  p.residual = residual;
+  p.ldr = ldr;
+  p.h = h;
+  p.ldh = ldh;
+  p.weight = weight;
+  p.eps = eps;
+  p.M = M;
+  p.K = K;
+  p.y = y;
+  p.ldy = ldy;
+  return p;
+}
+
+int w8a8_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, uint16_t* h, int64_t ldh,
+                  const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* y, int64_t ldy, void* stream) {
+  return rms_norm("rms_norm", w8a8::kNormBf16, norm_args(x, ldx, residual, ldr, h, ldh, weight, eps, M, K, y, ldy),
+                  stream);
+}
+
+int w8a8_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, uint16_t* h, int64_t ldh,
+                        const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* y, int64_t ldy, int8_t* q,
+                        int64_t ldq, float* scale, void* stream) {
+  w8a8::NormArgs p = norm_args(x, ldx, residual, ldr, h, ldh, weight, eps, M, K, y, ldy);
+  p.q = reinterpret_cast<uint8_t*>(q);
+  p.ldq = ldq;
+  p.scale = scale;
+  return rms_norm("rms_norm_quant", w8a8::kNormInt8, p, stream);
+}
+
+int w8a8_fp8b_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, uint16_t* h,
+                             int64_t ldh, const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* y,
+                             int64_t ldy, int scale_alg, uint8_t* q, float* scale, void* stream) {
+  w8a8::NormArgs p = norm_args(x, ldx, residual, ldr, h, ldh, weight, eps, M, K, y, ldy);
+  p.q = q;
+  p.ldq = fp8b_pad(K);
+  p.scale = scale;
+  p.scale_alg = scale_alg;
+  return rms_norm("fp8b_rms_norm_quant", w8a8::kNormFp8b, p, stream);
+}
+
+int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, uint16_t* h,
+                           int64_t ldh, const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* y,
+                           int64_t ldy, int scale_alg, uint8_t* e4m3, uint8_t* e8m0, void* stream) {
+  w8a8::NormArgs p = norm_args(x, ldx, residual, ldr, h, ldh, weight, eps, M, K, y, ldy);
+  p.q = e4m3;
+  p.ldq = K;
+  p.scale = e8m0;
+  p.scale_alg = scale_alg;
+  return rms_norm("mx_rms_norm_quant", w8a8::kNormMx, p, stream);
+}
+
+// ---------------------------------------------------------------------------
+// products with a fused epilogue
+// ---------------------------------------------------------------------------
+namespace {
+
+w8a8::FusedGemm fused_int8(const int8_t* q, int64_t ldq, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
+                           const float* w_scale, int64_t N) {
+  w8a8::FusedGemm p{};
+  p.type = w8a8::kFusedInt8;
+  p.a = reinterpret_cast<const uint8_t*>(q);
+  p.lda = ldq;
+  p.kbytes = K;
+  p.a_rows = p.M = M;
+  p.w = reinterpret_cast<const uint8_t*>(w_packed);
+  p.NB = w8a8::ceil_div(N, 16);
+  p.KP = w8a8::ceil_div(K, 64);
+  p.N = N;
+  p.a_scale = x_scale;
+  p.w_scale = w_scale;
+  return p;
+}
+
+w8a8::FusedGemm fused_bf16(const uint16_t* x, int64_t ldx, int64_t rows, int64_t M, int64_t K, const void* w_packed,
+                           int64_t N, int act) {
+  w8a8::FusedGemm p{};
+  p.type = w8a8::kFusedBf16;
+  p.a = reinterpret_cast<const uint8_t*>(x);
+  p.lda = 2 * ldx;
+  p.kbytes = 2 * K;
+  p.a_rows = rows;
+  p.M = M;
+  p.w = reinterpret_cast<const uint8_t*>(w_packed);
+  p.NB = w8a8::round_up(N, 32) / 16;
+  p.KP = 2 * w8a8::ceil_div(K, 64);
+  p.N = N;
+  p.act = act;
+  return p;
+}
+
+// Rows copied into the workspace, where the kernel wants them aligned.
+int fused_room(const char* who, const w8a8::FusedGemm& p, const void* workspace, int64_t ws_bytes) {
+  if (!w8a8::fused_needs_copy(p)) return W8A8_OK;
+  const int64_t need = w8a8::fused_copy_bytes(p.M, p.kbytes);
+  if (!workspace || ws_bytes < need || !aligned(workspace, 256))
+    return fail(W8A8_ERR_WORKSPACE, "%s: needs %lld workspace bytes (256-byte aligned), got %lld", who, (long long)need,
+                (long long)ws_bytes);
+  return W8A8_OK;
+}
+
+}  // namespace
+
+int64_t w8a8_linear_fused_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return w8a8::fused_copy_bytes(M, K);
+}
+
+int w8a8_linear_fused(const int8_t* q, int64_t ldq, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
+                      const float* w_scale, int64_t N, const uint16_t* bias, int act, const uint16_t* residual,
+                      int64_t ldr, uint16_t* y, int64_t ldy, void* workspace, int64_t ws_bytes, void* stream) {
+  int st = check_fp8b("linear_fused", M, N, K);
+  if (st) return st;
+  st = check_act("linear_fused", act, false);
+  if (st) return st;
+  if (ldq < K || ldy < N || (residual && ldr < N))
+    return fail(W8A8_ERR_SHAPE, "linear_fused: a row stride is below the row width (ldq=%lld ldy=%lld ldr=%lld)",
+                (long long)ldq, (long long)ldy, (long long)ldr);
+  if (M == 0) return ok();
+  if (!q || !x_scale || !w_packed || !w_scale || !y) return fail(W8A8_ERR_NULL, "linear_fused: null pointer");
+  if (!aligned(w_packed, 16) || !aligned(x_scale, 4) || !aligned(w_scale, 4) || !aligned(bias, 2) ||
+      !aligned(residual, 2) || !aligned(y, 2))
+    return fail(W8A8_ERR_ALIGN, "linear_fused: w_packed needs 16-byte, scales 4-byte, BF16 2-byte alignment");
+  w8a8::FusedGemm p = fused_int8(q, ldq, x_scale, M, K, w_packed, w_scale, N);
+  p.bias = bias;
+  p.act = act;
+  p.residual = residual;
+  p.ldr = ldr;
+  p.y = y;
+  p.ldy = ldy;
+  st = fused_room("linear_fused", p, workspace, ws_bytes);
+  if (st) return st;
+  return launched(w8a8::launch_fused_gemm(p, workspace, (hipStream_t)stream), "linear_fused");
+}
+
+int64_t w8a8_bf16_packed_bytes(int64_t E, int64_t N, int64_t K) {
+  if (E < 0 || N < 0 || K < 0) return -1;
+  return E * w8a8::bf16_packed_bytes(N, K);
+}
+
+int w8a8_bf16_prepack_weight(const uint16_t* w, int64_t E, int64_t N, int64_t K, int act, void* w_packed, void* stream) {
+  int st = check_fp8b("bf16_prepack_weight", 0, N, K);
+  if (st) return st;
+  st = check_act("bf16_prepack_weight", act, true);
+  if (st) return st;
+  if (E < 1) return fail(W8A8_ERR_SHAPE, "bf16_prepack_weight: need E >= 1");
+  if (act == W8A8_ACT_SWIGLU && N % 2)
+    return fail(W8A8_ERR_SHAPE, "bf16_prepack_weight: SwiGLU needs an even N, got %lld", (long long)N);
+  if (!w || !w_packed) return fail(W8A8_ERR_NULL, "bf16_prepack_weight: null pointer");
+  if (!aligned(w, 2) || !aligned(w_packed, 16))
+    return fail(W8A8_ERR_ALIGN, "bf16_prepack_weight: w needs 2-byte and w_packed 16-byte alignment");
+  return launched(w8a8::launch_bf16_prepack(w, E, N, K, act == W8A8_ACT_SWIGLU, w_packed, (hipStream_t)stream),
+                  "bf16_prepack_weight");
+}
+
+int64_t w8a8_bf16_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0) return 0;
+  return w8a8::fused_copy_bytes(M, 2 * K);
+}
+
+int w8a8_bf16_linear(const uint16_t* x, int64_t ldx, int64_t M, int64_t K, const void* w_packed, int64_t N,
+                     const uint16_t* bias, int act, const uint16_t* residual, int64_t ldr, void* y, int64_t ldy, int out,
+                     void* workspace, int64_t ws_bytes, void* stream) {
+  int st = check_fp8b("bf16_linear", M, N, K);
+  if (st) return st;
+  st = check_act("bf16_linear", act, true);
+  if (st) return st;
+  if (out != W8A8_OUT_BF16 && out != W8A8_OUT_F32)
+    return fail(W8A8_ERR_UNSUPPORTED, "bf16_linear: unknown output kind %d", out);
+  if (act == W8A8_ACT_SWIGLU && N % 2)
+    return fail(W8A8_ERR_SHAPE, "bf16_linear: SwiGLU needs an even N, got %lld", (long long)N);
+  const int64_t width = act == W8A8_ACT_SWIGLU ? N / 2 : N;
+  if (ldx < K || ldy < width || (residual && ldr < width))
+    return fail(W8A8_ERR_SHAPE, "bf16_linear: a row stride is below the row width (ldx=%lld ldy=%lld ldr=%lld)",
+                (long long)ldx, (long long)ldy, (long long)ldr);
+  if (M == 0) return ok();
+  if (!x || !w_packed || !y) return fail(W8A8_ERR_NULL, "bf16_linear: null pointer");
+  if (!aligned(w_packed, 16) || !aligned(x, 2) || !aligned(bias, 2) || !aligned(residual, 2) ||
+      !aligned(y, out == W8A8_OUT_F32 ? 4 : 2))
+    return fail(W8A8_ERR_ALIGN, "bf16_linear: w_packed needs 16-byte, BF16 2-byte, float 4-byte alignment");
+  w8a8::FusedGemm p = fused_bf16(x, ldx, M, M, K, w_packed, N, act);
+  p.bias = bias;
+  p.residual = residual;
+  p.ldr = ldr;
+  p.y = y;
+  p.ldy = ldy;
+  p.f32 = out == W8A8_OUT_F32;
+  st = fused_room("bf16_linear", p, workspace, ws_bytes);
+  if (st) return st;
+  return launched(w8a8::launch_fused_gemm(p, workspace, (hipStream_t)stream), "bf16_linear");
+}
+
+static int check_bf16_grouped(const char* who, int64_t R, int64_t E, int64_t N, int64_t K) {
+  int st = check_fp8b(who, R, N, K);
+  if (st) return st;
+  if (E < 1) return fail(W8A8_ERR_SHAPE, "%s: need E >= 1", who);
+  if (E > kMaxExperts) return fail(W8A8_ERR_UNSUPPORTED, "%s: at most %lld experts", who, (long long)kMaxExperts);
+  if (K < 8) return fail(W8A8_ERR_UNSUPPORTED, "%s: needs K >= 8", who);
+  if (w8a8::fused_grid(R, E, w8a8::round_up(N, 32)) >= (int64_t)1 << 23)  // of 512 threads
+    return fail(W8A8_ERR_UNSUPPORTED, "%s: R = %lld rows of N = %lld columns are past one launch", who, (long long)R,
+                (long long)N);
+  return W8A8_OK;
+}
+
+int64_t w8a8_bf16_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K) {
+  if (R <= 0 || E <= 0 || N <= 0 || K <= 0) return 0;
+  return w8a8::fused_sched_bytes(R, E);
+}
+
+int w8a8_bf16_grouped_gemm(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_t* row_index,
+                           const int64_t* group_list, int64_t R, int64_t E, int64_t N, int64_t K, const void* w_packed,
+                           int act, uint16_t* y, void* workspace, int64_t ws_bytes, void* stream) {
+  int st = check_bf16_grouped("bf16_grouped_gemm", R, E, N, K);
+  if (st) return st;
+  st = check_act("bf16_grouped_gemm", act, true);
+  if (st) return st;
+  if (act == W8A8_ACT_SWIGLU && N % 2)
+    return fail(W8A8_ERR_SHAPE, "bf16_grouped_gemm: SwiGLU needs an even N, got %lld", (long long)N);
+  if (ldx < K) return fail(W8A8_ERR_SHAPE, "bf16_grouped_gemm: ldx = %lld is below the row width", (long long)ldx);
+  if (R == 0) return ok();
+  if (x_rows < 1 || x_rows >= kFp8MaxM || (!row_index && x_rows < R))
+    return fail(W8A8_ERR_SHAPE, "bf16_grouped_gemm: x_rows = %lld rows do not cover R = %lld", (long long)x_rows,
+                (long long)R);
+  if (!x || !group_list || !w_packed || !y) return fail(W8A8_ERR_NULL, "bf16_grouped_gemm: null pointer");
+  if (!aligned(x, 2) || !aligned(row_index, 4) || !aligned(group_list, 8) || !aligned(w_packed, 16) || !aligned(y, 2))
+    return fail(W8A8_ERR_ALIGN, "bf16_grouped_gemm: misaligned buffer");
+  const int64_t need = w8a8::fused_sched_bytes(R, E);
+  if (!workspace || ws_bytes < need || !aligned(workspace, 256))
+    return fail(W8A8_ERR_WORKSPACE, "bf16_grouped_gemm: needs %lld workspace bytes (256-byte aligned), got %lld",
+                (long long)need, (long long)ws_bytes);
+  st = check_group_list("bf16_grouped_gemm", group_list, E, R, stream);
+  if (st) return st;
+  w8a8::FusedGemm p = fused_bf16(x, ldx, x_rows, R, K, w_packed, N, act);
+  p.row_index = row_index;
+  p.group_list = group_list;
+  p.E = E;
+  p.y = y;
+  p.ldy = act == W8A8_ACT_SWIGLU ? N / 2 : N;
+  p.ws = workspace;
+  const hipError_t err = w8a8::launch_fused_schedule(group_list, E, R, workspace, (hipStream_t)stream);
+  if (err != hipSuccess) return launched(err, "bf16_grouped_gemm: schedule");
+  return launched(w8a8::launch_fused_gemm(p, nullptr, (hipStream_t)stream), "bf16_grouped_gemm");
 }
 
 }  // extern "C"

@@ -22,8 +22,10 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "bf16_io.hpp"
 #include "device_common.hpp"
-#include "dpp_row.hpp"
+#include "epilogue.hpp"
+#include "fp8_codes.hpp"
 #include "fp8b.hpp"
 #include "launch.hpp"
 
@@ -33,12 +35,6 @@ typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFp8BlockBytes = 2048;  // 16 rows x 128 k: two 1 KB pieces of 64 k
-
-// fp32 -> BF16 with the hardware conversion: half to even, NaN stays NaN
-__device__ __forceinline__ uint16_t to_bf16(float f) {
-  const __bf16 b = (__bf16)f;
-  return __builtin_bit_cast(uint16_t, b);
-}
 
 // ---------------------------------------------------------------------------
 // Schedule of a grouped product: int32 count (256 bytes), then int4 {expert,
@@ -127,98 +123,6 @@ hipError_t launch_fp8b_schedule(const int64_t* group_list, int64_t E, int64_t R,
 // ---------------------------------------------------------------------------
 // quant
 // ---------------------------------------------------------------------------
-// Scale of a block from the bits of its largest magnitude. alg 1: the smallest
-// power of two (at least 2^-126) not below amax / 448. NaN stays NaN.
-__device__ __forceinline__ float block_scale(uint32_t amax_bits, int alg) {
-  const float s = __uint_as_float(amax_bits) / 448.0f;
-  if (alg == 0 || !(s > 0.0f) || !(s <= 3.402823466e38f)) return s;
-  return __uint_as_float((__float_as_uint(s) + 0x7FFFFFu) & 0xFF800000u);
-}
-
-// fl(x / s) clamped to +-448. With y = fl(1 / s) correctly rounded, q = fl(x y) and
-// r = x - q s (exact in one fused operation), fl(q + r y) is the correctly rounded
-// quotient (P. Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990): three operations instead of the division's
-// eleven, the reciprocal shared by the block. Exact means no underflow: with s in
-// [2^-80, 2^80] r is representable for every quotient above 2^-22, and a smaller
-// one has code 0 anyway, whose sign is x's (x = -0 gives q + r y = +0). Other
-// scales divide.
-__device__ __forceinline__ float quotient(float x, float s, float y) {
-  const float q = x * y;
-  const float t = __builtin_fmaf(__builtin_fmaf(-q, s, x), y, q);
-  return __builtin_amdgcn_fmed3f(__builtin_copysignf(t, x), -448.0f, 448.0f);
-}
-
-__device__ __forceinline__ uint2 pack_codes(const float (&t)[8]) {
-  int lo = 0, hi = 0;
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], lo, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], lo, true);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[4], t[5], hi, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[6], t[7], hi, true);
-  return uint2{(uint32_t)lo, (uint32_t)hi};
-}
-
-// Codes of this lane's 8 values of a block of 128 held by 16 lanes, and its scale.
-__device__ __forceinline__ uint2 quant_block(const float (&v)[8], int alg, float& s) {
-  uint32_t am = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) am = max(am, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  s = block_scale(row_max_u32(am), alg);
-  float t[8];
-  if (s >= 0x1p-80f && s <= 0x1p+80f) {
-    const float y = 1.0f / s;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = quotient(v[j], s, y);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      t[j] = s > 0.0f ? v[j] / s : 0.0f;  // s NaN: 0
-      // an infinity over its infinite scale stays NaN (the limits alone would make it -448)
-      if (!__builtin_isnan(t[j])) t[j] = fminf(fmaxf(t[j], -448.0f), 448.0f);
-    }
-  }
-  return pack_codes(t);
-}
-
-// 16 and 8 bytes at any BF16 address: gfx950 loads and stores them in one
-// instruction, at full rate where they happen to be aligned, so odd widths need no
-// path of their own (in single values the quantizer took 20.3 us for 4096 x 4097,
-// now 10.1, and a product's outputs 52 us for 5366 x 4089 x 197, now 34)
-struct __attribute__((packed, aligned(2))) Bytes16 {
-  uint32_t w[4];
-};
-struct __attribute__((packed, aligned(2))) Bytes8 {
-  uint32_t w[2];
-};
-
-// 8 values from src, n of them in the row (0 past it), and with PAIR 8 more from
-// src + next (under one branch, so that both loads are in flight together)
-template <bool PAIR>
-__device__ __forceinline__ void load8(const uint16_t* src, int64_t next, int64_t n, float (&v)[8], float (&u)[8]) {
-  Bytes16 a{}, b{};
-  if (n >= 8) {
-    a = *reinterpret_cast<const Bytes16*>(src);
-    if (PAIR) b = *reinterpret_cast<const Bytes16*>(src + next);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j < n) {
-        a.w[j / 2] |= (uint32_t)src[j] << (16 * (j & 1));
-        if (PAIR) b.w[j / 2] |= (uint32_t)src[next + j] << (16 * (j & 1));
-      }
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = __uint_as_float(a.w[j] << 16);
-    v[2 * j + 1] = __uint_as_float(a.w[j] & 0xFFFF0000u);
-    if (PAIR) {
-      u[2 * j] = __uint_as_float(b.w[j] << 16);
-      u[2 * j + 1] = __uint_as_float(b.w[j] & 0xFFFF0000u);
-    }
-  }
-}
-
 // ACT 1 quantizes swiglu_fixed, the INT8 quantizer's sequence of single roundings (its
 // exponential is within 1.2 ulp): one SwiGLU for both, whose codes can be pinned bit by
 // bit. It keeps the vector unit busy without a pause (16384 x 2048: 49 to 52 us, HBM 35).
@@ -382,10 +286,32 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// four neighbouring outputs of one row
+// Four neighbouring outputs of one row. EPI: the activation and the residual too, on the
+// fp32 sums (kernels of their own: the plain ones keep their registers).
+template <bool EPI>
 __device__ __forceinline__ void store4(const Fp8bGemm& p, int64_t m, int64_t n, const f32x4& v) {
   if (n >= p.N) return;
   uint16_t* y = p.y + m * p.ldy + n;
+  if (EPI) {
+    const int left = (int)min((int64_t)4, p.N - n);
+    float b[4], r[4];
+    if (p.bias) load_bf16x4(p.bias + n, left, b);
+    if (p.residual) load_bf16x4(p.residual + m * p.ldr + n, left, r);
+    uint16_t o[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const float a = activate(p.act, p.bias ? v[t] + b[t] : v[t]);
+      o[t] = to_bf16(p.residual ? a + r[t] : a);
+    }
+    if (left == 4) {
+      *reinterpret_cast<Bytes8*>(y) = Bytes8{{o[0] | ((uint32_t)o[1] << 16), o[2] | ((uint32_t)o[3] << 16)}};
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (t < left) y[t] = o[t];
+    }
+    return;
+  }
   if (n + 4 <= p.N) {
     float b[4] = {0.f, 0.f, 0.f, 0.f};
     if (p.bias) {
@@ -419,7 +345,7 @@ __device__ __forceinline__ void store4(const Fp8bGemm& p, int64_t m, int64_t n, 
 // the difference, past that the LDS carries as much as the MFMAs take: 256 experts of
 // 4096 x 4096, 2 / 32 / 64 / 128 rows each, exact 699 / 752 / 839 / 1282 us, else 695 /
 // 748 / 788 / 931 (6.2 to 4.6 TB/s).
-template <int MB, int NBW, bool EXACT>
+template <int MB, int NBW, bool EXACT, bool EPI = false>
 struct StreamTile {
   static constexpr int kAhead = 3, kSets = kAhead + 1;  // blocks of weights in flight
   static constexpr int kWaves = 8;
@@ -623,7 +549,7 @@ struct StreamTile {
       const int r = m * 16 + (lane & 15);
       if (r < rows) {
 #pragma unroll
-        for (int j = 0; j < NBW; ++j) store4(p, row0 + r, (int64_t)(nbw + j) * 16 + (lane >> 4) * 4, acc[m][j]);
+        for (int j = 0; j < NBW; ++j) store4<EPI>(p, row0 + r, (int64_t)(nbw + j) * 16 + (lane >> 4) * 4, acc[m][j]);
       }
     }
   }
@@ -668,9 +594,9 @@ __global__ __launch_bounds__(512) void fp8b_grouped_kernel(Fp8bGemm p, int NT) {
 }
 
 // Dense: tiles of one height.
-template <int MB, int NBW>
+template <int MB, int NBW, bool EPI>
 __global__ __launch_bounds__(512) void fp8b_dense_kernel(Fp8bGemm p) {
-  using T = StreamTile<MB, NBW, false>;
+  using T = StreamTile<MB, NBW, false, EPI>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
   const int64_t row0 = (int64_t)blockIdx.x * (MB * 16);
   T::run(p, smem, 0, row0, (int)min((int64_t)(MB * 16), p.M - row0), blockIdx.y * 8 * NBW);
@@ -697,6 +623,7 @@ __global__ __launch_bounds__(512) void fp8b_dense_kernel(Fp8bGemm p) {
 // reads and sums) 140 us on zeros, 169 on normal data (the clock gives way to the
 // power that the data takes), the sums 5 / 20, LDS reads 9 / 7, DMA 15 / 42, barriers
 // 27 / 17.
+template <bool EPI>
 struct WideTile {
   static constexpr int kOperand = 32768;           // one operand of one stage
   static constexpr int kScaleBytes = 1280;         // 256 row scales (and what the last wavefront's DMA runs over)
@@ -853,12 +780,18 @@ struct WideTile {
       for (int kb = KB - 2; kb < KB; ++kb) step(kb, std::true_type{});
 #pragma unroll
       for (int j = 1; j < 4; ++j) add_scaled(acc[7][j], part[j], sc);
+      // EPI: the lane number read here, not kept (with what follows from it) over the K loop
+      int el = lane;
+      if (EPI) {
+        el = threadIdx.x & 63;
+        asm volatile("" : "+v"(el));
+      }
 #pragma unroll
       for (int m = 0; m < 8; ++m) {
-        const int r = wm * 128 + m * 16 + (lane & 15);
+        const int r = wm * 128 + m * 16 + (el & 15);
         if (r < cur.rows) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) store4(p, cur.row0 + r, (int64_t)(cur.nb0 + wn * 4 + j) * 16 + (lane >> 4) * 4, acc[m][j]);
+          for (int j = 0; j < 4; ++j) store4<EPI>(p, cur.row0 + r, (int64_t)(cur.nb0 + wn * 4 + j) * 16 + (el >> 4) * 4, acc[m][j]);
         }
       }
       if (!after.rows) break;
@@ -871,13 +804,15 @@ struct WideTile {
 // Dense: one workgroup a CU; XCD x (workgroups b with b % 8 == x) walks over its own
 // contiguous eighth of the tiles, 8 rows of tiles at a time, so that the tiles it
 // runs together share panels in its L2.
+template <bool EPI>
 __global__ __launch_bounds__(512) void fp8b_wide_kernel(Fp8bGemm p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[WideTile::kLdsBytes];
+  using T = WideTile<EPI>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
   const int64_t MT = (p.M + 255) / 256, NT = (p.N + 255) / 256, total = MT * NT;
   const int64_t per = (total + 7) / 8, first = (blockIdx.x % 8) * per, end = min(first + per, total);
   int64_t t = first + blockIdx.x / 8;
-  WideTile::run(p, smem, [&]() __attribute__((always_inline)) {
-    WideTile::Where w{0, 0, 0};
+  T::run(p, smem, [&]() __attribute__((always_inline)) {
+    typename T::Where w{0, 0, 0};
     if (t < end) {
       const int64_t top = t / (8 * NT) * 8, gm = min((int64_t)8, MT - top), r = t % (8 * NT);
       w.row0 = (top + r % gm) * 256;
@@ -904,7 +839,7 @@ __global__ __launch_bounds__(512) void fp8b_wide_kernel(Fp8bGemm p) {
 constexpr int kDecodeWaves = 8;
 constexpr int64_t kFusedValues = 8192;  // M x K quantized by every workgroup, at most
 
-template <int MB, int NBW, int U, bool FUSED>
+template <int MB, int NBW, int U, bool FUSED, bool EPI>
 __global__ __launch_bounds__(kDecodeWaves * 64) void fp8b_decode_kernel(Fp8bGemm p) {
   __shared__ f32x4 red[kDecodeWaves][MB * NBW][kWave];
   extern __shared__ __attribute__((aligned(16))) uint8_t qlds[];  // FUSED: codes [M][128 KB], scales [KB][M]
@@ -1027,7 +962,7 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fp8b_decode_kernel(Fp8bGemm
 #pragma unroll
   for (int v = 1; v < kDecodeWaves; ++v) sum += red[v][wave][lane];
   const int r = m0 + (wave / NBW) * 16 + (lane & 15);
-  if (r < M) store4(p, r, (int64_t)(nb0 + wave % NBW) * 16 + (lane >> 4) * 4, sum);
+  if (r < M) store4<EPI>(p, r, (int64_t)(nb0 + wave % NBW) * 16 + (lane >> 4) * 4, sum);
 }
 
 // Whether a BF16 x of M rows is quantized inside the decode kernel: every
@@ -1040,21 +975,31 @@ bool fp8b_fused_ok(int64_t M, int64_t K) {
 
 // U: a wavefront's blocks of K, at most as many as registers hold (sets without a
 // block of their own load the last one again)
-template <int MB, int NBW, bool FUSED>
+template <int MB, int NBW, bool FUSED, bool EPI>
 static void launch_decode(const Fp8bGemm& p, hipStream_t stream) {
   constexpr int kMost = MB * NBW >= 8 ? 2 : MB * NBW >= 4 ? 4 : 8;
   const int64_t blocks = ceil_div(p.KB, kDecodeWaves);
-  auto fn = blocks <= 2 ? fp8b_decode_kernel<MB, NBW, 2, FUSED>
-          : blocks <= 4 ? fp8b_decode_kernel<MB, NBW, std::min(4, kMost), FUSED> : fp8b_decode_kernel<MB, NBW, kMost, FUSED>;
+  auto fn = blocks <= 2 ? fp8b_decode_kernel<MB, NBW, 2, FUSED, EPI>
+          : blocks <= 4 ? fp8b_decode_kernel<MB, NBW, std::min(4, kMost), FUSED, EPI>
+                        : fp8b_decode_kernel<MB, NBW, kMost, FUSED, EPI>;
   hipLaunchKernelGGL(fn, dim3((unsigned)ceil_div(ceil_div(p.N, 16), NBW), (unsigned)ceil_div(p.M, 16 * MB)),
                      dim3(kDecodeWaves * 64), FUSED ? (size_t)(p.M * p.KB * (kFp8Block + 4)) : 0, stream, p);
 }
 
+// whether the epilogue is more than a bias
+static bool fp8b_epilogue(const Fp8bGemm& p) { return p.act != W8A8_ACT_NONE || p.residual; }
+
 hipError_t launch_fp8b_linear_fused(const Fp8bGemm& p, hipStream_t stream) {
   // a workgroup a CU at most, if pairs of column blocks reach that
   // (1 x 16384 x 7168: 28.9 us one by one, 26.7 in pairs)
-  if (ceil_div(p.N, 16) <= 256) launch_decode<1, 1, true>(p, stream);
-  else launch_decode<1, 2, true>(p, stream);
+  const bool pairs = ceil_div(p.N, 16) > 256;
+  if (fp8b_epilogue(p)) {
+    if (pairs) launch_decode<1, 2, true, true>(p, stream);
+    else launch_decode<1, 1, true, true>(p, stream);
+  } else {
+    if (pairs) launch_decode<1, 2, true, false>(p, stream);
+    else launch_decode<1, 1, true, false>(p, stream);
+  }
   return hipGetLastError();
 }
 
@@ -1100,25 +1045,26 @@ static DenseKernel dense_kernel(const Fp8bGemm& p) {
   return best;
 }
 
-template <int MB, int NBW>
+template <int MB, int NBW, bool EPI>
 static void launch_dense_tiles(const Fp8bGemm& p, hipStream_t stream) {
-  hipLaunchKernelGGL((fp8b_dense_kernel<MB, NBW>),
+  hipLaunchKernelGGL((fp8b_dense_kernel<MB, NBW, EPI>),
                      dim3((unsigned)ceil_div(p.M, MB * 16), (unsigned)ceil_div(p.N, 128 * NBW)), dim3(512), 0, stream, p);
 }
 
+template <bool EPI>
 static hipError_t launch_dense(const Fp8bGemm& p, hipStream_t stream) {
   switch (dense_kernel(p)) {
-    case kDecode16: launch_decode<1, 1, false>(p, stream); break;
-    case kDecode16x32: launch_decode<1, 2, false>(p, stream); break;
-    case kDecode32: launch_decode<2, 2, false>(p, stream); break;
-    case kDecode64: launch_decode<4, 2, false>(p, stream); break;
-    case kTile32: launch_dense_tiles<2, 1>(p, stream); break;
-    case kTile64: launch_dense_tiles<4, 1>(p, stream); break;
-    case kTile64x256: launch_dense_tiles<4, 2>(p, stream); break;
-    case kTile128: launch_dense_tiles<8, 2>(p, stream); break;
+    case kDecode16: launch_decode<1, 1, false, EPI>(p, stream); break;
+    case kDecode16x32: launch_decode<1, 2, false, EPI>(p, stream); break;
+    case kDecode32: launch_decode<2, 2, false, EPI>(p, stream); break;
+    case kDecode64: launch_decode<4, 2, false, EPI>(p, stream); break;
+    case kTile32: launch_dense_tiles<2, 1, EPI>(p, stream); break;
+    case kTile64: launch_dense_tiles<4, 1, EPI>(p, stream); break;
+    case kTile64x256: launch_dense_tiles<4, 2, EPI>(p, stream); break;
+    case kTile128: launch_dense_tiles<8, 2, EPI>(p, stream); break;
     case kTile256: {
       const int64_t tiles = ceil_div(p.M, 256) * ceil_div(p.N, 256);
-      hipLaunchKernelGGL(fp8b_wide_kernel, dim3((unsigned)std::min<int64_t>(256, round_up(tiles, 8))), dim3(512), 0,
+      hipLaunchKernelGGL(fp8b_wide_kernel<EPI>, dim3((unsigned)std::min<int64_t>(256, round_up(tiles, 8))), dim3(512), 0,
                          stream, p);
       break;
     }
@@ -1128,7 +1074,7 @@ static hipError_t launch_dense(const Fp8bGemm& p, hipStream_t stream) {
 
 hipError_t launch_fp8b_gemm(const Fp8bGemm& p, hipStream_t stream) {
   if (p.M == 0 || p.N == 0) return hipSuccess;
-  if (!p.group_list) return launch_dense(p, stream);
+  if (!p.group_list) return fp8b_epilogue(p) ? launch_dense<true>(p, stream) : launch_dense<false>(p, stream);
   constexpr int NBW = kGroupedNBW;
   const int64_t NT = grouped_columns(p.N);
   const dim3 grid((unsigned)fp8b_grid_tiles(p.M, p.E, p.N));

@@ -31,6 +31,9 @@ struct Fp8bGemm {
   const float* w_scale;      // [E][ceil(N/128)][KB]
   int64_t N;
   const uint16_t* bias;      // [N] or null
+  int act;                   // dense: w8a8_act of the epilogue, not SwiGLU
+  const uint16_t* residual;  // dense: BF16 [M, N], row stride ldr, or null
+  int64_t ldr;
   uint16_t* y;               // BF16 [M, N], row stride ldy
   int64_t ldy;
   const int64_t* group_list; // [E] or null

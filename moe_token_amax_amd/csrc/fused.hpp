@@ -1,0 +1,55 @@
+// Internal launchers of the products with a fused epilogue (host side): INT8 codes,
+// and BF16 rows dense and grouped by expert. Arguments are checked by the C ABI layer
+// before these are called.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace w8a8 {
+
+enum FusedType { kFusedInt8 = 0, kFusedBf16 = 1 };
+
+// One product y = act(a w^T + bias) + residual.
+struct FusedGemm {
+  int type;                  // FusedType
+  const uint8_t* a;          // rows of kbytes bytes, row stride lda bytes
+  int64_t lda, kbytes;
+  int64_t a_rows;            // rows of a (dense: M)
+  const int32_t* row_index;  // grouped: row of a for every output row, or null (the row itself)
+  int64_t M;                 // output rows
+  const uint8_t* w;          // 1 KB blocks [e][n / 16][64 bytes of k]
+  int64_t NB;                // 16-column blocks of an expert
+  int64_t KP;                // 64-byte pieces of K
+  int64_t N;                 // weight rows
+  const float* a_scale;      // INT8: [M]
+  const float* w_scale;      // INT8: [N]
+  const uint16_t* bias;      // [N] or null
+  int act;                   // w8a8_act; SwiGLU: blocks 2 i are gate rows, 2 i + 1 up rows, N / 2 outputs
+  const uint16_t* residual;  // BF16 [M, outputs], row stride ldr, or null
+  int64_t ldr;
+  void* y;                   // BF16 or (f32) float [M, outputs], row stride ldy
+  int64_t ldy;
+  int f32;
+  const int64_t* group_list; // [E] or null
+  int64_t E;
+  const void* ws;            // grouped: the schedule written by launch_fused_schedule
+};
+
+int64_t bf16_packed_bytes(int64_t N, int64_t K);  // of one [N, K] weight
+// pairs: the halves [0, N / 2) and [N / 2, N) of the rows in alternating 16-row blocks
+hipError_t launch_bf16_prepack(const uint16_t* w, int64_t E, int64_t N, int64_t K, bool pairs, void* packed,
+                               hipStream_t stream);
+
+// Rows that the tiles' copies can take as they are: 16-byte aligned, whole 16-byte
+// pieces. Others are copied (zero-padded) to `room` first where those tiles run.
+bool fused_rows_ok(const FusedGemm& p);
+bool fused_needs_copy(const FusedGemm& p);
+int64_t fused_copy_bytes(int64_t M, int64_t kbytes);
+hipError_t launch_fused_gemm(FusedGemm p, void* room, hipStream_t stream);
+
+int64_t fused_sched_bytes(int64_t R, int64_t E);
+int64_t fused_grid(int64_t R, int64_t E, int64_t N);  // workgroups of a grouped product
+hipError_t launch_fused_schedule(const int64_t* group_list, int64_t E, int64_t R, void* ws, hipStream_t stream);
+
+}  // namespace w8a8

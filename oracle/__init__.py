@@ -18,6 +18,8 @@ Sources (web pages, cited by title and section):
     (``oracle/w4a16_ref.py``).
   * [DSV4] again for the static W8A8 scheme (``oracle/static_ref.py``) and for
     the INT8 dispatch and combine around the MoE chain (``oracle/moe_io_ref.py``).
+  * the RMS norm, the fused epilogues and the BF16 products (``oracle/fused_ref.py``) are
+    this library's own definitions, next to the pages' path.
 
 Parity status per function is listed in ``oracle/w8a8_ref.py``'s header.
 """
@@ -28,5 +30,6 @@ from . import moe_io_ref as moe_io  # noqa: F401
 from . import mx_moe_ref as mx_moe  # noqa: F401
 from . import w4a16_ref as w4a16  # noqa: F401
 from . import fp8b_ref as fp8b  # noqa: F401
+from . import fused_ref as fused  # noqa: F401
 from .w8a8_ref import *  # noqa: F401,F403
 from .w8a8_ref import __all__  # noqa: F401

@@ -26,7 +26,7 @@ import numpy as np
 from .mx_ref import e4m3_decode, e4m3_encode
 from .w8a8_ref import bf16_to_f32, swiglu
 
-__all__ = ["BLOCK", "blocks", "quant", "dequant", "weight_dequant", "product64", "cut_bound", "gate"]
+__all__ = ["BLOCK", "blocks", "quant", "quant_f32", "dequant", "weight_dequant", "product64", "cut_bound", "gate"]
 
 BLOCK = 128
 
@@ -41,6 +41,11 @@ def quant(x_bits, act: int = 0, scale_alg: int = 0):
         v = swiglu(x_bits, x_bits.shape[1] // 2)
     else:
         v = bf16_to_f32(x_bits)
+    return quant_f32(v, scale_alg)
+
+
+def quant_f32(v, scale_alg: int = 0):
+    """float32 [M, K] -> codes [M, 128 B], scales [B, M]."""
     v = np.asarray(v, np.float32)
     M, K = v.shape
     B = blocks(K)
