@@ -1536,10 +1536,10 @@ w8a8::FusedGemm fused_bf16(const uint16_t* x, int64_t ldx, int64_t rows, int64_t
   return p;
 }
 
-// Rows copied into the workspace, where the kernel wants them aligned.
+// Rows copied into the workspace, or sums of the parts of K, where the product has them.
 int fused_room(const char* who, const w8a8::FusedGemm& p, const void* workspace, int64_t ws_bytes) {
-  if (!w8a8::fused_needs_copy(p)) return W8A8_OK;
-  const int64_t need = w8a8::fused_copy_bytes(p.M, p.kbytes);
+  const int64_t need = w8a8::fused_room_bytes(p);
+  if (need == 0) return W8A8_OK;
   if (!workspace || ws_bytes < need || !aligned(workspace, 256))
     return fail(W8A8_ERR_WORKSPACE, "%s: needs %lld workspace bytes (256-byte aligned), got %lld", who, (long long)need,
                 (long long)ws_bytes);
@@ -1550,7 +1550,7 @@ int fused_room(const char* who, const w8a8::FusedGemm& p, const void* workspace,
 
 int64_t w8a8_linear_fused_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
-  return w8a8::fused_copy_bytes(M, K);
+  return w8a8::fused_most_bytes(w8a8::kFusedInt8, M, N, K);
 }
 
 int w8a8_linear_fused(const int8_t* q, int64_t ldq, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
@@ -1602,7 +1602,7 @@ int w8a8_bf16_prepack_weight(const uint16_t* w, int64_t E, int64_t N, int64_t K,
 
 int64_t w8a8_bf16_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
-  return w8a8::fused_copy_bytes(M, 2 * K);
+  return w8a8::fused_most_bytes(w8a8::kFusedBf16, M, N, K);
 }
 
 int w8a8_bf16_linear(const uint16_t* x, int64_t ldx, int64_t M, int64_t K, const void* w_packed, int64_t N,
@@ -1684,7 +1684,7 @@ int w8a8_bf16_grouped_gemm(const uint16_t* x, int64_t ldx, int64_t x_rows, const
   p.y = y;
   p.ldy = act == W8A8_ACT_SWIGLU ? N / 2 : N;
   p.ws = workspace;
-  const hipError_t err = w8a8::launch_fused_schedule(group_list, E, R, workspace, (hipStream_t)stream);
+  const hipError_t err = w8a8::launch_fused_schedule(p, workspace, (hipStream_t)stream);
   if (err != hipSuccess) return launched(err, "bf16_grouped_gemm: schedule");
   return launched(w8a8::launch_fused_gemm(p, nullptr, (hipStream_t)stream), "bf16_grouped_gemm");
 }

@@ -56,9 +56,6 @@ struct Elem<kFusedBf16> {
   }
 };
 
-__device__ __forceinline__ int bits_of(int32_t v) { return v; }
-__device__ __forceinline__ int bits_of(float v) { return __float_as_int(v); }
-
 constexpr int kStepBytes = 128;
 constexpr int kPiece = 1024;  // 16 rows x 64 bytes
 
@@ -244,9 +241,10 @@ __global__ __launch_bounds__(256) void fused_copy_kernel(const uint8_t* __restri
 
 // ---------------------------------------------------------------------------
 // Schedule of a grouped product: int32 count (256 bytes), then int4 {expert, first row,
-// rows, 0} for every tile, in expert order: at most kTileRows rows of one expert.
+// rows, 0} for every tile, in expert order: wide tiles of at most 256 rows of one expert
+// while more than kWideFrom are left, then at most kTileRows.
 // ---------------------------------------------------------------------------
-constexpr int kTileRows = 128;
+constexpr int kTileRows = 128, kWideRows = 256, kWideFrom = 160;
 constexpr int kGroupedNBW = 2;
 
 int64_t fused_max_tiles(int64_t R, int64_t E) { return R / kTileRows + std::min(R, E); }
@@ -256,7 +254,7 @@ int64_t fused_grid(int64_t R, int64_t E, int64_t N) { return round_up(fused_max_
 
 // one workgroup of 256 threads, four experts each (E <= 1024)
 __global__ __launch_bounds__(256) void fused_schedule_kernel(const int64_t* __restrict__ group_list, int E, int64_t R,
-                                                             int* count, int4* tiles) {
+                                                             int wide, int* count, int4* tiles) {
   __shared__ int64_t wrows[4];
   __shared__ int wtiles[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -284,7 +282,8 @@ __global__ __launch_bounds__(256) void fused_schedule_kernel(const int64_t* __re
     row0[i] = min(ri, R);
     ri += n[i];
     n[i] = min(n[i], R - row0[i]);
-    t += (int)((n[i] + kTileRows - 1) / kTileRows);
+    const int64_t full = wide ? n[i] / kWideRows : 0, left = n[i] - full * kWideRows;
+    t += (int)(full + (wide && left > kWideFrom ? 1 : (left + kTileRows - 1) / kTileRows));
   }
   int ti = t;
 #pragma unroll
@@ -299,14 +298,20 @@ __global__ __launch_bounds__(256) void fused_schedule_kernel(const int64_t* __re
   ti -= t;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    for (int64_t r = 0; r < n[i]; r += kTileRows)
-      tiles[ti++] = int4{4 * tid + i, (int)(row0[i] + r), (int)min((int64_t)kTileRows, n[i] - r), 0};
+    for (int64_t r = 0; r < n[i];) {
+      const int64_t left = n[i] - r, rows = min(left, (int64_t)(wide && left > kWideFrom ? kWideRows : kTileRows));
+      tiles[ti++] = int4{4 * tid + i, (int)(row0[i] + r), (int)rows, 0};
+      r += rows;
+    }
 }
 
-hipError_t launch_fused_schedule(const int64_t* group_list, int64_t E, int64_t R, void* ws, hipStream_t stream) {
-  hipLaunchKernelGGL(fused_schedule_kernel, dim3(1), dim3(256), 0, stream, group_list, (int)E, R,
-                     reinterpret_cast<int*>(ws), reinterpret_cast<int4*>(reinterpret_cast<char*>(ws) + 256));
-  return hipGetLastError();
+// Place of 16-byte chunk c (0..7) of row r (0..15) of a 16 x 128-byte block in LDS, for
+// rows loaded as whole lines (a load whose neighbouring lanes lie in different rows costs
+// the L1 a look-up for every 16 bytes, this one for every 128: tiles of 64 x 128 took 0.39
+// us a step) and read as operands, 16 rows of one chunk: both ways 16 lanes meet all 64
+// banks.
+__device__ __forceinline__ uint32_t turned(int r, int c) {
+  return (c >> 2) * kPiece + (c & 3) * 256 + ((r ^ (2 * c)) & 15) * 16;
 }
 
 // ---------------------------------------------------------------------------
@@ -319,7 +324,7 @@ hipError_t launch_fused_schedule(const int64_t* group_list, int64_t E, int64_t R
 template <int TY, int MB, int NBW>
 struct StreamTile {
   using Acc = typename Elem<TY>::Acc4;
-  static constexpr int kAhead = 3, kSets = kAhead + 1;            // steps of weights in flight
+  static constexpr int kSets = 4, kAhead = kSets - 1;          // steps of weights in flight
   static constexpr int kWaves = 8;
   static constexpr int kPieces = (2 * MB + kWaves - 1) / kWaves;  // 16-byte pieces a thread stages per step
   static constexpr int kBufBytes = MB * 2 * kPiece;
@@ -332,25 +337,28 @@ struct StreamTile {
     i32x4 v[NBW][2];
   };
 
-  __device__ __forceinline__ static void run(const FusedGemm& p, uint8_t* smem, int e, int64_t row0, int rows, int nb0) {
+  // Steps [k0, k1) of K. part: the sums go there as they are (a tile's kPartBytes, one 16 x
+  // 16 block after the other), for the join of a product whose K is split.
+  static constexpr int64_t kPartBytes = (int64_t)kWaves * MB * NBW * kPiece;
+
+  __device__ __forceinline__ static void run(const FusedGemm& p, uint8_t* smem, int e, int64_t row0, int rows, int nb0,
+                                             int k0, int k1, uint8_t* part) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int NB = (int)p.NB, KP = (int)p.KP, KB = (KP + 1) / 2;
     const uint32_t last = (uint32_t)p.kbytes - 16;
     const int nbw = nb0 + wave * NBW;
-    // sources of this thread's pieces: piece (m-block, half) = wave + 8 i, lane: row
-    // l % 16, 16 bytes at l / 16. Rows past the tile read its last row; they only feed
-    // outputs that are never stored.
+    // This thread's pieces of a step: 8 rows x 128 bytes (whole cache lines) each, piece
+    // wave + 8 i, lane: row l / 8, 16-byte chunk l % 8. Rows past the tile read its last
+    // row; they only feed outputs that are never stored.
     const uint8_t* ap[kPieces];
-    uint32_t at[kPieces];
+    const uint32_t at = (lane & 7) * 16;
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-      const int piece = wave + kWaves * i;
-      const int r = min((piece >> 1) * 16 + (lane & 15), rows - 1);
+      const int r = min((wave + kWaves * i) * 8 + (lane >> 3), rows - 1);
       int64_t src = row0 + r;
       if (p.row_index) src = max((int64_t)0, min((int64_t)p.row_index[src], p.a_rows - 1));
       ap[i] = p.a + src * p.lda;
-      at[i] = (piece & 1) * 64 + (lane >> 4) * 16;
     }
     const uint8_t* wp[NBW];
 #pragma unroll
@@ -360,30 +368,32 @@ struct StreamTile {
 
     auto load_w = [&](Weights& w, int kb) __attribute__((always_inline)) {
       // an odd last piece is read twice: a is zero there
-      const int64_t k0 = min(2 * kb, KP - 1), k1 = min(2 * kb + 1, KP - 1);
+      kb = min(kb, k1 - 1);
+      const int64_t c0 = 2 * kb, c1 = min(2 * kb + 1, KP - 1);
 #pragma unroll
       for (int j = 0; j < NBW; ++j) {
-        w.v[j][0] = *reinterpret_cast<const i32x4*>(wp[j] + k0 * kPiece + l16);
-        w.v[j][1] = *reinterpret_cast<const i32x4*>(wp[j] + k1 * kPiece + l16);
+        w.v[j][0] = *reinterpret_cast<const i32x4*>(wp[j] + c0 * kPiece + l16);
+        w.v[j][1] = *reinterpret_cast<const i32x4*>(wp[j] + c1 * kPiece + l16);
       }
     };
     auto load_a = [&](Stage& st, int kb) __attribute__((always_inline)) {
-      const uint32_t k = (uint32_t)min(kb, KB - 1) * kStepBytes;
+      const uint32_t k = (uint32_t)min(kb, k1 - 1) * kStepBytes;
 #pragma unroll
       for (int i = 0; i < kPieces; ++i)
-        if (2 * MB >= kWaves * (i + 1) || wave + kWaves * i < 2 * MB) st.a[i] = load16(ap[i], k + at[i], last);
+        if (2 * MB >= kWaves * (i + 1) || wave + kWaves * i < 2 * MB) st.a[i] = load16(ap[i], k + at, last);
     };
     auto store_a = [&](Stage& st, uint8_t* buf, int kb) __attribute__((always_inline)) {
-      if (kb >= KB - 1) {  // the last step (or a copy of it)
-        const int past = (KB - 1) * kStepBytes - (int)last;
+      if (min(kb, k1 - 1) == KB - 1) {  // the last step (or a copy of it)
+        const int past = (KB - 1) * kStepBytes - (int)last + (int)at;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) st.a[i] = fix16(st.a[i], past + (int)at[i]);
+        for (int i = 0; i < kPieces; ++i) st.a[i] = fix16(st.a[i], past);
       }
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
         const int piece = wave + kWaves * i;
         if (2 * MB >= kWaves * (i + 1) || piece < 2 * MB)
-          *reinterpret_cast<i32x4*>(buf + piece * kPiece + l16) = st.a[i];
+          *reinterpret_cast<i32x4*>(buf + (piece >> 1) * 2 * kPiece + turned((piece & 1) * 8 + (lane >> 3), lane & 7)) =
+              st.a[i];
       }
     };
 
@@ -393,68 +403,106 @@ struct StreamTile {
 #pragma unroll
       for (int j = 0; j < NBW; ++j) acc[m][j] = Acc{0, 0, 0, 0};
 
-    constexpr int kD = MB < 2 ? MB : 2;
+    constexpr int kD = MB * NBW > 2 ? 2 : MB, kF = 2 * kD;
     struct Frag {
       i32x4 v[2];
     };
-    Frag f[4];
+    Frag f[kF];
+    const uint32_t r0 = turned(lane & 15, lane >> 4);  // the second half's chunks: 4 more, so ^ 128
     auto read_a = [&](Frag& d, const uint8_t* buf, int m) __attribute__((always_inline)) {
-      d.v[0] = *reinterpret_cast<const i32x4*>(buf + m * 2 * kPiece + l16);
-      d.v[1] = *reinterpret_cast<const i32x4*>(buf + m * 2 * kPiece + kPiece + l16);
+      d.v[0] = *reinterpret_cast<const i32x4*>(buf + m * 2 * kPiece + r0);
+      d.v[1] = *reinterpret_cast<const i32x4*>(buf + m * 2 * kPiece + (r0 ^ 128) + kPiece);
     };
-    // Step kb: weights in set kb % 4, rows in buffer kb % 4. The weights of kb + 3 and the
-    // rows of kb + 3 are loaded; kb is multiplied, each operand read kD row blocks before
-    // its MFMAs (the first ones in the step before, so that no wavefront waits for LDS
-    // right behind the barrier); the rows of kb + 2 go to their buffer, last read in step
-    // kb - 2, and are read from the end of step kb + 1 on, behind the barrier of step kb.
-    // Loads past the last step read it again.
+    // Step kb: weights in set (kb - k0) % 4, rows in that buffer. The weights of kb + 3 and
+    // the rows of kb + 5 are loaded; kb is multiplied, each operand read kD row blocks
+    // before its MFMAs (the first ones in the step before, so that no wavefront waits for
+    // LDS right behind the barrier); the rows of kb + 2, loaded three steps ago, go to their
+    // buffer, last read in step kb - 2, and are read from the end of step kb + 1 on, behind
+    // the barrier of step kb. Loads past the last step read it again.
     Weights w[kSets];
-    Stage st[2];
-    load_a(st[0], 0);
-    load_a(st[1], 1);
+    Stage st[4];  // rows of step d in st[(d - k0 - 2) % 4]
+    {
+      // the order of the steps before k0, so that the waits of the loop fit its start too
+      Stage first[2];
+      load_a(first[0], k0);
+      load_a(first[1], k0 + 1);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) load_w(w[i], i);
-    store_a(st[0], smem, 0);
-    load_a(st[0], 2);
-    store_a(st[1], smem + kBufBytes, 1);
+      for (int i = 0; i < kAhead; ++i) {
+        load_a(st[i], k0 + 2 + i);
+        load_w(w[i], k0 + i);
+      }
+      store_a(first[0], smem, k0);
+      store_a(first[1], smem + kBufBytes, k0 + 1);
+    }
     lds_barrier();
 #pragma unroll
     for (int i = 0; i < kD; ++i) read_a(f[i], smem, i);
     auto step = [&](int kb, auto STEP) __attribute__((always_inline)) {
       constexpr int I = decltype(STEP)::value;
-      const uint8_t* buf = smem + I * kBufBytes;
+      const uint8_t* buf = smem + I % 4 * kBufBytes;
       const uint8_t* next = smem + ((I + 1) % 4) * kBufBytes;
-      load_a(st[(I + 1) & 1], kb + 3);
+      load_a(st[(I + 3) & 3], kb + 5);
       load_w(w[(I + kAhead) % kSets], kb + kAhead);
       const auto& wk = w[I].v;
 #pragma unroll
       for (int m = 0; m < MB; ++m) {
-        read_a(f[(I * MB + m + kD) % 4], m + kD < MB ? buf : next, (m + kD) % MB);
+        read_a(f[(I * MB + m + kD) % kF], m + kD < MB ? buf : next, (m + kD) % MB);
         __builtin_amdgcn_sched_barrier(0);
-        const Frag& a = f[(I * MB + m) % 4];
+        const Frag& a = f[(I * MB + m) % kF];
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
           for (int j = 0; j < NBW; ++j) acc[m][j] = Elem<TY>::mma16(wk[j][q], a.v[q], acc[m][j]);
         __builtin_amdgcn_sched_barrier(0);
       }
-      store_a(st[I & 1], smem + ((I + 2) % 4) * kBufBytes, kb + 2);
+      store_a(st[I & 3], smem + ((I + 2) % 4) * kBufBytes, kb + 2);
       lds_barrier();
     };
-    // one call site per register set, and exits rather than skipped steps (see the
-    // block-scaled tile: remainders put the sets in scratch, skipped steps shorten the
-    // waits)
-    for (int kb = 0;; kb += kSets) {
+    // Whole rounds of the register sets without an exit between, then the rest in a line
+    // of its own: an exit inside the round, though it only leaves the loop, makes the
+    // compiler's waits at its head drain the loads in flight
+    int kb = k0;
+#pragma unroll 1
+    for (; kb + kSets <= k1; kb += kSets) {
       step(kb, std::integral_constant<int, 0>{});
-      if (kb + 1 >= KB) break;
       step(kb + 1, std::integral_constant<int, 1>{});
-      if (kb + 2 >= KB) break;
       step(kb + 2, std::integral_constant<int, 2>{});
-      if (kb + 3 >= KB) break;
       step(kb + 3, std::integral_constant<int, 3>{});
-      if (kb + 4 >= KB) break;
+    }
+    if (kb < k1) {
+      step(kb, std::integral_constant<int, 0>{});
+      if (kb + 1 < k1) {
+        step(kb + 1, std::integral_constant<int, 1>{});
+        if (kb + 2 < k1) step(kb + 2, std::integral_constant<int, 2>{});
+      }
+    }
+    if (part) {
+#pragma unroll
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int j = 0; j < NBW; ++j)
+          *reinterpret_cast<Acc*>(part + ((wave * MB + m) * NBW + j) * kPiece + l16) = acc[m][j];
+      return;
     }
     const bool swiglu = p.act == W8A8_ACT_SWIGLU;
+    if (NBW == 1 && swiglu) {
+      // gate blocks lie in even wavefronts, their up blocks in the next: through LDS
+      lds_barrier();  // every wavefront is done with its operands
+      Acc* room = reinterpret_cast<Acc*>(smem) + (wave >> 1) * MB * kWave + lane;
+      if (wave & 1) {
+#pragma unroll
+        for (int m = 0; m < MB; ++m) room[m * kWave] = acc[m][0];
+      }
+      lds_barrier();
+      if (wave & 1) return;
+#pragma unroll
+      for (int m = 0; m < MB; ++m) {
+        const int r = m * 16 + (lane & 15);
+        const Acc up = room[m * kWave];
+        if (r < rows) emit_block<TY>(p, row0 + r, nbw, lane, acc[m][0], row_scale<TY>(p, row0 + r), &up);
+      }
+      return;
+    }
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
       const int r = m * 16 + (lane & 15);
@@ -474,46 +522,58 @@ struct StreamTile {
 // tile height by the rows there are
 template <int TY, int NBW>
 __device__ __forceinline__ void stream_tile(const FusedGemm& p, uint8_t* smem, int e, int64_t row0, int rows, int nb0) {
-  if (rows <= 16) StreamTile<TY, 1, NBW>::run(p, smem, e, row0, rows, nb0);
-  else if (rows <= 32) StreamTile<TY, 2, NBW>::run(p, smem, e, row0, rows, nb0);
-  else if (rows <= 64) StreamTile<TY, 4, NBW>::run(p, smem, e, row0, rows, nb0);
-  else if (rows <= 96) StreamTile<TY, 6, NBW>::run(p, smem, e, row0, rows, nb0);
-  else StreamTile<TY, 8, NBW>::run(p, smem, e, row0, rows, nb0);
+  const int KB = (int)(p.KP + 1) / 2;
+  if (rows <= 16) StreamTile<TY, 1, NBW>::run(p, smem, e, row0, rows, nb0, 0, KB, nullptr);
+  else if (rows <= 32) StreamTile<TY, 2, NBW>::run(p, smem, e, row0, rows, nb0, 0, KB, nullptr);
+  else if (rows <= 64) StreamTile<TY, 4, NBW>::run(p, smem, e, row0, rows, nb0, 0, KB, nullptr);
+  else if (rows <= 96) StreamTile<TY, 6, NBW>::run(p, smem, e, row0, rows, nb0, 0, KB, nullptr);
+  else StreamTile<TY, 8, NBW>::run(p, smem, e, row0, rows, nb0, 0, KB, nullptr);
 }
 
-// Grouped: every row tile times NT column groups; workgroup b runs on XCD b % 8. A
-// tile's column groups go to two XCDs (one if NT is odd), whose L2 they read the tile's
-// rows through, 4 or 8 tiles at a time.
-constexpr int kSpreadTiles = 64;
-
-template <int TY, int NBW>
-__global__ __launch_bounds__(512) void fused_grouped_kernel(FusedGemm p, int NT) {
-  using T = StreamTile<TY, 8, NBW>;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
-  const int count = *reinterpret_cast<const int*>(p.ws);
-  int t, c;
-  if (count >= kSpreadTiles) {
-    const int spread = NT % 2 ? 1 : 2;
-    const int x = blockIdx.x % 8, j = blockIdx.x / 8, per = NT / spread;
-    t = j / per * (8 / spread) + x / spread;
-    c = x % spread + j % per * spread;
-  } else {
-    t = blockIdx.x / NT;
-    c = blockIdx.x % NT;
-  }
-  if (t >= count) return;
-  const int4 tile = reinterpret_cast<const int4*>(reinterpret_cast<const char*>(p.ws) + 256)[t];
-  stream_tile<TY, NBW>(p, smem, __builtin_amdgcn_readfirstlane(tile.x), __builtin_amdgcn_readfirstlane(tile.y),
-                       __builtin_amdgcn_readfirstlane(tile.z), c * 8 * NBW);
-}
-
-// Dense: tiles of one height.
+// Dense: tiles of one height. S > 1: K in S parts of `per` steps each, whose sums
+// fused_join_kernel adds.
 template <int TY, int MB, int NBW>
-__global__ __launch_bounds__(512) void fused_dense_kernel(FusedGemm p) {
+__global__ __launch_bounds__(512) void fused_dense_kernel(FusedGemm p, int S, int per, uint8_t* part) {
   using T = StreamTile<TY, MB, NBW>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
   const int64_t row0 = (int64_t)blockIdx.x * (MB * 16);
-  T::run(p, smem, 0, row0, (int)min((int64_t)(MB * 16), p.M - row0), blockIdx.y * 8 * NBW);
+  const int KB = (int)(p.KP + 1) / 2, k0 = blockIdx.z * per;
+  uint8_t* mine = nullptr;
+  if (S > 1) mine = part + (((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * T::kPartBytes;
+  T::run(p, smem, 0, row0, (int)min((int64_t)(MB * 16), p.M - row0), blockIdx.y * 8 * NBW, k0, min(KB, k0 + per), mine);
+}
+
+// The S parts of every 16 x 16 block, in their order, and the epilogue: a wavefront a
+// block (SwiGLU: a pair of blocks).
+template <int TY, int MB, int NBW>
+__global__ __launch_bounds__(256) void fused_join_kernel(FusedGemm p, int S, int rows_of_tiles, int64_t tiles,
+                                                         const uint8_t* part) {
+  using Acc = typename Elem<TY>::Acc4;
+  constexpr int kBlocks = 8 * MB * NBW;  // of a tile
+  const int lane = threadIdx.x & 63;
+  const int64_t b = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t tile = b / kBlocks;
+  if (tile >= tiles) return;
+  const int at = (int)(b % kBlocks), wave = at / (MB * NBW), m = at / NBW % MB, j = at % NBW;
+  const int64_t nb = tile / rows_of_tiles * (8 * NBW) + wave * NBW + j;
+  const int64_t r = tile % rows_of_tiles * (MB * 16) + m * 16 + (lane & 15);
+  const bool swiglu = p.act == W8A8_ACT_SWIGLU;
+  if ((swiglu && (nb & 1)) || nb >= p.NB) return;
+  auto total = [&](int64_t off) __attribute__((always_inline)) {
+    const uint8_t* src = part + tile * kBlocks * kPiece + off * kPiece + lane * 16;
+    Acc sum = *reinterpret_cast<const Acc*>(src);
+#pragma unroll 8
+    for (int s = 1; s < S; ++s) sum += *reinterpret_cast<const Acc*>(src + s * tiles * kBlocks * kPiece);
+    return sum;
+  };
+  const Acc sum = total(at);
+  // the up block: the next of this wavefront's, or the next wavefront's
+  if (swiglu) {
+    const Acc up = total(NBW == 1 ? at + MB : at + 1);
+    if (r < p.M) emit_block<TY>(p, r, nb, lane, sum, row_scale<TY>(p, r), &up);
+  } else if (r < p.M) {
+    emit_block<TY, Acc>(p, r, nb, lane, sum, row_scale<TY>(p, r), nullptr);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -528,20 +588,24 @@ constexpr int kDecodeWaves = 8;
 template <int TY, int MB, int NBW, int U>
 __global__ __launch_bounds__(kDecodeWaves * 64) void fused_decode_kernel(FusedGemm p) {
   using Acc = typename Elem<TY>::Acc4;
-  __shared__ Acc red[kDecodeWaves][MB * NBW][kWave];
+  // a wavefront's rows on their way into operand order, two steps; then the sums
+  constexpr int kTurn = 2 * MB * 2 * kPiece, kRed = MB * NBW * kPiece;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kDecodeWaves * (kTurn > kRed ? kTurn : kRed)];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int NB = (int)p.NB, KP = (int)p.KP, KB = (KP + 1) / 2, M = (int)p.M;
   const uint32_t last = (uint32_t)p.kbytes - 16;
   const int nb0 = blockIdx.x * NBW, m0 = blockIdx.y * MB * 16;
-  const uint32_t l16 = lane * 16, at = (lane >> 4) * 16;
+  const uint32_t l16 = lane * 16, at = (lane & 7) * 16;
   const uint8_t* wp[NBW];
 #pragma unroll
   for (int j = 0; j < NBW; ++j)  // blocks past the last read it; their outputs are never stored
     wp[j] = p.w + (int64_t)min(nb0 + j, NB - 1) * KP * kPiece;
-  const uint8_t* ap[MB];  // rows past the last read it; they only feed outputs that are never stored
+  const uint8_t* ap[MB][2];  // rows past the last read it; they only feed outputs that are never stored
 #pragma unroll
-  for (int m = 0; m < MB; ++m) ap[m] = p.a + (int64_t)min(m0 + m * 16 + (lane & 15), M - 1) * p.lda;
+  for (int m = 0; m < MB; ++m)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) ap[m][h] = p.a + (int64_t)min(m0 + m * 16 + h * 8 + (lane >> 3), M - 1) * p.lda;
 
   i32x4 w[U][NBW][2], a[U][MB][2];
   // step k (clamped) into set u
@@ -556,10 +620,9 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fused_decode_kernel(FusedGe
   auto load_a = [&](int u, int kb) __attribute__((always_inline)) {
     const uint32_t k = (uint32_t)min(kb, KB - 1) * kStepBytes + at;
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      a[u][m][0] = load16(ap[m], k, last);
-      a[u][m][1] = load16(ap[m], k + 64, last);
-    }
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) a[u][m][h] = load16(ap[m][h], k, last);
   };
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -571,28 +634,46 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fused_decode_kernel(FusedGe
   for (int m = 0; m < MB; ++m)
 #pragma unroll
     for (int j = 0; j < NBW; ++j) acc[m][j] = Acc{0, 0, 0, 0};
-  auto mul = [&](int u, int kb) __attribute__((always_inline)) {
+  uint8_t* const mine = smem + wave * kTurn;
+  const uint32_t to0 = turned(lane >> 3, lane & 7), to1 = turned(8 + (lane >> 3), lane & 7);
+  const uint32_t from = turned(lane & 15, lane >> 4);
+  // the rows of set u, step kb (this wavefront's n-th), into LDS: one step ahead of its product
+  auto turn = [&](int u, int kb, int n) __attribute__((always_inline)) {
+    uint8_t* buf = mine + (n & 1) * MB * 2 * kPiece;
     if (kb == KB - 1) {  // wave-uniform
       const int past = (KB - 1) * kStepBytes - (int)last + (int)at;
 #pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        a[u][m][0] = fix16(a[u][m][0], past);
-        a[u][m][1] = fix16(a[u][m][1], past + 64);
-      }
+      for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) a[u][m][h] = fix16(a[u][m][h], past);
     }
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+      *reinterpret_cast<i32x4*>(buf + m * 2 * kPiece + to0) = a[u][m][0];
+      *reinterpret_cast<i32x4*>(buf + m * 2 * kPiece + to1) = a[u][m][1];
+    }
+  };
+  auto mul = [&](int u, int n) __attribute__((always_inline)) {
+    const uint8_t* buf = mine + (n & 1) * MB * 2 * kPiece;
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
-      for (int m = 0; m < MB; ++m)
+      for (int m = 0; m < MB; ++m) {
+        const i32x4 x = *reinterpret_cast<const i32x4*>(buf + m * 2 * kPiece + q * kPiece + (q ? from ^ 128 : from));
 #pragma unroll
-        for (int j = 0; j < NBW; ++j) acc[m][j] = Elem<TY>::mma16(w[u][j][q], a[u][m][q], acc[m][j]);
+        for (int j = 0; j < NBW; ++j) acc[m][j] = Elem<TY>::mma16(w[u][j][q], x, acc[m][j]);
+      }
   };
   __builtin_amdgcn_sched_barrier(0);  // every first load in flight before the first product
   int kb0 = wave;
+  static_assert(U % 2 == 0, "the two LDS buffers alternate over a round");
+  turn(0, kb0, 0);
   for (; kb0 + kDecodeWaves * U < KB; kb0 += kDecodeWaves * U) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      mul(u, kb0 + u * kDecodeWaves);
+      // set 0 again at the end: refilled in this round
+      turn((u + 1) % U, kb0 + (u + 1) * kDecodeWaves, u + 1);
+      mul(u, u);
       load_a(u, kb0 + (u + U) * kDecodeWaves);
       load_w(u, kb0 + (u + U) * kDecodeWaves);
       __builtin_amdgcn_sched_barrier(0);
@@ -602,9 +683,12 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fused_decode_kernel(FusedGe
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (kb0 + u * kDecodeWaves >= KB) break;  // wave-uniform: clamped steps add nothing
-      mul(u, kb0 + u * kDecodeWaves);
+      if (u + 1 < U) turn(u + 1, kb0 + (u + 1) * kDecodeWaves, u + 1);
+      mul(u, u);
     }
   }
+  __syncthreads();  // every wavefront is done with its rows
+  auto red = reinterpret_cast<Acc(*)[MB * NBW][kWave]>(smem);
 #pragma unroll
   for (int m = 0; m < MB; ++m)
 #pragma unroll
@@ -635,14 +719,17 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fused_decode_kernel(FusedGe
 // 128 x 64 as 4 x 2 blocks of the 32 x 32 MFMA), both operands through LDS by DMA.
 //
 // LDS: two stages of one step, each 32 pieces of 8 rows x 128 bytes of a (whole cache
-// lines; slot l of a piece holds row l / 8, 16-byte chunk (l % 8) ^ (l / 8), so that the
-// rows of an operand lie in different banks) and 32 pieces of packed weight; and 4 KB a
+// lines; 16-byte chunk c of row r in slot c ^ (r / 2 % 8), so that 16 rows of an operand
+// lie in all 64 banks) and 32 pieces of packed weight; and 4 KB a
 // wavefront through which the sums are turned into whole lines of y.
 // Step kb, in four quarters of 32 bytes of K: the operands of a quarter are read while
 // the one before is multiplied; before the last quarter's MFMAs "own DMA of kb + 1
-// landed, own reads of kb done, s_barrier", then the DMA of kb + 2 into the stage of
-// kb. A workgroup walks over its tiles without a gap: the last two steps of a tile load
-// the first two of the next one, which land while the tile is stored.
+// landed, own reads of kb done, s_barrier", then the rows of kb + 2 into the stage of
+// kb, and its weights in the next step's first quarter (all eight copies at once: the
+// queue of the vector memory holds up the wavefront's products, 395 us for BF16 8192 x
+// 4096 x 7168 where this form takes 382; one a product: 406). A workgroup walks over its
+// tiles without a gap: the last two steps of a tile load the first two of the next one,
+// which land while the tile is stored.
 // ---------------------------------------------------------------------------
 static __device__ __align__(16) uint8_t zeros16[16];
 
@@ -657,89 +744,42 @@ struct WideTile {
   struct Where {
     int rows, nb0;  // rows, first column block; rows 0: no tile
     int64_t row0;
+    int e;          // expert
   };
 
-  // This wavefront's 32 x 32 block of sums (m, n): rows row0 + 32 of `rows`, weight rows
-  // from block nb. Turned through LDS (16-byte chunk c of row r at c ^ (r % 8)), so that
-  // a lane holds 8 neighbouring columns and four (SwiGLU: two) lanes a row.
-  __device__ __forceinline__ static void store_block(const FusedGemm& p, uint8_t* turn, const Acc& acc, int64_t row0,
-                                                     int rows, int nb) {
-    const int lane = threadIdx.x & 63;
-    if (rows <= 0) return;  // the same in every lane
-    const int64_t width = outputs_of(p);
-    const bool swiglu = p.act == W8A8_ACT_SWIGLU;
+  // A 32 x 32 block of sums into LDS: 16-byte chunk c of row r at c ^ (r % 8).
+  __device__ __forceinline__ static void turn_block(uint8_t* turn, const Acc& acc, int lane) {
     uint8_t* mine = turn + (lane & 31) * 128;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      i32x4 v;
+      typename Elem<TY>::Acc4 v;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) v[t] = bits_of(acc[4 * g + t]);
-      *reinterpret_cast<i32x4*>(mine + (((2 * g + (lane >> 5)) ^ (lane & 7)) * 16)) = v;
+      for (int t = 0; t < 4; ++t) v[t] = acc[4 * g + t];
+      *reinterpret_cast<typename Elem<TY>::Acc4*>(mine + (((2 * g + (lane >> 5)) ^ (lane & 7)) * 16)) = v;
     }
     // the same wavefront reads it back: in order, no barrier
     __builtin_amdgcn_wave_barrier();
-    auto read8 = [&](int r, int c8, float (&v)[8], float xs, const float (&ws)[8]) __attribute__((always_inline)) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const i32x4 u = *reinterpret_cast<const i32x4*>(turn + r * 128 + (((2 * c8 + h) ^ (r & 7)) * 16));
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-          v[4 * h + t] = TY == kFusedInt8 ? scaled(p, (int32_t)u[t], xs, ws[4 * h + t]) : __int_as_float(u[t]);
-      }
-    };
-    const int lanes = swiglu ? 2 : 4;                   // a row
-    const int c8 = lane % lanes;
-    const int64_t c = (int64_t)(swiglu ? nb / 2 : nb) * 16 + c8 * 8;
-    const int64_t n = width - c;                        // columns there are
-    float b[8], b2[8], ws[8];
-#pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      const int64_t ct = min(c + t, width - 1);
-      b[t] = p.bias ? bf16_to_f32(p.bias[ct]) : 0.0f;
-      b2[t] = p.bias && swiglu ? bf16_to_f32(p.bias[width + ct]) : 0.0f;
-      ws[t] = TY == kFusedInt8 ? p.w_scale[ct] : 0.0f;
-    }
-    for (int r = lane / lanes; r < 32; r += 64 / lanes) {
-      const int64_t m = row0 + r;
-      const bool in = r < rows && n > 0;
-      float v[8], u[8];
-      const float xs = in ? row_scale<TY>(p, m) : 0.0f;
-      read8(r, c8, v, xs, ws);
-      if (swiglu) read8(r, c8 + 2, u, xs, ws);
-      if (!in) continue;
-      float res[8], none[8];
-      if (p.residual) load8<false>(p.residual + m * p.ldr + c, 0, n, res, none);
-      float o[8];
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        float z = p.bias ? v[t] + b[t] : v[t];
-        if (swiglu) z = times_sigmoid(z, z) * (p.bias ? u[t] + b2[t] : u[t]);
-        else z = activate(p.act, z);
-        o[t] = p.residual ? z + res[t] : z;
-      }
-      if (p.f32) {
-        float* y = reinterpret_cast<float*>(p.y) + m * p.ldy + c;
-        if (n >= 8) {
-          *reinterpret_cast<Floats4*>(y) = Floats4{{o[0], o[1], o[2], o[3]}};
-          *reinterpret_cast<Floats4*>(y + 4) = Floats4{{o[4], o[5], o[6], o[7]}};
-        } else {
-#pragma unroll
-          for (int t = 0; t < 8; ++t)
-            if (t < n) y[t] = o[t];
-        }
+  }
+
+  // The turned block: rows row0 + 32 of `rows`, weight rows from block nb. A lane takes 4
+  // neighbouring columns, eight (SwiGLU: four) lanes a row.
+  __device__ __forceinline__ static void store_block(const FusedGemm& p, const uint8_t* turn, int64_t row0, int rows,
+                                                     int nb, int lane) {
+    using Acc4 = typename Elem<TY>::Acc4;
+    const bool swiglu = p.act == W8A8_ACT_SWIGLU;
+    const int shift = swiglu ? 2 : 3;
+    const int64_t c = (int64_t)(swiglu ? nb / 2 : nb) * 16 + (lane & ((1 << shift) - 1)) * 4;
+#pragma unroll 1
+    for (int r = lane >> shift; r < min(rows, 32); r += 64 >> shift) {
+      const uint8_t* row = turn + r * 128;
+      const int c4 = lane & ((1 << shift) - 1);
+      const Acc4 v = *reinterpret_cast<const Acc4*>(row + ((c4 ^ (r & 7)) * 16));
+      const float xs = row_scale<TY>(p, row0 + r);
+      if (swiglu) {
+        const Acc4 up = *reinterpret_cast<const Acc4*>(row + (((c4 + 4) ^ (r & 7)) * 16));
+        emit4<TY>(p, row0 + r, c, outputs_of(p), v, xs, &up);
       } else {
-        uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + m * p.ldy + c;
-        uint32_t q[8];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) q[t] = to_bf16(o[t]);
-        if (n >= 8) {
-          *reinterpret_cast<Bytes16*>(y) =
-              Bytes16{{q[0] | (q[1] << 16), q[2] | (q[3] << 16), q[4] | (q[5] << 16), q[6] | (q[7] << 16)}};
-        } else {
-#pragma unroll
-          for (int t = 0; t < 8; ++t)
-            if (t < n) y[t] = (uint16_t)q[t];
-        }
+        emit4<TY, Acc4>(p, row0 + r, c, outputs_of(p), v, xs, nullptr);
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -753,30 +793,33 @@ struct WideTile {
     const int wm = wave >> 2, wn = wave & 3;
     const int NB = (int)p.NB, KP = (int)p.KP, KB = (KP + 1) / 2;
     const uint32_t l16 = lane * 16;
-    const uint32_t chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+    const uint32_t chunk = ((lane & 7) ^ (lane >> 4)) * 16;  // of even pieces; odd ones: ^ 64
     const bool ragged = p.kbytes != (int64_t)KB * kStepBytes;
     const uint8_t* abase;    // the tile's first row
     uint32_t aoff[4];        // this wavefront's four pieces of a: bytes from abase
     const uint8_t* wp[2];    // its two weight blocks
     auto sources = [&](const Where& t) __attribute__((always_inline)) {
-      abase = p.a + t.row0 * p.lda;
       // rows past the tile read its last
+      abase = p.row_index ? p.a : p.a + t.row0 * p.lda;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        aoff[i] = (uint32_t)(min((wave * 4 + i) * 8 + (lane >> 3), t.rows - 1) * (uint32_t)p.lda + chunk);
+      for (int i = 0; i < 4; ++i) {
+        int r = min((wave * 4 + i) * 8 + (lane >> 3), t.rows - 1);
+        if (p.row_index) r = (int)max((int64_t)0, min((int64_t)p.row_index[t.row0 + r], p.a_rows - 1));
+        aoff[i] = (uint32_t)r * (uint32_t)p.lda + (chunk ^ (i & 1) * 64);
+      }
 #pragma unroll
       for (int j = 0; j < 2; ++j)  // past the last block, that one (never stored)
-        wp[j] = p.w + (int64_t)min(t.nb0 + wave * 2 + j, NB - 1) * KP * kPiece;
+        wp[j] = p.w + ((int64_t)t.e * NB + min(t.nb0 + wave * 2 + j, NB - 1)) * KP * kPiece;
     };
     // Addresses are a wave-uniform base and a 32-bit lane offset; the empty asm keeps
     // the compiler from hoisting their sums into register pairs.
-    auto dma = [&](int k, int stage) __attribute__((always_inline)) {
+    auto dma_a = [&](int k, int stage) __attribute__((always_inline)) {
       W8A8_LDS uint8_t* dst = (W8A8_LDS uint8_t*)smem + stage * kStage;
       const uint8_t* ab = abase + (int64_t)k * kStepBytes;
       if (ragged && k == KB - 1) {  // the same in every lane
-        const bool in = (int64_t)k * kStepBytes + chunk < p.kbytes;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          const bool in = (int64_t)k * kStepBytes + (chunk ^ (i & 1) * 64) < p.kbytes;
           const uint8_t* src = in ? ab + aoff[i] : zeros16;
           __builtin_amdgcn_global_load_lds(src, (W8A8_LDS void*)(dst + (wave * 4 + i) * 1024), 16, 0, 0);
         }
@@ -788,6 +831,9 @@ struct WideTile {
           __builtin_amdgcn_global_load_lds(ab + o, (W8A8_LDS void*)(dst + (wave * 4 + i) * 1024), 16, 0, 0);
         }
       }
+    };
+    auto dma_w = [&](int k, int stage) __attribute__((always_inline)) {
+      W8A8_LDS uint8_t* dst = (W8A8_LDS uint8_t*)smem + stage * kStage;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint32_t o = l16;
@@ -797,7 +843,7 @@ struct WideTile {
       }
     };
     // operands of quarter s: 32 rows (l % 32), 16 bytes at l / 32 of its 32
-    const uint32_t ar = (wm * 128 + (lane & 31)) * 128, a7 = lane & 7;
+    const uint32_t ar = (wm * 128 + (lane & 31)) * 128, a7 = (lane >> 1) & 7;
     const uint32_t br = kOperand + ((wn * 4 + ((lane >> 4) & 1)) * 2) * kPiece + (lane & 15) * 16 + (lane >> 5) * 256;
     struct Ops {
       i32x4 a[4], b[2];
@@ -813,8 +859,10 @@ struct WideTile {
     Where cur = next();
     if (!cur.rows) return;
     sources(cur);
-    dma(0, 0);
-    dma(1, 1);
+    dma_a(0, 0);
+    dma_w(0, 0);
+    dma_a(1, 1);
+    dma_w(1, 1);
     wait_vm_barrier<8>();  // stage 0 there
     Ops ops[2];
     read(ops[0], smem, 0);
@@ -827,7 +875,7 @@ struct WideTile {
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int t = 0; t < 16; ++t) acc[i][j][t] = 0;
-      Where after{0, 0, 0};
+      Where after{};
       // TAIL: the tile's last two steps, whose DMA is the next tile's first
       auto step = [&](int kb, auto TAIL) __attribute__((always_inline)) {
         const uint8_t* st = smem + stage * kStage;
@@ -842,37 +890,72 @@ struct WideTile {
           __builtin_amdgcn_sched_barrier(0);
           if (s < 3) {
             read(ops[(s + 1) & 1], st, s + 1);
+            // the weights of kb + 1, behind the rows that the step before asked for
+            if (s == 0 && kb > 0) {
+              if constexpr (decltype(TAIL)::value) {
+                if (kb < KB - 1) dma_w(kb + 1, stage ^ 1);
+                else if (after.rows) dma_w(0, stage ^ 1);
+              } else {
+                dma_w(kb + 1, stage ^ 1);
+              }
+            }
+            if constexpr (decltype(TAIL)::value) {
+              if (s == 1 && kb == KB - 2) {  // every copy of this tile is on its way
+                after = next();
+                if (after.rows) sources(after);
+              }
+            }
           } else {
             // own reads of this stage done, own DMA of the next one landed, everyone
             // there: the next stage may be read and this one refilled
             wait_vm_barrier<0>();
-            if constexpr (decltype(TAIL)::value) {
-              if (after.rows) dma(kb + 2 - KB, stage);
-            } else {
-              dma(kb + 2, stage);
-            }
             read(ops[0], nx, 0);
           }
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int i = 1; i < 4; ++i)
+          for (int i = 1; i < 4; ++i) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) acc[i][j] = Elem<TY>::mma32(o.b[j], o.a[i], acc[i][j]);
+            if (s == 3 && i == 1) {
+              __builtin_amdgcn_sched_barrier(0);
+              if constexpr (decltype(TAIL)::value) {
+                if (after.rows) {
+                  dma_a(kb + 2 - KB, stage);
+                  if (kb == KB - 1) dma_w(1, stage);
+                }
+              } else {
+                dma_a(kb + 2, stage);
+              }
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
           __builtin_amdgcn_sched_barrier(0);
         }
         stage ^= 1;
       };
       for (int kb = 0; kb + 2 < KB; ++kb) step(kb, std::false_type{});
-      after = next();
-      if (after.rows) sources(after);
       for (int kb = KB - 2; kb < KB; ++kb) step(kb, std::true_type{});
       uint8_t* turn = smem + 2 * kStage + wave * kTurn;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          store_block(p, turn, acc[i][j], cur.row0 + wm * 128 + i * 32, cur.rows - (wm * 128 + i * 32),
-                      cur.nb0 + wn * 4 + j * 2);
+      // the lane number read here, not kept (with what follows from it) over the K loop;
+      // one copy of the epilogue, behind a choice of the block's registers
+      int el = threadIdx.x & 63;
+      asm volatile("" : "+v"(el));
+#pragma unroll 1
+      for (int b = 0; b < 8; ++b) {
+        const int i = b >> 1, j = b & 1, rows = cur.rows - (wm * 128 + i * 32);
+        if (rows <= 0) break;
+        switch (b) {
+          case 0: turn_block(turn, acc[0][0], el); break;
+          case 1: turn_block(turn, acc[0][1], el); break;
+          case 2: turn_block(turn, acc[1][0], el); break;
+          case 3: turn_block(turn, acc[1][1], el); break;
+          case 4: turn_block(turn, acc[2][0], el); break;
+          case 5: turn_block(turn, acc[2][1], el); break;
+          case 6: turn_block(turn, acc[3][0], el); break;
+          case 7: turn_block(turn, acc[3][1], el); break;
+        }
+        store_block(p, turn, cur.row0 + wm * 128 + i * 32, rows, cur.nb0 + wn * 4 + j * 2, el);
+      }
       if (!after.rows) break;
       cur = after;
     }
@@ -889,7 +972,7 @@ __global__ __launch_bounds__(512) void fused_wide_kernel(FusedGemm p) {
   const int64_t per = (total + 7) / 8, first = (blockIdx.x % 8) * per, end = min(first + per, total);
   int64_t t = first + blockIdx.x / 8;
   WideTile<TY>::run(p, smem, [&]() __attribute__((always_inline)) {
-    typename WideTile<TY>::Where w{0, 0, 0};
+    typename WideTile<TY>::Where w{};
     if (t < end) {
       const int64_t top = t / (8 * NT) * 8, gm = min((int64_t)8, MT - top), r = t % (8 * NT);
       w.row0 = (top + r % gm) * 256;
@@ -901,6 +984,43 @@ __global__ __launch_bounds__(512) void fused_wide_kernel(FusedGemm p) {
   });
 }
 
+// Grouped: every row tile times NT column groups; workgroup b runs on XCD b % 8. A
+// tile's column groups go to two XCDs (one if NT is odd), whose L2 they read the tile's
+// rows through, 4 or 8 tiles at a time.
+constexpr int kSpreadTiles = 64;
+
+template <int TY, int NBW>
+__global__ __launch_bounds__(512) void fused_grouped_kernel(FusedGemm p, int NT) {
+  using T = WideTile<TY>;
+  static_assert(StreamTile<TY, 8, NBW>::kLdsBytes <= T::kLdsBytes && NBW == 2, "one column group, one LDS");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
+  const int count = *reinterpret_cast<const int*>(p.ws);
+  int t, c;
+  if (count >= kSpreadTiles) {
+    const int spread = NT % 2 ? 1 : 2;
+    const int x = blockIdx.x % 8, j = blockIdx.x / 8, per = NT / spread;
+    t = j / per * (8 / spread) + x / spread;
+    c = x % spread + j % per * spread;
+  } else {
+    t = blockIdx.x / NT;
+    c = blockIdx.x % NT;
+  }
+  if (t >= count) return;
+  const int4 tile = reinterpret_cast<const int4*>(reinterpret_cast<const char*>(p.ws) + 256)[t];
+  const int e = __builtin_amdgcn_readfirstlane(tile.x), row0 = __builtin_amdgcn_readfirstlane(tile.y);
+  const int rows = __builtin_amdgcn_readfirstlane(tile.z);
+  if (rows > kTileRows) {
+    int left = 1;
+    T::run(p, smem, [&]() __attribute__((always_inline)) {
+      typename T::Where w{};
+      if (left-- > 0) w = typename T::Where{rows, c * 8 * NBW, row0, e};
+      return w;
+    });
+  } else {
+    stream_tile<TY, NBW>(p, smem, e, row0, rows, c * 8 * NBW);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -909,21 +1029,66 @@ bool fused_rows_ok(const FusedGemm& p) {
   return p.lda % 16 == 0 && p.lda < (int64_t)1 << 24 && p.kbytes % 16 == 0 && ((uintptr_t)p.a & 15) == 0;
 }
 
-enum FusedKernel { kDecode16, kDecode16x32, kDecode32, kDecode64, kTile32, kTile64, kTile128, kTile256 };
-
-static FusedKernel fused_kernel(const FusedGemm& p) {
-  if (p.M > 1024 && p.KP > 2) return kTile256;  // its pipeline is two steps deep
-  if (p.M > 64) return kTile128;
-  if (p.M > 32) return kDecode64;
-  if (p.M > 16) return kDecode32;
-  return p.act == W8A8_ACT_SWIGLU ? kDecode16x32 : kDecode16;
+// whether experts of many rows take wide tiles: two steps of K, rows as they copy them,
+// 32-bit offsets from a's first row where rows are read through an index
+static bool grouped_wide(const FusedGemm& p) {
+  return p.KP > 2 && fused_rows_ok(p) && (!p.row_index || p.a_rows * p.lda < (int64_t)1 << 32);
 }
 
-bool fused_needs_copy(const FusedGemm& p) {
-  return p.kbytes < 16 || (fused_kernel(p) == kTile256 && !fused_rows_ok(p));
+hipError_t launch_fused_schedule(const FusedGemm& p, void* ws, hipStream_t stream) {
+  hipLaunchKernelGGL(fused_schedule_kernel, dim3(1), dim3(256), 0, stream, p.group_list, (int)p.E, p.M,
+                     (int)grouped_wide(p), reinterpret_cast<int*>(ws),
+                     reinterpret_cast<int4*>(reinterpret_cast<char*>(ws) + 256));
+  return hipGetLastError();
+}
+
+enum FusedKernel { kDecode16, kDecode16x32, kDecode32, kDecode64, kTile32, kTile64, kTile64x256, kTile128, kTile256 };
+
+struct FusedPlan {
+  FusedKernel kernel;
+  int S;               // parts of K (tiles)
+};
+
+static FusedPlan fused_plan(int type, int64_t M, int64_t NB, int64_t KP, bool swiglu) {
+  if (M > 1024 && KP > 2) return FusedPlan{kTile256, 1};  // its pipeline is two steps deep
+  if (M > 64) return FusedPlan{kTile128, 1};
+  if (M > 32) return FusedPlan{kDecode64, 1};
+  if (M > 16) return FusedPlan{kDecode32, 1};
+  return FusedPlan{swiglu ? kDecode16x32 : kDecode16, 1};
+}
+
+static FusedPlan plan_of(const FusedGemm& p) {
+  return fused_plan(p.type, p.M, p.NB, p.KP, p.act == W8A8_ACT_SWIGLU);
 }
 
 int64_t fused_copy_bytes(int64_t M, int64_t kbytes) { return round_up(kbytes, kStepBytes) * M; }
+
+// sums of the parts of K
+static int64_t part_bytes(const FusedPlan& plan, int64_t M, int64_t NB) {
+  if (plan.S == 1) return 0;
+  const int rows = plan.kernel == kTile32 ? 32 : plan.kernel == kTile128 ? 128 : 64;
+  const int cols = plan.kernel == kTile64x256 || plan.kernel == kTile128 ? 256 : 128;
+  return (int64_t)plan.S * round_up(M, rows) * round_up(NB * 16, cols) * 4;
+}
+
+int64_t fused_room_bytes(const FusedGemm& p) {
+  const FusedPlan plan = plan_of(p);
+  if (p.kbytes < 16 || (plan.kernel == kTile256 && !fused_rows_ok(p))) return fused_copy_bytes(p.M, p.kbytes);
+  return part_bytes(plan, p.M, p.NB);
+}
+
+int64_t fused_most_bytes(int type, int64_t M, int64_t N, int64_t K) {
+  const int64_t kbytes = type == kFusedInt8 ? K : 2 * K;
+  const int64_t NB = type == kFusedInt8 ? ceil_div(N, 16) : round_up(N, 32) / 16;
+  const int64_t KP = type == kFusedInt8 ? ceil_div(K, 64) : 2 * ceil_div(K, 64);
+  int64_t most = 0;
+  for (const bool swiglu : {false, true}) {
+    const FusedPlan plan = fused_plan(type, M, NB, KP, swiglu);
+    const bool copy = kbytes < 16 || plan.kernel == kTile256;
+    most = std::max(most, copy ? fused_copy_bytes(M, kbytes) : part_bytes(plan, M, NB));
+  }
+  return most;
+}
 
 // U: a wavefront's steps of K, at most as many as registers hold (sets without a step of
 // their own load the last one again)
@@ -938,21 +1103,29 @@ static void launch_decode(const FusedGemm& p, hipStream_t stream) {
 }
 
 template <int TY, int MB, int NBW>
-static void launch_tiles(const FusedGemm& p, hipStream_t stream) {
-  hipLaunchKernelGGL((fused_dense_kernel<TY, MB, NBW>),
-                     dim3((unsigned)ceil_div(p.M, MB * 16), (unsigned)ceil_div(p.NB, 8 * NBW)), dim3(512), 0, stream, p);
+static void launch_tiles(const FusedGemm& p, int S, void* room, hipStream_t stream) {
+  const int64_t mt = ceil_div(p.M, MB * 16), nt = ceil_div(p.NB, 8 * NBW);
+  const int per = (int)ceil_div(ceil_div(p.KP, 2), S);
+  S = (int)ceil_div(ceil_div(p.KP, 2), per);  // no empty part
+  uint8_t* part = reinterpret_cast<uint8_t*>(room);
+  hipLaunchKernelGGL((fused_dense_kernel<TY, MB, NBW>), dim3((unsigned)mt, (unsigned)nt, (unsigned)S), dim3(512), 0,
+                     stream, p, S, per, part);
+  if (S > 1)
+    hipLaunchKernelGGL((fused_join_kernel<TY, MB, NBW>), dim3((unsigned)(mt * nt * 2 * MB * NBW)), dim3(256), 0, stream, p,
+                       S, (int)mt, mt * nt, part);
 }
 
 template <int TY>
-static hipError_t launch_dense(const FusedGemm& p, FusedKernel kernel, hipStream_t stream) {
-  switch (kernel) {
+static hipError_t launch_dense(const FusedGemm& p, const FusedPlan& plan, void* room, hipStream_t stream) {
+  switch (plan.kernel) {
     case kDecode16: launch_decode<TY, 1, 1>(p, stream); break;
     case kDecode16x32: launch_decode<TY, 1, 2>(p, stream); break;
     case kDecode32: launch_decode<TY, 2, 2>(p, stream); break;
     case kDecode64: launch_decode<TY, 4, 2>(p, stream); break;
-    case kTile32: launch_tiles<TY, 2, 2>(p, stream); break;
-    case kTile64: launch_tiles<TY, 4, 2>(p, stream); break;
-    case kTile128: launch_tiles<TY, 8, 2>(p, stream); break;
+    case kTile32: launch_tiles<TY, 2, 1>(p, plan.S, room, stream); break;
+    case kTile64: launch_tiles<TY, 4, 1>(p, plan.S, room, stream); break;
+    case kTile64x256: launch_tiles<TY, 4, 2>(p, plan.S, room, stream); break;
+    case kTile128: launch_tiles<TY, 8, 2>(p, plan.S, room, stream); break;
     case kTile256: {
       const int64_t tiles = ceil_div(p.M, 256) * ceil_div(p.NB, 16);
       hipLaunchKernelGGL(fused_wide_kernel<TY>, dim3((unsigned)std::min<int64_t>(256, round_up(tiles, 8))), dim3(512), 0,
@@ -971,8 +1144,8 @@ hipError_t launch_fused_gemm(FusedGemm p, void* room, hipStream_t stream) {
                        dim3(512), 0, stream, p, (int)NT);
     return hipGetLastError();
   }
-  const FusedKernel kernel = fused_kernel(p);
-  if (fused_needs_copy(p)) {
+  const FusedPlan plan = plan_of(p);
+  if (p.kbytes < 16 || (plan.kernel == kTile256 && !fused_rows_ok(p))) {
     const int64_t per = round_up(p.kbytes, kStepBytes) / 16;
     hipLaunchKernelGGL(fused_copy_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(p.M * per, 256), 1 << 16)), dim3(256),
                        0, stream, p.a, p.M, p.lda, p.kbytes, per, reinterpret_cast<uint8_t*>(room));
@@ -981,7 +1154,8 @@ hipError_t launch_fused_gemm(FusedGemm p, void* room, hipStream_t stream) {
     p.a = reinterpret_cast<const uint8_t*>(room);
     p.lda = p.kbytes = per * 16;
   }
-  return p.type == kFusedInt8 ? launch_dense<kFusedInt8>(p, kernel, stream) : launch_dense<kFusedBf16>(p, kernel, stream);
+  return p.type == kFusedInt8 ? launch_dense<kFusedInt8>(p, plan, room, stream)
+                              : launch_dense<kFusedBf16>(p, plan, room, stream);
 }
 
 }  // namespace w8a8

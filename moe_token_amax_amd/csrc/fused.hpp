@@ -41,15 +41,16 @@ int64_t bf16_packed_bytes(int64_t N, int64_t K);  // of one [N, K] weight
 hipError_t launch_bf16_prepack(const uint16_t* w, int64_t E, int64_t N, int64_t K, bool pairs, void* packed,
                                hipStream_t stream);
 
-// Rows that the tiles' copies can take as they are: 16-byte aligned, whole 16-byte
-// pieces. Others are copied (zero-padded) to `room` first where those tiles run.
-bool fused_rows_ok(const FusedGemm& p);
-bool fused_needs_copy(const FusedGemm& p);
-int64_t fused_copy_bytes(int64_t M, int64_t kbytes);
+// Workspace of a dense product: rows copied (zero-padded) where the wide tiles need them
+// 16-byte aligned and whole, or the sums of the parts of a split K; and the most that a
+// product of these sizes can need.
+int64_t fused_room_bytes(const FusedGemm& p);
+int64_t fused_most_bytes(int type, int64_t M, int64_t N, int64_t K);
 hipError_t launch_fused_gemm(FusedGemm p, void* room, hipStream_t stream);
 
 int64_t fused_sched_bytes(int64_t R, int64_t E);
 int64_t fused_grid(int64_t R, int64_t E, int64_t N);  // workgroups of a grouped product
-hipError_t launch_fused_schedule(const int64_t* group_list, int64_t E, int64_t R, void* ws, hipStream_t stream);
+// the tile list of p's group_list, rows and operands, into p.ws
+hipError_t launch_fused_schedule(const FusedGemm& p, void* ws, hipStream_t stream);
 
 }  // namespace w8a8
