@@ -1587,9 +1587,7 @@ def linear_fused(q: torch.Tensor, x_scale: torch.Tensor, w_packed: torch.Tensor,
         raise ValueError("y shape mismatch")
     yp, ldy = _rows_at(y, torch.bfloat16, "y")
     rp, ldr = _residual(residual, (M, N))
-    aligned = at % 16 == 0 and ldq % 16 == 0 and K % 16 == 0  # no copy, no workspace
-    room, ws, ws_n = (None, None, 0) if aligned and workspace is None else \
-        _room(workspace, q.device, linear_fused_workspace_bytes, M, N, K)
+    room, ws, ws_n = _room(workspace, q.device, linear_fused_workspace_bytes, M, N, K)
     _check(lib.w8a8_linear_fused(at, ldq, _at(x_scale, torch.float32, "x_scale", 1), M, K, wp,
                                  _at(w_scale, torch.float32, "w_scale", 1), N, _at(bias, torch.bfloat16, "bias", 1), act,
                                  rp, ldr, yp, ldy, ws, ws_n, _stream()))
@@ -1652,9 +1650,7 @@ def bf16_linear(x: torch.Tensor, w_packed: torch.Tensor, N: int, bias: torch.Ten
         raise ValueError("y shape mismatch")
     yp, ldy = _rows_at(y, torch.float32 if out == OUT_F32 else torch.bfloat16, "y")
     rp, ldr = _residual(residual, (M, width))
-    aligned = at % 16 == 0 and ldx % 8 == 0 and K % 8 == 0  # no copy, no workspace
-    room, ws, ws_n = (None, None, 0) if aligned and workspace is None else \
-        _room(workspace, x.device, bf16_linear_workspace_bytes, M, N, K)
+    room, ws, ws_n = _room(workspace, x.device, bf16_linear_workspace_bytes, M, N, K)
     _check(lib.w8a8_bf16_linear(at, ldx, M, K, wp, N, _at(bias, torch.bfloat16, "bias", 1), act, rp, ldr, yp, ldy, out,
                                 ws, ws_n, _stream()))
     return y

@@ -42,6 +42,26 @@ __device__ __forceinline__ float activate(int act, float v) {
   }
 }
 
+// four values behind one choice
+__device__ __forceinline__ void activate4(int act, float (&v)[4]) {
+#define W8A8_EACH(expr)                            \
+  {                                                \
+    _Pragma("unroll") for (int t = 0; t < 4; ++t) { \
+      const float x = v[t];                        \
+      v[t] = expr;                                 \
+    }                                              \
+    break;                                         \
+  }
+  switch (act) {
+    case W8A8_ACT_RELU: W8A8_EACH(activate(W8A8_ACT_RELU, x))
+    case W8A8_ACT_SILU: W8A8_EACH(activate(W8A8_ACT_SILU, x))
+    case W8A8_ACT_GELU: W8A8_EACH(activate(W8A8_ACT_GELU, x))
+    case W8A8_ACT_GELU_TANH: W8A8_EACH(activate(W8A8_ACT_GELU_TANH, x))
+    default: break;
+  }
+#undef W8A8_EACH
+}
+
 // up to 4 neighbouring BF16 values (0 past n of them)
 __device__ __forceinline__ void load_bf16x4(const uint16_t* src, int n, float (&v)[4]) {
   if (n >= 4) {

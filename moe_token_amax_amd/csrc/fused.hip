@@ -117,68 +117,157 @@ struct __attribute__((packed, aligned(4))) Floats4 {
   float v[4];
 };
 
-// Four neighbouring outputs (m, c .. c + 3) of `width`, from the sums of the weight rows
-// n .. n + 3 (and of their partners `up`, rows n2 .. for SwiGLU).
-template <int TY, class Acc>
-__device__ __forceinline__ void emit4(const FusedGemm& p, int64_t m, int64_t c, int64_t width, const Acc& acc, float xs,
-                                      const Acc* up) {
-  if (c >= width) return;
-  const int n = (int)min((int64_t)4, width - c);
-  float b[4] = {0.f, 0.f, 0.f, 0.f}, b2[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f}, ws[4];
-  if (p.bias) {
-    load_bf16x4(p.bias + c, n, b);
-    if (up) load_bf16x4(p.bias + width + c, n, b2);
-  }
-  if (p.residual) load_bf16x4(p.residual + m * p.ldr + c, n, r);
+__device__ __forceinline__ int64_t outputs_of(const FusedGemm& p) { return p.act == W8A8_ACT_SWIGLU ? p.N / 2 : p.N; }
+
+// What is added where there is no bias or no residual, -0 (v + -0 is v, also where v is
+// -0): a pair of it in BF16.
+constexpr uint32_t kNothing2 = 0x80008000u;
+
+// A lane's four neighbouring output columns c .. c + 3: what belongs to them and not to a
+// row, loaded once for all the rows of a tile. WHOLE: the columns exist, for every lane
+// of the wavefront (a path of its own: with a choice at every access the epilogue of a
+// 128 x 256 tile took 8 us).
+struct Cols {
+  int c;
+  int n;  // of the four that exist; 0: none
+  float bias[4], second[4];  // second: INT8 the columns' scales, SwiGLU the up half's bias
+};
+
+__device__ __forceinline__ float bf16_of(const Bytes8& u, int t) {
+  return __uint_as_float(t & 1 ? u.w[t >> 1] & 0xFFFF0000u : u.w[t >> 1] << 16);
+}
+
+// n of four BF16 values as they lie in memory, -0 past them
+template <bool WHOLE>
+__device__ __forceinline__ Bytes8 load_raw4(const uint16_t* src, int n) {
+  if (WHOLE) return *reinterpret_cast<const Bytes8*>(src);
+  uint32_t u[4];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) ws[t] = TY == kFusedInt8 ? p.w_scale[c + min(t, n - 1)] : 0.0f;
-  float o[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    float v = scaled(p, acc[t], xs, ws[t]);
-    if (p.bias) v = v + b[t];
-    if (up) {
-      float u = (float)(*up)[t];
-      if (p.bias) u = u + b2[t];
-      v = times_sigmoid(v, v) * u;
-    } else {
-      v = activate(p.act, v);
-    }
-    o[t] = p.residual ? v + r[t] : v;
-  }
-  if (p.f32) {
-    float* y = reinterpret_cast<float*>(p.y) + m * p.ldy + c;
-    if (n == 4) {
-      *reinterpret_cast<Floats4*>(y) = Floats4{{o[0], o[1], o[2], o[3]}};
+  for (int t = 0; t < 4; ++t) u[t] = t < n ? src[t] : kNothing2 & 0xFFFFu;
+  return Bytes8{{u[0] | (u[1] << 16), u[2] | (u[3] << 16)}};
+}
+
+template <int TY, bool WHOLE>
+__device__ __forceinline__ Cols load_cols(const FusedGemm& p, int64_t c) {
+  const int64_t width = outputs_of(p);
+  const bool swiglu = TY == kFusedBf16 && p.act == W8A8_ACT_SWIGLU;
+  Cols o;
+  o.c = (int)c;
+  o.n = WHOLE ? 4 : (int)max((int64_t)0, min((int64_t)4, width - c));
+  Bytes8 b{{kNothing2, kNothing2}}, u = b;
+  Floats4 f{};
+  if (p.bias) b = load_raw4<WHOLE>(p.bias + c, o.n);
+  if (swiglu && p.bias) u = load_raw4<WHOLE>(p.bias + width + c, o.n);
+  if (TY == kFusedInt8) {
+    if (WHOLE) {
+      f = *reinterpret_cast<const Floats4*>(p.w_scale + c);
     } else {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        if (t < n) y[t] = o[t];
+        if (t < o.n) f.v[t] = p.w_scale[c + t];
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    o.bias[t] = bf16_of(b, t);
+    o.second[t] = TY == kFusedInt8 ? f.v[t] : bf16_of(u, t);
+  }
+  return o;
+}
+
+// Takes the columns' values here: their loads are waited for now and not in a loop that
+// stores, where each such wait is one for the stores too (loads and stores count as one;
+// 0.9 us for every 16 rows).
+__device__ __forceinline__ void arrived(Cols& o) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) asm volatile("" : "+v"(o.bias[t]), "+v"(o.second[t]));
+}
+
+// the residual of row m at the lane's columns, as it lies in memory
+template <bool WHOLE>
+__device__ __forceinline__ Bytes8 load_residual(const FusedGemm& p, int64_t m, const Cols& o) {
+  return load_raw4<WHOLE>(p.residual + m * p.ldr + o.c, o.n);
+}
+
+// The outputs of row m from the sums of its four weight rows (SwiGLU: and of their
+// partners `up`).
+// ACT: p.act, or kAnyAct
+constexpr int kAnyAct = -1;
+
+template <int TY, bool WHOLE, int ACT, class Acc>
+__device__ __forceinline__ void emit4(const FusedGemm& p, int64_t m, const Cols& o, float xs, const Bytes8& res,
+                                      const Acc& acc, const Acc& up) {
+  float v[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) v[t] = scaled(p, acc[t], xs, o.second[t]) + o.bias[t];
+  const int act = ACT == kAnyAct ? p.act : ACT;
+  if (TY == kFusedBf16 && act == W8A8_ACT_SWIGLU) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) v[t] = times_sigmoid(v[t], v[t]) * ((float)up[t] + o.second[t]);
+  } else {
+    activate4(act, v);
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) v[t] = v[t] + bf16_of(res, t);
+  if (p.f32) {
+    float* y = reinterpret_cast<float*>(p.y) + m * p.ldy + o.c;
+    if (WHOLE) {
+      *reinterpret_cast<Floats4*>(y) = Floats4{{v[0], v[1], v[2], v[3]}};
+    } else {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (t < o.n) y[t] = v[t];
     }
   } else {
-    uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + m * p.ldy + c;
+    uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + m * p.ldy + o.c;
     uint32_t q[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) q[t] = to_bf16(o[t]);
-    if (n == 4) {
+    for (int t = 0; t < 4; ++t) q[t] = to_bf16(v[t]);
+    if (WHOLE) {
       *reinterpret_cast<Bytes8*>(y) = Bytes8{{q[0] | (q[1] << 16), q[2] | (q[3] << 16)}};
     } else {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        if (t < n) y[t] = (uint16_t)q[t];
+        if (t < o.n) y[t] = (uint16_t)q[t];
     }
   }
 }
 
-__device__ __forceinline__ int64_t outputs_of(const FusedGemm& p) { return p.act == W8A8_ACT_SWIGLU ? p.N / 2 : p.N; }
+// run(ACT) for p.act, so that a loop over rows holds no choice of it (some ten branches
+// an output: 0.7 us for every 16 rows of a tile)
+template <int TY, class Run>
+__device__ __forceinline__ void for_act(const FusedGemm& p, Run run) {
+  switch (p.act) {  // the same in every lane
+    case W8A8_ACT_SWIGLU:
+      if constexpr (TY == kFusedBf16) run(std::integral_constant<int, W8A8_ACT_SWIGLU>{});
+      break;
+    case W8A8_ACT_RELU: run(std::integral_constant<int, W8A8_ACT_RELU>{}); break;
+    case W8A8_ACT_SILU: run(std::integral_constant<int, W8A8_ACT_SILU>{}); break;
+    case W8A8_ACT_GELU: run(std::integral_constant<int, W8A8_ACT_GELU>{}); break;
+    case W8A8_ACT_GELU_TANH: run(std::integral_constant<int, W8A8_ACT_GELU_TANH>{}); break;
+    default: run(std::integral_constant<int, W8A8_ACT_NONE>{}); break;
+  }
+}
+
+// first output column of the 16 x 16 blocks from nb on (SwiGLU: nb even)
+__device__ __forceinline__ int64_t first_col(const FusedGemm& p, int64_t nb) {
+  return (p.act == W8A8_ACT_SWIGLU ? nb / 2 : nb) * 16;
+}
 
 // The 16 x 16 block nb of weight rows against the rows of m: this lane's four outputs.
-// SwiGLU: nb even (gate), `up` the block after it.
+template <int TY, bool WHOLE, class Acc>
+__device__ __forceinline__ void emit_one(const FusedGemm& p, int64_t m, int64_t c, const Acc& acc, const Acc& up) {
+  const Cols o = load_cols<TY, WHOLE>(p, c);
+  Bytes8 res{{kNothing2, kNothing2}};
+  if (p.residual) res = load_residual<WHOLE>(p, m, o);
+  emit4<TY, WHOLE, kAnyAct>(p, m, o, row_scale<TY>(p, m), res, acc, up);
+}
 template <int TY, class Acc>
-__device__ __forceinline__ void emit_block(const FusedGemm& p, int64_t m, int64_t nb, int lane, const Acc& acc, float xs,
-                                           const Acc* up) {
-  const int64_t c = (up ? nb / 2 : nb) * 16 + (lane >> 4) * 4;
-  emit4<TY>(p, m, c, outputs_of(p), acc, xs, up);
+__device__ __forceinline__ void emit_block(const FusedGemm& p, int64_t m, int64_t nb, int lane, const Acc& acc,
+                                           const Acc& up) {
+  const int64_t c0 = first_col(p, nb), c = c0 + (lane >> 4) * 4;
+  if (c0 + 16 <= outputs_of(p)) emit_one<TY, true>(p, m, c, acc, up);  // wave-uniform
+  else emit_one<TY, false>(p, m, c, acc, up);
 }
 
 // ---------------------------------------------------------------------------
@@ -328,7 +417,10 @@ struct StreamTile {
   static constexpr int kWaves = 8;
   static constexpr int kPieces = (2 * MB + kWaves - 1) / kWaves;  // 16-byte pieces a thread stages per step
   static constexpr int kBufBytes = MB * 2 * kPiece;
-  static constexpr int kLdsBytes = 4 * kBufBytes;
+  static constexpr int kThreads = kWaves * kWave;
+  static constexpr int kSumBytes = MB * 16 * 128 * NBW * 4;
+  static constexpr int kStoreBytes = kSumBytes + MB * 16 * 4;  // sums, row scales
+  static constexpr int kLdsBytes = 4 * kBufBytes > kStoreBytes ? 4 * kBufBytes : kStoreBytes;
 
   struct Stage {
     i32x4 a[kPieces];
@@ -484,39 +576,78 @@ struct StreamTile {
           *reinterpret_cast<Acc*>(part + ((wave * MB + m) * NBW + j) * kPiece + l16) = acc[m][j];
       return;
     }
-    const bool swiglu = p.act == W8A8_ACT_SWIGLU;
-    if (NBW == 1 && swiglu) {
-      // gate blocks lie in even wavefronts, their up blocks in the next: through LDS
-      lds_barrier();  // every wavefront is done with its operands
-      Acc* room = reinterpret_cast<Acc*>(smem) + (wave >> 1) * MB * kWave + lane;
-      if (wave & 1) {
+    int et = threadIdx.x;
+    asm volatile("" : "+v"(et));  // read here, not kept over the K loop
+    const int64_t c0 = first_col(p, nb0), width = outputs_of(p);
+    if (c0 + (p.act == W8A8_ACT_SWIGLU ? 64 * NBW : 128 * NBW) <= width) store_tile<true>(p, smem, acc, row0, rows, c0, et);
+    else store_tile<false>(p, smem, acc, row0, rows, c0, et);
+  }
+
+  // The sums through LDS, from where the wavefronts store whole rows of the tile in a loop
+  // of few branches (unrolled, with the choices at every output, the epilogue of a 128 x 256
+  // tile was 65 KB of code and took XX us).
+  template <bool WHOLE>
+  __device__ __forceinline__ static void store_tile(const FusedGemm& p, uint8_t* smem, const Acc (&acc)[MB][NBW],
+                                                    int64_t row0, int rows, int64_t c0, int tid) {
+    const int shift = p.act == W8A8_ACT_SWIGLU ? kTurnShift - 1 : kTurnShift;  // log2 of a row's lanes
+    const int c4 = tid & ((1 << shift) - 1);
+    float* scales = reinterpret_cast<float*>(smem + kSumBytes);
+    float xs = 0.0f;
+    if (TY == kFusedInt8) xs = row_scale<TY>(p, row0 + min(tid, rows - 1));
+    Cols cols = load_cols<TY, WHOLE>(p, c0 + c4 * 4);
+    lds_barrier();  // every wavefront is done with its operands
 #pragma unroll
-        for (int m = 0; m < MB; ++m) room[m * kWave] = acc[m][0];
-      }
-      lds_barrier();
-      if (wave & 1) return;
+    for (int m = 0; m < MB; ++m)
 #pragma unroll
-      for (int m = 0; m < MB; ++m) {
-        const int r = m * 16 + (lane & 15);
-        const Acc up = room[m * kWave];
-        if (r < rows) emit_block<TY>(p, row0 + r, nbw, lane, acc[m][0], row_scale<TY>(p, row0 + r), &up);
-      }
-      return;
+      for (int j = 0; j < NBW; ++j)
+        *reinterpret_cast<Acc*>(smem + sums_at(m * 16 + (tid & 15), ((tid >> 6) * NBW + j) * 4 + ((tid >> 4) & 3))) =
+            acc[m][j];
+    if (TY == kFusedInt8 && tid < MB * 16) scales[tid] = xs;
+    lds_barrier();
+    arrived(cols);
+    if constexpr (WHOLE) {
+      for_act<TY>(p, [&](auto ACT) __attribute__((always_inline)) {
+        store_rows<WHOLE, decltype(ACT)::value>(p, smem, scales, cols, row0, rows, tid);
+      });
+    } else {
+      store_rows<WHOLE, kAnyAct>(p, smem, scales, cols, row0, rows, tid);
     }
+  }
+
+  template <bool WHOLE, int ACT>
+  __device__ __forceinline__ static void store_rows(const FusedGemm& p, const uint8_t* smem, const float* scales,
+                                                    const Cols& cols, int64_t row0, int rows, int tid) {
+    const bool swiglu = ACT == kAnyAct ? p.act == W8A8_ACT_SWIGLU : ACT == W8A8_ACT_SWIGLU;
+    const int shift = swiglu ? kTurnShift - 1 : kTurnShift;
+    const int c4 = tid & ((1 << shift) - 1);
+    const int chunk = swiglu ? (c4 >> 2) * 8 + (c4 & 3) : c4;  // 16 gate columns, then their 16 up columns
+    constexpr int kRows = 4;  // of a lane at a time, their residual together
+#pragma unroll 1
+    for (int r0 = tid >> shift; r0 < rows; r0 += kRows * kThreads >> shift) {
+      Bytes8 res[kRows];
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
-      const int r = m * 16 + (lane & 15);
-      if (r < rows) {
-        const float xs = row_scale<TY>(p, row0 + r);
-        if (NBW == 2 && swiglu) {
-          emit_block<TY>(p, row0 + r, nbw, lane, acc[m][0], xs, &acc[m][NBW - 1]);
-        } else {
+      for (int k = 0; k < kRows; ++k) res[k] = Bytes8{{kNothing2, kNothing2}};
+      if (p.residual) {
 #pragma unroll
-          for (int j = 0; j < NBW; ++j) emit_block<TY, Acc>(p, row0 + r, nbw + j, lane, acc[m][j], xs, nullptr);
+        for (int k = 0; k < kRows; ++k)
+          res[k] = load_residual<WHOLE>(p, row0 + min(r0 + (k * kThreads >> shift), rows - 1), cols);
+      }
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        const int r = r0 + (k * kThreads >> shift);
+        if (r < rows) {
+          const Acc v = *reinterpret_cast<const Acc*>(smem + sums_at(r, chunk));
+          const Acc up = *reinterpret_cast<const Acc*>(smem + sums_at(r, chunk ^ 4));
+          emit4<TY, WHOLE, ACT>(p, row0 + r, cols, TY == kFusedInt8 ? scales[r] : 0.0f, res[k], v, up);
         }
       }
     }
   }
+
+  // Sums on their way to whole rows: rows of 128 NBW columns, 16-byte chunk c of row r in
+  // slot c ^ r % 16, so that a column's 16 chunks lie in all 64 banks.
+  static constexpr int kTurnShift = NBW == 2 ? 6 : 5;  // log2 of the 16-byte chunks of a row
+  __device__ __forceinline__ static int sums_at(int r, int c) { return (r << (kTurnShift + 4)) + ((c ^ (r & 15)) << 4); }
 };
 
 // tile height by the rows there are
@@ -570,9 +701,9 @@ __global__ __launch_bounds__(256) void fused_join_kernel(FusedGemm p, int S, int
   // the up block: the next of this wavefront's, or the next wavefront's
   if (swiglu) {
     const Acc up = total(NBW == 1 ? at + MB : at + 1);
-    if (r < p.M) emit_block<TY>(p, r, nb, lane, sum, row_scale<TY>(p, r), &up);
+    if (r < p.M) emit_block<TY>(p, r, nb, lane, sum, up);
   } else if (r < p.M) {
-    emit_block<TY, Acc>(p, r, nb, lane, sum, row_scale<TY>(p, r), nullptr);
+    emit_block<TY>(p, r, nb, lane, sum, sum);
   }
 }
 
@@ -705,13 +836,8 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fused_decode_kernel(FusedGe
   if (wave >= MB * per) return;
   const int64_t r = m0 + (wave / per) * 16 + (lane & 15);
   if (r >= M) return;
-  const float xs = row_scale<TY>(p, r);
-  if (swiglu) {
-    const Acc gate = total(wave * 2), up = total(wave * 2 + 1);
-    emit_block<TY>(p, r, nb0, lane, gate, xs, &up);
-  } else {
-    emit_block<TY, Acc>(p, r, nb0 + wave % NBW, lane, total(wave), xs, nullptr);
-  }
+  const Acc sum = total(swiglu ? wave * 2 : wave);
+  emit_block<TY>(p, r, nb0 + wave % per, lane, sum, swiglu ? total(wave * 2 + 1) : sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -733,7 +859,7 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fused_decode_kernel(FusedGe
 // ---------------------------------------------------------------------------
 static __device__ __align__(16) uint8_t zeros16[16];
 
-template <int TY>
+template <int TY, bool DENSE>
 struct WideTile {
   using Acc = typename Elem<TY>::Acc16;
   static constexpr int kOperand = 32768;  // one operand of one stage
@@ -747,42 +873,90 @@ struct WideTile {
     int e;          // expert
   };
 
-  // A 32 x 32 block of sums into LDS: 16-byte chunk c of row r at c ^ (r % 8).
-  __device__ __forceinline__ static void turn_block(uint8_t* turn, const Acc& acc, int lane) {
-    uint8_t* mine = turn + (lane & 31) * 128;
+  // 16 of a 32 x 32 block's rows (half h) into LDS, beside those of the block to its
+  // right: rows of 64 columns, 16-byte chunk c of row r in slot c ^ r.
+  __device__ __forceinline__ static void turn_block(uint8_t* turn, const Acc& acc, int j, int h, int lane) {
+    if (((lane >> 4) & 1) == h) {
+      uint8_t* mine = turn + (lane & 15) * 256;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      typename Elem<TY>::Acc4 v;
+      for (int g = 0; g < 4; ++g) {
+        typename Elem<TY>::Acc4 v;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) v[t] = acc[4 * g + t];
-      *reinterpret_cast<typename Elem<TY>::Acc4*>(mine + (((2 * g + (lane >> 5)) ^ (lane & 7)) * 16)) = v;
-    }
-    // the same wavefront reads it back: in order, no barrier
-    __builtin_amdgcn_wave_barrier();
-  }
-
-  // The turned block: rows row0 + 32 of `rows`, weight rows from block nb. A lane takes 4
-  // neighbouring columns, eight (SwiGLU: four) lanes a row.
-  __device__ __forceinline__ static void store_block(const FusedGemm& p, const uint8_t* turn, int64_t row0, int rows,
-                                                     int nb, int lane) {
-    using Acc4 = typename Elem<TY>::Acc4;
-    const bool swiglu = p.act == W8A8_ACT_SWIGLU;
-    const int shift = swiglu ? 2 : 3;
-    const int64_t c = (int64_t)(swiglu ? nb / 2 : nb) * 16 + (lane & ((1 << shift) - 1)) * 4;
-#pragma unroll 1
-    for (int r = lane >> shift; r < min(rows, 32); r += 64 >> shift) {
-      const uint8_t* row = turn + r * 128;
-      const int c4 = lane & ((1 << shift) - 1);
-      const Acc4 v = *reinterpret_cast<const Acc4*>(row + ((c4 ^ (r & 7)) * 16));
-      const float xs = row_scale<TY>(p, row0 + r);
-      if (swiglu) {
-        const Acc4 up = *reinterpret_cast<const Acc4*>(row + (((c4 + 4) ^ (r & 7)) * 16));
-        emit4<TY>(p, row0 + r, c, outputs_of(p), v, xs, &up);
-      } else {
-        emit4<TY, Acc4>(p, row0 + r, c, outputs_of(p), v, xs, nullptr);
+        for (int t = 0; t < 4; ++t) v[t] = acc[4 * g + t];
+        *reinterpret_cast<typename Elem<TY>::Acc4*>(mine + (((8 * j + 2 * g + (lane >> 5)) ^ (lane & 15)) * 16)) = v;
       }
     }
-    __builtin_amdgcn_wave_barrier();
+  }
+
+  // One copy of the epilogue behind a choice of the rows' registers. A lane takes 4
+  // neighbouring columns, 16 (SwiGLU: eight) lanes a row, so every fourth (eighth) row.
+  // What it loads is there before it stores: row scales in two registers, the residual of
+  // 32 rows at a time.
+  template <bool WHOLE, bool RES, int ACT>
+  __device__ __forceinline__ static void store_tile(const FusedGemm& p, uint8_t* turn, const Acc (&acc)[4][2], int64_t row0,
+                                                    int rows, int64_t c0, int lane) {
+    using Acc4 = typename Elem<TY>::Acc4;
+    const bool swiglu = ACT == kAnyAct ? p.act == W8A8_ACT_SWIGLU : ACT == W8A8_ACT_SWIGLU;
+    const int shift = swiglu ? 3 : 4;
+    const int c4 = lane & ((1 << shift) - 1);
+    const int c = swiglu ? (c4 >> 2) * 8 + (c4 & 3) : c4;  // 16 gate columns, then their 16 up columns
+    Cols cols = load_cols<TY, WHOLE>(p, c0 + c4 * 4);
+    float xs[2] = {0.0f, 0.0f};  // of rows lane and 64 + lane
+    if (TY == kFusedInt8) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) xs[h] = row_scale<TY>(p, row0 + min(h * 64 + lane, rows - 1));
+    }
+    arrived(cols);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) asm volatile("" : "+v"(xs[h]));
+    auto row_of = [&](int k) __attribute__((always_inline)) { return (lane >> shift) + (k * 64 >> shift); };
+#pragma unroll 1
+    for (int h = 0; h < 4; ++h) {
+      if (rows <= h * 32) break;
+      Bytes8 ahead[2][4];
+      if (RES) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            ahead[i][k] = load_residual<WHOLE>(p, row0 + min(h * 32 + i * 16 + min(row_of(k), 15), rows - 1), cols);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) asm volatile("" : "+v"(ahead[i][k].w[0]), "+v"(ahead[i][k].w[1]));
+      }
+      const float scale = h > 1 ? xs[1] : xs[0];
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const int first = h * 32 + i * 16;
+        if (rows <= first) break;
+        Bytes8 res[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) res[k] = RES ? i ? ahead[1][k] : ahead[0][k] : Bytes8{{kNothing2, kNothing2}};
+        // (the same wavefront writes and reads its LDS: in order, no barrier)
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int I = 0; I < 4; ++I)
+          if (h == I) {
+            asm volatile("");
+            turn_block(turn, acc[I][0], 0, i & 1, lane);
+            turn_block(turn, acc[I][1], 1, i & 1, lane);
+          }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = row_of(k);
+          const float row_xs = TY == kFusedInt8 ? __shfl(scale, (first + (r & 15)) & 63) : 0.0f;
+          if (r < min(rows - first, 16)) {
+            const Acc4 v = *reinterpret_cast<const Acc4*>(turn + r * 256 + ((c ^ r) * 16));
+            const Acc4 up = *reinterpret_cast<const Acc4*>(turn + r * 256 + ((c ^ 4 ^ r) * 16));
+            if (!WHOLE && p.residual) res[k] = load_residual<WHOLE>(p, row0 + first + r, cols);
+            emit4<TY, WHOLE, ACT>(p, row0 + first + r, cols, row_xs, res[k], v, up);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
   }
 
   // next(): this workgroup's next tile. At least two steps of K.
@@ -793,17 +967,29 @@ struct WideTile {
     const int wm = wave >> 2, wn = wave & 3;
     const int NB = (int)p.NB, KP = (int)p.KP, KB = (KP + 1) / 2;
     const uint32_t l16 = lane * 16;
-    const uint32_t chunk = ((lane & 7) ^ (lane >> 4)) * 16;  // of even pieces; odd ones: ^ 64
+    // a lane number that is read here, not kept (with what follows from it) over the K loop
+    auto fresh_lane = [&]() __attribute__((always_inline)) {
+      int v = threadIdx.x & 63;
+      asm volatile("" : "+v"(v));
+      return v;
+    };
+    // of even pieces; odd ones: ^ 64
+    auto own_chunk = [&]() __attribute__((always_inline)) {
+      const int sl = fresh_lane();
+      return (uint32_t)((sl & 7) ^ (sl >> 4)) * 16;
+    };
     const bool ragged = p.kbytes != (int64_t)KB * kStepBytes;
     const uint8_t* abase;    // the tile's first row
     uint32_t aoff[4];        // this wavefront's four pieces of a: bytes from abase
     const uint8_t* wp[2];    // its two weight blocks
     auto sources = [&](const Where& t) __attribute__((always_inline)) {
+      const int sl = fresh_lane();
+      const uint32_t chunk = own_chunk();
       // rows past the tile read its last
       abase = p.row_index ? p.a : p.a + t.row0 * p.lda;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        int r = min((wave * 4 + i) * 8 + (lane >> 3), t.rows - 1);
+        int r = min((wave * 4 + i) * 8 + (sl >> 3), t.rows - 1);
         if (p.row_index) r = (int)max((int64_t)0, min((int64_t)p.row_index[t.row0 + r], p.a_rows - 1));
         aoff[i] = (uint32_t)r * (uint32_t)p.lda + (chunk ^ (i & 1) * 64);
       }
@@ -817,6 +1003,7 @@ struct WideTile {
       W8A8_LDS uint8_t* dst = (W8A8_LDS uint8_t*)smem + stage * kStage;
       const uint8_t* ab = abase + (int64_t)k * kStepBytes;
       if (ragged && k == KB - 1) {  // the same in every lane
+        const uint32_t chunk = own_chunk();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const bool in = (int64_t)k * kStepBytes + (chunk ^ (i & 1) * 64) < p.kbytes;
@@ -909,7 +1096,11 @@ struct WideTile {
             // own reads of this stage done, own DMA of the next one landed, everyone
             // there: the next stage may be read and this one refilled
             wait_vm_barrier<0>();
-            read(ops[0], nx, 0);
+            if constexpr (decltype(TAIL)::value) {
+              if (kb < KB - 1) read(ops[0], nx, 0);  // the next tile's first: behind the epilogue
+            } else {
+              read(ops[0], nx, 0);
+            }
           }
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -936,28 +1127,22 @@ struct WideTile {
       for (int kb = 0; kb + 2 < KB; ++kb) step(kb, std::false_type{});
       for (int kb = KB - 2; kb < KB; ++kb) step(kb, std::true_type{});
       uint8_t* turn = smem + 2 * kStage + wave * kTurn;
-      // the lane number read here, not kept (with what follows from it) over the K loop;
-      // one copy of the epilogue, behind a choice of the block's registers
-      int el = threadIdx.x & 63;
-      asm volatile("" : "+v"(el));
-#pragma unroll 1
-      for (int b = 0; b < 8; ++b) {
-        const int i = b >> 1, j = b & 1, rows = cur.rows - (wm * 128 + i * 32);
-        if (rows <= 0) break;
-        switch (b) {
-          case 0: turn_block(turn, acc[0][0], el); break;
-          case 1: turn_block(turn, acc[0][1], el); break;
-          case 2: turn_block(turn, acc[1][0], el); break;
-          case 3: turn_block(turn, acc[1][1], el); break;
-          case 4: turn_block(turn, acc[2][0], el); break;
-          case 5: turn_block(turn, acc[2][1], el); break;
-          case 6: turn_block(turn, acc[3][0], el); break;
-          case 7: turn_block(turn, acc[3][1], el); break;
-        }
-        store_block(p, turn, cur.row0 + wm * 128 + i * 32, rows, cur.nb0 + wn * 4 + j * 2, el);
+      const int el = fresh_lane();
+      const int64_t c0 = first_col(p, cur.nb0 + wn * 4);
+      const int64_t row0 = cur.row0 + wm * 128;
+      const int rows = cur.rows - wm * 128;
+      if (c0 + (p.act == W8A8_ACT_SWIGLU ? 32 : 64) > outputs_of(p)) {
+        store_tile<false, false, kAnyAct>(p, turn, acc, row0, rows, c0, el);
+      } else if (DENSE && p.residual) {
+        store_tile<true, true, kAnyAct>(p, turn, acc, row0, rows, c0, el);
+      } else {
+        for_act<TY>(p, [&](auto ACT) __attribute__((always_inline)) {
+          store_tile<true, false, decltype(ACT)::value>(p, turn, acc, row0, rows, c0, el);
+        });
       }
       if (!after.rows) break;
       cur = after;
+      read(ops[0], smem + stage * kStage, 0);
     }
   }
 };
@@ -967,12 +1152,12 @@ struct WideTile {
 // runs together share panels in its L2.
 template <int TY>
 __global__ __launch_bounds__(512) void fused_wide_kernel(FusedGemm p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[WideTile<TY>::kLdsBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[WideTile<TY, true>::kLdsBytes];
   const int64_t MT = (p.M + 255) / 256, NT = (p.NB + 15) / 16, total = MT * NT;
   const int64_t per = (total + 7) / 8, first = (blockIdx.x % 8) * per, end = min(first + per, total);
   int64_t t = first + blockIdx.x / 8;
-  WideTile<TY>::run(p, smem, [&]() __attribute__((always_inline)) {
-    typename WideTile<TY>::Where w{};
+  WideTile<TY, true>::run(p, smem, [&]() __attribute__((always_inline)) {
+    typename WideTile<TY, true>::Where w{};
     if (t < end) {
       const int64_t top = t / (8 * NT) * 8, gm = min((int64_t)8, MT - top), r = t % (8 * NT);
       w.row0 = (top + r % gm) * 256;
@@ -991,7 +1176,7 @@ constexpr int kSpreadTiles = 64;
 
 template <int TY, int NBW>
 __global__ __launch_bounds__(512) void fused_grouped_kernel(FusedGemm p, int NT) {
-  using T = WideTile<TY>;
+  using T = WideTile<TY, false>;
   static_assert(StreamTile<TY, 8, NBW>::kLdsBytes <= T::kLdsBytes && NBW == 2, "one column group, one LDS");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
   const int count = *reinterpret_cast<const int*>(p.ws);
