@@ -751,9 +751,9 @@ int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* resid
  *             weights prepacked for it
  *   residual  device, BF16 [M, outputs], row stride ldr, or NULL; may be y itself
  *   bias      device, BF16 [N] or NULL
- *   workspace the call's workspace_bytes, 256-byte aligned, rewritten; needed only
- *             for rows that are not 16-byte aligned whole 16-byte pieces, of many
- *             rows or of fewer than 16 bytes (else NULL / 0 is fine)
+ *   workspace the call's workspace_bytes, 256-byte aligned, rewritten: sums of a K
+ *             that is split over workgroups, rows copied to 16-byte alignment (0 bytes:
+ *             NULL is fine)
  *
  * w8a8_linear_fused [DSV4 §二 npu_quant_matmul]: INT8 codes q [M, K], row stride ldq,
  *   x_scale float [M] (from w8a8_dynamic_quant_ld or w8a8_rms_norm_quant), a weight

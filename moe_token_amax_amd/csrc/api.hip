@@ -1536,14 +1536,15 @@ w8a8::FusedGemm fused_bf16(const uint16_t* x, int64_t ldx, int64_t rows, int64_t
   return p;
 }
 
-// Rows copied into the workspace, or sums of the parts of K, where the product has them.
-int fused_room(const char* who, const w8a8::FusedGemm& p, const void* workspace, int64_t ws_bytes) {
-  const int64_t need = w8a8::fused_room_bytes(p);
-  if (need == 0) return W8A8_OK;
-  if (!workspace || ws_bytes < need || !aligned(workspace, 256))
+// A dense product: the workspace that its plan needs (copied rows, sums of the parts of K),
+// and the launch.
+int run_fused(const char* who, const w8a8::FusedGemm& p, void* workspace, int64_t ws_bytes, void* stream) {
+  const w8a8::FusedPlan plan = w8a8::fused_plan(p);
+  const int64_t need = w8a8::fused_room_bytes(p, plan);
+  if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256)))
     return fail(W8A8_ERR_WORKSPACE, "%s: needs %lld workspace bytes (256-byte aligned), got %lld", who, (long long)need,
                 (long long)ws_bytes);
-  return W8A8_OK;
+  return launched(w8a8::launch_fused_gemm(p, plan, workspace, (hipStream_t)stream), who);
 }
 
 }  // namespace
@@ -1575,9 +1576,7 @@ int w8a8_linear_fused(const int8_t* q, int64_t ldq, const float* x_scale, int64_
   p.ldr = ldr;
   p.y = y;
   p.ldy = ldy;
-  st = fused_room("linear_fused", p, workspace, ws_bytes);
-  if (st) return st;
-  return launched(w8a8::launch_fused_gemm(p, workspace, (hipStream_t)stream), "linear_fused");
+  return run_fused("linear_fused", p, workspace, ws_bytes, stream);
 }
 
 int64_t w8a8_bf16_packed_bytes(int64_t E, int64_t N, int64_t K) {
@@ -1632,9 +1631,7 @@ int w8a8_bf16_linear(const uint16_t* x, int64_t ldx, int64_t M, int64_t K, const
   p.y = y;
   p.ldy = ldy;
   p.f32 = out == W8A8_OUT_F32;
-  st = fused_room("bf16_linear", p, workspace, ws_bytes);
-  if (st) return st;
-  return launched(w8a8::launch_fused_gemm(p, workspace, (hipStream_t)stream), "bf16_linear");
+  return run_fused("bf16_linear", p, workspace, ws_bytes, stream);
 }
 
 static int check_bf16_grouped(const char* who, int64_t R, int64_t E, int64_t N, int64_t K) {
@@ -1686,7 +1683,7 @@ int w8a8_bf16_grouped_gemm(const uint16_t* x, int64_t ldx, int64_t x_rows, const
   p.ws = workspace;
   const hipError_t err = w8a8::launch_fused_schedule(p, workspace, (hipStream_t)stream);
   if (err != hipSuccess) return launched(err, "bf16_grouped_gemm: schedule");
-  return launched(w8a8::launch_fused_gemm(p, nullptr, (hipStream_t)stream), "bf16_grouped_gemm");
+  return launched(w8a8::launch_fused_grouped(p, (hipStream_t)stream), "bf16_grouped_gemm");
 }
 
 }  // extern "C"

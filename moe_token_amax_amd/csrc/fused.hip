@@ -662,16 +662,29 @@ __device__ __forceinline__ void stream_tile(const FusedGemm& p, uint8_t* smem, i
 }
 
 // Dense: tiles of one height. S > 1: K in S parts of `per` steps each, whose sums
-// fused_join_kernel adds.
+// fused_join_kernel adds. Workgroup b runs on XCD b % 8: each XCD takes its own
+// contiguous eighth of the tiles, rows first, so that its L2 reads the weights of its
+// columns once (BF16 195 x 4684 x 4720, 32-row tiles: 60.7 us in launch order, here 35.7;
+// 1024 x 4096 x 4096, 64 x 256 tiles: 56.2, 45.6; 4096 x 512 x 2048, 64-row tiles: 15.1,
+// 16.2).
 template <int TY, int MB, int NBW>
 __global__ __launch_bounds__(512) void fused_dense_kernel(FusedGemm p, int S, int per, uint8_t* part) {
   using T = StreamTile<TY, MB, NBW>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
-  const int64_t row0 = (int64_t)blockIdx.x * (MB * 16);
-  const int KB = (int)(p.KP + 1) / 2, k0 = blockIdx.z * per;
+  uint32_t bx = blockIdx.x, by = blockIdx.y, bz = blockIdx.z;
+  const uint64_t total = (uint64_t)gridDim.x * gridDim.y * gridDim.z;
+  if (total < (uint64_t)1 << 31) {
+    const uint32_t b = bx + gridDim.x * (by + gridDim.y * bz), n = (uint32_t)total;
+    const uint32_t t = b % 8 * (n / 8) + min(b % 8, n % 8) + b / 8;
+    bx = t % gridDim.x;
+    by = t / gridDim.x % gridDim.y;
+    bz = t / gridDim.x / gridDim.y;
+  }
+  const int64_t row0 = (int64_t)bx * (MB * 16);
+  const int KB = (int)(p.KP + 1) / 2, k0 = bz * per;
   uint8_t* mine = nullptr;
-  if (S > 1) mine = part + (((int64_t)blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * T::kPartBytes;
-  T::run(p, smem, 0, row0, (int)min((int64_t)(MB * 16), p.M - row0), blockIdx.y * 8 * NBW, k0, min(KB, k0 + per), mine);
+  if (S > 1) mine = part + (((int64_t)bz * gridDim.y + by) * gridDim.x + bx) * T::kPartBytes;
+  T::run(p, smem, 0, row0, (int)min((int64_t)(MB * 16), p.M - row0), by * 8 * NBW, k0, min(KB, k0 + per), mine);
 }
 
 // The S parts of every 16 x 16 block, in their order, and the epilogue: a wavefront a
@@ -1229,37 +1242,85 @@ hipError_t launch_fused_schedule(const FusedGemm& p, void* ws, hipStream_t strea
 
 enum FusedKernel { kDecode16, kDecode16x32, kDecode32, kDecode64, kTile32, kTile64, kTile64x256, kTile128, kTile256 };
 
-struct FusedPlan {
-  FusedKernel kernel;
-  int S;               // parts of K (tiles)
+// What a product takes with each kernel, in us, by a model fitted to 1500 products of
+// either type, M 1 .. 8192, N 32 .. 16384, K 64 .. 16384 (the kernel it picks is 2 %
+// slower in the mean than the best of them, in one product of a hundred 1.5 times):
+//   launch + rounds * round + steps * max(first, rounds * step) + (split) join + parts
+// rounds: workgroups over twice the CUs (wide: whole turns of one workgroup a CU); steps:
+// 128-byte steps of K a workgroup goes through; first: such a step where the chip is not
+// full. INT8 and BF16 take the same time for the same bytes of K. A split of K is taken
+// into as many parts as give the chip half a workgroup, one or two a CU.
+struct FusedCost {
+  int rows, cols;
+  double launch, round, first, step, join, part;  // part: per MB of partial sums
+};
+constexpr FusedCost kCost[] = {
+    {16, 16, 2.56, 0.579, 0.0441, 0.163, 0, 0},       {16, 32, 2.79, 0.82, 0.0676, 0.264, 0, 0},
+    {32, 32, 3.13, 1.36, 0.0841, 0.34, 0, 0},         {64, 32, 3.6, 3.75, 0.12, 0.439, 0, 0},
+    {32, 128, 3.25, 1.9, 0.257, 0.589, 3.07, 0.437},  {64, 128, 4.04, 2.55, 0.322, 0.809, 2.9, 0.255},
+    {64, 256, 5.09, 6.77, 0.517, 1.38, 0, 0},         {128, 256, 7.37, 11.9, 0.808, 2.19, 2.18, 0.0812},
+    {256, 256, 3.36, 10.9, 1.23, 1.3, 0, 0},
 };
 
-static FusedPlan fused_plan(int type, int64_t M, int64_t NB, int64_t KP, bool swiglu) {
-  if (M > 1024 && KP > 2) return FusedPlan{kTile256, 1};  // its pipeline is two steps deep
-  if (M > 64) return FusedPlan{kTile128, 1};
-  if (M > 32) return FusedPlan{kDecode64, 1};
-  if (M > 16) return FusedPlan{kDecode32, 1};
-  return FusedPlan{swiglu ? kDecode16x32 : kDecode16, 1};
+static FusedPlan cheapest(int64_t M, int64_t NB, int64_t KP, bool swiglu, double& least) {
+  const int64_t KB = ceil_div(KP, 2);
+  FusedPlan best{kTile64, 1, false};
+  least = 1e300;
+  for (int k = kDecode16; k <= kTile256; ++k) {
+    const FusedCost& c = kCost[k];
+    if (k == kDecode16 && swiglu) continue;           // pairs of blocks
+    if (k <= kTile32 && M > (int64_t)1 << 20) continue;  // their grids' limits
+    if (c.rows * 128 < M || (k > kTile64 && c.rows >= 4 * M)) continue;  // never the best: no need to look
+    if (k == kTile256 && KP <= 2) continue;           // its pipeline is two steps deep
+    const int64_t tiles = ceil_div(M, c.rows) * ceil_div(NB * 16, c.cols);
+    auto consider = [&](int64_t S) {
+      const int64_t per = ceil_div(KB, S);
+      S = ceil_div(KB, per);  // no empty part
+      const int64_t n = tiles * S;
+      const double rounds = k == kTile256 ? (double)ceil_div(n, 256) : n / 512.0;
+      double t = c.launch + rounds * c.round + per * std::max(c.first, rounds * c.step);
+      if (S > 1) t += c.join + c.part * (double)(n * c.rows * c.cols * 4) * 1e-6;
+      if (t < least) {
+        least = t;
+        best = FusedPlan{k, (int)S, false};
+      }
+    };
+    consider(1);
+    if (k != kTile32 && k != kTile64 && k != kTile128) continue;  // (64 x 256 gained nothing)
+    for (const int64_t slots : {128, 256, 512}) {
+      const int64_t S = slots / tiles;
+      if (S >= 2 && KB >= 3 * S) consider(S);
+    }
+  }
+  return best;
 }
 
-static FusedPlan plan_of(const FusedGemm& p) {
-  return fused_plan(p.type, p.M, p.NB, p.KP, p.act == W8A8_ACT_SWIGLU);
+// Rows that are not 4-byte aligned load at a quarter to a half less speed: copied to
+// whole aligned steps first where a quarter of the product's time is more than the copy's
+// (BF16 300 x 1000 x 5761: 24.1 us as they are, YY with the copy; 20 x 129 x 5761: 9.4).
+static bool copy_pays(int64_t M, int64_t kbytes, double time) {
+  return 0.25 * time > 2.5 + 0.5e-6 * (double)(M * kbytes);
 }
 
-int64_t fused_copy_bytes(int64_t M, int64_t kbytes) { return round_up(kbytes, kStepBytes) * M; }
+static int64_t copy_bytes(int64_t M, int64_t kbytes) { return round_up(round_up(kbytes, kStepBytes) * M, 256); }
 
 // sums of the parts of K
 static int64_t part_bytes(const FusedPlan& plan, int64_t M, int64_t NB) {
   if (plan.S == 1) return 0;
-  const int rows = plan.kernel == kTile32 ? 32 : plan.kernel == kTile128 ? 128 : 64;
-  const int cols = plan.kernel == kTile64x256 || plan.kernel == kTile128 ? 256 : 128;
-  return (int64_t)plan.S * round_up(M, rows) * round_up(NB * 16, cols) * 4;
+  const FusedCost& c = kCost[plan.kernel];
+  return (int64_t)plan.S * round_up(M, c.rows) * round_up(NB * 16, c.cols) * 4;
 }
 
-int64_t fused_room_bytes(const FusedGemm& p) {
-  const FusedPlan plan = plan_of(p);
-  if (p.kbytes < 16 || (plan.kernel == kTile256 && !fused_rows_ok(p))) return fused_copy_bytes(p.M, p.kbytes);
-  return part_bytes(plan, p.M, p.NB);
+FusedPlan fused_plan(const FusedGemm& p) {
+  double time;
+  FusedPlan plan = cheapest(p.M, p.NB, p.KP, p.act == W8A8_ACT_SWIGLU, time);
+  const bool apart = ((uintptr_t)p.a | p.lda | p.kbytes) & 3;
+  plan.copy = p.kbytes < 16 || (plan.kernel == kTile256 && !fused_rows_ok(p)) || (apart && copy_pays(p.M, p.kbytes, time));
+  return plan;
+}
+
+int64_t fused_room_bytes(const FusedGemm& p, const FusedPlan& plan) {
+  return (plan.copy ? copy_bytes(p.M, p.kbytes) : 0) + part_bytes(plan, p.M, p.NB);
 }
 
 int64_t fused_most_bytes(int type, int64_t M, int64_t N, int64_t K) {
@@ -1268,9 +1329,11 @@ int64_t fused_most_bytes(int type, int64_t M, int64_t N, int64_t K) {
   const int64_t KP = type == kFusedInt8 ? ceil_div(K, 64) : 2 * ceil_div(K, 64);
   int64_t most = 0;
   for (const bool swiglu : {false, true}) {
-    const FusedPlan plan = fused_plan(type, M, NB, KP, swiglu);
-    const bool copy = kbytes < 16 || plan.kernel == kTile256;
-    most = std::max(most, copy ? fused_copy_bytes(M, kbytes) : part_bytes(plan, M, NB));
+    double time;
+    const FusedPlan plan = cheapest(M, NB, KP, swiglu, time);
+    const bool copy = kbytes < 16 || plan.kernel == kTile256 || copy_pays(M, kbytes, time);
+    most = std::max(most, (copy ? copy_bytes(M, kbytes) : 0) + part_bytes(plan, M, NB));
+    if (plan.kernel != kDecode16) break;  // the same for SwiGLU
   }
   return most;
 }
@@ -1321,22 +1384,23 @@ static hipError_t launch_dense(const FusedGemm& p, const FusedPlan& plan, void* 
   return hipGetLastError();
 }
 
-hipError_t launch_fused_gemm(FusedGemm p, void* room, hipStream_t stream) {
-  if (p.M == 0 || p.N == 0) return hipSuccess;
-  if (p.group_list) {
-    const int64_t NT = grouped_columns(p.NB * 16);
-    hipLaunchKernelGGL((fused_grouped_kernel<kFusedBf16, kGroupedNBW>), dim3((unsigned)fused_grid(p.M, p.E, p.NB * 16)),
-                       dim3(512), 0, stream, p, (int)NT);
-    return hipGetLastError();
-  }
-  const FusedPlan plan = plan_of(p);
-  if (p.kbytes < 16 || (plan.kernel == kTile256 && !fused_rows_ok(p))) {
+hipError_t launch_fused_grouped(const FusedGemm& p, hipStream_t stream) {
+  const int64_t NT = grouped_columns(p.NB * 16);
+  hipLaunchKernelGGL((fused_grouped_kernel<kFusedBf16, kGroupedNBW>), dim3((unsigned)fused_grid(p.M, p.E, p.NB * 16)),
+                     dim3(512), 0, stream, p, (int)NT);
+  return hipGetLastError();
+}
+
+hipError_t launch_fused_gemm(FusedGemm p, const FusedPlan& plan, void* room, hipStream_t stream) {
+  if (plan.copy) {
     const int64_t per = round_up(p.kbytes, kStepBytes) / 16;
+    uint8_t* rows = reinterpret_cast<uint8_t*>(room);
     hipLaunchKernelGGL(fused_copy_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(p.M * per, 256), 1 << 16)), dim3(256),
-                       0, stream, p.a, p.M, p.lda, p.kbytes, per, reinterpret_cast<uint8_t*>(room));
+                       0, stream, p.a, p.M, p.lda, p.kbytes, per, rows);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    p.a = reinterpret_cast<const uint8_t*>(room);
+    room = rows + copy_bytes(p.M, p.kbytes);
+    p.a = rows;
     p.lda = p.kbytes = per * 16;
   }
   return p.type == kFusedInt8 ? launch_dense<kFusedInt8>(p, plan, room, stream)

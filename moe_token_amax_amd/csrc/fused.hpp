@@ -41,16 +41,24 @@ int64_t bf16_packed_bytes(int64_t N, int64_t K);  // of one [N, K] weight
 hipError_t launch_bf16_prepack(const uint16_t* w, int64_t E, int64_t N, int64_t K, bool pairs, void* packed,
                                hipStream_t stream);
 
-// Workspace of a dense product: rows copied (zero-padded) where the wide tiles need them
-// 16-byte aligned and whole, or the sums of the parts of a split K; and the most that a
-// product of these sizes can need.
-int64_t fused_room_bytes(const FusedGemm& p);
+// How a dense product runs, chosen from its sizes and alignment.
+struct FusedPlan {
+  int kernel;  // of fused.hip's
+  int S;       // parts of K (tiles)
+  bool copy;   // rows copied to whole, aligned, zero-padded steps first
+};
+FusedPlan fused_plan(const FusedGemm& p);
+// Workspace: the copied rows, then the sums of the parts; and the most that a product of
+// these sizes can need, whatever its rows' alignment.
+int64_t fused_room_bytes(const FusedGemm& p, const FusedPlan& plan);
 int64_t fused_most_bytes(int type, int64_t M, int64_t N, int64_t K);
-hipError_t launch_fused_gemm(FusedGemm p, void* room, hipStream_t stream);
+// M, N >= 1
+hipError_t launch_fused_gemm(FusedGemm p, const FusedPlan& plan, void* room, hipStream_t stream);
 
 int64_t fused_sched_bytes(int64_t R, int64_t E);
 int64_t fused_grid(int64_t R, int64_t E, int64_t N);  // workgroups of a grouped product
 // the tile list of p's group_list, rows and operands, into p.ws
 hipError_t launch_fused_schedule(const FusedGemm& p, void* ws, hipStream_t stream);
+hipError_t launch_fused_grouped(const FusedGemm& p, hipStream_t stream);
 
 }  // namespace w8a8

@@ -317,6 +317,7 @@ static hipError_t launch_format(const NormArgs& p, hipStream_t stream) {
     launch<FMT, 1, 4>(p, stream);
   } else if (p.M > 512 && chunks <= 16 * 64) {
     if (chunks <= 8 * 64) launch<FMT, 2, 4>(p, stream);
+    else if (chunks <= 12 * 64) launch<FMT, 3, 4>(p, stream);
     else launch<FMT, 4, 4>(p, stream);
   } else if (chunks <= 16 * 64) {
     launch<FMT, 1, 16>(p, stream);

@@ -124,8 +124,10 @@ def test_prepack_refusals_and_sizes(w):
     assert w.bf16_packed_bytes(1, 4096, 7168) == 4096 * 7168 * 2
     assert w.bf16_packed_bytes(3, 17, 65) == 3 * 32 * 128 * 2                    # N to 32, K to 64
     assert w._bf16_packed(3, 17, 65) == w.bf16_packed_bytes(3, 17, 65)
-    assert w.linear_fused_workspace_bytes(3, 16, 200) == 3 * 256
-    assert w.bf16_linear_workspace_bytes(3, 16, 200) == 3 * 512
+    assert w.linear_fused_workspace_bytes(3, 16, 200) == w.bf16_linear_workspace_bytes(3, 16, 200) == 0
+    assert w.linear_fused_workspace_bytes(3, 16, 15) == w.bf16_linear_workspace_bytes(3, 16, 7) == 512  # rows copied
+    assert w.bf16_linear_workspace_bytes(8192, 4096, 7169) >= 8192 * 2 * 7232
+    assert w.bf16_linear_workspace_bytes(300, 300, 16000) >= 2 * 300 * 300 * 4  # sums of the parts of K
     assert w.bf16_linear_workspace_bytes(0, 16, 200) == 0
     assert w.bf16_grouped_workspace_bytes(0, 4, 16, 64) == 0
 
