@@ -1640,7 +1640,7 @@ static int check_bf16_grouped(const char* who, int64_t R, int64_t E, int64_t N, 
   if (E < 1) return fail(W8A8_ERR_SHAPE, "%s: need E >= 1", who);
   if (E > kMaxExperts) return fail(W8A8_ERR_UNSUPPORTED, "%s: at most %lld experts", who, (long long)kMaxExperts);
   if (K < 8) return fail(W8A8_ERR_UNSUPPORTED, "%s: needs K >= 8", who);
-  if (w8a8::fused_grid(R, E, w8a8::round_up(N, 32)) >= (int64_t)1 << 23)  // of 512 threads
+  if (w8a8::fused_grid(R, E, N, K) >= (int64_t)1 << 23)  // of 512 threads
     return fail(W8A8_ERR_UNSUPPORTED, "%s: R = %lld rows of N = %lld columns are past one launch", who, (long long)R,
                 (long long)N);
   return W8A8_OK;
@@ -1648,7 +1648,7 @@ static int check_bf16_grouped(const char* who, int64_t R, int64_t E, int64_t N, 
 
 int64_t w8a8_bf16_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K) {
   if (R <= 0 || E <= 0 || N <= 0 || K <= 0) return 0;
-  return w8a8::fused_sched_bytes(R, E);
+  return w8a8::fused_sched_bytes(R, E, N, K);
 }
 
 int w8a8_bf16_grouped_gemm(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_t* row_index,
@@ -1668,7 +1668,7 @@ int w8a8_bf16_grouped_gemm(const uint16_t* x, int64_t ldx, int64_t x_rows, const
   if (!x || !group_list || !w_packed || !y) return fail(W8A8_ERR_NULL, "bf16_grouped_gemm: null pointer");
   if (!aligned(x, 2) || !aligned(row_index, 4) || !aligned(group_list, 8) || !aligned(w_packed, 16) || !aligned(y, 2))
     return fail(W8A8_ERR_ALIGN, "bf16_grouped_gemm: misaligned buffer");
-  const int64_t need = w8a8::fused_sched_bytes(R, E);
+  const int64_t need = w8a8::fused_sched_bytes(R, E, N, K);
   if (!workspace || ws_bytes < need || !aligned(workspace, 256))
     return fail(W8A8_ERR_WORKSPACE, "bf16_grouped_gemm: needs %lld workspace bytes (256-byte aligned), got %lld",
                 (long long)need, (long long)ws_bytes);
@@ -1681,9 +1681,7 @@ int w8a8_bf16_grouped_gemm(const uint16_t* x, int64_t ldx, int64_t x_rows, const
   p.y = y;
   p.ldy = act == W8A8_ACT_SWIGLU ? N / 2 : N;
   p.ws = workspace;
-  const hipError_t err = w8a8::launch_fused_schedule(p, workspace, (hipStream_t)stream);
-  if (err != hipSuccess) return launched(err, "bf16_grouped_gemm: schedule");
-  return launched(w8a8::launch_fused_grouped(p, (hipStream_t)stream), "bf16_grouped_gemm");
+  return launched(w8a8::launch_fused_grouped(p, workspace, (hipStream_t)stream), "bf16_grouped_gemm");
 }
 
 }  // extern "C"

@@ -331,19 +331,15 @@ __global__ __launch_bounds__(256) void fused_copy_kernel(const uint8_t* __restri
 // ---------------------------------------------------------------------------
 // Schedule of a grouped product: int32 count (256 bytes), then int4 {expert, first row,
 // rows, 0} for every tile, in expert order: wide tiles of at most 256 rows of one expert
-// while more than kWideFrom are left, then at most kTileRows.
+// while more than kWideFrom are left, then at most tile_rows.
 // ---------------------------------------------------------------------------
 constexpr int kTileRows = 128, kWideRows = 256, kWideFrom = 160;
-constexpr int kGroupedNBW = 2;
 
-int64_t fused_max_tiles(int64_t R, int64_t E) { return R / kTileRows + std::min(R, E); }
-int64_t fused_sched_bytes(int64_t R, int64_t E) { return 256 + 16 * fused_max_tiles(R, E); }
-static int64_t grouped_columns(int64_t N) { return ceil_div(N, 128 * kGroupedNBW); }
-int64_t fused_grid(int64_t R, int64_t E, int64_t N) { return round_up(fused_max_tiles(R, E), 8) * grouped_columns(N); }
+static int64_t max_tiles(int64_t R, int64_t E, int tile_rows) { return R / tile_rows + std::min(R, E); }
 
 // one workgroup of 256 threads, four experts each (E <= 1024)
 __global__ __launch_bounds__(256) void fused_schedule_kernel(const int64_t* __restrict__ group_list, int E, int64_t R,
-                                                             int wide, int* count, int4* tiles) {
+                                                             int wide, int tile_rows, int* count, int4* tiles) {
   __shared__ int64_t wrows[4];
   __shared__ int wtiles[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -372,7 +368,7 @@ __global__ __launch_bounds__(256) void fused_schedule_kernel(const int64_t* __re
     ri += n[i];
     n[i] = min(n[i], R - row0[i]);
     const int64_t full = wide ? n[i] / kWideRows : 0, left = n[i] - full * kWideRows;
-    t += (int)(full + (wide && left > kWideFrom ? 1 : (left + kTileRows - 1) / kTileRows));
+    t += (int)(full + (wide && left > kWideFrom ? 1 : (left + tile_rows - 1) / tile_rows));
   }
   int ti = t;
 #pragma unroll
@@ -388,7 +384,7 @@ __global__ __launch_bounds__(256) void fused_schedule_kernel(const int64_t* __re
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     for (int64_t r = 0; r < n[i];) {
-      const int64_t left = n[i] - r, rows = min(left, (int64_t)(wide && left > kWideFrom ? kWideRows : kTileRows));
+      const int64_t left = n[i] - r, rows = min(left, (int64_t)(wide && left > kWideFrom ? kWideRows : tile_rows));
       tiles[ti++] = int4{4 * tid + i, (int)(row0[i] + r), (int)rows, 0};
       r += rows;
     }
@@ -649,17 +645,6 @@ struct StreamTile {
   static constexpr int kTurnShift = NBW == 2 ? 6 : 5;  // log2 of the 16-byte chunks of a row
   __device__ __forceinline__ static int sums_at(int r, int c) { return (r << (kTurnShift + 4)) + ((c ^ (r & 15)) << 4); }
 };
-
-// tile height by the rows there are
-template <int TY, int NBW>
-__device__ __forceinline__ void stream_tile(const FusedGemm& p, uint8_t* smem, int e, int64_t row0, int rows, int nb0) {
-  const int KB = (int)(p.KP + 1) / 2;
-  if (rows <= 16) StreamTile<TY, 1, NBW>::run(p, smem, e, row0, rows, nb0, 0, KB, nullptr);
-  else if (rows <= 32) StreamTile<TY, 2, NBW>::run(p, smem, e, row0, rows, nb0, 0, KB, nullptr);
-  else if (rows <= 64) StreamTile<TY, 4, NBW>::run(p, smem, e, row0, rows, nb0, 0, KB, nullptr);
-  else if (rows <= 96) StreamTile<TY, 6, NBW>::run(p, smem, e, row0, rows, nb0, 0, KB, nullptr);
-  else StreamTile<TY, 8, NBW>::run(p, smem, e, row0, rows, nb0, 0, KB, nullptr);
-}
 
 // Dense: tiles of one height. S > 1: K in S parts of `per` steps each, whose sums
 // fused_join_kernel adds. Workgroup b runs on XCD b % 8: each XCD takes its own
@@ -1187,11 +1172,13 @@ __global__ __launch_bounds__(512) void fused_wide_kernel(FusedGemm p) {
 // rows through, 4 or 8 tiles at a time.
 constexpr int kSpreadTiles = 64;
 
+// NBW 2: tiles of 128 rows x 256 columns, and wide ones; NBW 1: 64 rows x 128 columns,
+// for products that would not fill the chip with those.
 template <int TY, int NBW>
 __global__ __launch_bounds__(512) void fused_grouped_kernel(FusedGemm p, int NT) {
   using T = WideTile<TY, false>;
-  static_assert(StreamTile<TY, 8, NBW>::kLdsBytes <= T::kLdsBytes && NBW == 2, "one column group, one LDS");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::kLdsBytes];
+  static_assert(StreamTile<TY, 8, 2>::kLdsBytes <= T::kLdsBytes, "one LDS");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[NBW == 2 ? T::kLdsBytes : StreamTile<TY, 4, 1>::kLdsBytes];
   const int count = *reinterpret_cast<const int*>(p.ws);
   int t, c;
   if (count >= kSpreadTiles) {
@@ -1206,16 +1193,29 @@ __global__ __launch_bounds__(512) void fused_grouped_kernel(FusedGemm p, int NT)
   if (t >= count) return;
   const int4 tile = reinterpret_cast<const int4*>(reinterpret_cast<const char*>(p.ws) + 256)[t];
   const int e = __builtin_amdgcn_readfirstlane(tile.x), row0 = __builtin_amdgcn_readfirstlane(tile.y);
-  const int rows = __builtin_amdgcn_readfirstlane(tile.z);
-  if (rows > kTileRows) {
-    int left = 1;
-    T::run(p, smem, [&]() __attribute__((always_inline)) {
-      typename T::Where w{};
-      if (left-- > 0) w = typename T::Where{rows, c * 8 * NBW, row0, e};
-      return w;
-    });
-  } else {
-    stream_tile<TY, NBW>(p, smem, e, row0, rows, c * 8 * NBW);
+  const int rows = __builtin_amdgcn_readfirstlane(tile.z), nb0 = c * 8 * NBW, KB = (int)(p.KP + 1) / 2;
+  auto run = [&](auto MB) __attribute__((always_inline)) {
+    StreamTile<TY, decltype(MB)::value, NBW>::run(p, smem, e, row0, rows, nb0, 0, KB, nullptr);
+  };
+  if (rows <= 16) {
+    run(std::integral_constant<int, 1>{});
+  } else if (rows <= 32) {
+    run(std::integral_constant<int, 2>{});
+  } else if (NBW == 1 || rows <= 64) {
+    run(std::integral_constant<int, 4>{});
+  } else if constexpr (NBW == 2) {
+    if (rows <= 96) {
+      run(std::integral_constant<int, 6>{});
+    } else if (rows <= kTileRows) {
+      run(std::integral_constant<int, 8>{});
+    } else {
+      int left = 1;
+      T::run(p, smem, [&]() __attribute__((always_inline)) {
+        typename T::Where w{};
+        if (left-- > 0) w = typename T::Where{rows, nb0, row0, e};
+        return w;
+      });
+    }
   }
 }
 
@@ -1225,19 +1225,6 @@ __global__ __launch_bounds__(512) void fused_grouped_kernel(FusedGemm p, int NT)
 // (offsets within a tile's 256 rows have 32 bits)
 bool fused_rows_ok(const FusedGemm& p) {
   return p.lda % 16 == 0 && p.lda < (int64_t)1 << 24 && p.kbytes % 16 == 0 && ((uintptr_t)p.a & 15) == 0;
-}
-
-// whether experts of many rows take wide tiles: two steps of K, rows as they copy them,
-// 32-bit offsets from a's first row where rows are read through an index
-static bool grouped_wide(const FusedGemm& p) {
-  return p.KP > 2 && fused_rows_ok(p) && (!p.row_index || p.a_rows * p.lda < (int64_t)1 << 32);
-}
-
-hipError_t launch_fused_schedule(const FusedGemm& p, void* ws, hipStream_t stream) {
-  hipLaunchKernelGGL(fused_schedule_kernel, dim3(1), dim3(256), 0, stream, p.group_list, (int)p.E, p.M,
-                     (int)grouped_wide(p), reinterpret_cast<int*>(ws),
-                     reinterpret_cast<int4*>(reinterpret_cast<char*>(ws) + 256));
-  return hipGetLastError();
 }
 
 enum FusedKernel { kDecode16, kDecode16x32, kDecode32, kDecode64, kTile32, kTile64, kTile64x256, kTile128, kTile256 };
@@ -1262,6 +1249,11 @@ constexpr FusedCost kCost[] = {
     {256, 256, 3.36, 10.9, 1.23, 1.3, 0, 0},
 };
 
+static double tiles_time(const FusedCost& c, int64_t tiles, int64_t steps) {
+  const double rounds = tiles / 512.0;
+  return c.launch + rounds * c.round + (double)steps * std::max(c.first, rounds * c.step);
+}
+
 static FusedPlan cheapest(int64_t M, int64_t NB, int64_t KP, bool swiglu, double& least) {
   const int64_t KB = ceil_div(KP, 2);
   FusedPlan best{kTile64, 1, false};
@@ -1277,8 +1269,7 @@ static FusedPlan cheapest(int64_t M, int64_t NB, int64_t KP, bool swiglu, double
       const int64_t per = ceil_div(KB, S);
       S = ceil_div(KB, per);  // no empty part
       const int64_t n = tiles * S;
-      const double rounds = k == kTile256 ? (double)ceil_div(n, 256) : n / 512.0;
-      double t = c.launch + rounds * c.round + per * std::max(c.first, rounds * c.step);
+      double t = tiles_time(c, k == kTile256 ? 512 * ceil_div(n, 256) : n, per);
       if (S > 1) t += c.join + c.part * (double)(n * c.rows * c.cols * 4) * 1e-6;
       if (t < least) {
         least = t;
@@ -1384,10 +1375,47 @@ static hipError_t launch_dense(const FusedGemm& p, const FusedPlan& plan, void* 
   return hipGetLastError();
 }
 
-hipError_t launch_fused_grouped(const FusedGemm& p, hipStream_t stream) {
-  const int64_t NT = grouped_columns(p.NB * 16);
-  hipLaunchKernelGGL((fused_grouped_kernel<kFusedBf16, kGroupedNBW>), dim3((unsigned)fused_grid(p.M, p.E, p.NB * 16)),
-                     dim3(512), 0, stream, p, (int)NT);
+// Rows of a grouped product's tiles (128 rows: of 256 columns, 64: of 128), from the most
+// tiles that there can be, by the cost of a dense product of as many. In us, 64 and 128:
+// 1003 rows, 7 experts of 1412 x 1000 17.4, 37.8; 128 rows, 256 experts of 4096 x 4096 524,
+// 546; 8192 rows, 16 experts of 2048 x 2048 126, 120; 16384 rows, 64 experts of 4096 x 4096
+// 1273, 743.
+static int grouped_rows(int64_t R, int64_t E, int64_t NB, int64_t KP) {
+  double t[2];
+  for (int i = 0; i < 2; ++i) {
+    const FusedCost& c = kCost[i ? kTile128 : kTile64];
+    t[i] = tiles_time(c, max_tiles(R, E, c.rows) * ceil_div(NB * 16, c.cols), ceil_div(KP, 2));
+  }
+  return kCost[t[1] < t[0] ? kTile128 : kTile64].rows;
+}
+
+static int64_t grouped_columns(int64_t NB, int tile_rows) { return ceil_div(NB, tile_rows == kTileRows ? 16 : 8); }
+
+static int64_t blocks_of(int64_t N) { return round_up(N, 32) / 16; }
+static int64_t pieces_of(int64_t K) { return 2 * ceil_div(K, 64); }
+
+int64_t fused_sched_bytes(int64_t R, int64_t E, int64_t N, int64_t K) {
+  return 256 + 16 * max_tiles(R, E, grouped_rows(R, E, blocks_of(N), pieces_of(K)));
+}
+
+int64_t fused_grid(int64_t R, int64_t E, int64_t N, int64_t K) {
+  const int rows = grouped_rows(R, E, blocks_of(N), pieces_of(K));
+  return round_up(max_tiles(R, E, rows), 8) * grouped_columns(blocks_of(N), rows);
+}
+
+// Wide tiles for experts of many rows: two steps of K, rows as they copy them, 32-bit
+// offsets from a's first row where rows are read through an index.
+hipError_t launch_fused_grouped(const FusedGemm& p, void* ws, hipStream_t stream) {
+  const int rows = grouped_rows(p.M, p.E, p.NB, p.KP);
+  const bool wide = rows == kTileRows && p.KP > 2 && fused_rows_ok(p) &&
+                    (!p.row_index || p.a_rows * p.lda < (int64_t)1 << 32);
+  hipLaunchKernelGGL(fused_schedule_kernel, dim3(1), dim3(256), 0, stream, p.group_list, (int)p.E, p.M, (int)wide, rows,
+                     reinterpret_cast<int*>(ws), reinterpret_cast<int4*>(reinterpret_cast<char*>(ws) + 256));
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const int64_t NT = grouped_columns(p.NB, rows), grid = round_up(max_tiles(p.M, p.E, rows), 8) * NT;
+  auto fn = rows == kTileRows ? fused_grouped_kernel<kFusedBf16, 2> : fused_grouped_kernel<kFusedBf16, 1>;
+  hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(512), 0, stream, p, (int)NT);
   return hipGetLastError();
 }
 

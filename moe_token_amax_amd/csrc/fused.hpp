@@ -33,7 +33,7 @@ struct FusedGemm {
   int f32;
   const int64_t* group_list; // [E] or null
   int64_t E;
-  const void* ws;            // grouped: the schedule written by launch_fused_schedule
+  const void* ws;            // grouped: the tile list
 };
 
 int64_t bf16_packed_bytes(int64_t N, int64_t K);  // of one [N, K] weight
@@ -55,10 +55,10 @@ int64_t fused_most_bytes(int type, int64_t M, int64_t N, int64_t K);
 // M, N >= 1
 hipError_t launch_fused_gemm(FusedGemm p, const FusedPlan& plan, void* room, hipStream_t stream);
 
-int64_t fused_sched_bytes(int64_t R, int64_t E);
-int64_t fused_grid(int64_t R, int64_t E, int64_t N);  // workgroups of a grouped product
-// the tile list of p's group_list, rows and operands, into p.ws
-hipError_t launch_fused_schedule(const FusedGemm& p, void* ws, hipStream_t stream);
-hipError_t launch_fused_grouped(const FusedGemm& p, hipStream_t stream);
+// Grouped (R = p.M rows): bytes of the tile list, workgroups, and the launch, which
+// writes the list into p.ws first.
+int64_t fused_sched_bytes(int64_t R, int64_t E, int64_t N, int64_t K);
+int64_t fused_grid(int64_t R, int64_t E, int64_t N, int64_t K);
+hipError_t launch_fused_grouped(const FusedGemm& p, void* ws, hipStream_t stream);
 
 }  // namespace w8a8

@@ -463,3 +463,121 @@ def test_two_streams_at_once(w):
             w.bf16_linear(x, wp, N, y=y, workspace=room[i % 2])
     sync()
     assert all(torch.equal(y, want) for y in ys)
+
+
+# ------------------------------------------------------------------ every kernel and split
+PLANS = [  # M, N, K of BF16 (INT8: twice the K)
+    (23, 22, 62), (107, 4, 4386), (38, 3440, 206), (52, 1984, 1172), (103, 2662, 1546), (75, 22, 8540), (180, 302, 9000),
+    (654, 942, 2031), (227, 20, 9528), (340, 1502, 3400), (700, 4134, 1000), (389, 8070, 1104), (4325, 134, 5911),
+    (5629, 1438, 455), (2448, 5190, 67), (2500, 4202, 1111)]
+
+
+def _sample(M):
+    return np.unique(np.clip(np.r_[0:2, 15:18, 31:34, 63:66, 126:130, 255:258, M // 2:M // 2 + 3, M - 3:M], 0, M - 1))
+
+
+@pytest.mark.parametrize("kind,act", [("bf16", "none"), ("bf16", "swiglu"), ("bf16", "gelu"), ("int8", "silu"), ("int8", "none")])
+@pytest.mark.parametrize("M,N,K", PLANS)
+def test_every_kernel(w, M, N, K, kind, act):
+    """Low and high tiles, K whole and in parts, with and without the epilogue's operands;
+    sampled rows against 64 bits."""
+    show(f"{kind} {M} x {N} x {K} {act}")
+    rng = np.random.default_rng(M + N + K)
+    width = N // 2 if act == "swiglu" else N
+    with_res = act != "gelu"
+    b, r = _bf16(rng, N, scale=0.3), _bf16(rng, M, width)
+    room = torch.full((M + 2, width), 7.0, dtype=torch.bfloat16, device=DEV)
+    kw = dict(bias=bf16_dev(b), act=_act_id(w, act), residual=bf16_dev(r) if with_res else None)
+    pick = _sample(M)
+    if kind == "bf16":
+        x, wt = _acts(rng, M, K), _bf16(rng, N, K, scale=1 / math.sqrt(K))
+        w.bf16_linear(bf16_dev(x), w.bf16_prepack_weight(bf16_dev(wt), act=_act_id(w, act)), N, y=room[1:M + 1], **kw)
+        v, dv = _bf16_value(x[pick], wt, b)
+    else:
+        q, s, wi, ws = _int8_operands(rng, M, N, 2 * K)
+        w.linear_fused(dev(q), dev(s), w.prepack_weight(dev(wi)), dev(ws), N, y=room[1:M + 1], **kw)
+        v = (q[pick].astype(np.float64) @ wi.T.astype(np.float64)) * s[pick].astype(np.float64)[:, None] * ws.astype(np.float64)
+        dv = 3.1 * U * np.abs(v)                          # acc to fp32, two products
+        v = v + _f64(b)
+        dv = dv + U * (np.abs(v) + dv)
+    sync()
+    assert (room[0] == 7).all() and (room[M + 1] == 7).all()
+    y = room[1:M + 1]
+    _hold(y[torch.from_numpy(pick).to(DEV)], *_epilogue(v, dv, act, r[pick] if with_res else None), f"{M}x{N}x{K}")
+    assert torch.isfinite(y.float()).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("M,N,K,lo", [(700, 4134, 1001, 1), (300, 1000, 5761, 3), (2500, 4202, 1111, 1), (340, 1502, 3403, 5)])
+def test_rows_that_are_copied(w, M, N, K, lo, kind):
+    """Rows at odd addresses, NaN (INT8: codes) around them."""
+    rng = np.random.default_rng(K)
+    pick = _sample(M)
+    if kind == "bf16":
+        x, wt = _acts(rng, M, K), _bf16(rng, N, K, scale=1 / math.sqrt(K))
+        wide = torch.full((M, K + 6), float("nan"), dtype=torch.bfloat16, device=DEV)
+        wide[:, lo:lo + K] = bf16_dev(x)
+        y = w.bf16_linear(wide[:, lo:lo + K], w.bf16_prepack_weight(bf16_dev(wt)), N)
+        sync()
+        _hold(y[torch.from_numpy(pick).to(DEV)], *_epilogue(*_bf16_value(x[pick], wt), "none"))
+        return
+    q, s, wi, ws = _int8_operands(rng, M, N, K)
+    wide = torch.full((M, K + 6), 99, dtype=torch.int8, device=DEV)
+    wide[:, lo:lo + K] = dev(q)
+    wp = w.prepack_weight(dev(wi))
+    a = w.linear_fused(wide[:, lo:lo + K], dev(s), wp, dev(ws), N)
+    b = w.linear(dev(q), dev(s), wp, dev(ws), N)
+    sync()
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+@pytest.mark.parametrize("act,index,lo", [("none", True, 0), ("swiglu", False, 0), ("gelu", True, 3)])
+@pytest.mark.parametrize("counts,N,K", [([900, 0, 513, 161, 160, 1466], 4130, 700), ([2700, 300], 4200, 1000)])
+def test_grouped_of_many_rows(w, counts, N, K, act, index, lo):
+    """Tiles of 128 and of 256 rows; rows through an index, rows at odd addresses."""
+    rng = np.random.default_rng(N + K)
+    E, R, T = len(counts), sum(counts) + 5, 777
+    x = _acts(rng, T if index else R, K)
+    wide = torch.full((len(x), K + 8), float("nan"), dtype=torch.bfloat16, device=DEV)
+    wide[:, lo:lo + K] = bf16_dev(x)
+    rows = rng.integers(0, T, R).astype(np.int32) if index else np.arange(R)
+    wt = _bf16(rng, E, N, K, scale=1 / math.sqrt(K))
+    width = N // 2 if act == "swiglu" else N
+    y = torch.full((R, width), 7.0, dtype=torch.bfloat16, device=DEV)
+    w.bf16_grouped_gemm(wide[:, lo:lo + K], dev(np.array(counts, np.int64)),
+                        w.bf16_prepack_weight(bf16_dev(wt), act=_act_id(w, act)), N, act=_act_id(w, act),
+                        row_index=dev(rows) if index else None, y=y)
+    sync()
+    assert (y[sum(counts):] == 7).all() and torch.isfinite(y.float()).all()
+    first = 0
+    for e, n in enumerate(counts):
+        if n:
+            pick = first + _sample(n)
+            v, dv = _bf16_value(x[rows[pick]], wt[e])
+            _hold(y[torch.from_numpy(pick).to(DEV)], *_epilogue(v, dv, act), f"expert {e}")
+        first += n
+
+
+def test_split_sums_captured_and_replayed(w):
+    """A product whose K is split, in a graph that is replayed with new rows and its own
+    workspace, with eager work on the same stream between."""
+    rng = np.random.default_rng(9)
+    M, N, K = 180, 302, 9000
+    wt = _bf16(rng, N, K, scale=1 / math.sqrt(K))
+    wp = w.bf16_prepack_weight(bf16_dev(wt))
+    assert w.bf16_linear_workspace_bytes(M, N, K) >= 2 * M * N * 4
+    x = torch.zeros((M, K), dtype=torch.bfloat16, device=DEV)
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=DEV)
+    room = torch.empty((w.bf16_linear_workspace_bytes(M, N, K),), dtype=torch.uint8, device=DEV)
+    w.bf16_linear(x, wp, N, y=y, workspace=room)
+    sync()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        w.bf16_linear(x, wp, N, y=y, workspace=room)
+    for i in range(4):
+        x.copy_(bf16_dev(_acts(rng, M, K)))
+        room.fill_(255)                                   # nothing of the call before is used
+        g.replay()
+        eager = w.bf16_linear(x, wp, N)
+        sync()
+        assert torch.equal(y.view(torch.int16), eager.view(torch.int16)), i
