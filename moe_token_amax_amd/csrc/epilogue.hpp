@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/w8a8.h"
 #include "bf16_io.hpp"
 #include "device_common.hpp"
@@ -60,6 +62,42 @@ __device__ __forceinline__ void activate4(int act, float (&v)[4]) {
     default: break;
   }
 #undef W8A8_EACH
+}
+
+constexpr int kAnyAct = -1;
+
+// run(ACT) for act, so that a loop over rows holds no choice of it (some ten branches an
+// output: 0.7 us for every 16 rows of a tile)
+template <bool SWIGLU, class Run>
+__device__ __forceinline__ void for_act(int act, Run run) {
+  switch (act) {  // the same in every lane
+    case W8A8_ACT_SWIGLU:
+      if constexpr (SWIGLU) run(std::integral_constant<int, W8A8_ACT_SWIGLU>{});
+      break;
+    case W8A8_ACT_RELU: run(std::integral_constant<int, W8A8_ACT_RELU>{}); break;
+    case W8A8_ACT_SILU: run(std::integral_constant<int, W8A8_ACT_SILU>{}); break;
+    case W8A8_ACT_GELU: run(std::integral_constant<int, W8A8_ACT_GELU>{}); break;
+    case W8A8_ACT_GELU_TANH: run(std::integral_constant<int, W8A8_ACT_GELU_TANH>{}); break;
+    default: run(std::integral_constant<int, W8A8_ACT_NONE>{}); break;
+  }
+}
+
+// What is added where there is no bias or no residual, -0 (v + -0 is v, also where v is
+// -0): a pair of it in BF16.
+constexpr uint32_t kNothing2 = 0x80008000u;
+
+__device__ __forceinline__ float bf16_of(const Bytes8& u, int t) {
+  return __uint_as_float(t & 1 ? u.w[t >> 1] & 0xFFFF0000u : u.w[t >> 1] << 16);
+}
+
+// n of four BF16 values as they lie in memory, -0 past them. WHOLE: n is 4.
+template <bool WHOLE>
+__device__ __forceinline__ Bytes8 load_raw4(const uint16_t* src, int n) {
+  if (WHOLE) return *reinterpret_cast<const Bytes8*>(src);
+  uint32_t u[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) u[t] = t < n ? src[t] : kNothing2 & 0xFFFFu;
+  return Bytes8{{u[0] | (u[1] << 16), u[2] | (u[3] << 16)}};
 }
 
 // up to 4 neighbouring BF16 values (0 past n of them)

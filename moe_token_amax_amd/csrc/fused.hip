@@ -119,10 +119,6 @@ struct __attribute__((packed, aligned(4))) Floats4 {
 
 __device__ __forceinline__ int64_t outputs_of(const FusedGemm& p) { return p.act == W8A8_ACT_SWIGLU ? p.N / 2 : p.N; }
 
-// What is added where there is no bias or no residual, -0 (v + -0 is v, also where v is
-// -0): a pair of it in BF16.
-constexpr uint32_t kNothing2 = 0x80008000u;
-
 // A lane's four neighbouring output columns c .. c + 3: what belongs to them and not to a
 // row, loaded once for all the rows of a tile. WHOLE: the columns exist, for every lane
 // of the wavefront (a path of its own: with a choice at every access the epilogue of a
@@ -132,20 +128,6 @@ struct Cols {
   int n;  // of the four that exist; 0: none
   float bias[4], second[4];  // second: INT8 the columns' scales, SwiGLU the up half's bias
 };
-
-__device__ __forceinline__ float bf16_of(const Bytes8& u, int t) {
-  return __uint_as_float(t & 1 ? u.w[t >> 1] & 0xFFFF0000u : u.w[t >> 1] << 16);
-}
-
-// n of four BF16 values as they lie in memory, -0 past them
-template <bool WHOLE>
-__device__ __forceinline__ Bytes8 load_raw4(const uint16_t* src, int n) {
-  if (WHOLE) return *reinterpret_cast<const Bytes8*>(src);
-  uint32_t u[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) u[t] = t < n ? src[t] : kNothing2 & 0xFFFFu;
-  return Bytes8{{u[0] | (u[1] << 16), u[2] | (u[3] << 16)}};
-}
 
 template <int TY, bool WHOLE>
 __device__ __forceinline__ Cols load_cols(const FusedGemm& p, int64_t c) {
@@ -192,8 +174,6 @@ __device__ __forceinline__ Bytes8 load_residual(const FusedGemm& p, int64_t m, c
 // The outputs of row m from the sums of its four weight rows (SwiGLU: and of their
 // partners `up`).
 // ACT: p.act, or kAnyAct
-constexpr int kAnyAct = -1;
-
 template <int TY, bool WHOLE, int ACT, class Acc>
 __device__ __forceinline__ void emit4(const FusedGemm& p, int64_t m, const Cols& o, float xs, const Bytes8& res,
                                       const Acc& acc, const Acc& up) {
@@ -230,22 +210,6 @@ __device__ __forceinline__ void emit4(const FusedGemm& p, int64_t m, const Cols&
       for (int t = 0; t < 4; ++t)
         if (t < o.n) y[t] = (uint16_t)q[t];
     }
-  }
-}
-
-// run(ACT) for p.act, so that a loop over rows holds no choice of it (some ten branches
-// an output: 0.7 us for every 16 rows of a tile)
-template <int TY, class Run>
-__device__ __forceinline__ void for_act(const FusedGemm& p, Run run) {
-  switch (p.act) {  // the same in every lane
-    case W8A8_ACT_SWIGLU:
-      if constexpr (TY == kFusedBf16) run(std::integral_constant<int, W8A8_ACT_SWIGLU>{});
-      break;
-    case W8A8_ACT_RELU: run(std::integral_constant<int, W8A8_ACT_RELU>{}); break;
-    case W8A8_ACT_SILU: run(std::integral_constant<int, W8A8_ACT_SILU>{}); break;
-    case W8A8_ACT_GELU: run(std::integral_constant<int, W8A8_ACT_GELU>{}); break;
-    case W8A8_ACT_GELU_TANH: run(std::integral_constant<int, W8A8_ACT_GELU_TANH>{}); break;
-    default: run(std::integral_constant<int, W8A8_ACT_NONE>{}); break;
   }
 }
 
@@ -330,10 +294,11 @@ __global__ __launch_bounds__(256) void fused_copy_kernel(const uint8_t* __restri
 
 // ---------------------------------------------------------------------------
 // Schedule of a grouped product: int32 count (256 bytes), then int4 {expert, first row,
-// rows, 0} for every tile, in expert order: wide tiles of at most 256 rows of one expert
-// while more than kWideFrom are left, then at most tile_rows.
+// rows, 0} for every tile: in expert order the wide tiles of at most 256 rows of one
+// expert, while more than kTileRows are left, then (what takes longest starts first) the
+// tiles of at most tile_rows.
 // ---------------------------------------------------------------------------
-constexpr int kTileRows = 128, kWideRows = 256, kWideFrom = 160;
+constexpr int kTileRows = 128, kWideRows = 256;
 
 static int64_t max_tiles(int64_t R, int64_t E, int tile_rows) { return R / tile_rows + std::min(R, E); }
 
@@ -341,7 +306,7 @@ static int64_t max_tiles(int64_t R, int64_t E, int tile_rows) { return R / tile_
 __global__ __launch_bounds__(256) void fused_schedule_kernel(const int64_t* __restrict__ group_list, int E, int64_t R,
                                                              int wide, int tile_rows, int* count, int4* tiles) {
   __shared__ int64_t wrows[4];
-  __shared__ int wtiles[4];
+  __shared__ int64_t wtiles[4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   // counts past R are a caller error: such rows own no tile
   int64_t n[4], sum = 0;
@@ -360,34 +325,42 @@ __global__ __launch_bounds__(256) void fused_schedule_kernel(const int64_t* __re
   __syncthreads();
   for (int w = 0; w < wave; ++w) ri += wrows[w];
   ri -= sum;
-  int64_t row0[4];
-  int t = 0;
+  // tiles, wide ones in the upper half
+  int64_t row0[4], t = 0;
+  auto wide_tiles = [&](int64_t rows) { return wide ? rows / kWideRows + (rows % kWideRows > kTileRows) : 0; };
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     row0[i] = min(ri, R);
     ri += n[i];
     n[i] = min(n[i], R - row0[i]);
-    const int64_t full = wide ? n[i] / kWideRows : 0, left = n[i] - full * kWideRows;
-    t += (int)(full + (wide && left > kWideFrom ? 1 : (left + tile_rows - 1) / tile_rows));
+    const int64_t full = wide_tiles(n[i]), left = max(n[i] - full * kWideRows, (int64_t)0);
+    t += (full << 32) + (left + tile_rows - 1) / tile_rows;
   }
-  int ti = t;
+  int64_t ti = t;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(ti, d, 64);
+    const int64_t o = __shfl_up(ti, d, 64);
     if (lane >= d) ti += o;
   }
   if (lane == 63) wtiles[wave] = ti;
   __syncthreads();
-  for (int w = 0; w < wave; ++w) ti += wtiles[w];
-  if (tid == 255) *count = ti;
+  int64_t all = 0;
+  for (int w = 0; w < 4; ++w) {
+    if (w < wave) ti += wtiles[w];
+    all += wtiles[w];
+  }
+  const int wides = (int)(all >> 32);
+  if (tid == 0) *count = wides + (int)all;
   ti -= t;
+  int at = (int)(ti >> 32), low = wides + (int)ti;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    for (int64_t r = 0; r < n[i];) {
-      const int64_t left = n[i] - r, rows = min(left, (int64_t)(wide && left > kWideFrom ? kWideRows : tile_rows));
-      tiles[ti++] = int4{4 * tid + i, (int)(row0[i] + r), (int)rows, 0};
-      r += rows;
-    }
+  for (int i = 0; i < 4; ++i) {
+    int64_t r = 0;
+    for (int64_t k = wide_tiles(n[i]); k; --k, r += kWideRows)
+      tiles[at++] = int4{4 * tid + i, (int)(row0[i] + r), (int)min(n[i] - r, (int64_t)kWideRows), 0};
+    for (; r < n[i]; r += tile_rows)
+      tiles[low++] = int4{4 * tid + i, (int)(row0[i] + r), (int)min(n[i] - r, (int64_t)tile_rows), 0};
+  }
 }
 
 // Place of 16-byte chunk c (0..7) of row r (0..15) of a 16 x 128-byte block in LDS, for
@@ -602,7 +575,7 @@ struct StreamTile {
     lds_barrier();
     arrived(cols);
     if constexpr (WHOLE) {
-      for_act<TY>(p, [&](auto ACT) __attribute__((always_inline)) {
+      for_act<TY == kFusedBf16>(p.act, [&](auto ACT) __attribute__((always_inline)) {
         store_rows<WHOLE, decltype(ACT)::value>(p, smem, scales, cols, row0, rows, tid);
       });
     } else {
@@ -1134,7 +1107,7 @@ struct WideTile {
       } else if (DENSE && p.residual) {
         store_tile<true, true, kAnyAct>(p, turn, acc, row0, rows, c0, el);
       } else {
-        for_act<TY>(p, [&](auto ACT) __attribute__((always_inline)) {
+        for_act<TY == kFusedBf16>(p.act, [&](auto ACT) __attribute__((always_inline)) {
           store_tile<true, false, decltype(ACT)::value>(p, turn, acc, row0, rows, c0, el);
         });
       }

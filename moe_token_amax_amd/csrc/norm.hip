@@ -307,6 +307,11 @@ static void launch(const NormArgs& p, hipStream_t stream) {
                      dim3(WPR >= 4 ? WPR * kWave : 256), 0, stream, p);
 }
 
+// Few rows: as many wavefronts a row as its chunks fill (64 x 4096 to INT8 4.2 us, with two
+// chunks a lane 5.2). Many: more chunks a lane, so that fewer wavefronts meet at a barrier
+// for each row (8192 x 7168 101 us, with a wavefront for every 64 chunks 127; 1024 x 7168
+// 22.4 both ways), and no more than a row has (1237 x 4097 to E4M3 16.3 with three a lane,
+// 17.6 with four).
 template <int FMT>
 static hipError_t launch_format(const NormArgs& p, hipStream_t stream) {
   const int64_t chunks = FMT == kNormFp8b ? ceil_div(p.K, 128) * 16 : ceil_div(p.K, 8);
@@ -319,6 +324,8 @@ static hipError_t launch_format(const NormArgs& p, hipStream_t stream) {
     if (chunks <= 8 * 64) launch<FMT, 2, 4>(p, stream);
     else if (chunks <= 12 * 64) launch<FMT, 3, 4>(p, stream);
     else launch<FMT, 4, 4>(p, stream);
+  } else if (chunks <= 8 * 64) {
+    launch<FMT, 1, 8>(p, stream);
   } else if (chunks <= 16 * 64) {
     launch<FMT, 1, 16>(p, stream);
   } else if (chunks <= 2 * 16 * 64) {
