@@ -378,6 +378,9 @@ __device__ __forceinline__ uint32_t turned(int r, int c) {
 // weights from global memory straight into operand registers, kAhead steps ahead: every
 // weight byte of the tile is read once and never passes through LDS. The rows, which
 // all eight share, go through LDS one step at a time (four buffers, one barrier a step).
+// Bound by what the L2 hands a CU, 32 bytes a clock: 64 x 128 take 24 KB a step, 0.32 us
+// (at 128 x 256 48 KB and 0.81 us, of which the MFMAs are 0.43). 1024 x 4096 x 4096 in
+// BF16: 64 x 128 49.8 us, 64 x 256 45.6, 128 x 256 59.7.
 // ---------------------------------------------------------------------------
 template <int TY, int MB, int NBW>
 struct StreamTile {
@@ -554,7 +557,7 @@ struct StreamTile {
 
   // The sums through LDS, from where the wavefronts store whole rows of the tile in a loop
   // of few branches (unrolled, with the choices at every output, the epilogue of a 128 x 256
-  // tile was 65 KB of code and took XX us).
+  // tile was 65 KB of code; 4096 x 4096 x 64 took 22.0 us in tiles of 64 x 128, now 17.6).
   template <bool WHOLE>
   __device__ __forceinline__ static void store_tile(const FusedGemm& p, uint8_t* smem, const Acc (&acc)[MB][NBW],
                                                     int64_t row0, int rows, int64_t c0, int tid) {
@@ -683,7 +686,9 @@ __global__ __launch_bounds__(256) void fused_join_kernel(FusedGemm p, int S, int
 // workgroup owns NBW 16-column blocks and 16 MB rows over the whole K; its eight
 // wavefronts take every eighth step, with U steps of weights and rows in flight each,
 // straight from global memory into operand registers and each set refilled as soon as
-// it is multiplied, and their sums meet in LDS in a fixed order.
+// it is multiplied, and their sums meet in LDS in a fixed order. Bound by the weights'
+// stream (BF16 1 x 4096 x 7168 9.4 us, 6.2 TB/s) and with tens of rows by what the L2 hands
+// a CU (256 x 256 x 7168: 4 KB a step, 8.2 us).
 // ---------------------------------------------------------------------------
 constexpr int kDecodeWaves = 8;
 
@@ -827,6 +832,9 @@ __global__ __launch_bounds__(kDecodeWaves * 64) void fused_decode_kernel(FusedGe
 // 4096 x 7168 where this form takes 382; one a product: 406). A workgroup walks over its
 // tiles without a gap: the last two steps of a tile load the first two of the next one,
 // which land while the tile is stored.
+// BF16 8192^3 850 us (1.29 PFLOP/s; the vendor library's bare product 803), INT8 8192 x
+// 4096 x 7168 203 (2.37 POPS; 238). A copy of the kernel that only multiplies takes 669 of
+// the 850 at the clock that the data's power leaves, one without its copies 746.
 // ---------------------------------------------------------------------------
 static __device__ __align__(16) uint8_t zeros16[16];
 
@@ -1146,7 +1154,10 @@ __global__ __launch_bounds__(512) void fused_wide_kernel(FusedGemm p) {
 constexpr int kSpreadTiles = 64;
 
 // NBW 2: tiles of 128 rows x 256 columns, and wide ones; NBW 1: 64 rows x 128 columns,
-// for products that would not fill the chip with those.
+// for products that would not fill the chip with those. 128 rows over 256 experts of 4096 x
+// 4096 524 us (the weights at 6.2 TB/s); 16384 rows over 64 such experts 726 (0.76
+// PFLOP/s: experts' last rows in lower tiles, 3.2 GB from HBM where 2.2 would do). Walking on
+// from wide tile to wide tile, as the dense kernel does, gained nothing (749, 754).
 template <int TY, int NBW>
 __global__ __launch_bounds__(512) void fused_grouped_kernel(FusedGemm p, int NT) {
   using T = WideTile<TY, false>;
@@ -1203,46 +1214,49 @@ bool fused_rows_ok(const FusedGemm& p) {
 enum FusedKernel { kDecode16, kDecode16x32, kDecode32, kDecode64, kTile32, kTile64, kTile64x256, kTile128, kTile256 };
 
 // What a product takes with each kernel, in us, by a model fitted to 1500 products of
-// either type, M 1 .. 8192, N 32 .. 16384, K 64 .. 16384 (the kernel it picks is 2 %
-// slower in the mean than the best of them, in one product of a hundred 1.5 times):
-//   launch + rounds * round + steps * max(first, rounds * step) + (split) join + parts
+// either type, M 1 .. 8192, N 32 .. 16384, K 64 .. 16384 (the kernel it picks is 1.7 %
+// slower in the mean than the best of them, in one product of a hundred 1.3 times):
+//   launch + rounds * round + steps * max(first, filling * step) + (split) join + parts
 // rounds: workgroups over twice the CUs (wide: whole turns of one workgroup a CU); steps:
 // 128-byte steps of K a workgroup goes through; first: such a step where the chip is not
-// full. INT8 and BF16 take the same time for the same bytes of K. A split of K is taken
+// full; filling: rounds, for the decode kernels three quarters of the way to whole turns of
+// one workgroup a CU. INT8 and BF16 take the same time for the same bytes of K. A split of K is taken
 // into as many parts as give the chip half a workgroup, one or two a CU.
 struct FusedCost {
   int rows, cols;
   double launch, round, first, step, join, part;  // part: per MB of partial sums
 };
 constexpr FusedCost kCost[] = {
-    {16, 16, 2.56, 0.579, 0.0441, 0.163, 0, 0},       {16, 32, 2.79, 0.82, 0.0676, 0.264, 0, 0},
-    {32, 32, 3.13, 1.36, 0.0841, 0.34, 0, 0},         {64, 32, 3.6, 3.75, 0.12, 0.439, 0, 0},
+    {16, 16, 2.5, 0.706, 0.0407, 0.124, 0, 0},        {16, 32, 2.7, 1.05, 0.061, 0.196, 0, 0},
+    {32, 32, 3.01, 1.73, 0.0356, 0.242, 0, 0},        {64, 32, 3.51, 4.25, 0.122, 0.326, 0, 0},
     {32, 128, 3.25, 1.9, 0.257, 0.589, 3.07, 0.437},  {64, 128, 4.04, 2.55, 0.322, 0.809, 2.9, 0.255},
     {64, 256, 5.09, 6.77, 0.517, 1.38, 0, 0},         {128, 256, 7.37, 11.9, 0.808, 2.19, 2.18, 0.0812},
     {256, 256, 3.36, 10.9, 1.23, 1.3, 0, 0},
 };
 
-static double tiles_time(const FusedCost& c, int64_t tiles, int64_t steps) {
-  const double rounds = tiles / 512.0;
-  return c.launch + rounds * c.round + (double)steps * std::max(c.first, rounds * c.step);
+static double tiles_time(int kernel, int64_t tiles, int64_t steps) {
+  const FusedCost& c = kCost[kernel];
+  const double turns = (double)ceil_div(tiles, 256), rounds = kernel == kTile256 ? turns : tiles / 512.0;
+  const double filling = kernel <= kDecode64 ? 0.25 * rounds + 0.375 * turns : rounds;
+  return c.launch + rounds * c.round + (double)steps * std::max(c.first, filling * c.step);
 }
 
-static FusedPlan cheapest(int64_t M, int64_t NB, int64_t KP, bool swiglu, double& least) {
+static FusedPlan cheapest(int64_t M, int64_t NB, int64_t KP, bool swiglu) {
   const int64_t KB = ceil_div(KP, 2);
   FusedPlan best{kTile64, 1, false};
-  least = 1e300;
+  double least = 1e300;
   for (int k = kDecode16; k <= kTile256; ++k) {
     const FusedCost& c = kCost[k];
     if (k == kDecode16 && swiglu) continue;           // pairs of blocks
-    if (k <= kTile32 && M > (int64_t)1 << 20) continue;  // their grids' limits
-    if (c.rows * 128 < M || (k > kTile64 && c.rows >= 4 * M)) continue;  // never the best: no need to look
+    // never the best, and the low tiles' grids have limits
+    if ((k <= kTile32 && M > c.rows * 128) || (k > kTile64 && c.rows >= 4 * M)) continue;
     if (k == kTile256 && KP <= 2) continue;           // its pipeline is two steps deep
     const int64_t tiles = ceil_div(M, c.rows) * ceil_div(NB * 16, c.cols);
     auto consider = [&](int64_t S) {
       const int64_t per = ceil_div(KB, S);
       S = ceil_div(KB, per);  // no empty part
       const int64_t n = tiles * S;
-      double t = tiles_time(c, k == kTile256 ? 512 * ceil_div(n, 256) : n, per);
+      double t = tiles_time(k, n, per);
       if (S > 1) t += c.join + c.part * (double)(n * c.rows * c.cols * 4) * 1e-6;
       if (t < least) {
         least = t;
@@ -1259,13 +1273,9 @@ static FusedPlan cheapest(int64_t M, int64_t NB, int64_t KP, bool swiglu, double
   return best;
 }
 
-// Rows that are not 4-byte aligned load at a quarter to a half less speed: copied to
-// whole aligned steps first where a quarter of the product's time is more than the copy's
-// (BF16 300 x 1000 x 5761: 24.1 us as they are, YY with the copy; 20 x 129 x 5761: 9.4).
-static bool copy_pays(int64_t M, int64_t kbytes, double time) {
-  return 0.25 * time > 2.5 + 0.5e-6 * (double)(M * kbytes);
-}
-
+// Copied first: rows of less than a load, and rows that wide tiles cannot copy by DMA. (The
+// other kernels load any address: BF16 300 x 1000 x 5761 16.9 us, with a copy 17.0; K 5760
+// 15.7.)
 static int64_t copy_bytes(int64_t M, int64_t kbytes) { return round_up(round_up(kbytes, kStepBytes) * M, 256); }
 
 // sums of the parts of K
@@ -1276,10 +1286,8 @@ static int64_t part_bytes(const FusedPlan& plan, int64_t M, int64_t NB) {
 }
 
 FusedPlan fused_plan(const FusedGemm& p) {
-  double time;
-  FusedPlan plan = cheapest(p.M, p.NB, p.KP, p.act == W8A8_ACT_SWIGLU, time);
-  const bool apart = ((uintptr_t)p.a | p.lda | p.kbytes) & 3;
-  plan.copy = p.kbytes < 16 || (plan.kernel == kTile256 && !fused_rows_ok(p)) || (apart && copy_pays(p.M, p.kbytes, time));
+  FusedPlan plan = cheapest(p.M, p.NB, p.KP, p.act == W8A8_ACT_SWIGLU);
+  plan.copy = p.kbytes < 16 || (plan.kernel == kTile256 && !fused_rows_ok(p));
   return plan;
 }
 
@@ -1293,9 +1301,8 @@ int64_t fused_most_bytes(int type, int64_t M, int64_t N, int64_t K) {
   const int64_t KP = type == kFusedInt8 ? ceil_div(K, 64) : 2 * ceil_div(K, 64);
   int64_t most = 0;
   for (const bool swiglu : {false, true}) {
-    double time;
-    const FusedPlan plan = cheapest(M, NB, KP, swiglu, time);
-    const bool copy = kbytes < 16 || plan.kernel == kTile256 || copy_pays(M, kbytes, time);
+    const FusedPlan plan = cheapest(M, NB, KP, swiglu);
+    const bool copy = kbytes < 16 || plan.kernel == kTile256;
     most = std::max(most, (copy ? copy_bytes(M, kbytes) : 0) + part_bytes(plan, M, NB));
     if (plan.kernel != kDecode16) break;  // the same for SwiGLU
   }
@@ -1356,8 +1363,9 @@ static hipError_t launch_dense(const FusedGemm& p, const FusedPlan& plan, void* 
 static int grouped_rows(int64_t R, int64_t E, int64_t NB, int64_t KP) {
   double t[2];
   for (int i = 0; i < 2; ++i) {
-    const FusedCost& c = kCost[i ? kTile128 : kTile64];
-    t[i] = tiles_time(c, max_tiles(R, E, c.rows) * ceil_div(NB * 16, c.cols), ceil_div(KP, 2));
+    const int k = i ? kTile128 : kTile64;
+    const FusedCost& c = kCost[k];
+    t[i] = tiles_time(k, max_tiles(R, E, c.rows) * ceil_div(NB * 16, c.cols), ceil_div(KP, 2));
   }
   return kCost[t[1] < t[0] ? kTile128 : kTile64].rows;
 }

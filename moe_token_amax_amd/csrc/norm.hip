@@ -160,7 +160,8 @@ __device__ __forceinline__ void write_chunk(const NormArgs& p, int64_t row, int 
 
 // WPR wavefronts a row, CPL chunks of 8 values a lane: the row stays in registers
 // between the sum, the maximum and the codes, and is read once. A workgroup walks over
-// its rows and keeps the weight of its columns.
+// its rows and keeps the weight of its columns. HBM-bound: 8192 x 7168 with residual to
+// INT8 97 us (411 MB, 4.25 TB/s; a copy 5.3), to E4M3 88; one row 4.7 (two sums, a launch).
 template <int FMT, int CPL, int WPR>
 __global__ __launch_bounds__(WPR >= 4 ? WPR * kWave : 256) void rms_norm_kernel(NormArgs p) {
   constexpr int kThreadsRow = WPR * kWave, kRows = WPR >= 4 ? 1 : 4 / WPR;

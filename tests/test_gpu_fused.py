@@ -467,9 +467,9 @@ def test_two_streams_at_once(w):
 
 # ------------------------------------------------------------------ every kernel and split
 PLANS = [  # M, N, K of BF16 (INT8: twice the K)
-    (23, 22, 62), (107, 4, 4386), (38, 3440, 206), (52, 1984, 1172), (103, 2662, 1546), (75, 22, 8540), (180, 302, 9000),
+    (23, 22, 62), (107, 4, 4386), (38, 3440, 206), (52, 1984, 1172), (64, 4096, 3584), (103, 2662, 1546), (75, 22, 8540), (180, 302, 9000),
     (654, 942, 2031), (227, 20, 9528), (340, 1502, 3400), (700, 4134, 1000), (389, 8070, 1104), (4325, 134, 5911),
-    (5629, 1438, 455), (2448, 5190, 67), (2500, 4202, 1111)]
+    (5629, 1438, 455), (2448, 5190, 67), (2500, 4202, 1111), (40001, 66, 130), (70000, 18, 30)]
 
 
 def _sample(M):
@@ -509,8 +509,8 @@ def test_every_kernel(w, M, N, K, kind, act):
 
 @pytest.mark.parametrize("kind", ["bf16", "int8"])
 @pytest.mark.parametrize("M,N,K,lo", [(700, 4134, 1001, 1), (300, 1000, 5761, 3), (2500, 4202, 1111, 1), (340, 1502, 3403, 5)])
-def test_rows_that_are_copied(w, M, N, K, lo, kind):
-    """Rows at odd addresses, NaN (INT8: codes) around them."""
+def test_rows_at_odd_addresses(w, M, N, K, lo, kind):
+    """As they are, and copied (wide tiles); NaN (INT8: codes) around them."""
     rng = np.random.default_rng(K)
     pick = _sample(M)
     if kind == "bf16":
@@ -562,7 +562,7 @@ def test_split_sums_captured_and_replayed(w):
     """A product whose K is split, in a graph that is replayed with new rows and its own
     workspace, with eager work on the same stream between."""
     rng = np.random.default_rng(9)
-    M, N, K = 180, 302, 9000
+    M, N, K = 340, 1502, 3400
     wt = _bf16(rng, N, K, scale=1 / math.sqrt(K))
     wp = w.bf16_prepack_weight(bf16_dev(wt))
     assert w.bf16_linear_workspace_bytes(M, N, K) >= 2 * M * N * 4
