@@ -467,8 +467,8 @@ def test_two_streams_at_once(w):
 
 # ------------------------------------------------------------------ every kernel and split
 PLANS = [  # M, N, K of BF16 (INT8: twice the K)
-    (23, 22, 62), (107, 4, 4386), (38, 3440, 206), (52, 1984, 1172), (64, 4096, 3584), (103, 2662, 1546), (75, 22, 8540), (180, 302, 9000),
-    (654, 942, 2031), (227, 20, 9528), (340, 1502, 3400), (700, 4134, 1000), (389, 8070, 1104), (4325, 134, 5911),
+    (23, 22, 62), (107, 4, 4386), (38, 3440, 206), (52, 1984, 1172), (64, 4096, 3584), (103, 2662, 1546), (75, 22, 8540),
+    (180, 302, 9000), (654, 942, 2031), (227, 20, 9528), (340, 1502, 3400), (700, 4134, 1000), (389, 8070, 1104), (4325, 134, 5911),
     (5629, 1438, 455), (2448, 5190, 67), (2500, 4202, 1111), (40001, 66, 130), (70000, 18, 30)]
 
 
@@ -488,6 +488,9 @@ def test_every_kernel(w, M, N, K, kind, act):
     b, r = _bf16(rng, N, scale=0.3), _bf16(rng, M, width)
     room = torch.full((M + 2, width), 7.0, dtype=torch.bfloat16, device=DEV)
     kw = dict(bias=bf16_dev(b), act=_act_id(w, act), residual=bf16_dev(r) if with_res else None)
+    if act in ("swiglu", "silu"):                         # in place
+        room[1:M + 1] = kw["residual"]
+        kw["residual"] = room[1:M + 1]
     pick = _sample(M)
     if kind == "bf16":
         x, wt = _acts(rng, M, K), _bf16(rng, N, K, scale=1 / math.sqrt(K))
@@ -581,3 +584,56 @@ def test_split_sums_captured_and_replayed(w):
         eager = w.bf16_linear(x, wp, N)
         sync()
         assert torch.equal(y.view(torch.int16), eager.view(torch.int16)), i
+
+
+@pytest.mark.parametrize("M,N,K,act", [(2500, 4202, 1112, "gelu"), (1037, 530, 1111, "none")])
+def test_offsets_past_32_bits(w, M, N, K, act):
+    """Rows 4 MB apart: x, residual and y are columns of one buffer of 4 to 10 GB."""
+    show(f"{M} rows 4 MB apart")
+    rng = np.random.default_rng(M)
+    big = torch.empty((M, 1 << 21), dtype=torch.bfloat16, device=DEV)
+    x, wt, r = _acts(rng, M, K), _bf16(rng, N, K, scale=1 / math.sqrt(K)), _bf16(rng, M, N)
+    xs, rs, ys = big[:, 8:8 + K], big[:, 20001:20001 + N], big[:, 40000:40000 + N]
+    xs.copy_(bf16_dev(x))
+    rs.copy_(bf16_dev(r))
+    wp = w.bf16_prepack_weight(bf16_dev(wt))
+    w.bf16_linear(xs, wp, N, act=_act_id(w, act), residual=rs, y=ys)
+    rows = rng.integers(0, M, M + 3).astype(np.int32)
+    counts = [M // 2, 0, M - M // 2]
+    g = w.bf16_grouped_gemm(xs, dev(np.array(counts, np.int64)), torch.cat([wp, wp, wp]), N, act=_act_id(w, act),
+                            row_index=dev(rows))
+    n, hn = w.rms_norm(xs, None, 1e-6), big[:, 60000:60000 + K]
+    w.rms_norm(xs, None, 1e-6, y=hn)
+    sync()
+    pick = _sample(M)
+    at = torch.from_numpy(pick).to(DEV)
+    _hold(ys[at], *_epilogue(*_bf16_value(x[pick], wt), act, r[pick]))
+    _hold(g[at], *_epilogue(*_bf16_value(x[rows[pick]], wt), act))
+    same = w.rms_norm(xs.contiguous(), None, 1e-6)
+    assert torch.equal(n.view(torch.int16), same.view(torch.int16)) and torch.equal(hn.contiguous().view(torch.int16),
+                                                                                 same.view(torch.int16))
+
+
+def test_eager_calls_beside_a_replayed_graph_on_another_stream(w):
+    """Two products at once, each with its own workspace."""
+    rng = np.random.default_rng(4)
+    M, N, K = 340, 1502, 3400
+    wp = w.bf16_prepack_weight(bf16_dev(_bf16(rng, N, K, scale=1 / math.sqrt(K))))
+    xs = [bf16_dev(_acts(rng, M, K)) for _ in range(2)]
+    want = [w.bf16_linear(x, wp, N) for x in xs]
+    y = torch.empty_like(want[0])
+    room = torch.empty((w.bf16_linear_workspace_bytes(M, N, K),), dtype=torch.uint8, device=DEV)
+    sync()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        w.bf16_linear(xs[0], wp, N, y=y, workspace=room)
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        y.zero_()
+        sync()
+        g.replay()
+        with torch.cuda.stream(side):
+            z = w.bf16_linear(xs[1], wp, N)
+        sync()
+        assert torch.equal(y.view(torch.int16), want[0].view(torch.int16))
+        assert torch.equal(z.view(torch.int16), want[1].view(torch.int16))
