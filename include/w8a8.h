@@ -73,6 +73,15 @@ typedef enum {
   W8A8_ACT_GELU_TANH = 5  /* v / 2 (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) */
 } w8a8_act;
 
+/* How a product runs on given rows, and the workspace that it needs. */
+typedef struct {
+  int32_t tile_rows, tile_cols;  /* outputs of a workgroup */
+  int32_t k_parts;               /* parts of K, summed apart and joined */
+  int32_t copied;                /* 1: the rows are copied to 16-byte alignment first */
+  int64_t tiles;                 /* tiles of the output */
+  int64_t workspace_bytes;
+} w8a8_plan;
+
 /* Largest K (reduction length) accepted: K * 127 * 127 stays below 2^31. */
 #define W8A8_MAX_K 133144
 
@@ -753,7 +762,10 @@ int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* resid
  *   bias      device, BF16 [N] or NULL
  *   workspace the call's workspace_bytes, 256-byte aligned, rewritten: sums of a K
  *             that is split over workgroups, rows copied to 16-byte alignment (0 bytes:
- *             NULL is fine)
+ *             NULL is fine). w8a8_linear_fused_plan and w8a8_bf16_linear_plan give the
+ *             bytes of a call on these rows (their address and stride; nothing is read):
+ *             none for aligned rows of a product whose K is whole, where workspace_bytes
+ *             counts their copy
  *
  * w8a8_linear_fused [DSV4 §二 npu_quant_matmul]: INT8 codes q [M, K], row stride ldq,
  *   x_scale float [M] (from w8a8_dynamic_quant_ld or w8a8_rms_norm_quant), a weight
@@ -782,6 +794,7 @@ int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* resid
  * calls that may overlap need two.
  */
 int64_t w8a8_linear_fused_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int w8a8_linear_fused_plan(const int8_t* q, int64_t ldq, int64_t M, int64_t N, int64_t K, w8a8_plan* plan);
 int w8a8_linear_fused(const int8_t* q, int64_t ldq, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
                       const float* w_scale, int64_t N, const uint16_t* bias, int act, const uint16_t* residual,
                       int64_t ldr, uint16_t* y, int64_t ldy, void* workspace, int64_t ws_bytes, void* stream);
@@ -792,6 +805,7 @@ int w8a8_fp8b_linear_fused(const void* x, int64_t ldx, const float* x_scale, int
 int64_t w8a8_bf16_packed_bytes(int64_t E, int64_t N, int64_t K);
 int w8a8_bf16_prepack_weight(const uint16_t* w, int64_t E, int64_t N, int64_t K, int act, void* w_packed, void* stream);
 int64_t w8a8_bf16_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+int w8a8_bf16_linear_plan(const uint16_t* x, int64_t ldx, int64_t M, int64_t N, int64_t K, int act, w8a8_plan* plan);
 int w8a8_bf16_linear(const uint16_t* x, int64_t ldx, int64_t M, int64_t K, const void* w_packed, int64_t N,
                      const uint16_t* bias, int act, const uint16_t* residual, int64_t ldr, void* y, int64_t ldy, int out,
                      void* workspace, int64_t ws_bytes, void* stream);

@@ -99,12 +99,15 @@ __all__ = [
     "rms_norm_quant",
     "fp8b_rms_norm_quant",
     "mx_rms_norm_quant",
+    "Plan",
     "linear_fused_workspace_bytes",
+    "linear_fused_plan",
     "linear_fused",
     "fp8b_linear_fused",
     "bf16_packed_bytes",
     "bf16_prepack_weight",
     "bf16_linear_workspace_bytes",
+    "bf16_linear_plan",
     "bf16_linear",
     "bf16_grouped_workspace_bytes",
     "bf16_grouped_gemm",
@@ -243,6 +246,7 @@ def _load():
                                                   ctypes.c_double, _c_i64, _c_i64, _c_p, _c_i64, ctypes.c_int,
                                                   _c_p, _c_p, _c_p]),
         "w8a8_linear_fused_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64]),
+        "w8a8_linear_fused_plan": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p]),
         "w8a8_linear_fused": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p,
                                              ctypes.c_int, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p]),
         "w8a8_fp8b_linear_fused": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p,
@@ -251,6 +255,7 @@ def _load():
         "w8a8_bf16_packed_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64]),
         "w8a8_bf16_prepack_weight": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, ctypes.c_int, _c_p, _c_p]),
         "w8a8_bf16_linear_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64]),
+        "w8a8_bf16_linear_plan": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, ctypes.c_int, _c_p]),
         "w8a8_bf16_linear": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, ctypes.c_int, _c_p,
                                             _c_i64, _c_p, _c_i64, ctypes.c_int, _c_p, _c_i64, _c_p]),
         "w8a8_bf16_grouped_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_i64]),
@@ -1561,8 +1566,37 @@ def mx_rms_norm_quant(x: torch.Tensor, weight: torch.Tensor | None, eps: float =
 ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 2, 3, 4, 5
 
 
+class Plan(ctypes.Structure):
+    """How a product runs on given rows, and the workspace that it needs (w8a8_plan)."""
+
+    _fields_ = [("tile_rows", ctypes.c_int32), ("tile_cols", ctypes.c_int32), ("k_parts", ctypes.c_int32),
+                ("copied", ctypes.c_int32), ("tiles", _c_i64), ("workspace_bytes", _c_i64)]
+
+
+def _plan(query, *args) -> Plan:
+    plan = Plan()
+    _check(query(*args, ctypes.byref(plan)))
+    return plan
+
+
+def _planned_room(ws: torch.Tensor | None, device, query, *args):
+    """_room of what the plan of this call needs; (None, None, 0) if that is nothing."""
+    if ws is None:
+        need = _plan(query, *args).workspace_bytes
+        if not need:
+            return None, None, 0
+        ws = torch.empty((need,), dtype=torch.uint8, device=device)
+    return ws, _at(ws, torch.uint8, "workspace", 1), ws.numel()
+
+
 def linear_fused_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(lib.w8a8_linear_fused_workspace_bytes(M, N, K))
+
+
+def linear_fused_plan(q: torch.Tensor, N: int) -> Plan:
+    """How linear_fused runs on these rows, and the workspace bytes that it needs."""
+    at, ldq = _rows_at(q, torch.int8, "q")
+    return _plan(lib.w8a8_linear_fused_plan, at, ldq, q.shape[0], N, q.shape[1])
 
 
 def linear_fused(q: torch.Tensor, x_scale: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor, N: int,
@@ -1587,7 +1621,7 @@ def linear_fused(q: torch.Tensor, x_scale: torch.Tensor, w_packed: torch.Tensor,
         raise ValueError("y shape mismatch")
     yp, ldy = _rows_at(y, torch.bfloat16, "y")
     rp, ldr = _residual(residual, (M, N))
-    room, ws, ws_n = _room(workspace, q.device, linear_fused_workspace_bytes, M, N, K)
+    room, ws, ws_n = _planned_room(workspace, q.device, lib.w8a8_linear_fused_plan, at, ldq, M, N, K)
     _check(lib.w8a8_linear_fused(at, ldq, _at(x_scale, torch.float32, "x_scale", 1), M, K, wp,
                                  _at(w_scale, torch.float32, "w_scale", 1), N, _at(bias, torch.bfloat16, "bias", 1), act,
                                  rp, ldr, yp, ldy, ws, ws_n, _stream()))
@@ -1627,6 +1661,12 @@ def bf16_linear_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(lib.w8a8_bf16_linear_workspace_bytes(M, N, K))
 
 
+def bf16_linear_plan(x: torch.Tensor, N: int, act: int = ACT_NONE) -> Plan:
+    """How bf16_linear runs on these rows, and the workspace bytes that it needs."""
+    at, ldx = _rows_at(x, torch.bfloat16, "x")
+    return _plan(lib.w8a8_bf16_linear_plan, at, ldx, x.shape[0], N, x.shape[1], act)
+
+
 def bf16_linear(x: torch.Tensor, w_packed: torch.Tensor, N: int, bias: torch.Tensor | None = None,
                 act: int = ACT_NONE, residual: torch.Tensor | None = None, out: int = OUT_BF16,
                 y: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
@@ -1650,7 +1690,7 @@ def bf16_linear(x: torch.Tensor, w_packed: torch.Tensor, N: int, bias: torch.Ten
         raise ValueError("y shape mismatch")
     yp, ldy = _rows_at(y, torch.float32 if out == OUT_F32 else torch.bfloat16, "y")
     rp, ldr = _residual(residual, (M, width))
-    room, ws, ws_n = _room(workspace, x.device, bf16_linear_workspace_bytes, M, N, K)
+    room, ws, ws_n = _planned_room(workspace, x.device, lib.w8a8_bf16_linear_plan, at, ldx, M, N, K, act)
     _check(lib.w8a8_bf16_linear(at, ldx, M, K, wp, N, _at(bias, torch.bfloat16, "bias", 1), act, rp, ldr, yp, ldy, out,
                                 ws, ws_n, _stream()))
     return y

@@ -1547,11 +1547,32 @@ int run_fused(const char* who, const w8a8::FusedGemm& p, void* workspace, int64_
   return launched(w8a8::launch_fused_gemm(p, plan, workspace, (hipStream_t)stream), who);
 }
 
+int plan_fused(const w8a8::FusedGemm& p, w8a8_plan* plan) {
+  *plan = w8a8_plan{};
+  if (p.M) {
+    const w8a8::FusedPlan f = w8a8::fused_plan(p);
+    w8a8::fused_tile(f, &plan->tile_rows, &plan->tile_cols);
+    plan->tiles = w8a8::ceil_div(p.M, plan->tile_rows) * w8a8::ceil_div(p.NB * 16, plan->tile_cols);
+    plan->k_parts = f.S;
+    plan->copied = f.copy;
+    plan->workspace_bytes = w8a8::fused_room_bytes(p, f);
+  }
+  return ok();
+}
+
 }  // namespace
 
 int64_t w8a8_linear_fused_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
   return w8a8::fused_most_bytes(w8a8::kFusedInt8, M, N, K);
+}
+
+int w8a8_linear_fused_plan(const int8_t* q, int64_t ldq, int64_t M, int64_t N, int64_t K, w8a8_plan* plan) {
+  int st = check_fp8b("linear_fused_plan", M, N, K);
+  if (st) return st;
+  if (ldq < K) return fail(W8A8_ERR_SHAPE, "linear_fused_plan: ldq = %lld is below the row width", (long long)ldq);
+  if (!plan) return fail(W8A8_ERR_NULL, "linear_fused_plan: null pointer");
+  return plan_fused(fused_int8(q, ldq, nullptr, M, K, nullptr, nullptr, N), plan);
 }
 
 int w8a8_linear_fused(const int8_t* q, int64_t ldq, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
@@ -1602,6 +1623,16 @@ int w8a8_bf16_prepack_weight(const uint16_t* w, int64_t E, int64_t N, int64_t K,
 int64_t w8a8_bf16_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   if (M <= 0 || N <= 0 || K <= 0) return 0;
   return w8a8::fused_most_bytes(w8a8::kFusedBf16, M, N, K);
+}
+
+int w8a8_bf16_linear_plan(const uint16_t* x, int64_t ldx, int64_t M, int64_t N, int64_t K, int act, w8a8_plan* plan) {
+  int st = check_fp8b("bf16_linear_plan", M, N, K);
+  if (st) return st;
+  st = check_act("bf16_linear_plan", act, true);
+  if (st) return st;
+  if (ldx < K) return fail(W8A8_ERR_SHAPE, "bf16_linear_plan: ldx = %lld is below the row width", (long long)ldx);
+  if (!plan) return fail(W8A8_ERR_NULL, "bf16_linear_plan: null pointer");
+  return plan_fused(fused_bf16(x, ldx, M, M, K, nullptr, N, act), plan);
 }
 
 int w8a8_bf16_linear(const uint16_t* x, int64_t ldx, int64_t M, int64_t K, const void* w_packed, int64_t N,

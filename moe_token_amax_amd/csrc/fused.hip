@@ -1291,6 +1291,11 @@ FusedPlan fused_plan(const FusedGemm& p) {
   return plan;
 }
 
+void fused_tile(const FusedPlan& plan, int32_t* rows, int32_t* cols) {
+  *rows = kCost[plan.kernel].rows;
+  *cols = kCost[plan.kernel].cols;
+}
+
 int64_t fused_room_bytes(const FusedGemm& p, const FusedPlan& plan) {
   return (plan.copy ? copy_bytes(p.M, p.kbytes) : 0) + part_bytes(plan, p.M, p.NB);
 }

@@ -48,6 +48,8 @@ struct FusedPlan {
   bool copy;   // rows copied to whole, aligned, zero-padded steps first
 };
 FusedPlan fused_plan(const FusedGemm& p);
+// rows and columns of its tiles
+void fused_tile(const FusedPlan& plan, int32_t* rows, int32_t* cols);
 // Workspace: the copied rows, then the sums of the parts; and the most that a product of
 // these sizes can need, whatever its rows' alignment.
 int64_t fused_room_bytes(const FusedGemm& p, const FusedPlan& plan);

@@ -1,0 +1,83 @@
+"""Plans and workspace sizes of the fused linears and the BF16 expert products (CPU
+only): queries, and calls that fail their checks before anything is launched."""
+
+from __future__ import annotations
+
+import ctypes
+import random
+
+import pytest
+
+OK, NULL, SHAPE, UNSUPPORTED, WORKSPACE = 0, 1, 2, 4, 5
+P = 256                       # an address that is never read
+
+
+@pytest.fixture(scope="module")
+def w():
+    import moe_token_amax_amd as w
+    return w
+
+
+def _plan(w, kind, M, N, K, at=P, ld=None, act=0):
+    p = w.Plan()
+    ld = K if ld is None else ld
+    if kind == "int8":
+        st = w.lib.w8a8_linear_fused_plan(at, ld, M, N, K, ctypes.byref(p))
+    else:
+        st = w.lib.w8a8_bf16_linear_plan(at, ld, M, N, K, act, ctypes.byref(p))
+    assert st == OK, w.lib.w8a8_last_error()
+    return p
+
+
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+def test_aligned_rows_need_no_room_for_a_copy(w, kind):
+    """Prompts on wide tiles: their rows are copied, and room for that is asked for, only
+    where an address, a stride or a width keeps the tiles from loading them."""
+    p = _plan(w, kind, 8192, 4096, 7168)
+    assert (p.tile_rows, p.tile_cols, p.k_parts, p.copied, p.tiles) == (256, 256, 1, 0, 512)
+    assert p.workspace_bytes == 0
+    bytes_row = 7168 * (1 if kind == "int8" else 2)
+    for kw in (dict(at=P + 2), dict(ld=7170)):
+        p = _plan(w, kind, 8192, 4096, 7168, **kw)
+        assert p.copied == 1 and p.workspace_bytes == 8192 * bytes_row
+    p = _plan(w, kind, 8192, 4096, 7166)
+    assert p.copied == 1 and p.workspace_bytes == 8192 * bytes_row    # to whole steps of 128 bytes
+
+
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+def test_a_call_asks_for_what_its_plan_says(w, kind):
+    """One byte less than the plan's is refused, and the size query covers every plan."""
+    rng = random.Random(3)
+    size = w.linear_fused_workspace_bytes if kind == "int8" else w.bf16_linear_workspace_bytes
+    asked = 0
+    for _ in range(3000):
+        M, N, K = (int(2 ** rng.uniform(0, b)) for b in (14, 14, 14))
+        act = rng.choice([0, 1]) if kind == "bf16" and N % 2 == 0 else 0
+        p = _plan(w, kind, M, N, K, P + rng.choice([0, 2]), K + rng.choice([0, 1, 8]), act)
+        assert 0 <= p.workspace_bytes <= size(M, N, K)
+        assert (p.k_parts > 1 or p.copied == 1) == (p.workspace_bytes > 0)
+        p = _plan(w, kind, M, N, K, act=act)
+        if not p.workspace_bytes:
+            continue
+        asked += 1
+        a, n = ctypes.c_void_p(P), p.workspace_bytes - 1
+        if kind == "int8":
+            st = w.lib.w8a8_linear_fused(a, K, a, M, K, a, a, N, None, 0, None, 0, a, N, a, n, None)
+        else:
+            st = w.lib.w8a8_bf16_linear(a, K, M, K, a, N, None, act, None, 0, a, N, 0, a, n, None)
+        assert st == WORKSPACE and b"%d workspace bytes" % p.workspace_bytes in w.lib.w8a8_last_error()
+    assert asked > 200
+
+
+def test_plan_refusals(w):
+    L, p = w.lib, w.Plan()
+    at = ctypes.byref(p)
+    assert L.w8a8_linear_fused_plan(P, 64, -1, 8, 64, at) == SHAPE
+    assert L.w8a8_linear_fused_plan(P, 63, 4, 8, 64, at) == SHAPE
+    assert L.w8a8_linear_fused_plan(P, 64, 4, 8, 64, None) == NULL
+    assert L.w8a8_bf16_linear_plan(P, 64, 4, 0, 64, 0, at) == SHAPE
+    assert L.w8a8_bf16_linear_plan(P, 63, 4, 8, 64, 0, at) == SHAPE
+    assert L.w8a8_bf16_linear_plan(P, 64, 4, 8, 64, 6, at) == UNSUPPORTED
+    assert L.w8a8_bf16_linear_plan(P, 64, 4, 8, 64, 0, None) == NULL
+    for st in (L.w8a8_linear_fused_plan(None, 64, 0, 8, 64, at), L.w8a8_bf16_linear_plan(None, 64, 0, 8, 64, 0, at)):
+        assert st == OK and p.tiles == p.workspace_bytes == 0
