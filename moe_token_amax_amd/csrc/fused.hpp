@@ -51,7 +51,7 @@ FusedPlan fused_plan(const FusedGemm& p);
 // rows and columns of its tiles
 void fused_tile(const FusedPlan& plan, int32_t* rows, int32_t* cols);
 // Workspace: the copied rows, then the sums of the parts; and the most that a product of
-// these sizes can need, whatever its rows' alignment.
+// these columns and at most M rows can need, whatever its rows' alignment.
 int64_t fused_room_bytes(const FusedGemm& p, const FusedPlan& plan);
 int64_t fused_most_bytes(int type, int64_t M, int64_t N, int64_t K);
 // M, N >= 1

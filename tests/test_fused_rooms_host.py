@@ -81,3 +81,20 @@ def test_plan_refusals(w):
     assert L.w8a8_bf16_linear_plan(P, 64, 4, 8, 64, 0, None) == NULL
     for st in (L.w8a8_linear_fused_plan(None, 64, 0, 8, 64, at), L.w8a8_bf16_linear_plan(None, 64, 0, 8, 64, 0, at)):
         assert st == OK and p.tiles == p.workspace_bytes == 0
+
+
+# rows at the borders of the tiles, one by one to 600, then up to prompts
+ROWS = sorted(set(range(600)) | {16 * i + d for i in range(38, 300, 3) for d in (-1, 0, 1)} |
+              {8191, 8192, 8193, 32767, 32769, 65536, 1 << 20})
+
+
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+@pytest.mark.parametrize("N,K", [(4096, 7168), (4122, 6000), (1776, 7549), (16, 16384), (100, 130), (7168, 2048), (20, 15),
+                                 (30000, 100)])
+def test_linear_workspace_never_falls_as_rows_grow(w, kind, N, K):
+    """A room made for the largest batch serves every smaller one."""
+    size = w.linear_fused_workspace_bytes if kind == "int8" else w.bf16_linear_workspace_bytes
+    sizes = [size(M, N, K) for M in ROWS]
+    assert sizes[0] == 0
+    falls = [(ROWS[i], sizes[i], ROWS[i + 1], sizes[i + 1]) for i in range(len(ROWS) - 1) if sizes[i] > sizes[i + 1]]
+    assert not falls, falls[:3]
