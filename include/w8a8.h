@@ -789,7 +789,7 @@ int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* resid
  *   row row_index[r] of x (clamped to [0, x_rows)), or row r if row_index is NULL; y
  *   BF16 [R, outputs]; no bias, no residual. Rows past the counts are left as they
  *   are. workspace: w8a8_bf16_grouped_workspace_bytes(R, E, N, K) bytes, 256-byte
- *   aligned (the tile list). E <= 1024, K >= 8.
+ *   aligned (the tile list); never less for more rows. E <= 1024, K >= 8.
  * 1 <= K <= W8A8_MAX_K, N <= 2^22, M, R < 2^28 - 16, a grouped product of fewer than
  * 2^23 tiles of 128 rows x 256 columns. Workspaces are rewritten by every call: two
  * calls that may overlap need two.

@@ -1679,7 +1679,7 @@ static int check_bf16_grouped(const char* who, int64_t R, int64_t E, int64_t N, 
 
 int64_t w8a8_bf16_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K) {
   if (R <= 0 || E <= 0 || N <= 0 || K <= 0) return 0;
-  return w8a8::fused_sched_bytes(R, E, N, K);
+  return w8a8::fused_most_sched_bytes(R, E);
 }
 
 int w8a8_bf16_grouped_gemm(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_t* row_index,

@@ -1303,8 +1303,8 @@ int64_t fused_room_bytes(const FusedGemm& p, const FusedPlan& plan) {
 // Never falls as M grows, so that a room made for the most rows serves every batch. A plan
 // depends on the rows through ceil(M / 16) alone, and K is split only where 256 tiles at
 // most leave slots: the row counts up to that are gone through (2048 plans at most, 0.3 ms;
-// for 4096 columns). The copy is counted for every M that could come to the wide
-// tiles, whether or not the fewer rows' cost took them there.
+// 30 us for 4096 columns). The copy is counted for every M that could come to the wide
+// tiles, whether or not their cost takes it there.
 int64_t fused_most_bytes(int type, int64_t M, int64_t N, int64_t K) {
   const int64_t kbytes = type == kFusedInt8 ? K : 2 * K;
   const int64_t NB = type == kFusedInt8 ? ceil_div(N, 16) : round_up(N, 32) / 16;
@@ -1391,6 +1391,9 @@ static int64_t pieces_of(int64_t K) { return 2 * ceil_div(K, 64); }
 int64_t fused_sched_bytes(int64_t R, int64_t E, int64_t N, int64_t K) {
   return 256 + 16 * max_tiles(R, E, grouped_rows(R, E, blocks_of(N), pieces_of(K)));
 }
+
+// the list of the low tiles, the longest: taller ones begin at some row count
+int64_t fused_most_sched_bytes(int64_t R, int64_t E) { return 256 + 16 * max_tiles(R, E, kCost[kTile64].rows); }
 
 int64_t fused_grid(int64_t R, int64_t E, int64_t N, int64_t K) {
   const int rows = grouped_rows(R, E, blocks_of(N), pieces_of(K));

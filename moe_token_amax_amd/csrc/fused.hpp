@@ -57,9 +57,10 @@ int64_t fused_most_bytes(int type, int64_t M, int64_t N, int64_t K);
 // M, N >= 1
 hipError_t launch_fused_gemm(FusedGemm p, const FusedPlan& plan, void* room, hipStream_t stream);
 
-// Grouped (R = p.M rows): bytes of the tile list, workgroups, and the launch, which
-// writes the list into p.ws first.
+// Grouped (R = p.M rows): bytes of the tile list, the most that at most R rows can need,
+// workgroups, and the launch, which writes the list into p.ws first.
 int64_t fused_sched_bytes(int64_t R, int64_t E, int64_t N, int64_t K);
+int64_t fused_most_sched_bytes(int64_t R, int64_t E);
 int64_t fused_grid(int64_t R, int64_t E, int64_t N, int64_t K);
 hipError_t launch_fused_grouped(const FusedGemm& p, void* ws, hipStream_t stream);
 

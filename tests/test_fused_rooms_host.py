@@ -98,3 +98,25 @@ def test_linear_workspace_never_falls_as_rows_grow(w, kind, N, K):
     assert sizes[0] == 0
     falls = [(ROWS[i], sizes[i], ROWS[i + 1], sizes[i + 1]) for i in range(len(ROWS) - 1) if sizes[i] > sizes[i + 1]]
     assert not falls, falls[:3]
+
+
+@pytest.mark.parametrize("E,N,K", [(2, 5346, 1499), (8, 4096, 7168), (64, 8192, 4096), (256, 4096, 4096), (7, 1412, 1000),
+                                   (16, 2048, 2048), (1, 300, 200), (40, 30000, 512)])
+def test_grouped_workspace_never_falls_as_rows_grow(w, E, N, K):
+    sizes = [w.bf16_grouped_workspace_bytes(R, E, N, K) for R in ROWS]
+    assert sizes[0] == 0
+    falls = [(ROWS[i], sizes[i], ROWS[i + 1], sizes[i + 1]) for i in range(len(ROWS) - 1) if sizes[i] > sizes[i + 1]]
+    assert not falls, falls[:3]
+
+
+def test_grouped_workspace_covers_every_call(w):
+    """A call that is given a byte less than it needs says how much that is."""
+    rng = random.Random(4)
+    a = ctypes.c_void_p(P)
+    for _ in range(2000):
+        R, E, N, K = int(2 ** rng.uniform(0, 15)), int(2 ** rng.uniform(0, 10)), int(2 ** rng.uniform(0, 13)), \
+            int(2 ** rng.uniform(3, 13))
+        st = w.lib.w8a8_bf16_grouped_gemm(a, K, R, None, a, R, E, N, K, a, 0, a, a, 0, None)
+        assert st == WORKSPACE
+        need = int(w.lib.w8a8_last_error().split(b"needs ")[1].split()[0])
+        assert 256 < need <= w.bf16_grouped_workspace_bytes(R, E, N, K)
