@@ -774,7 +774,8 @@ int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* resid
  *   x_scale[m]) w_scale[n]) (+ bias, fl32), acc exact. Without activation and
  *   residual bit for bit w8a8_linear.
  * w8a8_fp8b_linear_fused: w8a8_fp8b_linear with the epilogue; the same arguments,
- *   workspace and products.
+ *   workspace and products. w8a8_fp8b_linear_plan: of either, for E4M3 rows (x_scale not
+ *   NULL; not read) or BF16 ones.
  * w8a8_bf16_linear: BF16 x [M, K], row stride ldx, times a BF16 weight, for the
  *   layers that a recipe leaves unquantized [DSV4 §一]: exact products, fp32 sums.
  *   out W8A8_OUT_BF16 or W8A8_OUT_F32 (router logits for w8a8_moe_gate).
@@ -799,6 +800,7 @@ int w8a8_linear_fused_plan(const int8_t* q, int64_t ldq, int64_t M, int64_t N, i
 int w8a8_linear_fused(const int8_t* q, int64_t ldq, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
                       const float* w_scale, int64_t N, const uint16_t* bias, int act, const uint16_t* residual,
                       int64_t ldr, uint16_t* y, int64_t ldy, void* workspace, int64_t ws_bytes, void* stream);
+int w8a8_fp8b_linear_plan(const float* x_scale, int64_t ldx, int64_t M, int64_t N, int64_t K, w8a8_plan* plan);
 int w8a8_fp8b_linear_fused(const void* x, int64_t ldx, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
                            const float* w_scale, int64_t N, const uint16_t* bias, int act, const uint16_t* residual,
                            int64_t ldr, uint16_t* y, int64_t ldy, int scale_alg, void* workspace, int64_t ws_bytes,

@@ -103,6 +103,7 @@ __all__ = [
     "linear_fused_workspace_bytes",
     "linear_fused_plan",
     "linear_fused",
+    "fp8b_linear_plan",
     "fp8b_linear_fused",
     "bf16_packed_bytes",
     "bf16_prepack_weight",
@@ -249,6 +250,7 @@ def _load():
         "w8a8_linear_fused_plan": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p]),
         "w8a8_linear_fused": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p,
                                              ctypes.c_int, _c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_p]),
+        "w8a8_fp8b_linear_plan": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p]),
         "w8a8_fp8b_linear_fused": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p,
                                                   ctypes.c_int, _c_p, _c_i64, _c_p, _c_i64, ctypes.c_int, _c_p,
                                                   _c_i64, _c_p]),
@@ -1289,6 +1291,14 @@ def fp8b_prepack_weight(w_e4m3: torch.Tensor, out: torch.Tensor | None = None) -
 
 def fp8b_linear_workspace_bytes(M: int, N: int, K: int) -> int:
     return int(lib.w8a8_fp8b_linear_workspace_bytes(M, N, K))
+
+
+def fp8b_linear_plan(x: torch.Tensor, N: int, x_scale: torch.Tensor | None = None, K: int | None = None) -> Plan:
+    """How fp8b_linear and fp8b_linear_fused run on these rows (BF16, or codes with their
+    x_scale), and the workspace bytes that they need."""
+    at, ldx = _rows_at(x, torch.bfloat16 if x_scale is None else torch.uint8, "x")
+    return _plan(lib.w8a8_fp8b_linear_plan, _at(x_scale, torch.float32, "x_scale", 2), ldx, x.shape[0], N,
+                 x.shape[1] if K is None else K)
 
 
 def _residual(t: torch.Tensor | None, shape):

@@ -1190,6 +1190,22 @@ static int check_act(const char* who, int act, bool swiglu) {
   return W8A8_OK;
 }
 
+int w8a8_fp8b_linear_plan(const float* x_scale, int64_t ldx, int64_t M, int64_t N, int64_t K, w8a8_plan* plan) {
+  int st = check_fp8b("fp8b_linear_plan", M, N, K);
+  if (st) return st;
+  if (ldx < (x_scale ? fp8b_pad(K) : K))
+    return fail(W8A8_ERR_SHAPE, "fp8b_linear_plan: ldx = %lld is below the row width", (long long)ldx);
+  if (!plan) return fail(W8A8_ERR_NULL, "fp8b_linear_plan: null pointer");
+  *plan = w8a8_plan{};
+  if (M == 0) return ok();
+  const w8a8::Fp8bGemm p = fp8b_args(nullptr, x_scale ? ldx : fp8b_pad(K), x_scale, M, M, K, nullptr, nullptr, N, nullptr);
+  w8a8::fp8b_tile(p, !x_scale && w8a8::fp8b_fused_ok(M, K), &plan->tile_rows, &plan->tile_cols);
+  plan->tiles = w8a8::ceil_div(M, plan->tile_rows) * w8a8::ceil_div(N, plan->tile_cols);
+  plan->k_parts = 1;
+  plan->workspace_bytes = x_scale ? 0 : w8a8_fp8b_linear_workspace_bytes(M, N, K);
+  return ok();
+}
+
 int w8a8_fp8b_linear_fused(const void* x, int64_t ldx, const float* x_scale, int64_t M, int64_t K, const void* w_packed,
                            const float* w_scale, int64_t N, const uint16_t* bias, int act, const uint16_t* residual,
                            int64_t ldr, uint16_t* y, int64_t ldy, int scale_alg, void* workspace, int64_t ws_bytes,

@@ -1051,10 +1051,12 @@ static void launch_decode(const Fp8bGemm& p, hipStream_t stream) {
 // whether the epilogue is more than a bias
 static bool fp8b_epilogue(const Fp8bGemm& p) { return p.act != W8A8_ACT_NONE || p.residual; }
 
+// whether pairs of column blocks reach a workgroup a CU at most (1 x 16384 x 7168: 28.9
+// us one by one, 26.7 in pairs)
+static bool fused_pairs(int64_t N) { return ceil_div(N, 16) > 256; }
+
 hipError_t launch_fp8b_linear_fused(const Fp8bGemm& p, hipStream_t stream) {
-  // a workgroup a CU at most, if pairs of column blocks reach that
-  // (1 x 16384 x 7168: 28.9 us one by one, 26.7 in pairs)
-  const bool pairs = ceil_div(p.N, 16) > 256;
+  const bool pairs = fused_pairs(p.N);
   if (fp8b_epilogue(p)) {
     if (pairs) launch_decode<1, 2, true, true>(p, stream);
     else launch_decode<1, 1, true, true>(p, stream);
@@ -1077,22 +1079,23 @@ hipError_t launch_fp8b_linear_fused(const Fp8bGemm& p, hipStream_t stream) {
 //     K 512:                   1 x 4096 3.1 / 4.3  64 x 4096 4.8 / 5.0  64 x 16384 12 / 6.3
 enum DenseKernel { kDecode16, kDecode16x32, kDecode32, kDecode64, kTile32, kTile64, kTile64x256, kTile128, kTile256 };
 
-static DenseKernel dense_kernel(const Fp8bGemm& p) {
-  struct Cost {
-    DenseKernel kernel;
-    int rows, cols;
-    double launch, round, first, full;
-    bool two;  // workgroups fit a CU
-  };
-  static const Cost kCosts[] = {
+struct Fp8bCost {
+  DenseKernel kernel;
+  int rows, cols;
+  double launch, round, first, full;
+  bool two;  // workgroups fit a CU
+};
+
+static const Fp8bCost& cheapest(const Fp8bGemm& p) {
+  static constexpr Fp8bCost kCosts[] = {
       {kDecode16, 16, 16, 1.2, 1.7, 0.08, 0.09, false},    {kDecode16x32, 16, 32, 1.9, 1.0, 0.08, 0.12, false},
       {kDecode32, 32, 32, 1.5, 1.4, 0.14, 0.20, false},    {kDecode64, 64, 32, 2.4, 2.7, 0.24, 0.28, false},
       {kTile32, 32, 128, 3.9, 0.0, 0.46, 1.37, true},      {kTile64, 64, 128, 4.1, 0.0, 0.54, 1.55, true},
       {kTile64x256, 64, 256, 0.0, 4.5, 0.09, 0.77, false}, {kTile128, 128, 256, 5.3, 4.6, 1.08, 0.85, false},
       {kTile256, 256, 256, 13.0, 1.2, 0.09, 1.44, false}};
-  DenseKernel best = kTile128;
+  const Fp8bCost* best = &kCosts[kTile128];
   double least = 1e30;
-  for (const Cost& c : kCosts) {
+  for (const Fp8bCost& c : kCosts) {
     // the wide tile's pipeline is two blocks deep and its row offsets have 32 bits
     if (c.kernel == kTile256 && (p.KB < 2 || p.a_rows * p.lda >= (int64_t)1 << 32)) continue;
     if (c.kernel < kTile32 && p.M > 65535 * 16) continue;  // their rows are the grid's second dimension
@@ -1101,10 +1104,21 @@ static DenseKernel dense_kernel(const Fp8bGemm& p) {
     const double us = c.launch + rounds * c.round + p.KB * std::max(c.first, rounds * c.full);
     if (us < least) {
       least = us;
-      best = c.kernel;
+      best = &c;
     }
   }
-  return best;
+  return *best;
+}
+
+void fp8b_tile(const Fp8bGemm& p, bool quant_inside, int32_t* rows, int32_t* cols) {
+  if (quant_inside) {
+    *rows = 16;
+    *cols = fused_pairs(p.N) ? 32 : 16;
+  } else {
+    const Fp8bCost& c = cheapest(p);
+    *rows = c.rows;
+    *cols = c.cols;
+  }
 }
 
 template <int MB, int NBW, bool EPI>
@@ -1115,7 +1129,7 @@ static void launch_dense_tiles(const Fp8bGemm& p, hipStream_t stream) {
 
 template <bool EPI>
 static hipError_t launch_dense(const Fp8bGemm& p, hipStream_t stream) {
-  switch (dense_kernel(p)) {
+  switch (cheapest(p).kernel) {
     case kDecode16: launch_decode<1, 1, false, EPI>(p, stream); break;
     case kDecode16x32: launch_decode<1, 2, false, EPI>(p, stream); break;
     case kDecode32: launch_decode<2, 2, false, EPI>(p, stream); break;

@@ -55,6 +55,8 @@ hipError_t launch_fp8b_quant_schedule(const uint16_t* x, int64_t M, int64_t K, i
                                       hipStream_t stream);
 hipError_t launch_fp8b_gemm(const Fp8bGemm& p, hipStream_t stream);
 bool fp8b_fused_ok(int64_t M, int64_t K);
+// rows and columns of a dense product's tiles
+void fp8b_tile(const Fp8bGemm& p, bool quant_inside, int32_t* rows, int32_t* cols);
 hipError_t launch_fp8b_linear_fused(const Fp8bGemm& p, hipStream_t stream);
 
 struct GateArgs {

@@ -79,8 +79,23 @@ def test_plan_refusals(w):
     assert L.w8a8_bf16_linear_plan(P, 63, 4, 8, 64, 0, at) == SHAPE
     assert L.w8a8_bf16_linear_plan(P, 64, 4, 8, 64, 6, at) == UNSUPPORTED
     assert L.w8a8_bf16_linear_plan(P, 64, 4, 8, 64, 0, None) == NULL
-    for st in (L.w8a8_linear_fused_plan(None, 64, 0, 8, 64, at), L.w8a8_bf16_linear_plan(None, 64, 0, 8, 64, 0, at)):
+    assert L.w8a8_fp8b_linear_plan(None, 63, 4, 8, 64, at) == SHAPE
+    assert L.w8a8_fp8b_linear_plan(P, 64, 4, 8, 64, at) == SHAPE      # codes: rows of 128
+    assert L.w8a8_fp8b_linear_plan(None, 64, 4, 8, 64, None) == NULL
+    for st in (L.w8a8_linear_fused_plan(None, 64, 0, 8, 64, at), L.w8a8_bf16_linear_plan(None, 64, 0, 8, 64, 0, at),
+               L.w8a8_fp8b_linear_plan(None, 64, 0, 8, 64, at)):
         assert st == OK and p.tiles == p.workspace_bytes == 0
+
+
+def test_fp8_plan(w):
+    p = w.Plan()
+    for M, N, K, codes, tile in [(1, 4096, 7168, False, (16, 16)), (1, 16384, 7168, False, (16, 32)),
+                                 (333, 1000, 2000, True, (64, 32)), (8192, 4096, 7168, True, (256, 256)),
+                                 (8192, 4096, 7168, False, (256, 256))]:
+        assert w.lib.w8a8_fp8b_linear_plan(P if codes else None, -(-K // 128) * 128, M, N, K, ctypes.byref(p)) == OK
+        assert (p.tile_rows, p.tile_cols, p.k_parts, p.copied) == (*tile, 1, 0)
+        assert p.tiles == -(-M // tile[0]) * -(-N // tile[1])
+        assert p.workspace_bytes == (0 if codes else w.fp8b_linear_workspace_bytes(M, N, K))
 
 
 # rows at the borders of the tiles, one by one to 600, then up to prompts

@@ -4,12 +4,16 @@ test_gpu_fused.py."""
 
 from __future__ import annotations
 
+import math
+
 import numpy as np
 import pytest
 import torch
 
+import oracle as O
 from tests.conftest import gpu_available
-from tests.gpu_util import DEV, dev, show, sync
+from tests.gpu_util import DEV, bf16_dev, dev, show, sync
+from tests.test_gpu_fused import _act_id, _acts, _bf16, _epilogue, _f64, _hold
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
@@ -45,3 +49,61 @@ def test_aligned_prompt_reserves_only_its_output(w, kind):
     sync()
     assert torch.cuda.max_memory_allocated() - before == 2 * M * N
     assert (y == K).all()
+
+
+def _rows_of_tiles(M):
+    """A row of every 128, in turn the first, the last and one between, and the last rows."""
+    at = np.arange(0, M, 128)
+    return np.unique(np.clip(np.r_[at + np.resize([0, 127, 37, 64], len(at)), M - 2:M], 0, M - 1))
+
+
+# 256 x 256 with more tiles than workgroups and last tiles of 1, 4 and 150 rows; blocks of
+# K even, odd and two; columns that end inside a wavefront's 64 or 16. 128 x 256.
+FP8 = [(8193, 4100, 512, "silu", True, True, True), (8193, 4100, 512, "none", False, True, False),
+       (4100, 4130, 640, "gelu", True, False, False), (4100, 4130, 640, "relu", True, True, True),
+       (8342, 4161, 200, "gelu_tanh", False, True, True), (8342, 4161, 200, "none", True, True, False),
+       (4097, 8200, 900, "silu", False, False, False), (4097, 8200, 900, "gelu", False, True, True)]
+FP8_128 = [(2000, 3000, 1000, "silu", True, True, True), (2000, 3000, 1000, "relu", False, False, False),
+           (1930, 2890, 1000, "gelu_tanh", True, True, False), (1930, 2890, 1000, "none", False, True, True)]
+
+
+@pytest.mark.parametrize("M,N,K,act,bias,res,place,tile", [(*c, (256, 256)) for c in FP8] + [(*c, (128, 256)) for c in FP8_128])
+def test_fp8_high_tiles_with_an_epilogue(w, M, N, K, act, bias, res, place, tile):
+    """The wide tiles that a workgroup walks over and the 128-row tiles, the residual in
+    place or beside; rows around the output untouched; codes given and quantized inside."""
+    show(f"fp8 {M} x {N} x {K} {act} bias {bias} residual {res} in place {place}")
+    rng = np.random.default_rng(M + 7 * N + 11 * K)
+    x = _acts(rng, M, K, 1.0)
+    cw = O.mx.e4m3_encode(np.clip(rng.standard_normal((N, K)) * 100.0, -448, 448))
+    sw = (rng.uniform(0.5, 1.5, (O.fp8b.blocks(N), O.fp8b.blocks(K))) / (100 * math.sqrt(K))).astype(np.float32)
+    b, r = (_bf16(rng, N, scale=0.3) if bias else None), (_bf16(rng, M, N) if res else None)
+    wp, xd, swd = w.fp8b_prepack_weight(dev(cw)), bf16_dev(x), dev(sw)
+    qd, sd = w.fp8b_quant(xd)
+    plan = w.fp8b_linear_plan(qd, N, x_scale=sd, K=K)
+    assert (plan.tile_rows, plan.tile_cols) == tile
+    assert tile[0] == 128 or plan.tiles > 256            # more than a workgroup a CU
+    assert w.fp8b_linear_plan(xd, N).tile_rows == tile[0]
+    room = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    y, rd = room[1:M + 1], bf16_dev(r) if res else None
+    if place:
+        y.copy_(rd)
+        rd = y
+    kw = dict(bias=bf16_dev(b) if bias else None, act=_act_id(w, act), y=y)
+    w.fp8b_linear_fused(qd, wp, swd, N, x_scale=sd, K=K, residual=rd, **kw)
+    sync()
+    assert (room[0] == 7).all() and (room[M + 1] == 7).all()
+    first = y.clone()
+    if place:
+        y.copy_(bf16_dev(r))
+    w.fp8b_linear_fused(xd, wp, swd, N, residual=rd, **kw)
+    sync()
+    assert torch.equal(first.view(torch.int16), y.view(torch.int16))
+    pick = _rows_of_tiles(M)
+    q, s = O.fp8b.quant(x[pick])
+    v = O.fp8b.product64(q, s, cw, sw, b)
+    A = np.abs(O.fp8b.dequant(q, s)) @ np.abs(O.fp8b.weight_dequant(cw, sw)).T
+    if bias:
+        A = A + np.abs(_f64(b))
+    dv = O.fp8b.cut_bound(q, s, cw, sw) + (18 + O.fp8b.blocks(K)) * 2.0 ** -23 * A
+    _hold(y[torch.from_numpy(pick).to(DEV)], *_epilogue(v, dv, act, r[pick] if res else None), f"{M}x{N}x{K}")
+    assert torch.isfinite(y.float()).all()
