@@ -98,6 +98,23 @@ def test_fp8_plan(w):
         assert p.workspace_bytes == (0 if codes else w.fp8b_linear_workspace_bytes(M, N, K))
 
 
+KERNELS = [(16, 16), (16, 32), (32, 32), (64, 32), (32, 128), (64, 128), (64, 256), (128, 256), (256, 256)]
+SPLITS = [(32, 128), (64, 128), (128, 256)]
+
+
+@pytest.mark.parametrize("kind,act", [("bf16", 0), ("bf16", 1), ("int8", 0)])
+def test_the_sizes_of_the_gpu_tests_reach_every_kernel_and_split(w, kind, act):
+    """test_every_kernel and the linears' sizes: pinned, so that another cost of a kernel
+    cannot move them off one unseen."""
+    from tests.test_gpu_fused import PLANS, SIZES
+    double = 2 if kind == "int8" else 1
+    plans = [_plan(w, kind, M, N + N % 2 if act else N, K * double, act=act) for M, N, K in PLANS] + \
+        [_plan(w, kind, M, N + N % 2 if act else N, K, act=act) for M, N, K in SIZES]
+    whole = {(p.tile_rows, p.tile_cols) for p in plans if p.k_parts == 1}
+    split = {(p.tile_rows, p.tile_cols) for p in plans if p.k_parts > 1}
+    assert whole == set(KERNELS[act:]) and split == set(SPLITS)      # SwiGLU: pairs of 16 columns
+
+
 # rows at the borders of the tiles, one by one to 600, then up to prompts
 ROWS = sorted(set(range(600)) | {16 * i + d for i in range(38, 300, 3) for d in (-1, 0, 1)} |
               {8191, 8192, 8193, 32767, 32769, 65536, 1 << 20})

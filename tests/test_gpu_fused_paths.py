@@ -13,7 +13,7 @@ import torch
 import oracle as O
 from tests.conftest import gpu_available
 from tests.gpu_util import DEV, bf16_dev, dev, show, sync
-from tests.test_gpu_fused import _act_id, _acts, _bf16, _epilogue, _f64, _hold
+from tests.test_gpu_fused import U, _act_id, _acts, _bf16, _bf16_value, _epilogue, _f64, _hold, _int8_operands
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
@@ -105,5 +105,50 @@ def test_fp8_high_tiles_with_an_epilogue(w, M, N, K, act, bias, res, place, tile
     if bias:
         A = A + np.abs(_f64(b))
     dv = O.fp8b.cut_bound(q, s, cw, sw) + (18 + O.fp8b.blocks(K)) * 2.0 ** -23 * A
+    _hold(y[torch.from_numpy(pick).to(DEV)], *_epilogue(v, dv, act, r[pick] if res else None), f"{M}x{N}x{K}")
+    assert torch.isfinite(y.float()).all()
+
+
+# K in elements of BF16 (INT8: twice as many): steps of 128 bytes odd, even and two, ragged
+# and whole; last tiles of 8, 1, 77 and 120 rows
+WALKED = [(8200, 4100, 520), (8193, 4100, 512), (8269, 8150, 96), (8312, 4354, 712)]
+
+
+@pytest.mark.parametrize("kind,act,bias,res,place", [("bf16", "none", False, True, False), ("bf16", "swiglu", True, True, True),
+                                                     ("bf16", "silu", True, False, False), ("int8", "gelu", True, True, True),
+                                                     ("int8", "none", True, False, False), ("int8", "relu", False, True, False)])
+@pytest.mark.parametrize("M,N,K", WALKED)
+def test_wide_tiles_that_a_workgroup_walks_over(w, M, N, K, kind, act, bias, res, place):
+    """More tiles than workgroups: the next tile's rows and weights land while one is
+    stored. Rows of every tile against float64, rows around the output untouched."""
+    show(f"{kind} {M} x {N} x {K} {act} bias {bias} residual {res} in place {place}")
+    rng = np.random.default_rng(M + 7 * N + 11 * K)
+    width = N // 2 if act == "swiglu" else N
+    b, r = (_bf16(rng, N, scale=0.3) if bias else None), (_bf16(rng, M, width) if res else None)
+    room = torch.full((M + 2, width), 7.0, dtype=torch.bfloat16, device=DEV)
+    y, rd = room[1:M + 1], bf16_dev(r) if res else None
+    if place:
+        y.copy_(rd)
+        rd = y
+    kw = dict(bias=bf16_dev(b) if bias else None, act=_act_id(w, act), residual=rd, y=y)
+    pick = _rows_of_tiles(M)
+    if kind == "bf16":
+        x, wt = _acts(rng, M, K), _bf16(rng, N, K, scale=1 / math.sqrt(K))
+        xd, wp = bf16_dev(x), w.bf16_prepack_weight(bf16_dev(wt), act=_act_id(w, act))
+        plan = w.bf16_linear_plan(xd, N, _act_id(w, act))
+        w.bf16_linear(xd, wp, N, **kw)
+        v, dv = _bf16_value(x[pick], wt, b)
+    else:
+        q, s, wi, ws = _int8_operands(rng, M, N, 2 * K)
+        qd = dev(q)
+        plan = w.linear_fused_plan(qd, N)
+        w.linear_fused(qd, dev(s), w.prepack_weight(dev(wi)), dev(ws), N, **kw)
+        v = (q[pick].astype(np.float64) @ wi.T.astype(np.float64)) * s[pick].astype(np.float64)[:, None] * ws.astype(np.float64)
+        dv = 4 * U * np.abs(v)
+        if bias:
+            v, dv = v + _f64(b), dv + 4 * U * np.abs(_f64(b))
+    sync()
+    assert (plan.tile_rows, plan.tile_cols, plan.copied) == (256, 256, 0) and plan.tiles > 512
+    assert (room[0] == 7).all() and (room[M + 1] == 7).all()
     _hold(y[torch.from_numpy(pick).to(DEV)], *_epilogue(v, dv, act, r[pick] if res else None), f"{M}x{N}x{K}")
     assert torch.isfinite(y.float()).all()
