@@ -790,7 +790,9 @@ int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* resid
  *   row row_index[r] of x (clamped to [0, x_rows)), or row r if row_index is NULL; y
  *   BF16 [R, outputs]; no bias, no residual. Rows past the counts are left as they
  *   are. workspace: w8a8_bf16_grouped_workspace_bytes(R, E, N, K) bytes, 256-byte
- *   aligned (the tile list); never less for more rows. E <= 1024, K >= 8.
+ *   aligned (the tile list); never less for more rows. w8a8_bf16_grouped_plan: the bytes
+ *   of this call, its highest tiles and at most how many (nothing is read). E <= 1024,
+ *   K >= 8.
  * 1 <= K <= W8A8_MAX_K, N <= 2^22, M, R < 2^28 - 16, a grouped product of fewer than
  * 2^23 tiles of 128 rows x 256 columns. Workspaces are rewritten by every call: two
  * calls that may overlap need two.
@@ -813,6 +815,8 @@ int w8a8_bf16_linear(const uint16_t* x, int64_t ldx, int64_t M, int64_t K, const
                      const uint16_t* bias, int act, const uint16_t* residual, int64_t ldr, void* y, int64_t ldy, int out,
                      void* workspace, int64_t ws_bytes, void* stream);
 int64_t w8a8_bf16_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64_t K);
+int w8a8_bf16_grouped_plan(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_t* row_index, int64_t R, int64_t E,
+                           int64_t N, int64_t K, w8a8_plan* plan);
 int w8a8_bf16_grouped_gemm(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_t* row_index,
                            const int64_t* group_list, int64_t R, int64_t E, int64_t N, int64_t K, const void* w_packed,
                            int act, uint16_t* y, void* workspace, int64_t ws_bytes, void* stream);

@@ -111,6 +111,7 @@ __all__ = [
     "bf16_linear_plan",
     "bf16_linear",
     "bf16_grouped_workspace_bytes",
+    "bf16_grouped_plan",
     "bf16_grouped_gemm",
 ]
 
@@ -261,6 +262,7 @@ def _load():
         "w8a8_bf16_linear": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, ctypes.c_int, _c_p,
                                             _c_i64, _c_p, _c_i64, ctypes.c_int, _c_p, _c_i64, _c_p]),
         "w8a8_bf16_grouped_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_i64]),
+        "w8a8_bf16_grouped_plan": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p]),
         "w8a8_bf16_grouped_gemm": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_i64, _c_i64,
                                                   _c_i64, _c_p, ctypes.c_int, _c_p, _c_p, _c_i64, _c_p]),
     }
@@ -1708,6 +1710,15 @@ def bf16_linear(x: torch.Tensor, w_packed: torch.Tensor, N: int, bias: torch.Ten
 
 def bf16_grouped_workspace_bytes(R: int, E: int, N: int, K: int) -> int:
     return int(lib.w8a8_bf16_grouped_workspace_bytes(R, E, N, K))
+
+
+def bf16_grouped_plan(x: torch.Tensor, E: int, N: int, row_index: torch.Tensor | None = None) -> Plan:
+    """How bf16_grouped_gemm runs on these rows: its highest tiles, at most how many, and
+    the workspace bytes that it needs."""
+    at, ldx = _rows_at(x, torch.bfloat16, "x")
+    R = x.shape[0] if row_index is None else row_index.shape[0]
+    return _plan(lib.w8a8_bf16_grouped_plan, at, ldx, x.shape[0], _at(row_index, torch.int32, "row_index", 1), R, E, N,
+                 x.shape[1])
 
 
 def bf16_grouped_gemm(x: torch.Tensor, group_list: torch.Tensor, w_packed: torch.Tensor, N: int, act: int = ACT_NONE,

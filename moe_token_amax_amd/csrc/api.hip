@@ -1698,6 +1698,24 @@ int64_t w8a8_bf16_grouped_workspace_bytes(int64_t R, int64_t E, int64_t N, int64
   return w8a8::fused_most_sched_bytes(R, E);
 }
 
+int w8a8_bf16_grouped_plan(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_t* row_index, int64_t R, int64_t E,
+                           int64_t N, int64_t K, w8a8_plan* plan) {
+  int st = check_bf16_grouped("bf16_grouped_plan", R, E, N, K);
+  if (st) return st;
+  if (ldx < K) return fail(W8A8_ERR_SHAPE, "bf16_grouped_plan: ldx = %lld is below the row width", (long long)ldx);
+  if (!plan) return fail(W8A8_ERR_NULL, "bf16_grouped_plan: null pointer");
+  *plan = w8a8_plan{};
+  if (R == 0) return ok();
+  w8a8::FusedGemm p = fused_bf16(x, ldx, x_rows, R, K, nullptr, N, W8A8_ACT_NONE);
+  p.row_index = row_index;
+  p.E = E;
+  w8a8::fused_grouped_tile(p, &plan->tile_rows, &plan->tile_cols);
+  plan->tiles = w8a8::fused_grid(R, E, N, K);
+  plan->k_parts = 1;
+  plan->workspace_bytes = w8a8::fused_sched_bytes(R, E, N, K);
+  return ok();
+}
+
 int w8a8_bf16_grouped_gemm(const uint16_t* x, int64_t ldx, int64_t x_rows, const int32_t* row_index,
                            const int64_t* group_list, int64_t R, int64_t E, int64_t N, int64_t K, const void* w_packed,
                            int act, uint16_t* y, void* workspace, int64_t ws_bytes, void* stream) {

@@ -1402,10 +1402,19 @@ int64_t fused_grid(int64_t R, int64_t E, int64_t N, int64_t K) {
 
 // Wide tiles for experts of many rows: two steps of K, rows as they copy them, 32-bit
 // offsets from a's first row where rows are read through an index.
+static bool grouped_wide(const FusedGemm& p, int rows) {
+  return rows == kTileRows && p.KP > 2 && fused_rows_ok(p) && (!p.row_index || p.a_rows * p.lda < (int64_t)1 << 32);
+}
+
+void fused_grouped_tile(const FusedGemm& p, int32_t* rows, int32_t* cols) {
+  const int low = grouped_rows(p.M, p.E, p.NB, p.KP);
+  *rows = grouped_wide(p, low) ? kWideRows : low;
+  *cols = low == kTileRows ? 256 : 128;
+}
+
 hipError_t launch_fused_grouped(const FusedGemm& p, void* ws, hipStream_t stream) {
   const int rows = grouped_rows(p.M, p.E, p.NB, p.KP);
-  const bool wide = rows == kTileRows && p.KP > 2 && fused_rows_ok(p) &&
-                    (!p.row_index || p.a_rows * p.lda < (int64_t)1 << 32);
+  const bool wide = grouped_wide(p, rows);
   hipLaunchKernelGGL(fused_schedule_kernel, dim3(1), dim3(256), 0, stream, p.group_list, (int)p.E, p.M, (int)wide, rows,
                      reinterpret_cast<int*>(ws), reinterpret_cast<int4*>(reinterpret_cast<char*>(ws) + 256));
   const hipError_t err = hipGetLastError();

@@ -62,6 +62,8 @@ hipError_t launch_fused_gemm(FusedGemm p, const FusedPlan& plan, void* room, hip
 int64_t fused_sched_bytes(int64_t R, int64_t E, int64_t N, int64_t K);
 int64_t fused_most_sched_bytes(int64_t R, int64_t E);
 int64_t fused_grid(int64_t R, int64_t E, int64_t N, int64_t K);
+// rows and columns of the highest tiles that an expert can get
+void fused_grouped_tile(const FusedGemm& p, int32_t* rows, int32_t* cols);
 hipError_t launch_fused_grouped(const FusedGemm& p, void* ws, hipStream_t stream);
 
 }  // namespace w8a8

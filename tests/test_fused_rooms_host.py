@@ -82,8 +82,12 @@ def test_plan_refusals(w):
     assert L.w8a8_fp8b_linear_plan(None, 63, 4, 8, 64, at) == SHAPE
     assert L.w8a8_fp8b_linear_plan(P, 64, 4, 8, 64, at) == SHAPE      # codes: rows of 128
     assert L.w8a8_fp8b_linear_plan(None, 64, 4, 8, 64, None) == NULL
+    assert L.w8a8_bf16_grouped_plan(P, 63, 4, None, 4, 2, 16, 64, at) == SHAPE
+    assert L.w8a8_bf16_grouped_plan(P, 64, 4, None, 4, 0, 16, 64, at) == SHAPE
+    assert L.w8a8_bf16_grouped_plan(P, 64, 4, None, 4, 1025, 16, 64, at) == UNSUPPORTED
+    assert L.w8a8_bf16_grouped_plan(P, 64, 4, None, 4, 2, 16, 64, None) == NULL
     for st in (L.w8a8_linear_fused_plan(None, 64, 0, 8, 64, at), L.w8a8_bf16_linear_plan(None, 64, 0, 8, 64, 0, at),
-               L.w8a8_fp8b_linear_plan(None, 64, 0, 8, 64, at)):
+               L.w8a8_fp8b_linear_plan(None, 64, 0, 8, 64, at), L.w8a8_bf16_grouped_plan(None, 64, 0, None, 0, 2, 8, 64, at)):
         assert st == OK and p.tiles == p.workspace_bytes == 0
 
 
@@ -96,6 +100,18 @@ def test_fp8_plan(w):
         assert (p.tile_rows, p.tile_cols, p.k_parts, p.copied) == (*tile, 1, 0)
         assert p.tiles == -(-M // tile[0]) * -(-N // tile[1])
         assert p.workspace_bytes == (0 if codes else w.fp8b_linear_workspace_bytes(M, N, K))
+
+
+def test_grouped_plan(w):
+    p, a = w.Plan(), ctypes.c_void_p(P)
+    for at, ld, rows, index, R, E, N, K, tile in [
+            (P, 1000, 1003, None, 1003, 7, 1412, 1000, (64, 128)), (P, 1400, 3600, None, 3600, 8, 4130, 1400, (256, 256)),
+            (P, 1401, 3600, None, 3600, 8, 4130, 1401, (128, 256)), (P + 2, 1400, 3600, None, 3600, 8, 4130, 1400, (128, 256)),
+            (P, 1400, 777, a, 3600, 8, 4130, 1400, (256, 256)), (P, 1 << 20, 4096, a, 3600, 8, 4130, 1400, (128, 256)),
+            (P, 1 << 20, 4096, None, 3600, 8, 4130, 1400, (256, 256))]:
+        assert w.lib.w8a8_bf16_grouped_plan(at, ld, rows, index, R, E, N, K, ctypes.byref(p)) == OK
+        assert (p.tile_rows, p.tile_cols, p.k_parts, p.copied) == (*tile, 1, 0)
+        assert 256 < p.workspace_bytes <= w.bf16_grouped_workspace_bytes(R, E, N, K)
 
 
 KERNELS = [(16, 16), (16, 32), (32, 32), (64, 32), (32, 128), (64, 128), (64, 256), (128, 256), (256, 256)]

@@ -152,3 +152,45 @@ def test_wide_tiles_that_a_workgroup_walks_over(w, M, N, K, kind, act, bias, res
     assert (room[0] == 7).all() and (room[M + 1] == 7).all()
     _hold(y[torch.from_numpy(pick).to(DEV)], *_epilogue(v, dv, act, r[pick] if res else None), f"{M}x{N}x{K}")
     assert torch.isfinite(y.float()).all()
+
+
+# experts whose rows end in every height of the low tiles, behind wide tiles and alone; and
+# with so many tiles (columns in 17 and in 16 groups) that they are spread over the XCDs
+HEIGHTS = [65, 80, 96, 97, 128, 129, 326, 608, 3, 17, 40, 0, 1700]
+MANY = [4000, 70, 4890]
+WIDE = [9000, 8070]
+
+
+@pytest.mark.parametrize("counts,N,K,lo,index,act,rows", [
+    (HEIGHTS, 4130, 1400, 0, False, "none", 256), (HEIGHTS, 4130, 1400, 0, True, "swiglu", 256),
+    (HEIGHTS, 4130, 1400, 3, False, "swiglu", 128), (HEIGHTS, 4130, 1401, 0, True, "gelu", 128),
+    (MANY, 4130, 700, 0, False, "none", 128), (MANY, 4000, 701, 1, True, "swiglu", 128),
+    (MANY, 4000, 1000, 0, True, "silu", 256), (WIDE, 2000, 1000, 0, True, "none", 256), (WIDE, 2100, 1000, 0, True, "gelu", 256)])
+def test_grouped_heights(w, counts, N, K, lo, index, act, rows):
+    """Tiles of up to 128 rows and wide ones, each shown to be there by the plan; an
+    expert's first rows, its last ones and the borders of its tiles."""
+    show(f"grouped {counts} {N} x {K} from column {lo} index {index} {act}")
+    rng = np.random.default_rng(N + K + lo)
+    E, R, T = len(counts), sum(counts) + 5, 777
+    x = _acts(rng, T if index else R, K)
+    wide = torch.full((len(x), K + 8), float("nan"), dtype=torch.bfloat16, device=DEV)
+    wide[:, lo:lo + K] = bf16_dev(x)
+    xd, at = wide[:, lo:lo + K], rng.integers(0, T, R).astype(np.int32) if index else np.arange(R)
+    ad = dev(at) if index else None
+    plan = w.bf16_grouped_plan(xd, E, N, row_index=ad)
+    assert (plan.tile_rows, plan.tile_cols) == (rows, 256)
+    wt = _bf16(rng, E, N, K, scale=1 / math.sqrt(K))
+    width = N // 2 if act == "swiglu" else N
+    y = torch.full((R, width), 7.0, dtype=torch.bfloat16, device=DEV)
+    w.bf16_grouped_gemm(xd, dev(np.array(counts, np.int64)), w.bf16_prepack_weight(bf16_dev(wt), act=_act_id(w, act)), N,
+                        act=_act_id(w, act), row_index=ad, y=y)
+    sync()
+    assert (y[sum(counts):] == 7).all() and torch.isfinite(y.float()).all()
+    first = 0
+    for e, n in enumerate(counts):
+        if n:
+            step = np.arange(0, n, 128)
+            pick = first + np.unique(np.clip(np.r_[step, step + 16, step + 63, step + 95, step + 127, n - 2:n], 0, n - 1))
+            v, dv = _bf16_value(x[at[pick]], wt[e])
+            _hold(y[torch.from_numpy(pick).to(DEV)], *_epilogue(v, dv, act), f"expert {e}")
+        first += n
