@@ -755,9 +755,12 @@ int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* resid
 /*
  * Products with bias, activation and residual in their epilogue: y = out(act(v) +
  * residual), v the fp32 value in front of the output's rounding (the only one).
- *   act       w8a8_act; evaluated in fp32 with the hardware's exponential (a few
- *             2^-24 relative; GELU within 2^-21 |v|). W8A8_ACT_SWIGLU only on BF16
- *             weights prepacked for it
+ *   act       w8a8_act; evaluated in fp32 with the hardware's exponential. SiLU, SwiGLU's
+ *             and GELU by tanh: within (6 |t| + 8) 2^-24 of the value, t the exponent's
+ *             argument; where t < -87, 0 may stand for a value under 2^-118 (SwiGLU: |up|
+ *             2^-118). GELU: within 2^-21 |v|, its far negative tail therefore right absolutely
+ *             and not relatively (off by 0.05 % of the value at -4, 0.4 % at -6, 2 % at -10).
+ *             W8A8_ACT_SWIGLU only on BF16 weights prepacked for it
  *   residual  device, BF16 [M, outputs], row stride ldr, or NULL; may be y itself
  *   bias      device, BF16 [N] or NULL
  *   workspace the call's workspace_bytes, 256-byte aligned, rewritten: sums of a K

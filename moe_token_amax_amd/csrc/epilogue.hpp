@@ -14,13 +14,16 @@ namespace w8a8 {
 
 // v / (1 + e^-t) by the hardware's exponential and reciprocal (1 ulp each; the
 // exponent's rounding makes it a few 2^-24 |t| more, far inside a BF16 step). Ends:
-// e^-t = inf gives v * 0, NaN stays NaN.
+// below t = -87 the reciprocal, which knows no subnormals, and then e^-t = inf give v * 0
+// for a value under 2^-118 (BF16 would hold it; scaling the exponential would cost every
+// output another reciprocal); NaN stays NaN.
 __device__ __forceinline__ float times_sigmoid(float v, float t) {
   return v * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t * -1.44269504f));
 }
 
 // v Phi(v): erfc by M. Abramowitz and I. Stegun, Handbook of Mathematical Functions,
-// 7.1.26 (within 1.5e-7), times e^(-v^2 / 2)
+// 7.1.26 (within 1.5e-7; of erfc itself 0.05 % at v = -4, 0.4 % at -6, 2 % at -10), times
+// e^(-v^2 / 2)
 __device__ __forceinline__ float gelu_erf(float v) {
   const float z = fabsf(v) * 0.70710678f;
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, z, 1.0f));

@@ -13,7 +13,7 @@ import torch
 import oracle as O
 from tests.conftest import gpu_available
 from tests.gpu_util import DEV, bf16_dev, dev, show, sync
-from tests.test_gpu_fused import U, _act_id, _acts, _bf16, _bf16_value, _epilogue, _f64, _hold, _int8_operands
+from tests.test_gpu_fused import F, U, _act_id, _acts, _bf16, _bf16_value, _epilogue, _f64, _hold, _int8_operands
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
@@ -194,3 +194,54 @@ def test_grouped_heights(w, counts, N, K, lo, index, act, rows):
             v, dv = _bf16_value(x[at[pick]], wt[e])
             _hold(y[torch.from_numpy(pick).to(DEV)], *_epilogue(v, dv, act), f"expert {e}")
         first += n
+
+
+def _activated(w, v_bits, act):
+    """fp32 outputs of the values themselves: a one-hot row times a column of them."""
+    wt = np.zeros((len(v_bits), 16), np.uint16)
+    wt[:, 0] = v_bits
+    x = np.zeros((1, 16), np.uint16)
+    x[0, 0] = 0x3F80
+    y = w.bf16_linear(bf16_dev(x), w.bf16_prepack_weight(bf16_dev(wt)), len(v_bits), act=_act_id(w, act), out=w.OUT_F32)
+    sync()
+    return y.cpu().numpy()[0].astype(np.float64)
+
+
+def test_gelu_tail_is_the_published_formula(w):
+    """v < 0: relative to 0.5 v t s(t) e^(-z^2) in 64 bits, z = |v| / sqrt 2, t = 1 / (1 + p z), s
+    the polynomial of the Handbook's 7.1.26, however small the value. Roundings (units of
+    2^-24): z 1.3 (constant 0.3, product 1); t: 3.3 of its divisor and 2 of the reciprocal;
+    a term a_k t^k of s: its coefficient, k + 1 additions at most five, 5.3 k, so at most 28 of
+    sum |a_k| t^k; the exponent z^2 log2 e: 2.6 + 1 + 2 of it, so 5.6 v^2 / 2 of the result, and 2
+    of the exponential; the products 4."""
+    v = O.f32_to_bf16(np.unique(np.r_[-np.linspace(0.01, 13, 4000), -np.geomspace(1e-30, 0.01, 300)]).astype(np.float32))
+    v = np.unique(v)
+    y, x = _activated(w, v, "gelu"), _f64(v)
+    z = -x / math.sqrt(2.0)
+    t = 1.0 / (1.0 + 0.3275911 * z)
+    a = [0.254829592, -0.284496736, 1.421413741, -1.453152027, 1.061405429]
+    s = sum(c * t ** k for k, c in enumerate(a))
+    size = sum(abs(c) * t ** k for k, c in enumerate(a))
+    want = 0.5 * x * t * s * np.exp(-z * z)
+    tol = 1.01 * (28.0 * size / s + 11.3 + 2.8 * x * x) * U * np.abs(want)
+    off = np.abs(y - want)
+    show(f"{len(v)} values, share of the tolerance used {float((off / tol).max()):.3f}")
+    assert (off <= tol).all(), x[off > tol][:3]
+    true = F.act64(x, "gelu")                             # and that formula, of the function
+    assert (np.abs(want - true) <= 0.75e-7 * np.abs(x)).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
+def test_sigmoid_tails_hold_their_relative_bound_until_they_vanish(w, act):
+    """Down to an exponent's argument of -87 within (6 |t| + 8) 2^-24 of the value; behind that
+    0 or the value, which is below 90 e^-87 (the reciprocal of 2^126 and the exponential's
+    overflow)."""
+    v = np.unique(O.f32_to_bf16(np.r_[-np.linspace(0.001, 110, 4000), np.linspace(0.001, 110, 1000)].astype(np.float32)))
+    y, x = _activated(w, v, act), _f64(v)
+    want = F.act64(x, act)
+    t = x if act == "silu" else 2 * math.sqrt(2 / math.pi) * (x + 0.044715 * x ** 3)
+    off = np.abs(y - want)
+    near = t >= -87.0
+    assert near.any() and (~near).any()
+    assert (off <= (6 * np.minimum(np.abs(t), 90) + 8) * U * np.abs(want))[near].all()
+    assert (off[~near] <= 2.0 ** -118).all() and (y[~near] <= 0).all()
