@@ -726,7 +726,7 @@ int w8a8_fp8b_moe_layer(const uint16_t* x, int64_t T, int64_t H, const int32_t* 
  *            x; without a residual it is not written and may be NULL)
  *   weight   device, BF16 [K], or NULL for 1
  *   y        device, BF16 [M, K], row stride ldy: the norm in BF16, or NULL
- *            (w8a8_rms_norm needs it)
+ *            (w8a8_rms_norm needs it); may be x, or h, whose sum it then replaces
  * h = BF16(fl32(x + residual)) or x; r = fl32(1 / sqrt(sum of h^2 / K + eps)), the
  * sum in doubles; n = fl32(fl32(h r) weight); y = BF16(n). The codes are of n, with
  * no rounding to BF16 between:
@@ -737,8 +737,11 @@ int w8a8_fp8b_moe_layer(const uint16_t* x, int64_t T, int64_t H, const int32_t* 
  *   w8a8_mx_rms_norm_quant: e4m3 [M, K] (8-byte aligned), e8m0 [M, K/32], the rule of
  *     w8a8_mx_quant; K % 32 == 0, else W8A8_ERR_UNSUPPORTED. A group with an infinity
  *     or NaN gets the byte 255 and codes NaN.
- * An infinity or NaN in a row makes the row's norm NaN: scale NaN, codes 0 (INT8,
- * blocks that hold one). 1 <= K <= W8A8_MAX_K, M < 2^31, eps >= 0 and finite.
+ * A NaN in a row (and a row of zeros where eps is 0) makes its whole norm NaN. An infinity
+ * makes r 0: NaN in its own place, 0 in all others. Where the norm is NaN, an INT8 row
+ * and an E4M3 block get the scale NaN and codes 0; the other blocks of a row with an
+ * infinity get scale and codes 0.
+ * 1 <= K <= W8A8_MAX_K, M < 2^31, eps >= 0 and finite.
  */
 int w8a8_rms_norm(const uint16_t* x, int64_t ldx, const uint16_t* residual, int64_t ldr, uint16_t* h, int64_t ldh,
                   const uint16_t* weight, double eps, int64_t M, int64_t K, uint16_t* y, int64_t ldy, void* stream);
