@@ -765,6 +765,9 @@ int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* resid
  *             and not relatively (off by 0.05 % of the value at -4, 0.4 % at -6, 2 % at -10).
  *             W8A8_ACT_SWIGLU only on BF16 weights prepacked for it
  *   residual  device, BF16 [M, outputs], row stride ldr, or NULL; may be y itself
+ *   y         shares no memory with the rows that are multiplied: their address gives
+ *             W8A8_ERR_UNSUPPORTED (w8a8_fp8b_linear_fused, which quantizes a BF16 x
+ *             first, takes it)
  *   bias      device, BF16 [N] or NULL
  *   workspace the call's workspace_bytes, 256-byte aligned, rewritten: sums of a K
  *             that is split over workgroups, rows copied to 16-byte alignment (0 bytes:

@@ -1236,7 +1236,8 @@ int w8a8_fp8b_linear_fused(const void* x, int64_t ldx, const float* x_scale, int
     if (!workspace || ws_bytes < need || !aligned(workspace, 256))
       return fail(W8A8_ERR_WORKSPACE, "fp8b_linear: BF16 input needs %lld workspace bytes (256-byte aligned), got %lld",
                   (long long)need, (long long)ws_bytes);
-    if (w8a8::fp8b_fused_ok(M, K)) {
+    // (over x itself y is written behind the quantizer's launch, not beside workgroups that read x)
+    if (w8a8::fp8b_fused_ok(M, K) && static_cast<const void*>(y) != x) {
       w8a8::Fp8bGemm p = fp8b_args(a, ldx, nullptr, M, M, K, w_packed, w_scale, N, y);
       p.bias = bias;
       p.act = act;
@@ -1560,6 +1561,7 @@ int run_fused(const char* who, const w8a8::FusedGemm& p, void* workspace, int64_
   if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256)))
     return fail(W8A8_ERR_WORKSPACE, "%s: needs %lld workspace bytes (256-byte aligned), got %lld", who, (long long)need,
                 (long long)ws_bytes);
+  if (p.y == p.a) return fail(W8A8_ERR_UNSUPPORTED, "%s: y lies over the rows, which every workgroup reads", who);
   return launched(w8a8::launch_fused_gemm(p, plan, workspace, (hipStream_t)stream), who);
 }
 
@@ -1737,6 +1739,7 @@ int w8a8_bf16_grouped_gemm(const uint16_t* x, int64_t ldx, int64_t x_rows, const
   if (!workspace || ws_bytes < need || !aligned(workspace, 256))
     return fail(W8A8_ERR_WORKSPACE, "bf16_grouped_gemm: needs %lld workspace bytes (256-byte aligned), got %lld",
                 (long long)need, (long long)ws_bytes);
+  if (y == x) return fail(W8A8_ERR_UNSUPPORTED, "bf16_grouped_gemm: y lies over the rows, which every workgroup reads");
   st = check_group_list("bf16_grouped_gemm", group_list, E, R, stream);
   if (st) return st;
   w8a8::FusedGemm p = fused_bf16(x, ldx, x_rows, R, K, w_packed, N, act);

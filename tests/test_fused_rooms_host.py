@@ -91,6 +91,16 @@ def test_plan_refusals(w):
         assert st == OK and p.tiles == p.workspace_bytes == 0
 
 
+def test_output_over_the_rows_is_refused(w):
+    """The workgroups of other columns still read the rows that one has written."""
+    L, a, b = w.lib, ctypes.c_void_p(P), ctypes.c_void_p(2 * P)
+    for M in (1, 64, 8192):
+        assert L.w8a8_bf16_linear(a, 4096, M, 4096, b, 4096, None, 0, a, 4096, a, 4096, 0, b, 1 << 30, None) == UNSUPPORTED
+        assert b"y lies over the rows" in L.w8a8_last_error()
+        assert L.w8a8_linear_fused(a, 4096, b, M, 4096, b, b, 64, None, 0, None, 0, a, 64, b, 1 << 30, None) == UNSUPPORTED
+    assert L.w8a8_bf16_grouped_gemm(a, 256, 8, None, b, 8, 2, 256, 256, b, 0, a, b, 1 << 20, None) == UNSUPPORTED
+
+
 def test_fp8_plan(w):
     p = w.Plan()
     for M, N, K, codes, tile in [(1, 4096, 7168, False, (16, 16)), (1, 16384, 7168, False, (16, 32)),

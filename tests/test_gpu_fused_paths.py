@@ -245,3 +245,20 @@ def test_sigmoid_tails_hold_their_relative_bound_until_they_vanish(w, act):
     assert near.any() and (~near).any()
     assert (off <= (6 * np.minimum(np.abs(t), 90) + 8) * U * np.abs(want))[near].all()
     assert (off[~near] <= 2.0 ** -118).all() and (y[~near] <= 0).all()
+
+
+@pytest.mark.parametrize("M,K", [(1, 4224), (1, 8192), (2, 300), (4, 2048), (16, 512), (17, 512), (200, 640)])
+def test_fp8_linear_over_its_rows(w, M, K):
+    """x, the residual and y are one buffer: x is quantized before any of y is written."""
+    show(f"fp8 {M} x {K} x {K} over its rows")
+    rng = np.random.default_rng(M + K)
+    x = _acts(rng, M, K)
+    cw = O.mx.e4m3_encode(np.clip(rng.standard_normal((K, K)) * 100.0, -448, 448))
+    sw = (rng.uniform(0.5, 1.5, (O.fp8b.blocks(K), O.fp8b.blocks(K))) / (100 * math.sqrt(K))).astype(np.float32)
+    wp, swd, xd = w.fp8b_prepack_weight(dev(cw)), dev(sw), bf16_dev(x)
+    want = w.fp8b_linear_fused(xd, wp, swd, K, act=w.ACT_SILU, residual=xd)
+    for _ in range(3):
+        h = bf16_dev(x)
+        w.fp8b_linear_fused(h, wp, swd, K, act=w.ACT_SILU, residual=h, y=h)
+        sync()
+        assert torch.equal(h.view(torch.int16), want.view(torch.int16))
