@@ -781,7 +781,10 @@ int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* resid
  *   x_scale float [M] (from w8a8_dynamic_quant_ld or w8a8_rms_norm_quant), a weight
  *   from w8a8_prepack_weight (E = 1) with w_scale float [N]; v = fl32(fl32(fp32(acc)
  *   x_scale[m]) w_scale[n]) (+ bias, fl32), acc exact. Without activation and
- *   residual bit for bit w8a8_linear.
+ *   residual bit for bit w8a8_linear, and faster from some rows on (64 x 4096 x 7168
+ *   11.7 us against 14.9, 333 x 1000 x 2048 5.4 against 36, 8192 x 4096 x 7168 201 against
+ *   228; one row 7.7 against 7.2). w8a8_linear takes BF16 rows and packed codes (191.7 for
+ *   the last) and gives INT32.
  * w8a8_fp8b_linear_fused: w8a8_fp8b_linear with the epilogue; the same arguments,
  *   workspace and products. w8a8_fp8b_linear_plan: of either, for E4M3 rows (x_scale not
  *   NULL; not read) or BF16 ones.

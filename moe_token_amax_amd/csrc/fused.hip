@@ -687,8 +687,10 @@ __global__ __launch_bounds__(256) void fused_join_kernel(FusedGemm p, int S, int
 // wavefronts take every eighth step, with U steps of weights and rows in flight each,
 // straight from global memory into operand registers and each set refilled as soon as
 // it is multiplied, and their sums meet in LDS in a fixed order. Bound by the weights'
-// stream (BF16 1 x 4096 x 7168 9.4 us, 6.2 TB/s) and with tens of rows by what the L2 hands
-// a CU (256 x 256 x 7168: 4 KB a step, 8.2 us).
+// stream (BF16 1 x 4096 x 7168: 12.7 us with the weights in HBM, 4.6 TB/s; 9.2 to 10.5 with
+// them in the memory-side cache) and with tens of rows by what the L2 hands a CU, 32 bytes a
+// clock (256 x 256 x 7168: 4 KB a step, 458 KB a CU, 8.0 us; INT8 64 x 4096 x 7168: as much in
+// tiles of 32 x 32, 11.6 from HBM).
 // ---------------------------------------------------------------------------
 constexpr int kDecodeWaves = 8;
 
@@ -1155,8 +1157,8 @@ constexpr int kSpreadTiles = 64;
 
 // NBW 2: tiles of 128 rows x 256 columns, and wide ones; NBW 1: 64 rows x 128 columns,
 // for products that would not fill the chip with those. 128 rows over 256 experts of 4096 x
-// 4096 524 us (the weights at 6.2 TB/s); 16384 rows over 64 such experts 726 (0.76
-// PFLOP/s: experts' last rows in lower tiles, 3.2 GB from HBM where 2.2 would do). Walking on
+// 4096 524 us (the weights at 6.1 TB/s); 16384 rows over 64 such experts 726 (0.76
+// PFLOP/s: experts' last rows in lower tiles, 3.2 GB past the L2s where 2.2 would do). Walking on
 // from wide tile to wide tile, as the dense kernel does, gained nothing (749, 754).
 template <int TY, int NBW>
 __global__ __launch_bounds__(512) void fused_grouped_kernel(FusedGemm p, int NT) {
@@ -1213,9 +1215,11 @@ bool fused_rows_ok(const FusedGemm& p) {
 
 enum FusedKernel { kDecode16, kDecode16x32, kDecode32, kDecode64, kTile32, kTile64, kTile64x256, kTile128, kTile256 };
 
-// What a product takes with each kernel, in us, by a model fitted to 1500 products of
-// either type, M 1 .. 8192, N 32 .. 16384, K 64 .. 16384 (the kernel it picks is 1.7 %
-// slower in the mean than the best of them, in one product of a hundred 1.3 times):
+// What a product takes with each kernel, in us, by a model fitted to measured products of
+// either type, M 1 .. 8192, N 32 .. 16384, K 64 .. 16384. Over 6375 others the kernel it
+// picks is 1.9 % slower in the mean than the best of them, in one of a hundred 1.3 times, at
+// worst 1.9 times (2183 x 205 x 10144); it ranks the kernels, as a time it is 0.85 to 1.12 of
+// the measured one for eight of ten:
 //   launch + rounds * round + steps * max(first, filling * step) + (split) join + parts
 // rounds: workgroups over twice the CUs (wide: whole turns of one workgroup a CU); steps:
 // 128-byte steps of K a workgroup goes through; first: such a step where the chip is not

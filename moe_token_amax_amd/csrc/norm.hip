@@ -161,7 +161,10 @@ __device__ __forceinline__ void write_chunk(const NormArgs& p, int64_t row, int 
 // WPR wavefronts a row, CPL chunks of 8 values a lane: the row stays in registers
 // between the sum, the maximum and the codes, and is read once. A workgroup walks over
 // its rows and keeps the weight of its columns. HBM-bound: 8192 x 7168 with residual to
-// INT8 97 us (411 MB, 4.25 TB/s; a copy 5.3), to E4M3 88; one row 4.7 (two sums, a launch).
+// INT8 97 us (411 MB, 4.25 TB/s; a copy 5.3), to E4M3 87, MX 84, BF16 alone 92 (470 MB); one
+// row 4.7 (a sum and a maximum over 16 wavefronts, one behind the other, and a launch), MX
+// 4.2, BF16 3.7. Odd addresses double the L1's look-ups, not the time (1237 x 4096 to E4M3
+// and BF16 13.2, with rows 4097 apart 13.7).
 template <int FMT, int CPL, int WPR>
 __global__ __launch_bounds__(WPR >= 4 ? WPR * kWave : 256) void rms_norm_kernel(NormArgs p) {
   constexpr int kThreadsRow = WPR * kWave, kRows = WPR >= 4 ? 1 : 4 / WPR;
@@ -312,7 +315,7 @@ static void launch(const NormArgs& p, hipStream_t stream) {
 // chunks a lane 5.2). Many: more chunks a lane, so that fewer wavefronts meet at a barrier
 // for each row (8192 x 7168 101 us, with a wavefront for every 64 chunks 127; 1024 x 7168
 // 22.4 both ways), and no more than a row has (1237 x 4097 to E4M3 16.3 with three a lane,
-// 17.6 with four).
+// 17.6 with four; the third is nearly empty there, 4096 columns take 13.2).
 template <int FMT>
 static hipError_t launch_format(const NormArgs& p, hipStream_t stream) {
   const int64_t chunks = FMT == kNormFp8b ? ceil_div(p.K, 128) * 16 : ceil_div(p.K, 8);
