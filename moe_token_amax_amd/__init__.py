@@ -1337,18 +1337,20 @@ def fp8b_linear_fused(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Te
         if K is not None and K != Kx:
             raise ValueError("K must be the width of a BF16 x")
         K = Kx
+        B = -(-K // 128)
     else:
         at, ldx = _rows_at(x, torch.uint8, "x")
         M = x.shape[0]
         K = x.shape[1] if K is None else K
-        if x.shape[1] != 128 * _fp8_blocks(K):
+        B = -(-K // 128)
+        if x.shape[1] != 128 * B:
             raise ValueError("E4M3 x must be [M, K rounded up to 128]")
-        if x_scale.shape != (_fp8_blocks(K), M):
+        if x_scale.shape != (B, M):
             raise ValueError("x_scale must be [ceil(K/128), M]")
     wp = _at(w_packed, torch.uint8, "w_packed", 1)
-    if w_packed.numel() < _fp8_packed(1, N, K):
+    if w_packed.numel() < 2048 * B * -(-N // 16):
         raise ValueError("w_packed too small for [N, K]")
-    if w_scale.shape != (_fp8_blocks(N), _fp8_blocks(K)):
+    if w_scale.shape != (-(-N // 128), B):
         raise ValueError("w_scale must be [ceil(N/128), ceil(K/128)]")
     if bias is not None and bias.shape != (N,):
         raise ValueError("bias shape mismatch")
@@ -1357,9 +1359,9 @@ def fp8b_linear_fused(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Te
     if y.shape != (M, N):
         raise ValueError("y shape mismatch")
     yp, ldy = _rows_at(y, torch.bfloat16, "y")
-    rp, ldr = _residual(residual, (M, N))
+    rp, ldr = (None, 0) if residual is None else _residual(residual, (M, N))
     room, ws, ws_n = (None, None, 0) if x_scale is not None else \
-        _room(workspace, x.device, fp8b_linear_workspace_bytes, M, N, K)
+        _room(workspace, x.device, lib.w8a8_fp8b_linear_workspace_bytes, M, N, K)
     _check(lib.w8a8_fp8b_linear_fused(at, ldx, _at(x_scale, torch.float32, "x_scale", 2), M, K, wp,
                                       _at(w_scale, torch.float32, "w_scale", 2), N,
                                       _at(bias, torch.bfloat16, "bias", 1), act, rp, ldr, yp, ldy, scale_alg, ws, ws_n,
