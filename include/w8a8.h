@@ -763,7 +763,8 @@ int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* resid
  *             argument; where t < -87, 0 may stand for a value under 2^-118 (SwiGLU: |up|
  *             2^-118). GELU: within 2^-21 |v|, its far negative tail therefore right absolutely
  *             and not relatively (off by 0.05 % of the value at -4, 0.4 % at -6, 2 % at -10).
- *             W8A8_ACT_SWIGLU only on BF16 weights prepacked for it
+ *             inf stays inf, -inf gives NaN (ReLU: 0), NaN stays NaN. W8A8_ACT_SWIGLU only on
+ *             BF16 weights prepacked for it
  *   residual  device, BF16 [M, outputs], row stride ldr, or NULL; may be y itself
  *   y         shares no memory with the rows that are multiplied: their address gives
  *             W8A8_ERR_UNSUPPORTED (w8a8_fp8b_linear_fused, which quantizes a BF16 x

@@ -40,6 +40,8 @@ def test_aligned_rows_need_no_room_for_a_copy(w, kind):
     for kw in (dict(at=P + 2), dict(ld=7170)):
         p = _plan(w, kind, 8192, 4096, 7168, **kw)
         assert p.copied == 1 and p.workspace_bytes == 8192 * bytes_row
+    p = _plan(w, kind, 8192, 4096, 7168, ld=1 << 24)                  # past 32-bit offsets in a tile
+    assert p.copied == 1 and p.workspace_bytes == 8192 * bytes_row
     p = _plan(w, kind, 8192, 4096, 7166)
     assert p.copied == 1 and p.workspace_bytes == 8192 * bytes_row    # to whole steps of 128 bytes
 

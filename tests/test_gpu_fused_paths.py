@@ -262,3 +262,39 @@ def test_fp8_linear_over_its_rows(w, M, K):
         w.fp8b_linear_fused(h, wp, swd, K, act=w.ACT_SILU, residual=h, y=h)
         sync()
         assert torch.equal(h.view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("E", [1021, 1023, 1024])
+def test_grouped_with_as_many_experts_as_there_can_be(w, E):
+    """The list's four experts a thread: the last ones among them, most of them empty."""
+    rng = np.random.default_rng(E)
+    N, K = 40, 72
+    counts = rng.integers(0, 3, E) * (rng.random(E) < 0.4)
+    counts[[0, E - 3, E - 1]] = 70, 5, 33
+    R = int(counts.sum()) + 3
+    x, wt = _acts(rng, R, K), _bf16(rng, E, N, K, scale=1 / math.sqrt(K))
+    y = torch.full((R, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    w.bf16_grouped_gemm(bf16_dev(x), dev(counts.astype(np.int64)), w.bf16_prepack_weight(bf16_dev(wt)), N, y=y)
+    sync()
+    assert (y[R - 3:] == 7).all()
+    e = np.repeat(np.arange(E), counts)
+    xs, ws = _f64(x[:R - 3]), _f64(wt)[e]
+    v, A = (ws * xs[:, None]).sum(2), np.abs(ws * xs[:, None]).sum(2)
+    _hold(y[:R - 3], v, 6 * math.sqrt(K) * U * A)
+
+
+@pytest.mark.parametrize("act", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_activations_of_infinities(w, act):
+    """inf stays, -inf times 0 is NaN (ReLU: 0), NaN stays; zeros stay zeros."""
+    v = np.array([0x7F80, 0xFF80, 0x7FC0, 0x0000, 0x8000] * 16, np.uint16)
+    wt = np.zeros((len(v), 16), np.uint16)
+    wt[:, 0] = v
+    wp = w.bf16_prepack_weight(bf16_dev(wt))
+    for M in (1, 40, 200):
+        x = np.zeros((M, 16), np.uint16)
+        x[:, 0] = 0x3F80
+        y = w.bf16_linear(bf16_dev(x), wp, len(v), act=_act_id(w, act), out=w.OUT_F32)
+        sync()
+        y = y.cpu().numpy().reshape(M, 16, 5)
+        assert (y[..., 0] == np.inf).all() and np.isnan(y[..., 2]).all() and (y[..., 3:] == 0).all()
+        assert (y[..., 1] == 0).all() if act == "relu" else np.isnan(y[..., 1]).all()
