@@ -776,7 +776,8 @@ int w8a8_mx_rms_norm_quant(const uint16_t* x, int64_t ldx, const uint16_t* resid
  *             bytes of a call on these rows (their address and stride; nothing is read):
  *             none for aligned rows of a product whose K is not split, where workspace_bytes
  *             counts their copy. workspace_bytes never falls as M grows: a room for the
- *             most rows serves every batch of the same N and K
+ *             most rows serves every batch of the same N and K (a query of 10 to 300 us on
+ *             the host, to be made once)
  *
  * w8a8_linear_fused [DSV4 §二 npu_quant_matmul]: INT8 codes q [M, K], row stride ldq,
  *   x_scale float [M] (from w8a8_dynamic_quant_ld or w8a8_rms_norm_quant), a weight
